@@ -355,6 +355,110 @@ int pkv_paged_attention_decode_chunked(void* out, const void* q, const int32_t* 
                                        void* workspace, size_t workspace_bytes, int32_t* device_status,
                                        void* stream);
 
+/* ==== Rotary position embedding ==============================================
+ *
+ * The step between a layer's query/key projection and its cache. The first
+ * rotary_dim dimensions of a row form rotary_dim/2 pairs, (i, i + rotary_dim/2) or, when
+ * `interleaved` is not 0, (2i, 2i + 1). At position p pair i turns by a = p * inv_freq[i]:
+ *     y_re = attn_factor * (x_re cos a - x_im sin a)
+ *     y_im = attn_factor * (x_re sin a + x_im cos a)
+ * in fp32, rounded once; the other dimensions are copied. Angles are reduced exactly (a
+ * position times a 64-bit fraction of a turn), so they hold at any position an int64
+ * names, negative ones too.
+ *
+ *   positions       [num_tokens], int32 (position_bytes 4) or int64 (8).
+ *   inv_freq        [rotary_dim / 2] double, device: radians per position. Scalings for
+ *                   long contexts (interpolated or banded frequencies) are in these numbers.
+ *   rotary_dim      a multiple of 16, at most the head size (64 or 128).
+ *   attn_factor     finite; 1 unless a scaling asks for another.
+ *   ..._stride      elements from one token's row to the next: a multiple of 8, at least
+ *                   heads * head_size (so a packed QKV projection is read in place). Rows
+ *                   are 16-byte aligned; a token's heads are contiguous.
+ *
+ * pkv_rotary_embed turns rows of num_heads heads from x into out (out == x with the same
+ * stride turns in place; any other overlap is undefined). inverse != 0 turns by -a: with
+ * it the call is the transpose of the forward one, which is its gradient.
+ *
+ * pkv_rotary_write turns a step's queries into q_out (q_out == q with the same stride
+ * allowed) and writes its turned keys and its values to their slots of the cache, as
+ * pkv_kv_cache_write / _int8 do (slot -1 skips the cache write, not the query; other
+ * out-of-range slots are skipped and flagged PKV_DEV_BAD_SLOT; two tokens on one slot
+ * race). Allowed (src_dtype, kv_dtype): (FP16, FP16), (BF16, BF16), (FP16, FP8_E5M2),
+ * (FP16, INT8; with `scales`, else NULL). A turned key goes from fp32 to the cache's type in
+ * one rounding (a pkv_rotary_embed followed by a cache write rounds to 16 bits between). */
+int pkv_rotary_embed(void* out, int64_t out_stride, const void* x, int64_t x_stride, pkv_dtype dtype,
+                     int32_t num_tokens, int32_t num_heads, int32_t head_size, const void* positions,
+                     int32_t position_bytes, const double* inv_freq, int32_t rotary_dim, int32_t interleaved,
+                     float attn_factor, int32_t inverse, void* stream);
+int pkv_rotary_write(void* q_out, int64_t q_out_stride, const void* q, int64_t q_stride, const void* key,
+                     int64_t key_stride, const void* value, int64_t value_stride, pkv_dtype src_dtype,
+                     int32_t num_tokens, int32_t num_q_heads, const void* positions, int32_t position_bytes,
+                     const int32_t* slot_mapping, const double* inv_freq, int32_t rotary_dim, int32_t interleaved,
+                     float attn_factor, void* k_cache, void* v_cache, float* scales, pkv_dtype kv_dtype,
+                     const pkv_cache_desc* cache, int32_t* device_status, void* stream);
+
+/* ==== Attention of a chunk of new tokens (prefill) ============================
+ *
+ * pkv_paged_attention_prefill — causal attention of every sequence's newest n_s tokens
+ * over its blocks: whole prompts, chunks of a prompt behind a cached past, single decode
+ * rows beside them. The counts are in DEVICE memory and unlimited; long chunks run on
+ * tcgen05 tensor cores at compute rates (the _chunked call above serves the same batches
+ * with host-side counts, through the decode kernels).
+ *
+ *   cu_q_lens     [num_seqs + 1] int32, device: sequence s owns rows cu_q_lens[s] ..
+ *                 cu_q_lens[s+1]-1 of q and out; n_s = 0 is allowed (no rows). A range that
+ *                 is decreasing or leaves [0, num_q_rows] gives the sequence no rows and sets
+ *                 PKV_DEV_BAD_CTX. Rows that no sequence owns are left as they are.
+ *   out, q        [num_q_rows][num_q_heads][head_size], contiguous, 16-byte aligned; bf16
+ *                 for a bf16 cache, else fp16. out must not overlap q or the cache.
+ *   context_lens  [num_seqs] int32, device: cached tokens INCLUDING the n_s new ones. Token
+ *                 j sees positions p <= context_lens[s] - n_s + j. Outside [n_s,
+ *                 max_blocks_per_seq * 16] it is clamped to [0, max_blocks_per_seq * 16]
+ *                 and flagged PKV_DEV_BAD_CTX; a token that sees no position gets zeros.
+ *   scales        an INT8 cache's row scales, else NULL.
+ *   scale         > 0 and finite.
+ *   workspace     device, 16-byte aligned, at least pkv_prefill_workspace_bytes(num_q_rows,
+ *                 num_seqs, num_q_heads, cache) bytes on the CURRENT device. As for the
+ *                 decode calls: contents need no initialisation, calls in flight at the
+ *                 same time must not share one, and a captured call may be replayed.
+ *   num_q_heads / num_kv_heads <= 64; num_q_rows * num_q_heads < 2^31.
+ * Scores, softmax statistics and sums are fp32; the probabilities enter the P V product in
+ * the query type. What lies behind a row's last visible position, in its blocks or in
+ * later tokens of its chunk, does not reach it, infinities and NaN included. */
+size_t pkv_prefill_workspace_bytes(int32_t num_q_rows, int32_t num_seqs, int32_t num_q_heads,
+                                   const pkv_cache_desc* cache);
+int pkv_paged_attention_prefill(void* out, const void* q, const int32_t* cu_q_lens, int32_t num_q_rows,
+                                int32_t num_seqs, int32_t num_q_heads, const void* k_cache, const void* v_cache,
+                                const float* scales, pkv_dtype kv_dtype, const pkv_cache_desc* cache,
+                                const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* context_lens,
+                                float scale, void* workspace, size_t workspace_bytes, int32_t* device_status,
+                                void* stream);
+
+/* ==== Accepting verified drafts ================================================
+ *
+ * pkv_kv_cache_accept — the cache side of a speculative verify (pkv_paged_attention_decode,
+ * _varlen or _tree): sequence s's last n_s positions hold its drafts; the accepted ones, in
+ * the order given, move together behind the context:
+ *     row base + i  <-  row base + accepted[s][i],  i < num_accepted[s],  base = context_lens[s] - n_s
+ * for every KV head of both caches (and an INT8 cache's row scales), all rows read before any
+ * is written, so any order and repeated indices are allowed; new_context_lens[s] = base +
+ * num_accepted[s]. Rows behind the new length keep what they held.
+ *
+ *   cu_q_lens     [num_seqs + 1] int32, device: n_s = cu_q_lens[s+1] - cu_q_lens[s], in
+ *                 [0, max_q_per_seq]; NULL: n_s = max_q_per_seq. max_q_per_seq <= 64.
+ *   accepted      [num_seqs][max_accepted] int32, device: draft indices in [0, n_s).
+ *   num_accepted  [num_seqs] int32, device, in [0, min(max_accepted, n_s)].
+ *   new_context_lens  [num_seqs] int32, device, or NULL; must not overlap context_lens.
+ * A sequence that breaks a rule on the device (an index or count out of range, context_lens
+ * outside [n_s, max_blocks_per_seq * 16]: PKV_DEV_BAD_CTX; a block id out of range:
+ * PKV_DEV_BAD_BLOCK) is left as it is, new_context_lens[s] = context_lens[s]. Blocks holding
+ * drafts must not be shared between sequences (pkv_seq_append sees to that). */
+int pkv_kv_cache_accept(void* k_cache, void* v_cache, float* scales, pkv_dtype kv_dtype, const pkv_cache_desc* cache,
+                        const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* context_lens,
+                        const int32_t* cu_q_lens, int32_t num_seqs, int32_t max_q_per_seq, const int32_t* accepted,
+                        int32_t max_accepted, const int32_t* num_accepted, int32_t* new_context_lens,
+                        int32_t* device_status, void* stream);
+
 /*
  * pkv_selftest_bounded_wait — exercises, on the device, the bounded wait every
  * decode kernel puts on its pipeline barriers: one thread waits on an mbarrier
@@ -427,6 +531,11 @@ int32_t pkv_seq_block_table(const pkv_allocator* a, int64_t seq, int32_t* out, i
  * evictable blocks) is too small, with nothing changed. */
 int pkv_seq_append(pkv_allocator* a, int64_t seq, int32_t n, int32_t* slots, int32_t* copy_src,
                    int32_t* copy_dst, int32_t* num_copies);
+
+/* Shortens the sequence to its first n tokens (rejected drafts of a speculative verify, a
+ * rolled-back answer); blocks that hold none of them lose one reference each.
+ * PKV_ERR_INVALID_ARGUMENT if the sequence is unknown or shorter than n. */
+int pkv_seq_truncate(pkv_allocator* a, int64_t seq, int32_t n);
 
 /* Prefix cache. pkv_prefix_insert caches the sequence's full blocks holding its
  * first n tokens (token ids in tokens[0..n)), under the chain of their

@@ -24,4 +24,5 @@ from .api import (  # noqa: F401
     library_path, load_library, alloc_kv_cache, PagedKVError,
     BlockAllocator, copy_blocks,
     alloc_kv_scales, kv_cache_write_int8, paged_attention_decode_int8, int8_codes,
+    rotary_inv_freq, rotary_embed, rotary_write, paged_attention_prefill, prefill_workspace_bytes, kv_cache_accept,
 )

@@ -98,6 +98,8 @@ def load_library(path: str | None = None):
         lib.pkv_seq_block_table.restype = i32
         lib.pkv_seq_append.argtypes = [vp, i64, i32, vp, vp, vp, vp]
         lib.pkv_seq_append.restype = ctypes.c_int
+        lib.pkv_seq_truncate.argtypes = [vp, i64, i32]
+        lib.pkv_seq_truncate.restype = ctypes.c_int
         lib.pkv_prefix_insert.argtypes = [vp, i64, vp, i32]
         lib.pkv_prefix_insert.restype = i32
         lib.pkv_seq_add_cached.argtypes = [vp, i64, vp, i32, vp]
@@ -124,6 +126,20 @@ def load_library(path: str | None = None):
             vp, vp, vp, vp, i32, i32, vp, vp, vp, ctypes.c_int, P(_CacheDesc), vp, i32, ctypes.c_float, vp,
             ctypes.c_size_t, vp, vp]
         lib.pkv_paged_attention_decode_chunked.restype = ctypes.c_int
+        cint, f32 = ctypes.c_int, ctypes.c_float
+        lib.pkv_rotary_embed.argtypes = [vp, i64, vp, i64, cint, i32, i32, i32, vp, i32, vp, i32, i32, f32, i32, vp]
+        lib.pkv_rotary_embed.restype = cint
+        lib.pkv_rotary_write.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, cint, i32, i32, vp, i32, vp, vp, i32,
+                                         i32, f32, vp, vp, vp, cint, P(_CacheDesc), vp, vp]
+        lib.pkv_rotary_write.restype = cint
+        lib.pkv_prefill_workspace_bytes.argtypes = [i32, i32, i32, P(_CacheDesc)]
+        lib.pkv_prefill_workspace_bytes.restype = ctypes.c_size_t
+        lib.pkv_paged_attention_prefill.argtypes = [vp, vp, vp, i32, i32, i32, vp, vp, vp, cint, P(_CacheDesc), vp,
+                                                    i32, vp, f32, vp, ctypes.c_size_t, vp, vp]
+        lib.pkv_paged_attention_prefill.restype = cint
+        lib.pkv_kv_cache_accept.argtypes = [vp, vp, vp, cint, P(_CacheDesc), vp, i32, vp, vp, i32, i32, vp, i32, vp,
+                                            vp, vp, vp]
+        lib.pkv_kv_cache_accept.restype = cint
         lib.pkv_selftest_bounded_wait.argtypes = [vp, ctypes.c_uint64, vp, vp]
         lib.pkv_selftest_bounded_wait.restype = ctypes.c_int
         lib.pkv_error_string.argtypes = [ctypes.c_int]
@@ -589,6 +605,278 @@ def paged_attention_decode_tree(out, q, tree_masks, k_cache, v_cache, block_tabl
 
 
 # ------------------------------------------------------------------------------------
+# Rotary embedding, prefill attention, acceptance of drafts
+# ------------------------------------------------------------------------------------
+
+def rotary_inv_freq(rotary_dim: int, base: float = 10000.0, *, scaling: str | None = None, factor: float = 1.0,
+                    original_context: int | None = None, low: float = 1.0, high: float | None = None,
+                    device=None):
+    """Frequencies of a rotary embedding: (inv_freq float64 [rotary_dim / 2], attn_factor).
+
+    inv_freq[i] = base^(-2i / rotary_dim) radians per position, changed for a context
+    ``factor`` times as long by ``scaling``:
+
+    * ``"linear"``: every frequency divided by factor.
+    * ``"base"``: base * factor^(rotary_dim / (rotary_dim - 2)), which divides the lowest
+      frequency by factor and leaves the highest.
+    * ``"bands"``: by the turns a pair makes over ``original_context`` positions:
+      at least ``high`` (default 4): kept; at most ``low`` (1): divided by factor; linear in
+      the turns between.
+    * ``"ramp"``: as bands with ``high`` 32, but linear in the pair's index between, and
+      attn_factor = 0.1 ln(factor) + 1.
+    """
+    rd = int(rotary_dim)
+    if rd < 2 or rd % 2 or not base > 0 or not factor > 0:
+        raise PagedKVError("rotary_dim must be even and positive, base and factor positive")
+    if scaling not in (None, "linear", "base", "bands", "ramp"):
+        raise PagedKVError(f"unknown rotary scaling {scaling!r}")
+    if scaling in ("bands", "ramp") and not (original_context and original_context > 0):
+        raise PagedKVError(f"scaling {scaling!r} needs original_context")
+    if scaling == "base":
+        if rd == 2:
+            raise PagedKVError("scaling 'base' needs rotary_dim > 2")
+        base = base * factor ** (rd / (rd - 2))
+    i = np.arange(rd // 2, dtype=np.float64)
+    inv = base ** (-2.0 * i / rd)
+    attn = 1.0
+    if scaling == "linear":
+        inv = inv / factor
+    elif scaling in ("bands", "ramp"):
+        high = (4.0 if scaling == "bands" else 32.0) if high is None else high
+        if not high > low > 0:
+            raise PagedKVError("the bands need high > low > 0")
+        if scaling == "bands":
+            keep = (original_context * inv / (2 * np.pi) - low) / (high - low)
+        else:
+            # the (fractional) pair that makes r turns: base^(-2i/rd) * context = 2 pi r
+            def pair(r):
+                return rd * np.log(original_context / (2 * np.pi * r)) / (2 * np.log(base))
+            first, last = max(np.floor(pair(high)), 0.0), min(np.ceil(pair(low)), rd - 1.0)
+            keep = 1.0 - (i - first) / max(last - first, 1e-3)
+            attn = 0.1 * float(np.log(factor)) + 1.0 if factor > 1 else 1.0
+        keep = np.clip(keep, 0.0, 1.0)
+        inv = inv * keep + inv / factor * (1.0 - keep)
+    return torch.from_numpy(inv).to(device=device or "cuda"), attn
+
+
+def _same_device(ref, tensors):
+    for n, t in tensors:
+        if t is not None and t.device != ref.device:
+            raise PagedKVError(f"{n} is on {t.device}, not on {ref.device}")
+
+
+def _status_word(status):
+    if status is not None and (status.dtype != torch.int32 or status.numel() < 1):
+        raise PagedKVError("device_status must be an int32 tensor")
+
+
+def _head_rows(name, t, heads=None, head_size=None) -> int:
+    """Token stride of a [tokens, heads, head_size] tensor whose tokens hold contiguous heads."""
+    if not t.is_cuda:
+        raise PagedKVError(f"{name} must be a CUDA tensor")
+    if t.dim() != 3 or (heads is not None and int(t.shape[1]) != heads) or \
+            (head_size is not None and int(t.shape[2]) != head_size):
+        raise PagedKVError(f"{name} must be [tokens, {heads or 'heads'}, {head_size or 'head_size'}], "
+                           f"got {tuple(t.shape)}")
+    H, D = int(t.shape[1]), int(t.shape[2])
+    if t.stride(2) != 1 or (H > 1 and t.stride(1) != D):
+        raise PagedKVError(f"the heads of a token of {name} must be contiguous")
+    stride = int(t.stride(0)) if int(t.shape[0]) > 1 else H * D
+    if stride < H * D or stride % 8:
+        raise PagedKVError(f"the tokens of {name} must be at least a row apart, in multiples of 8 elements")
+    return stride
+
+
+def _rotary_inputs(x, positions, inv_freq, attn_factor):
+    for n, t in (("positions", positions), ("inv_freq", inv_freq)):
+        _need_cuda_contig(n, t)
+    if positions.dtype not in (torch.int32, torch.int64) or positions.dim() != 1 or \
+            int(positions.shape[0]) != int(x.shape[0]):
+        raise PagedKVError("positions must be int32 or int64, one per token")
+    if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1:
+        raise PagedKVError("inv_freq must be float64 [rotary_dim / 2]")
+    if not np.isfinite(attn_factor):
+        raise PagedKVError("attn_factor must be finite")
+    rd = 2 * int(inv_freq.shape[0])
+    if rd < 16 or rd % 16 or rd > int(x.shape[2]):
+        raise PagedKVError(f"rotary_dim = {rd} must be a multiple of 16, at most the head size {int(x.shape[2])}")
+    return rd, positions.element_size()
+
+
+def rotary_embed(out, x, positions, inv_freq, *, interleaved: bool = False, attn_factor: float = 1.0,
+                 inverse: bool = False, stream=None):
+    """Turn the first 2 * len(inv_freq) dimensions of x [T, H, D] (fp16 or bf16) by
+    positions[t] * inv_freq[i], pairs (i, i + half) or (2i, 2i + 1), times attn_factor; the rest is
+    copied. out may be x. ``inverse`` turns back (the gradient of the forward call)."""
+    xs, os_ = _head_rows("x", x), _head_rows("out", out, int(x.shape[1]), int(x.shape[2]))
+    if int(out.shape[0]) != int(x.shape[0]) or out.dtype != x.dtype:
+        raise PagedKVError("out must have the shape and dtype of x")
+    rd, pb = _rotary_inputs(x, positions, inv_freq, attn_factor)
+    _same_device(x, (("out", out), ("positions", positions), ("inv_freq", inv_freq)))
+    with _on_device(x.device):
+        rc = load_library().pkv_rotary_embed(
+            _ptr(out), os_, _ptr(x), xs, _src_code(x), int(x.shape[0]), int(x.shape[1]), int(x.shape[2]),
+            _ptr(positions), pb, _ptr(inv_freq), rd, int(bool(interleaved)), float(attn_factor),
+            int(bool(inverse)), _stream_handle(stream, x.device))
+    _check(rc, "rotary_embed")
+    return out
+
+
+def rotary_write(q_out, q, key, value, positions, slot_mapping, k_cache, v_cache, inv_freq, kv_dtype=None, *,
+                 interleaved: bool = False, attn_factor: float = 1.0, scales=None, device_status=None, stream=None):
+    """A layer's rotary embedding and cache write in one pass: q [T, Hq, D] turned into q_out
+    (which may be q), key [T, Hkv, D] turned and written with value to the slots of the cache.
+    The inputs may be views of one packed QKV tensor (token strides of any multiple of 8).
+    An INT8 cache takes its row scales."""
+    qs = _head_rows("q", q)
+    d = _pair(k_cache, v_cache)
+    Hkv, D = int(k_cache.shape[1]), int(k_cache.shape[3])
+    qos = _head_rows("q_out", q_out, int(q.shape[1]), D)
+    ks, vs = _head_rows("key", key, Hkv, D), _head_rows("value", value, Hkv, D)
+    for n, t in (("slot_mapping", slot_mapping), ("k_cache", k_cache), ("v_cache", v_cache)):
+        _need_cuda_contig(n, t)
+    T = int(q.shape[0])
+    if int(q.shape[2]) != D or any(int(t.shape[0]) != T for t in (q_out, key, value)):
+        raise PagedKVError("q, q_out, key and value must hold the same tokens at the cache's head size")
+    if not q.dtype == q_out.dtype == key.dtype == value.dtype:
+        raise PagedKVError("q, q_out, key and value must share a dtype")
+    if slot_mapping.dtype != torch.int32 or slot_mapping.dim() != 1 or int(slot_mapping.shape[0]) != T:
+        raise PagedKVError("slot_mapping must be int32 with one slot per token")
+    rd, pb = _rotary_inputs(q, positions, inv_freq, attn_factor)
+    code = _kv_code(kv_dtype, k_cache)
+    _int8_scales(code, k_cache, scales)
+    _status_word(device_status)
+    _same_device(q, (("q_out", q_out), ("key", key), ("value", value), ("positions", positions),
+                     ("slot_mapping", slot_mapping), ("k_cache", k_cache), ("v_cache", v_cache),
+                     ("inv_freq", inv_freq), ("scales", scales), ("device_status", device_status)))
+    with _on_device(q.device):
+        rc = load_library().pkv_rotary_write(
+            _ptr(q_out), qos, _ptr(q), qs, _ptr(key), ks, _ptr(value), vs, _src_code(q), T, int(q.shape[1]),
+            _ptr(positions), pb, _ptr(slot_mapping), _ptr(inv_freq), rd, int(bool(interleaved)),
+            float(attn_factor), _ptr(k_cache), _ptr(v_cache), _ptr(scales), code, ctypes.byref(d),
+            _ptr(device_status), _stream_handle(stream, q.device))
+    _check(rc, "rotary_write")
+    return q_out
+
+
+_prefill_workspaces: dict = {}
+_PREFILL_COUNTER_BYTES = 4096   # the start of the workspace, where the split counters are
+
+
+def _prefill_workspace(nbytes: int, device, stream) -> torch.Tensor:
+    """Scratch of a prefill call: one buffer per (device, stream the call runs on), grown as
+    needed. A call that is being captured gets a buffer of its own from the graph's memory
+    pool (its counters cleared by a captured fill), so two graphs, or a graph and eager calls,
+    never share one and a later growth takes nothing away from a captured graph."""
+    on = contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+    with on:
+        if torch.cuda.is_current_stream_capturing():
+            ws = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+            ws[:_PREFILL_COUNTER_BYTES].zero_()
+            return ws
+        key = (str(device), torch.cuda.current_stream(device).cuda_stream)
+        ws = _prefill_workspaces.get(key)
+        if ws is None or ws.numel() < nbytes:
+            ws = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
+            _prefill_workspaces[key] = ws
+        return ws
+
+
+def prefill_workspace_bytes(num_q_rows: int, num_seqs: int, num_q_heads: int, k_cache) -> int:
+    """Bytes of workspace paged_attention_prefill needs for this problem on the cache's device."""
+    d = _desc(k_cache)
+    with torch.cuda.device(k_cache.device):
+        return int(load_library().pkv_prefill_workspace_bytes(int(num_q_rows), int(num_seqs), int(num_q_heads),
+                                                              ctypes.byref(d)))
+
+
+def paged_attention_prefill(out, q, cu_q_lens, k_cache, v_cache, block_tables, context_lens, scale: float,
+                            kv_dtype=None, *, scales=None, workspace=None, device_status=None, stream=None):
+    """Causal attention of every sequence's newest tokens over its blocks: whole prompts,
+    chunks of a prompt, single decode rows beside them, packed without padding. Sequence s
+    owns rows cu_q_lens[s]..cu_q_lens[s+1]-1 of q/out [rows, Hq, D] (int32, on the device; any
+    count from 0) and its token j sees positions <= context_lens[s] - n_s + j. An INT8 cache
+    takes its row scales."""
+    for nm, t in (("out", out), ("q", q), ("cu_q_lens", cu_q_lens), ("k_cache", k_cache), ("v_cache", v_cache),
+                  ("block_tables", block_tables), ("context_lens", context_lens)):
+        _need_cuda_contig(nm, t)
+    if (block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32
+            or cu_q_lens.dtype != torch.int32):
+        raise PagedKVError("block_tables, context_lens and cu_q_lens must be int32")
+    d, S = _decode_shapes(out, q, k_cache, v_cache, block_tables, context_lens)
+    code = _kv_code(kv_dtype, k_cache)
+    want = torch.bfloat16 if code == KV_BF16 else torch.float16
+    if q.dtype != want or out.dtype != want:
+        raise PagedKVError(f"q and out must be {want} over this cache")
+    if cu_q_lens.dim() != 1 or int(cu_q_lens.shape[0]) != S + 1:
+        raise PagedKVError("cu_q_lens must have num_seqs + 1 entries")
+    _int8_scales(code, k_cache, scales)
+    _status_word(device_status)
+    _same_device(q, (("out", out), ("cu_q_lens", cu_q_lens), ("k_cache", k_cache), ("v_cache", v_cache),
+                     ("block_tables", block_tables), ("context_lens", context_lens), ("scales", scales),
+                     ("workspace", workspace), ("device_status", device_status)))
+    R, Hq = int(q.shape[0]), int(q.shape[1])
+    lib = load_library()
+    with _on_device(q.device):
+        if workspace is None:
+            need = int(lib.pkv_prefill_workspace_bytes(R, S, Hq, ctypes.byref(d)))
+            workspace = _prefill_workspace(need, q.device, stream)
+        rc = lib.pkv_paged_attention_prefill(
+            _ptr(out), _ptr(q), _ptr(cu_q_lens), R, S, Hq, _ptr(k_cache), _ptr(v_cache), _ptr(scales), code,
+            ctypes.byref(d), _ptr(block_tables), int(block_tables.shape[1]), _ptr(context_lens), float(scale),
+            _ptr(workspace), int(workspace.numel() * workspace.element_size()), _ptr(device_status),
+            _stream_handle(stream, q.device))
+    _check(rc, "paged_attention_prefill")
+    return out
+
+
+def kv_cache_accept(k_cache, v_cache, block_tables, context_lens, accepted, num_accepted, new_context_lens,
+                    max_q_per_seq: int, kv_dtype=None, *, cu_q_lens=None, scales=None, device_status=None,
+                    stream=None):
+    """Keep the accepted drafts of a speculative verify: with base = context_lens[s] - n_s, cache
+    row base + i of sequence s becomes row base + accepted[s, i] for i < num_accepted[s] (all
+    rows read before any is written) and new_context_lens[s] = base + num_accepted[s]. n_s is
+    max_q_per_seq, or from cu_q_lens. accepted: int32 [num_seqs, max_accepted]; new_context_lens
+    may be None. An INT8 cache's row scales move along."""
+    for nm, t in (("k_cache", k_cache), ("v_cache", v_cache), ("block_tables", block_tables),
+                  ("context_lens", context_lens), ("accepted", accepted), ("num_accepted", num_accepted),
+                  ("new_context_lens", new_context_lens), ("cu_q_lens", cu_q_lens)):
+        if t is None and nm in ("new_context_lens", "cu_q_lens"):
+            continue
+        _need_cuda_contig(nm, t)
+        if nm not in ("k_cache", "v_cache") and t.dtype != torch.int32:
+            raise PagedKVError(f"{nm} must be int32")
+    d = _pair(k_cache, v_cache)
+    if context_lens.dim() != 1:
+        raise PagedKVError("context_lens must be 1-D [num_seqs]")
+    S = int(context_lens.shape[0])
+    if block_tables.dim() != 2 or int(block_tables.shape[0]) < S:
+        raise PagedKVError(f"block_tables must be [num_seqs, max_blocks_per_seq], got {tuple(block_tables.shape)}")
+    if accepted.dim() != 2 or int(accepted.shape[0]) != S or num_accepted.dim() != 1 or \
+            int(num_accepted.shape[0]) != S:
+        raise PagedKVError("accepted must be [num_seqs, max_accepted] and num_accepted [num_seqs]")
+    if new_context_lens is not None and (new_context_lens.dim() != 1 or int(new_context_lens.shape[0]) != S):
+        raise PagedKVError("new_context_lens must be [num_seqs]")
+    if cu_q_lens is not None and (cu_q_lens.dim() != 1 or int(cu_q_lens.shape[0]) != S + 1):
+        raise PagedKVError("cu_q_lens must have num_seqs + 1 entries")
+    code = _kv_code(kv_dtype, k_cache)
+    _int8_scales(code, k_cache, scales)
+    _status_word(device_status)
+    _same_device(k_cache, (("v_cache", v_cache), ("block_tables", block_tables), ("context_lens", context_lens),
+                           ("accepted", accepted), ("num_accepted", num_accepted),
+                           ("new_context_lens", new_context_lens), ("cu_q_lens", cu_q_lens), ("scales", scales),
+                           ("device_status", device_status)))
+    with _on_device(k_cache.device):
+        rc = load_library().pkv_kv_cache_accept(
+            _ptr(k_cache), _ptr(v_cache), _ptr(scales), code, ctypes.byref(d), _ptr(block_tables),
+            int(block_tables.shape[1]), _ptr(context_lens), _ptr(cu_q_lens), S, int(max_q_per_seq), _ptr(accepted),
+            int(accepted.shape[1]), _ptr(num_accepted), _ptr(new_context_lens), _ptr(device_status),
+            _stream_handle(stream, k_cache.device))
+    _check(rc, "kv_cache_accept")
+    return new_context_lens
+
+
+# ------------------------------------------------------------------------------------
 # Block pool (host) and block copy (device)
 # ------------------------------------------------------------------------------------
 
@@ -658,6 +946,11 @@ class BlockAllocator:
         _check(rc, "seq_append")
         copies = [(int(src.value), int(dst.value))] if nc.value else []
         return [int(slots[i]) for i in range(int(n))], copies
+
+    def truncate(self, seq: int, length: int):
+        """Shorten the sequence to its first ``length`` tokens; blocks that hold none of
+        them lose one reference each."""
+        _check(self._lib.pkv_seq_truncate(self._h, int(seq), int(length)), "seq_truncate")
 
     def prefix_insert(self, seq: int, tokens) -> int:
         arr = (ctypes.c_int32 * max(len(tokens), 1))(*[int(t) for t in tokens])

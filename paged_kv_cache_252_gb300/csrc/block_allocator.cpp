@@ -286,6 +286,18 @@ int pkv_seq_append(pkv_allocator* a, int64_t seq, int32_t n, int32_t* slots, int
   return PKV_OK;
 }
 
+int pkv_seq_truncate(pkv_allocator* a, int64_t seq, int32_t n) {
+  if (!a || n < 0) return PKV_ERR_INVALID_ARGUMENT;
+  auto it = a->seqs.find(seq);
+  if (it == a->seqs.end() || n > it->second.len) return PKV_ERR_INVALID_ARGUMENT;
+  Seq& s = it->second;
+  const size_t keep = static_cast<size_t>(blocks_for(n));
+  for (size_t k = keep; k < s.blocks.size(); ++k) a->dec_ref(s.blocks[k]);
+  s.blocks.resize(keep);
+  s.len = n;
+  return PKV_OK;
+}
+
 int32_t pkv_prefix_insert(pkv_allocator* a, int64_t seq, const int32_t* tokens, int32_t n) {
   if (!a || n < 0 || (n > 0 && !tokens)) return PKV_ERR_INVALID_ARGUMENT;
   auto it = a->seqs.find(seq);

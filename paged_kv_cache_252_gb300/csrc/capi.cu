@@ -275,6 +275,27 @@ cudaError_t launch(const void* fn, dim3 grid, dim3 block, size_t smem, cudaStrea
 
 }  // namespace
 
+namespace pkv {
+
+// Host helpers of the other translation units (pkv_internal.h).
+int device_sm_count(int* sms) {
+  std::lock_guard<std::mutex> lock(g_mu);
+  DeviceState* st = nullptr;
+  if (int rc = current_device_state(&st)) return rc;
+  *sms = st->sm_count;
+  return PKV_OK;
+}
+
+bool cache_desc_ok(const pkv_cache_desc* c) { return valid_cache(c); }
+
+int launch_overlapped(const void* fn, dim3 grid, dim3 block, size_t smem, void* stream, void** args) {
+  if (launch(fn, grid, block, smem, static_cast<cudaStream_t>(stream), args) == cudaSuccess) return PKV_OK;
+  cudaGetLastError();
+  return PKV_ERR_CUDA;
+}
+
+}  // namespace pkv
+
 extern "C" {
 
 #ifdef PKV_TIMELINE

@@ -8,29 +8,11 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include "pkv_codec.cuh"
 #include "pkv_internal.h"
 #include "pkv_ptx.cuh"
 
 namespace pkv {
-
-// fp16 bit pattern -> E5M2 byte. E5M2 keeps fp16's sign, exponent field and
-// bias and the top two mantissa bits, so rounding the 16-bit magnitude at bit 8
-// (round half to even: add 0x7F plus the bit that will become the last kept
-// mantissa bit) yields the E5M2 magnitude directly; a carry moves into the
-// exponent as it should. Results beyond the largest finite code 0x7B (57344),
-// including infinities, saturate to it; NaN becomes 0x7E; the sign is kept.
-__device__ __forceinline__ uint32_t e5m2_of_fp16(uint32_t h) {
-  const uint32_t mag = h & 0x7FFFu;
-  uint32_t r = (mag + 0x7Fu + ((mag >> 8) & 1u)) >> 8;
-  r = r > 0x7Bu ? 0x7Bu : r;
-  r = mag > 0x7C00u ? 0x7Eu : r;
-  return ((h >> 8) & 0x80u) | r;
-}
-
-__device__ __forceinline__ uint32_t e5m2x4(uint32_t lo_pair, uint32_t hi_pair) {
-  return e5m2_of_fp16(lo_pair & 0xFFFFu) | (e5m2_of_fp16(lo_pair >> 16) << 8) |
-         (e5m2_of_fp16(hi_pair & 0xFFFFu) << 16) | (e5m2_of_fp16(hi_pair >> 16) << 24);
-}
 
 __global__ void __launch_bounds__(256) kv_cache_write_kernel(const CacheWriteArgs a) {
   pdl_wait_prior_grid();
@@ -105,18 +87,12 @@ __global__ void __launch_bounds__(256) kv_cache_write_int8_kernel(const CacheWri
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    const float scale = __half2float(__float2half_ru(__fdiv_rn(amax, 127.0f)));
+    const float scale = int8_row_scale(amax);
     uint32_t packed = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (i >= per_lane) break;
-      float qv = 0.f;
-      if (scale != 0.f) {
-        qv = rintf(__fdiv_rn(x[i], scale));
-        qv = fmaxf(qv, -127.0f);
-        qv = fminf(qv, 127.0f);
-      }
-      packed |= static_cast<uint32_t>(static_cast<int>(qv) + 128) << (8 * i);
+      packed |= int8_byte(x[i], scale) << (8 * i);
     }
     const long long blk = slot / kBlockSize, off = slot - blk * kBlockSize;
     const long long row = (blk * a.num_kv_heads + h) * kBlockSize + off;

@@ -6,6 +6,8 @@
 #include <cstdint>
 #include <cuda_runtime.h>
 
+#include "pagedkv.h"
+
 namespace pkv {
 
 constexpr int kBlockSize = 16;       // tokens per KV block
@@ -147,6 +149,16 @@ const void* decode_kernel_ptr_int8(int d, int ntw);
 const void* decode_kernel_narrow_ptr_bf16(int d);
 const void* kv_cache_write_kernel_ptr();
 const void* kv_cache_write_int8_kernel_ptr();
+
+// ---- host helpers (capi.cu) -------------------------------------------------------
+// Multiprocessors of the current device; a pkv_status.
+int device_sm_count(int* sms);
+// Whether a cache descriptor names a cache this build handles.
+bool cache_desc_ok(const pkv_cache_desc* c);
+// Launch that may start while the stream's previous kernel drains (programmatic
+// dependent launch): the kernel waits for that grid before it reads its inputs.
+int launch_overlapped(const void* fn, dim3 grid, dim3 block, size_t smem, void* stream, void** args);
+inline bool aligned_to(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 struct CacheWriteArgs {
   const uint4* key;            // [T][Hkv][D] 16-bit elements, 8 per uint4

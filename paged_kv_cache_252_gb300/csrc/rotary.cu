@@ -1,0 +1,372 @@
+// Rotary position embedding of query and key rows, and its fusion with the cache write
+// (declared in include/pagedkv.h; "kernel1" of the KVCache Quant section of
+// "AI大模型推理速度翻倍，Colossal-Inference开源发布" is the writer it extends).
+//
+// A row's first rotary_dim dimensions form rotary_dim / 2 pairs (dimensions i and
+// i + rotary_dim/2, or 2i and 2i + 1 when interleaved). Pair i of a token at position p
+// turns by the angle a = p * inv_freq[i]:
+//   y_re = f (x_re cos a - x_im sin a),   y_im = f (x_re sin a + x_im cos a),
+// in fp32, rounded once to the output's type (a query's 16 bits, the key's cache type).
+//
+// Angles. p * inv_freq reaches 10^6 rad, where an fp32 product is off by 0.03 rad. One
+// turn is 2^64 here: each CTA converts inv_freq / 2 pi once to a 64-bit fraction of a turn
+// per position (fp64), and p times that step modulo 2^64 is the angle, the whole turns
+// gone exactly; its top bits as an fp32 number of half turns go to sincospif. The fp64 unit
+// is left with rotary_dim / 2 operations a CTA instead of one chain per (token, pair).
+//
+// Work. A row of D dimensions is D/16 items: an item is one pair of 16-byte chunks, eight
+// (re, im) pairs of the rotated part or sixteen plain dimensions (the unrotated tail, and
+// the whole of a value row), so every thread moves two 16-byte loads and two stores
+// whatever the layout. A CTA takes tiles of a few tokens: their cosines and sines go
+// through shared memory once, and the tile's items (all heads of q, key and value) are
+// spread over its threads. The D/16 lanes of one row are neighbours in a warp, which
+// gives the INT8 writer its row maximum by shuffles.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "pagedkv.h"
+#include "pkv_codec.cuh"
+#include "pkv_internal.h"
+#include "pkv_ptx.cuh"
+
+namespace pkv {
+
+constexpr int kRotaryThreads = 256;
+constexpr int kRotaryBatch = 2;          // items a thread loads before it stores any
+constexpr int kRotaryMaxPairs = 64;      // head size 128
+constexpr int kRotaryMaxTokens = 8;      // tokens of a CTA's tile
+
+struct RotaryArgs {
+  const uint16_t* q;           // rotated to q_out; token strides in elements
+  const uint16_t* key;
+  const uint16_t* value;
+  uint16_t* q_out;
+  long long q_stride, q_out_stride, key_stride, value_stride;
+  const void* positions;
+  const int32_t* slot_mapping; // null: no cache (queries only)
+  const double* inv_freq;      // [rotary_dim / 2]
+  void* k_cache;
+  void* v_cache;
+  float* scales;
+  int32_t* status;
+  long long num_slots;
+  int32_t num_tokens, num_q_heads, num_kv_heads;
+  int32_t items_row;           // D / 16, a power of two
+  int32_t log_items_row;
+  int32_t rot_items;           // rotary_dim / 16
+  int32_t tile;                // tokens of a CTA's tile
+  int32_t pos64, interleaved;
+  float factor, sign;          // sign -1 turns the other way
+};
+
+template <bool BF16>
+__device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (BF16) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    } else {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      x[2 * i] = f.x;
+      x[2 * i + 1] = f.y;
+    }
+  }
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    w[i] = BF16 ? pack_bf16x2(x[2 * i], x[2 * i + 1]) : pack_f16x2(x[2 * i], x[2 * i + 1]);
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// KV: the cache's element type (kKvBf16 means bf16 rows everywhere, the others fp16 rows).
+template <int KV>
+__global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const RotaryArgs a) {
+  constexpr bool BF16 = KV == kKvBf16;
+  __shared__ unsigned long long step[kRotaryMaxPairs];
+  __shared__ float2 cs[kRotaryMaxTokens * kRotaryMaxPairs];
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int pairs = a.rot_items * 8;
+  pdl_wait_prior_grid();
+  // inv_freq / 2 pi modulo one turn, as a 64-bit fraction. (Both products round to 2^-53
+  // of their value, as an fp64 angle would.)
+  if (tid < pairs) {
+    const double turns = a.inv_freq[tid] * 0.15915494309189533577;
+    step[tid] = __double2ull_rn((turns - floor(turns)) * 18446744073709551616.0);
+  }
+  const int heads = a.num_q_heads + 2 * a.num_kv_heads;
+  const int per_token = heads << a.log_items_row;
+  const int D = a.items_row * 16;
+  const int second = a.interleaved ? 8 : a.rot_items * 8;   // distance of an item's second chunk
+  for (long long t0 = static_cast<long long>(blockIdx.x) * a.tile; t0 < a.num_tokens;
+       t0 += static_cast<long long>(gridDim.x) * a.tile) {
+    const int nt = static_cast<int>(a.num_tokens - t0 < a.tile ? a.num_tokens - t0 : a.tile);
+    __syncthreads();   // steps written; the last tile's cosines read
+    for (int i = tid; i < nt * pairs; i += kRotaryThreads) {
+      const int t = i / pairs, j = i - t * pairs;
+      const long long p = a.pos64 ? static_cast<const long long*>(a.positions)[t0 + t]
+                                  : static_cast<const int32_t*>(a.positions)[t0 + t];
+      const long long phase = static_cast<long long>(static_cast<unsigned long long>(p) * step[j]);
+      float s, c;
+      sincospif(__ll2float_rn(phase) * 1.0842021724855044e-19f, &s, &c);   // 2^-63: half turns in [-1, 1]
+      cs[t * pairs + j] = make_float2(c * a.factor, s * a.factor * a.sign);
+    }
+    __syncthreads();
+    const int total = nt * per_token;
+    for (int i0 = tid; i0 < total; i0 += kRotaryThreads * kRotaryBatch) {
+      uint4 va[kRotaryBatch], vb[kRotaryBatch];
+#pragma unroll
+      for (int b = 0; b < kRotaryBatch; ++b) {
+        const int i = i0 + b * kRotaryThreads;
+        if (i >= total) break;
+        const int row = i >> a.log_items_row, c = i & (a.items_row - 1);
+        const int t = row / heads, h = row - t * heads;
+        const uint16_t* src;
+        if (h < a.num_q_heads) src = a.q + (t0 + t) * a.q_stride + h * D;
+        else if (h < a.num_q_heads + a.num_kv_heads) src = a.key + (t0 + t) * a.key_stride + (h - a.num_q_heads) * D;
+        else src = a.value + (t0 + t) * a.value_stride + (h - a.num_q_heads - a.num_kv_heads) * D;
+        const bool turn = c < a.rot_items && h < a.num_q_heads + a.num_kv_heads;
+        const int o1 = turn && !a.interleaved ? 8 * c : 16 * c;
+        const int o2 = o1 + (turn ? second : 8);
+        va[b] = *reinterpret_cast<const uint4*>(src + o1);
+        vb[b] = *reinterpret_cast<const uint4*>(src + o2);
+      }
+#pragma unroll
+      for (int b = 0; b < kRotaryBatch; ++b) {
+        const int i = i0 + b * kRotaryThreads;
+        if (i >= total) break;
+        const int row = i >> a.log_items_row, c = i & (a.items_row - 1);
+        const int t = row / heads, h = row - t * heads;
+        const bool is_v = h >= a.num_q_heads + a.num_kv_heads;
+        const bool turn = c < a.rot_items && !is_v;
+        const int o1 = turn && !a.interleaved ? 8 * c : 16 * c;
+        const int o2 = o1 + (turn ? second : 8);
+        float x[8], y[8];
+        if (turn) {
+          unpack8<BF16>(va[b], x);
+          unpack8<BF16>(vb[b], y);
+          const float2* w = cs + t * pairs + 8 * c;
+          if (a.interleaved) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float2 w0 = w[k], w1 = w[4 + k];
+              const float re0 = x[2 * k], im0 = x[2 * k + 1], re1 = y[2 * k], im1 = y[2 * k + 1];
+              x[2 * k] = re0 * w0.x - im0 * w0.y;
+              x[2 * k + 1] = re0 * w0.y + im0 * w0.x;
+              y[2 * k] = re1 * w1.x - im1 * w1.y;
+              y[2 * k + 1] = re1 * w1.y + im1 * w1.x;
+            }
+          } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const float2 wk = w[k];
+              const float re = x[k], im = y[k];
+              x[k] = re * wk.x - im * wk.y;
+              y[k] = re * wk.y + im * wk.x;
+            }
+          }
+        }
+        if (h < a.num_q_heads) {
+          uint16_t* dst = a.q_out + (t0 + t) * a.q_out_stride + h * D;
+          *reinterpret_cast<uint4*>(dst + o1) = turn ? pack8<BF16>(x) : va[b];
+          *reinterpret_cast<uint4*>(dst + o2) = turn ? pack8<BF16>(y) : vb[b];
+          continue;
+        }
+        const long long slot = a.slot_mapping[t0 + t];
+        const bool bad = slot < -1 || slot >= a.num_slots;
+        if (bad && a.status && c == 0) atomicOr(a.status, kDevBadSlot);
+        if (bad || slot == -1) continue;   // the whole row's lanes together
+        const int hk = h - a.num_q_heads - (is_v ? a.num_kv_heads : 0);
+        // row of the cache: (block * Hkv + head) * 16 + offset
+        const long long crow = ((slot >> 4) * a.num_kv_heads + hk) * kBlockSize + (slot & 15);
+        void* cache = is_v ? a.v_cache : a.k_cache;
+        if constexpr (KV == kKvF16 || KV == kKvBf16) {
+          uint16_t* dst = static_cast<uint16_t*>(cache) + crow * D;
+          *reinterpret_cast<uint4*>(dst + o1) = turn ? pack8<BF16>(x) : va[b];
+          *reinterpret_cast<uint4*>(dst + o2) = turn ? pack8<BF16>(y) : vb[b];
+        } else if constexpr (KV == kKvE5m2) {
+          uint8_t* dst = static_cast<uint8_t*>(cache) + crow * D;
+          uint2 w1, w2;
+          if (turn) {
+            // from fp32 in one rounding
+            w1.x = e5m2x2_of_f32(x[0], x[1]) | (e5m2x2_of_f32(x[2], x[3]) << 16);
+            w1.y = e5m2x2_of_f32(x[4], x[5]) | (e5m2x2_of_f32(x[6], x[7]) << 16);
+            w2.x = e5m2x2_of_f32(y[0], y[1]) | (e5m2x2_of_f32(y[2], y[3]) << 16);
+            w2.y = e5m2x2_of_f32(y[4], y[5]) | (e5m2x2_of_f32(y[6], y[7]) << 16);
+          } else {
+            w1 = make_uint2(e5m2x4(va[b].x, va[b].y), e5m2x4(va[b].z, va[b].w));
+            w2 = make_uint2(e5m2x4(vb[b].x, vb[b].y), e5m2x4(vb[b].z, vb[b].w));
+          }
+          *reinterpret_cast<uint2*>(dst + o1) = w1;
+          *reinterpret_cast<uint2*>(dst + o2) = w2;
+        } else {
+          if (!turn) {
+            unpack8<BF16>(va[b], x);
+            unpack8<BF16>(vb[b], y);
+          }
+          float amax = 0.f;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) amax = fmaxf(amax, fmaxf(fabsf(x[k]), fabsf(y[k])));
+          // The row's items_row lanes are aligned and either all here or none.
+          const unsigned group = ((1u << a.items_row) - 1u) << (lane & ~(a.items_row - 1));
+          for (int o = a.items_row >> 1; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(group, amax, o));
+          const float scale = int8_row_scale(amax);
+          uint2 w1 = make_uint2(0u, 0u), w2 = make_uint2(0u, 0u);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            w1.x |= int8_byte(x[k], scale) << (8 * k);
+            w1.y |= int8_byte(x[4 + k], scale) << (8 * k);
+            w2.x |= int8_byte(y[k], scale) << (8 * k);
+            w2.y |= int8_byte(y[4 + k], scale) << (8 * k);
+          }
+          uint8_t* dst = static_cast<uint8_t*>(cache) + crow * D;
+          *reinterpret_cast<uint2*>(dst + o1) = w1;
+          *reinterpret_cast<uint2*>(dst + o2) = w2;
+          if (c == 0) a.scales[(crow >> 4) * 32 + (is_v ? 16 : 0) + (crow & 15)] = scale;
+        }
+      }
+    }
+  }
+  pdl_launch_dependents();
+}
+
+}  // namespace pkv
+
+namespace {
+
+using namespace pkv;
+
+// Arguments both entry points share: types, sizes, alignment. Token strides are in elements.
+int rotary_common(RotaryArgs* a, pkv_dtype dtype, int32_t num_tokens, int32_t head_size, const void* positions,
+                  int32_t position_bytes, const double* inv_freq, int32_t rotary_dim, float attn_factor) {
+  if (dtype != PKV_FP16 && dtype != PKV_BF16) return PKV_ERR_UNSUPPORTED;
+  if (num_tokens < 0) return PKV_ERR_INVALID_ARGUMENT;
+  if (head_size != 64 && head_size != 128) return PKV_ERR_UNSUPPORTED;
+  if (rotary_dim < 16 || rotary_dim > head_size || rotary_dim % 16 != 0) return PKV_ERR_UNSUPPORTED;
+  if (position_bytes != 4 && position_bytes != 8) return PKV_ERR_INVALID_ARGUMENT;
+  if (!std::isfinite(attn_factor)) return PKV_ERR_INVALID_ARGUMENT;
+  if (num_tokens > 0 && (!positions || !inv_freq)) return PKV_ERR_INVALID_ARGUMENT;
+  if (!aligned_to(positions, static_cast<uintptr_t>(position_bytes)) || !aligned_to(inv_freq, 8))
+    return PKV_ERR_INVALID_ARGUMENT;
+  a->positions = positions;
+  a->pos64 = position_bytes == 8;
+  a->inv_freq = inv_freq;
+  a->num_tokens = num_tokens;
+  a->items_row = head_size / 16;
+  a->log_items_row = head_size == 128 ? 3 : 2;
+  a->rot_items = rotary_dim / 16;
+  a->factor = attn_factor;
+  a->sign = 1.f;
+  return PKV_OK;
+}
+
+// Rows of `heads` heads, 16-byte aligned, that do not overlap.
+bool rows_ok(const void* p, long long stride, int32_t heads, int32_t head_size) {
+  return p && aligned_to(p, 16) && stride % 8 == 0 && stride >= static_cast<long long>(heads) * head_size;
+}
+
+int rotary_launch(RotaryArgs& a, const void* fn, void* stream) {
+  int sms = 0;
+  if (int rc = device_sm_count(&sms)) return rc;
+  const long long heads = a.num_q_heads + 2ll * a.num_kv_heads;
+  if (heads * a.items_row * kRotaryMaxTokens >= (1ll << 31)) return PKV_ERR_UNSUPPORTED;
+  // Tokens of a tile: about four items a thread, but no fewer tiles than the GPU holds CTAs.
+  const long long per_token = heads * a.items_row;
+  long long tile = (4ll * kRotaryThreads + per_token - 1) / per_token;
+  const long long even = a.num_tokens / (sms * 4ll);
+  if (tile > even) tile = even;
+  if (tile > kRotaryMaxTokens) tile = kRotaryMaxTokens;
+  if (tile < 1) tile = 1;
+  a.tile = static_cast<int32_t>(tile);
+  long long blocks = (a.num_tokens + tile - 1) / tile;
+  if (blocks > sms * 6ll) blocks = sms * 6ll;
+  void* args[1] = {&a};
+  return launch_overlapped(fn, dim3(static_cast<unsigned>(blocks)), dim3(kRotaryThreads), 0, stream, args);
+}
+
+}  // namespace
+
+extern "C" {
+
+int pkv_rotary_embed(void* out, int64_t out_stride, const void* x, int64_t x_stride, pkv_dtype dtype,
+                     int32_t num_tokens, int32_t num_heads, int32_t head_size, const void* positions,
+                     int32_t position_bytes, const double* inv_freq, int32_t rotary_dim, int32_t interleaved,
+                     float attn_factor, int32_t inverse, void* stream) {
+  RotaryArgs a{};
+  if (int rc = rotary_common(&a, dtype, num_tokens, head_size, positions, position_bytes, inv_freq, rotary_dim,
+                             attn_factor))
+    return rc;
+  if (num_heads <= 0) return PKV_ERR_INVALID_ARGUMENT;
+  if (num_tokens == 0) return PKV_OK;
+  if (!rows_ok(out, out_stride, num_heads, head_size) || !rows_ok(x, x_stride, num_heads, head_size))
+    return PKV_ERR_INVALID_ARGUMENT;
+  a.q = static_cast<const uint16_t*>(x);
+  a.q_out = static_cast<uint16_t*>(out);
+  a.q_stride = x_stride;
+  a.q_out_stride = out_stride;
+  a.num_q_heads = num_heads;
+  a.interleaved = interleaved != 0;
+  if (inverse) a.sign = -1.f;
+  return rotary_launch(a, dtype == PKV_BF16 ? reinterpret_cast<const void*>(&rotary_kernel<kKvBf16>)
+                                            : reinterpret_cast<const void*>(&rotary_kernel<kKvF16>), stream);
+}
+
+int pkv_rotary_write(void* q_out, int64_t q_out_stride, const void* q, int64_t q_stride, const void* key,
+                     int64_t key_stride, const void* value, int64_t value_stride, pkv_dtype src_dtype,
+                     int32_t num_tokens, int32_t num_q_heads, const void* positions, int32_t position_bytes,
+                     const int32_t* slot_mapping, const double* inv_freq, int32_t rotary_dim, int32_t interleaved,
+                     float attn_factor, void* k_cache, void* v_cache, float* scales, pkv_dtype kv_dtype,
+                     const pkv_cache_desc* cache, int32_t* device_status, void* stream) {
+  if (!cache_desc_ok(cache)) return PKV_ERR_INVALID_ARGUMENT;
+  const bool pair_ok = (src_dtype == PKV_FP16 && (kv_dtype == PKV_FP16 || kv_dtype == PKV_FP8_E5M2 ||
+                                                  kv_dtype == PKV_INT8)) ||
+                       (src_dtype == PKV_BF16 && kv_dtype == PKV_BF16);
+  if (!pair_ok) return PKV_ERR_UNSUPPORTED;
+  RotaryArgs a{};
+  if (int rc = rotary_common(&a, src_dtype, num_tokens, cache->head_size, positions, position_bytes, inv_freq,
+                             rotary_dim, attn_factor))
+    return rc;
+  if (num_q_heads <= 0 || (kv_dtype == PKV_INT8) != (scales != nullptr)) return PKV_ERR_INVALID_ARGUMENT;
+  if (num_tokens == 0) return PKV_OK;
+  const int D = cache->head_size, Hkv = cache->num_kv_heads;
+  if (!rows_ok(q_out, q_out_stride, num_q_heads, D) || !rows_ok(q, q_stride, num_q_heads, D) ||
+      !rows_ok(key, key_stride, Hkv, D) || !rows_ok(value, value_stride, Hkv, D))
+    return PKV_ERR_INVALID_ARGUMENT;
+  if (!k_cache || !v_cache || !slot_mapping) return PKV_ERR_INVALID_ARGUMENT;
+  if (!aligned_to(k_cache, 16) || !aligned_to(v_cache, 16) || !aligned_to(scales, 16) ||
+      !aligned_to(slot_mapping, 4) || !aligned_to(device_status, 4))
+    return PKV_ERR_INVALID_ARGUMENT;
+  a.q = static_cast<const uint16_t*>(q);
+  a.key = static_cast<const uint16_t*>(key);
+  a.value = static_cast<const uint16_t*>(value);
+  a.q_out = static_cast<uint16_t*>(q_out);
+  a.q_stride = q_stride;
+  a.q_out_stride = q_out_stride;
+  a.key_stride = key_stride;
+  a.value_stride = value_stride;
+  a.slot_mapping = slot_mapping;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.scales = scales;
+  a.status = device_status;
+  a.num_slots = static_cast<long long>(cache->num_blocks) * kBlockSize;
+  a.num_q_heads = num_q_heads;
+  a.num_kv_heads = Hkv;
+  a.interleaved = interleaved != 0;
+  const void* fn = kv_dtype == PKV_FP16   ? reinterpret_cast<const void*>(&rotary_kernel<kKvF16>)
+                   : kv_dtype == PKV_BF16 ? reinterpret_cast<const void*>(&rotary_kernel<kKvBf16>)
+                   : kv_dtype == PKV_INT8 ? reinterpret_cast<const void*>(&rotary_kernel<kKvInt8>)
+                                          : reinterpret_cast<const void*>(&rotary_kernel<kKvE5m2>);
+  return rotary_launch(a, fn, stream);
+}
+
+}  // extern "C"
