@@ -195,8 +195,8 @@ int get_geometry(DeviceState* st, int kv, int d, int rows, GeomEntry** out) {
   return PKV_OK;
 }
 
-int encode_cache_map(CUtensorMap* map, const void* base, int kv, int d, long long total_rows,
-                     int half) {
+// The driver's tensor-map encoder, looked up on first use.
+int load_encoder() {
   std::call_once(g_encode_once, [] {
     void* fn = nullptr;
     cudaDriverEntryPointQueryResult q{};
@@ -207,7 +207,12 @@ int encode_cache_map(CUtensorMap* map, const void* base, int kv, int d, long lon
     }
     cudaGetLastError();
   });
-  if (!g_encode) return PKV_ERR_CUDA;
+  return g_encode ? PKV_OK : PKV_ERR_CUDA;
+}
+
+int encode_cache_map(CUtensorMap* map, const void* base, int kv, int d, long long total_rows,
+                     int half) {
+  if (int rc = load_encoder()) return rc;
   const int rb = tile_row_bytes(kv, d);
   const int esz = kv_elem_bytes(kv);
   const CUtensorMapDataType dt = esz == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16;
@@ -284,6 +289,41 @@ int device_sm_count(int* sms) {
   if (int rc = current_device_state(&st)) return rc;
   *sms = st->sm_count;
   return PKV_OK;
+}
+
+uint32_t next_call_epoch() {
+  // Counters from an earlier call carry an older epoch and count as zero, so a workspace
+  // never needs clearing. The epoch is the call number through a bijective 32-bit mix, so
+  // calls never share one (within 2^32 calls) and its values do not look like the small
+  // integers (lengths, block ids) a reused buffer may hold; 0 and 0xFFFFFFFF are skipped
+  // (zeroed and -1-filled memory).
+  uint32_t ep = 0;
+  do {
+    ep = call_epoch(++g_call_epoch);
+  } while (ep == 0u || ep == 0xFFFFFFFFu);
+  return ep;
+}
+
+int encode_tile_map(CUtensorMap* map, const void* cache, int kv, int d, long long total_rows, int half) {
+  return encode_cache_map(map, cache, kv, d, total_rows, half);
+}
+
+int encode_map_16bit(CUtensorMap* map, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
+                     const uint32_t* box) {
+  if (int rc = load_encoder()) return rc;
+  cuuint64_t gd[5], gs[4];
+  cuuint32_t bx[5], es[5];
+  for (int i = 0; i < rank; ++i) {
+    gd[i] = dims[i];
+    bx[i] = box[i];
+    es[i] = 1;
+    if (i + 1 < rank) gs[i] = strides[i];
+  }
+  const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, static_cast<cuuint32_t>(rank),
+                              const_cast<void*>(base), gd, gs, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? PKV_OK : PKV_ERR_CUDA;
 }
 
 bool cache_desc_ok(const pkv_cache_desc* c) { return valid_cache(c); }
@@ -502,16 +542,7 @@ int decode_impl(void* out, const void* q, const int32_t* cu_q_lens, int32_t num_
   a.stages = g.stages;
   a.slot_floats = partial_slot_floats(rows, d);
   a.scale_log2 = scale * 1.4426950408889634f;
-  // Counters from an earlier call carry an older epoch and count as zero, so the
-  // workspace never needs clearing. The epoch is the call number through a
-  // bijective 32-bit mix, so calls never share one (within 2^32 calls) and its
-  // values do not look like the small integers (lengths, block ids) a reused
-  // buffer may hold; 0 and 0xFFFFFFFF are skipped (zeroed and -1-filled memory).
-  uint32_t ep = 0;
-  do {
-    ep = call_epoch(++g_call_epoch);
-  } while (ep == 0u || ep == 0xFFFFFFFFu);
-  a.epoch = ep;
+  a.epoch = next_call_epoch();
   a.piece_cost = piece_cost(g.tc != 0, kv_dtype);
 #ifdef PKV_TIMELINE
   a.timeline = g_timeline;

@@ -4,6 +4,7 @@
 
 #include <cstddef>
 #include <cstdint>
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "pagedkv.h"
@@ -158,6 +159,14 @@ bool cache_desc_ok(const pkv_cache_desc* c);
 // Launch that may start while the stream's previous kernel drains (programmatic
 // dependent launch): the kernel waits for that grid before it reads its inputs.
 int launch_overlapped(const void* fn, dim3 grid, dim3 block, size_t smem, void* stream, void** args);
+// The tag of a call's piece counters: differs from every other call's.
+uint32_t next_call_epoch();
+// Tensor map of one 128-byte half of a cache's token rows (boxes of 16 rows), and of a
+// 16-bit tensor whose boxes are 128 bytes wide (128-byte swizzle; strides in bytes, of
+// dimensions 1 and up).
+int encode_tile_map(CUtensorMap* map, const void* cache, int kv, int d, long long total_rows, int half);
+int encode_map_16bit(CUtensorMap* map, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
+                     const uint32_t* box);
 inline bool aligned_to(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 struct CacheWriteArgs {

@@ -1,0 +1,728 @@
+// Attention of a chunk of new tokens over the paged cache on the 5th-generation tensor
+// core (tcgen05). For every unit (256 query rows of one sequence and KV head, see
+// prefill_plan.cuh) and KV tile of 128 positions, per row tile i of 128 rows:
+//   S_i (128 rows x 128 positions, fp32) = Q_i K^T          Q, K from shared memory
+//   P_i = 2^(S_i c - m_i + shift)                            softmax warps, one row a thread
+//   O_i (128 rows x D, fp32)  += P_i V                        P from tensor memory, V from shared
+// with one pass over the positions, running maxima m and sums l in fp32. The two row tiles
+// take turns: while one's scores are exponentiated the other's products run.
+//
+// Tensor memory (512 columns): O_0, O_1, S_0, S_1 at 0, 128, 256, 384. P_i (16-bit, 64
+// columns) takes the place of the first half of S_i, which its own threads have read; the
+// next S_i is issued behind the P V product that reads P_i (products execute in issue order).
+//
+// Warps: 0..3 and 4..7 the softmax of row tiles 0 and 1, warp 8 issues the products, warp 9
+// the copies (queries; for 16-bit caches also the K and V tiles: 16-token boxes through the
+// block table into the swizzled operand layout). One-byte caches add warps 12..15, which
+// load the tiles, widen them to fp16 and write the operand layout themselves.
+//
+// Masks. Only tiles that reach past some row's last position compare positions; a masked
+// score is -inf, its weight 0. V rows behind the context are zeroed (a stale NaN times
+// weight 0 would be NaN). A later token of the chunk that holds an infinity or NaN still
+// meets weight 0 of the rows before it: an output row with a non-finite element is
+// computed again by prefill_row, which reads only what the row sees.
+//
+// The running maximum moves only when a score exceeds it by more than kSlack (base 2), so
+// that O is rescaled a few times a row, not every tile. fp16 weights carry a shift of 2^7:
+// with the slack of 8 they stay below 2^15, and weights down to 2^-21 of the largest
+// keep full precision. An INT8 cache's V scale enters the weight with it (at most 516, so
+// slack 0 and shift 6); its K scale multiplies the scores.
+#pragma once
+
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+
+#include <cstdint>
+
+#include "pkv_internal.h"
+#include "pkv_ptx.cuh"
+#include "pkv_tc.cuh"
+#include "prefill_plan.cuh"
+#include "prefill_row.cuh"
+
+namespace pkv {
+
+template <int KV, int D>
+struct PfShape {
+  static constexpr bool kWiden = KV == kKvE5m2 || KV == kKvInt8;
+  static constexpr bool kBf16 = KV == kKvBf16;
+  static constexpr int kHalves = D / 64;
+  static constexpr int kThreads = kWiden ? 512 : 384;
+  // Register budgets (per thread of a warpgroup); their sum is the launch's total:
+  // 384 x 168 = 128 (200 + 200 + 104), 512 x 128 = 128 (184 + 184 + 56 + 88).
+  static constexpr int kLaunchRegs = kWiden ? 128 : 168;
+  static constexpr int kSoftmaxRegs = kWiden ? 184 : 200;
+  static constexpr int kIssueRegs = kWiden ? 56 : 104;
+  static constexpr int kWidenRegs = 88;
+  static constexpr int kStages = kWiden ? (D == 128 ? 4 : 8) : (D == 128 ? 5 : 10);
+  static constexpr uint32_t kHalfBytes = kPfTile * 128;             // 64 dimensions of a KV tile
+  static constexpr uint32_t kStageBytes = kHalves * kHalfBytes;
+  static constexpr uint32_t kQHalfBytes = kPfRows * 128;
+  static constexpr uint32_t kQBytes = kHalves * kQHalfBytes;
+  static constexpr float kSlack = KV == kKvInt8 ? 0.f : 8.f;
+  static constexpr float kShift = KV == kKvBf16 ? 0.f : (KV == kKvInt8 ? 6.f : 7.f);
+  // Row scales of an INT8 cache's tiles: tile t + kScaleRing is written once the K stage of
+  // tile t + kScaleRing - kStages / 2 is released, which is after the softmax of the tile before
+  // that one, so tile t's are no longer read when kScaleRing > kStages / 2.
+  static constexpr int kScaleRing = kStages;
+  // Shared memory from a 1024-aligned base.
+  static constexpr uint32_t kRing = kQBytes;
+  static constexpr uint32_t kScales = kRing + kStages * kStageBytes;   // INT8: [kScaleRing][K, V][128] floats
+  static constexpr uint32_t kBars = kScales + (KV == kKvInt8 ? kScaleRing * 2 * kPfTile * 4 : 0);
+  static constexpr uint32_t kMisc = kBars + (2 * kStages + 9 + kScaleRing) * 8;
+  static constexpr uint32_t kPos = kMisc + 256 + sizeof(PfStart);   // PfPos of each softmax warp
+  static constexpr uint32_t kSmem = kPos + 8 * sizeof(PfPos) + 1024;
+  static_assert(kSmem <= 227 * 1024, "shared memory of one CTA");
+};
+
+// One slot row tile: m[128], l[128], O[D / 8][128][8].
+__host__ __device__ constexpr int pf_slot_floats(int d) { return 256 + d * 128; }
+
+constexpr uint32_t kPfOCol = 0, kPfSCol = 256;
+
+// Bounded wait: gives up after kWaitLimitNs or once another warp has given up. Rows being
+// computed again (busy) take their time without counting.
+struct PfCtl {
+  volatile int abort;
+  volatile int busy;
+};
+__device__ __forceinline__ bool pf_wait_sleeping(uint32_t bar, uint32_t parity, PfCtl* ctl) {
+  uint64_t t0 = global_timer_ns();
+  for (;;) {
+    if (mbar_try_wait_sleep(bar, parity, kTcSleepNs)) return true;
+    if (ctl->abort) return false;
+    if (ctl->busy) t0 = global_timer_ns();
+    if (global_timer_ns() - t0 > kWaitLimitNs) return false;
+  }
+}
+__device__ __forceinline__ bool pf_wait(uint32_t bar, uint32_t parity, PfCtl* ctl) {
+  if (mbar_try_wait(bar, parity)) return true;
+  return pf_wait_sleeping(bar, parity, ctl);
+}
+
+// A warp's flagged rows again, reading only what they see.
+template <int KV, int D>
+__device__ __forceinline__ void pf_redo(const PrefillArgs& a, unsigned mask, int s, int qb, int past, int j0, int first,
+                                     int h, PfCtl* ctl) {
+  if ((threadIdx.x & 31) == 0) atomicAdd(const_cast<int*>(&ctl->busy), 1);
+  __syncwarp();
+  while (mask) {
+    const int r = first + __ffs(mask) - 1;
+    mask &= mask - 1;
+    const int j = j0 + r / a.group;
+    prefill_row<KV, D>(a, s, qb + j, h * a.group + r % a.group, max(past + j + 1, 0));
+  }
+  if ((threadIdx.x & 31) == 0) atomicSub(const_cast<int*>(&ctl->busy), 1);
+}
+
+// 16 one-byte elements -> 16 fp16 in two 16-byte chunks, exact.
+template <int KV>
+__device__ __forceinline__ void widen16(const uint4& v, uint4& lo, uint4& hi) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t o[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (KV == kKvE5m2) {
+      o[2 * i] = __byte_perm(w[i], 0, 0x1404);
+      o[2 * i + 1] = __byte_perm(w[i], 0, 0x3424);
+    } else {
+      // byte = code + 128: 0x64|byte is the fp16 value 1152 + code
+      const uint32_t a = __byte_perm(w[i], 0x64646464u, 0x4140), b = __byte_perm(w[i], 0x64646464u, 0x4342);
+      const __half2 off = __half2half2(__ushort_as_half(0x6480));   // 1152
+      const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&a), off);
+      const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&b), off);
+      o[2 * i] = *reinterpret_cast<const uint32_t*>(&x);
+      o[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&y);
+    }
+  }
+  lo = make_uint4(o[0], o[1], o[2], o[3]);
+  hi = make_uint4(o[4], o[5], o[6], o[7]);
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  return BF16 ? pack_bf16x2(lo, hi) : pack_f16x2(lo, hi);
+}
+
+template <int KV, int D>
+__global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
+    prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k0,
+                   const __grid_constant__ CUtensorMap tm_v0, const __grid_constant__ CUtensorMap tm_k1,
+                   const __grid_constant__ CUtensorMap tm_v1, const __grid_constant__ PrefillArgs a) {
+  using Sh = PfShape<KV, D>;
+  constexpr int NS = Sh::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const uint32_t base = smem_addr(smem);
+  const uint32_t full = base + Sh::kBars, empty = full + 8 * NS;
+  const uint32_t q_full = empty + 8 * NS, q_empty = q_full + 8;
+  const uint32_t s_full = q_empty + 8;      // [2] scores of row tile i written
+  const uint32_t p_ready = s_full + 16;     // [2] weights of row tile i written, O_i rescaled
+  const uint32_t o_done = p_ready + 16;     // [2] P V product of row tile i complete
+  const uint32_t final_bar = o_done + 16;
+  const uint32_t sc_full = final_bar + 8;   // [kScaleRing] row scales of a tile written (INT8)
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Sh::kMisc);
+  PfCtl* ctl = reinterpret_cast<PfCtl*>(smem + Sh::kMisc + 8);
+  volatile int* last_piece = reinterpret_cast<volatile int*>(smem + Sh::kMisc + 16);   // [2]
+  long long* scratch = reinterpret_cast<long long*>(smem + Sh::kMisc + 32);            // [16]
+  PfStart* start = reinterpret_cast<PfStart*>(smem + Sh::kMisc + 256);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int k = 0; k < NS; ++k) {
+      mbar_init(full + 8 * k, Sh::kWiden ? 128 : 1);
+      mbar_init(empty + 8 * k, 1);
+    }
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(s_full + 8 * i, 1);
+      mbar_init(p_ready + 8 * i, 4);
+      mbar_init(o_done + 8 * i, 1);
+    }
+    for (int i = 0; i < Sh::kScaleRing; ++i) mbar_init(sc_full + 8 * i, 128);
+    mbar_init(final_bar, 1);
+    ctl->abort = 0;
+    ctl->busy = 0;
+    fence_barrier_init();
+  }
+  if (warp == 8) {
+    tmem_alloc(smem_addr(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  if (warp == 9 && lane == 0) {
+    prefetch_tensormap(&tm_q);
+    prefetch_tensormap(&tm_k0);
+    prefetch_tensormap(&tm_v0);
+  }
+  tc_fence_before_sync();
+  pdl_wait_prior_grid();
+  pf_plan(a, scratch, start);   // its barriers also publish the set-up above
+  tc_fence_after_sync();
+  pdl_launch_dependents();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
+
+  if (start->any) {
+    if (warp < 8) {
+      // ------------------------------- softmax --------------------------------------
+      regs_grow<Sh::kSoftmaxRegs>();
+      const int i = warp >> 2;                      // row tile
+      const int r = tid & 127;                      // row of the tile, TMEM lane
+      const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+      const uint32_t s_col = lanes + kPfSCol + 128 * i, o_col = lanes + kPfOCol + 128 * i;
+      const uint32_t bar_s = s_full + 8 * i, bar_p = p_ready + 8 * i, bar_o = o_done + 8 * i;
+      const float c = a.scale_log2;
+      bool alive = true;
+      uint32_t cnt = 0;                             // tiles of this row tile so far
+      uint32_t seen = 0;                            // KV tiles of the CTA so far (INT8 scale ring)
+      auto wait = [&](uint32_t bar, uint32_t parity) {
+        if (!alive) return;
+        const bool ok = pf_wait(bar, parity, ctl);
+        if (!__all_sync(0xffffffffu, ok)) {
+          alive = false;
+          ctl->abort = 1;
+          if (lane == 0 && a.status) atomicOr(a.status, kDevTimeout);
+        }
+      };
+      volatile PfPos* keep = reinterpret_cast<volatile PfPos*>(smem + Sh::kPos) + warp;
+      for (PfWalk w(a, *start); !w.done(); w.advance()) {
+        uint32_t nth = seen;                        // KV tile of the CTA
+        int k, kb, limit, limit0;
+        {
+          const PfPiece pc(w);
+          if (!pc.any()) continue;
+          seen += pc.klast - pc.ka;
+          if (!pc.active(i)) continue;
+          const int ru = 128 * i + r;               // row of the unit
+          k = pc.ka;
+          kb = pc.kb[i];
+          // visible positions of this row and of the tile's first (<= 0: none)
+          limit = ru < pc.rows ? w.past() + pc.j0 + ru / a.group + 1 : 0;
+          limit0 = w.past() + pc.j0 + 128 * i / a.group + 1;
+        }
+        w.save(keep);
+        float m = -INFINITY, l = 0.f;
+        for (bool first = true; k < kb; ++k, ++cnt, ++nth, first = false) {
+          const int p0 = k * kPfTile;
+          wait(bar_s, cnt & 1);
+          const uint32_t slot = nth % Sh::kScaleRing;
+          if constexpr (KV == kKvInt8) wait(sc_full + 8 * slot, (nth / Sh::kScaleRing) & 1);
+          if (!alive) continue;
+          tc_fence_after_sync();
+          uint32_t sv[4][32];   // 32 scores each
+          tmem_ld128(s_col, sv[0], sv[1], sv[2], sv[3]);
+          if constexpr (KV == kKvInt8) {
+            const float4* ks = reinterpret_cast<const float4*>(smem + Sh::kScales) + slot * 64;
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+#pragma unroll
+              for (int e = 0; e < 32; e += 4) {
+                const float4 f = ks[8 * g + e / 4];
+                sv[g][e] = __float_as_uint(__uint_as_float(sv[g][e]) * f.x);
+                sv[g][e + 1] = __float_as_uint(__uint_as_float(sv[g][e + 1]) * f.y);
+                sv[g][e + 2] = __float_as_uint(__uint_as_float(sv[g][e + 2]) * f.z);
+                sv[g][e + 3] = __float_as_uint(__uint_as_float(sv[g][e + 3]) * f.w);
+              }
+            }
+          }
+          if (p0 + kPfTile > limit0) {
+            const int vis = limit - p0;
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) sv[g][e] = 32 * g + e < vis ? sv[g][e] : 0xFF800000u;
+            }
+          }
+          float mx4[4];
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            mx4[g] = __uint_as_float(sv[g][0]);
+#pragma unroll
+            for (int e = 1; e < 32; ++e) mx4[g] = fmaxf(mx4[g], __uint_as_float(sv[g][e]));
+          }
+          float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+          mx *= c;
+          const bool need = mx > m + Sh::kSlack;
+          if (__any_sync(0xffffffffu, need)) {
+            const float mn = need ? mx : m;
+            const float alpha = need ? fast_exp2(m - mn) : 1.f;   // 0 from -inf
+            m = mn;
+            l *= alpha;
+            if (!first) {
+              wait(bar_o, (cnt - 1) & 1);
+              if (alive) {
+                tc_fence_after_sync();
+#pragma unroll 1
+                for (int e = 0; e < D; e += 32) {
+                  uint32_t ov[32];
+                  tmem_ld32(o_col + e, ov);
+#pragma unroll
+                  for (int x = 0; x < 32; ++x) ov[x] = __float_as_uint(__uint_as_float(ov[x]) * alpha);
+                  tmem_st32(o_col + e, ov);
+                }
+              }
+            }
+          }
+          const float sub = Sh::kShift - (m == -INFINITY ? 0.f : m);
+          const uint64_t c2 = f32x2(c, c), sub2 = f32x2(sub, sub);
+          uint64_t l2 = f32x2(0.f, 0.f), l3 = l2;
+          const float4* vs = reinterpret_cast<const float4*>(smem + Sh::kScales) + slot * 64 + 32;
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            uint32_t pw[16];
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              const float2 x0 = f32x2_parts(
+                  f32x2_fma(f32x2(__uint_as_float(sv[g][e]), __uint_as_float(sv[g][e + 1])), c2, sub2));
+              const float2 x1 = f32x2_parts(
+                  f32x2_fma(f32x2(__uint_as_float(sv[g][e + 2]), __uint_as_float(sv[g][e + 3])), c2, sub2));
+              float q0 = fast_exp2(x0.x), q1 = fast_exp2(x0.y), q2 = fast_exp2(x1.x), q3 = fast_exp2(x1.y);
+              l2 = f32x2_add(l2, f32x2(q0, q1));
+              l3 = f32x2_add(l3, f32x2(q2, q3));
+              if constexpr (KV == kKvInt8) {
+                const float4 f = vs[8 * g + e / 4];
+                q0 *= f.x;
+                q1 *= f.y;
+                q2 *= f.z;
+                q3 *= f.w;
+              }
+              pw[e / 2] = pack2<Sh::kBf16>(q0, q1);
+              pw[e / 2 + 1] = pack2<Sh::kBf16>(q2, q3);
+            }
+            tmem_st16_async(s_col + 16 * g, pw);
+          }
+          const float2 ls = f32x2_parts(f32x2_add(l2, l3));
+          l += ls.x + ls.y;
+          tmem_st_wait();
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar_p);
+        }
+
+        // ---- end of the piece ----
+        w.restore(keep);
+        const PfPiece pc(w);
+        const int ru = 128 * i + r, j = pc.j0 + ru / a.group;
+        const bool real = ru < pc.rows;
+        wait(bar_o, (cnt - 1) & 1);
+        if (alive) tc_fence_after_sync();
+        uint16_t* dst = static_cast<uint16_t*>(a.out) +
+                        (static_cast<size_t>(w.p.qb + j) * a.num_q_heads + w.p.h * a.group + ru % a.group) * D;
+        bool odd = false;   // a real row whose result is not finite
+        if (pc.whole(i)) {
+          if (alive) {
+            const float inv = l > 0.f ? 1.f / l : 0.f;
+            float bad = l == 0.f && limit > 0 ? NAN : 0.f;
+#pragma unroll 1
+            for (int e = 0; e < D; e += 32) {
+              uint32_t ov[32];
+              tmem_ld32(o_col + e, ov);
+              uint32_t y[16];
+#pragma unroll
+              for (int x = 0; x < 32; x += 2) {
+                const float u = __uint_as_float(ov[x]), v = __uint_as_float(ov[x + 1]);
+                bad = fmaf(u, 0.f, fmaf(v, 0.f, bad));
+                y[x / 2] = pack2<Sh::kBf16>(u * inv, v * inv);
+              }
+              if (real) {
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                  *reinterpret_cast<uint4*>(dst + e + 8 * x) = make_uint4(y[4 * x], y[4 * x + 1], y[4 * x + 2], y[4 * x + 3]);
+              }
+            }
+            odd = real && !(bad == 0.f && l < INFINITY);
+          }
+        } else {
+          // A cut unit: this piece's m, l and O to its slot; the last of the row tile's pieces
+          // to finish adds them up in the order of their CTAs.
+          const int first = w.owner(0), pieces = w.owner(pc.kend[i] - 1) - first + 1;
+          const size_t slot_sz = pf_slot_floats(D);
+          auto slot_of = [&](int p) {
+            return a.partials + (static_cast<size_t>(2 * (first + p) + (p == 0 ? 1 : 0)) * a.slot_tiles + i) * slot_sz;
+          };
+          if (alive) {
+            float* sl = slot_of(blockIdx.x - first);
+            if (real) {
+              sl[r] = m;
+              sl[128 + r] = l;
+            }
+#pragma unroll 1
+            for (int e = 0; e < D; e += 32) {
+              uint32_t ov[32];
+              tmem_ld32(o_col + e, ov);
+              if (real) {
+#pragma unroll
+                for (int x = 0; x < 32; x += 4)
+                  *reinterpret_cast<uint4*>(sl + 256 + ((e + x) / 8 * 128 + r) * 8 + x % 8) =
+                      make_uint4(ov[x], ov[x + 1], ov[x + 2], ov[x + 3]);
+              }
+            }
+            tc_fence_before_sync();
+          }
+          fence_acq_rel_gpu();
+          named_bar_sync(1 + i, 128);
+          if (r == 0) {
+            unsigned long long* ctr = a.piece_counts + 2 * first + i;
+            const unsigned long long tag = static_cast<unsigned long long>(a.epoch) << 32;
+            unsigned long long old = *reinterpret_cast<volatile unsigned long long*>(ctr), want;
+            for (;;) {
+              const unsigned done = (old >> 32) == a.epoch ? static_cast<unsigned>(old) : 0u;
+              want = tag | (done + 1);
+              const unsigned long long got = atomicCAS(ctr, old, want);
+              if (got == old) break;
+              old = got;
+            }
+            const bool fin = static_cast<int>(static_cast<unsigned>(want)) == pieces;
+            if (fin) *reinterpret_cast<volatile unsigned long long*>(ctr) = 0ull;   // clear for a replay
+            last_piece[i] = fin;
+          }
+          named_bar_sync(1 + i, 128);
+          const bool mine = last_piece[i] != 0 && alive;
+          named_bar_sync(1 + i, 128);   // read before the next piece's flag
+          if (mine) {
+            fence_acq_rel_gpu();
+            if (real) {
+              float M = -INFINITY;
+              for (int p = 0; p < pieces; ++p) M = fmaxf(M, __ldcg(slot_of(p) + r));
+              const float mu = M == -INFINITY ? 0.f : M;
+              float L = 0.f;
+              for (int p = 0; p < pieces; ++p)
+                L += __ldcg(slot_of(p) + 128 + r) * fast_exp2(__ldcg(slot_of(p) + r) - mu);
+              const float inv = L > 0.f ? 1.f / L : 0.f;
+              float bad = L == 0.f && limit > 0 ? NAN : 0.f;
+#pragma unroll 1
+              for (int e = 0; e < D; e += 16) {
+                float o[16];
+#pragma unroll
+                for (int x = 0; x < 16; ++x) o[x] = 0.f;
+                for (int p = 0; p < pieces; ++p) {
+                  const float* sl = slot_of(p);
+                  const float wp = fast_exp2(__ldcg(sl + r) - mu);
+                  const float4* src0 = reinterpret_cast<const float4*>(sl + 256 + (e / 8 * 128 + r) * 8);
+                  const float4* src1 = src0 + 256;
+                  const float4 f[4] = {__ldcg(src0), __ldcg(src0 + 1), __ldcg(src1), __ldcg(src1 + 1)};
+#pragma unroll
+                  for (int x = 0; x < 4; ++x) {
+                    o[4 * x] = fmaf(wp, f[x].x, o[4 * x]);
+                    o[4 * x + 1] = fmaf(wp, f[x].y, o[4 * x + 1]);
+                    o[4 * x + 2] = fmaf(wp, f[x].z, o[4 * x + 2]);
+                    o[4 * x + 3] = fmaf(wp, f[x].w, o[4 * x + 3]);
+                  }
+                }
+                uint32_t y[8];
+#pragma unroll
+                for (int x = 0; x < 16; x += 2) {
+                  bad = fmaf(o[x], 0.f, fmaf(o[x + 1], 0.f, bad));
+                  y[x / 2] = pack2<Sh::kBf16>(o[x] * inv, o[x + 1] * inv);
+                }
+                *reinterpret_cast<uint4*>(dst + e) = make_uint4(y[0], y[1], y[2], y[3]);
+                *reinterpret_cast<uint4*>(dst + e + 8) = make_uint4(y[4], y[5], y[6], y[7]);
+              }
+              odd = !(bad == 0.f && L < INFINITY);
+            }
+          }
+        }
+        __syncwarp();
+        const unsigned again = __ballot_sync(0xffffffffu, odd);
+        if (again) pf_redo<KV, D>(a, again, w.p.s, w.p.qb, w.past(), pc.j0, 128 * i + 32 * (warp & 3), w.p.h, ctl);
+        tc_fence_before_sync();   // O_i is read before the next piece's product overwrites it
+      }
+    } else if (Sh::kWiden && warp >= 12) {
+      // ------------------------- widening loader (one-byte caches) --------------------
+      regs_shrink<Sh::kWidenRegs>();
+      if constexpr (Sh::kWiden) {
+        constexpr int LPR = D / 16;               // lanes of a row (16 bytes each)
+        constexpr int RPW = 32 / LPR;             // rows of a warp's load
+        constexpr int NL = kPfTile / (4 * RPW);   // loads of a thread per tile
+        const int wi = warp - 12, wt = tid - 384;
+        const int cc = lane % LPR;
+        uint32_t st = 0;
+        uint32_t tiles = 0;
+        bool alive = true;
+        for (PfWalk w(a, *start); !w.done() && alive; w.advance()) {
+          const PfPiece pc(w);
+          const int32_t* bt = a.block_tables + static_cast<size_t>(w.p.s) * a.max_blocks_per_seq;
+          for (int k = pc.ka; k < pc.klast && alive; ++k, ++tiles) {
+#pragma unroll 1
+            for (int v = 0; v < 2; ++v, ++st) {
+              const uint8_t* cache = static_cast<const uint8_t*>(v ? a.v_cache : a.k_cache);
+              uint4 x[NL];
+#pragma unroll
+              for (int q = 0; q < NL; ++q) {
+                const int row = (q * 4 + wi) * RPW + lane / LPR;
+                const int p = k * kPfTile + row;
+                x[q] = make_uint4(0u, 0u, 0u, 0u);
+                if constexpr (KV == kKvInt8) x[q] = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
+                if (p < w.p.ctx) {
+                  const int b = bt[p >> 4];
+                  if (static_cast<unsigned>(b) < static_cast<unsigned>(a.num_blocks))
+                    x[q] = __ldg(reinterpret_cast<const uint4*>(
+                        cache + ((static_cast<size_t>(b) * a.num_kv_heads + w.p.h) * kBlockSize + (p & 15)) * D + 16 * cc));
+                  else if (a.status) atomicOr(a.status, kDevBadBlock);
+                }
+              }
+              float scale = 0.f;
+              if constexpr (KV == kKvInt8) {
+                const int p = k * kPfTile + wt;
+                if (p < w.p.ctx) {
+                  const int b = bt[p >> 4];
+                  if (static_cast<unsigned>(b) < static_cast<unsigned>(a.num_blocks))
+                    scale = a.scales[(static_cast<size_t>(b) * a.num_kv_heads + w.p.h) * 32 + 16 * v + (p & 15)];
+                }
+              }
+              const uint32_t stage = st % NS, round = st / NS;
+              if (round > 0) {
+                const bool ok = pf_wait(empty + 8 * stage, (round - 1) & 1, ctl);
+                if (!__all_sync(0xffffffffu, ok)) {
+                  alive = false;
+                  ctl->abort = 1;
+                  if (lane == 0 && a.status) atomicOr(a.status, kDevTimeout);
+                  break;
+                }
+              }
+              uint8_t* dst = smem + Sh::kRing + stage * Sh::kStageBytes;
+#pragma unroll
+              for (int q = 0; q < NL; ++q) {
+                const int row = (q * 4 + wi) * RPW + lane / LPR;
+                uint4 lo, hi;
+                widen16<KV>(x[q], lo, hi);
+                // Elements 16 cc .. 16 cc + 15: chunks 2 (cc % 4), + 1 of half cc / 4. The upper
+                // half's lanes write their second chunk first, so that a row's eight lanes
+                // cover eight chunks (all banks) in each store.
+                uint8_t* d = dst + (cc >> 2) * Sh::kHalfBytes + row * 128;
+                const int c0 = 2 * (cc & 3) + (cc >> 2), c1 = 2 * (cc & 3) + 1 - (cc >> 2);
+                *reinterpret_cast<uint4*>(d + ((c0 ^ (row & 7)) << 4)) = (cc >> 2) ? hi : lo;
+                *reinterpret_cast<uint4*>(d + ((c1 ^ (row & 7)) << 4)) = (cc >> 2) ? lo : hi;
+              }
+              if constexpr (KV == kKvInt8)
+                reinterpret_cast<float*>(smem + Sh::kScales)[tiles % Sh::kScaleRing * 2 * kPfTile + v * kPfTile + wt] = scale;
+              fence_proxy_async_smem();
+              mbar_arrive(full + 8 * stage);
+              if (KV == kKvInt8 && v == 1) mbar_arrive(sc_full + 8 * (tiles % Sh::kScaleRing));
+            }
+          }
+        }
+      }
+    } else {
+      regs_shrink<Sh::kIssueRegs>();
+      if (warp == 8) {
+        // ----------------------------- product issue ----------------------------------
+        constexpr uint32_t id_s = idesc_kind_f16(128, 128, Sh::kBf16, 0, 0);   // Q (K-major) x K^T (K-major)
+        constexpr uint32_t id_o = idesc_kind_f16(128, D, Sh::kBf16, 0, 1);     // P (TMEM) x V (dimensions contiguous)
+        // An operand's later atoms: its first descriptor with the address field advanced
+        // (16-byte units; shared-memory addresses stay below 2^18, so it never carries).
+        const uint64_t dq = smem_desc_sw128(base, 0, 1024);
+        const uint64_t dk = smem_desc_sw128(base + Sh::kRing, 0, 1024);
+        const uint64_t dv = smem_desc_sw128(base + Sh::kRing, Sh::kHalfBytes, 1024);
+        uint32_t st = 0, cnt[2] = {0, 0}, piece = 0;
+        bool ok = true;
+        auto wait = [&](uint32_t bar, uint32_t parity) {
+          if (ok && !pf_wait(bar, parity, ctl)) ok = false;
+          ok = __all_sync(0xffffffffu, ok);
+          return ok;
+        };
+        auto issue_s = [&](int i, uint32_t stage) {
+          if (lane == 0) {
+            const uint64_t qa = dq + ((static_cast<uint32_t>(i) * 128 * 128) >> 4);
+            const uint64_t kb = dk + ((stage * Sh::kStageBytes) >> 4);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+              tc_mma_f16_ss(tmem + kPfSCol + 128 * i, qa + (((kk >> 2) * Sh::kQHalfBytes + (kk & 3) * 32) >> 4),
+                            kb + (((kk >> 2) * Sh::kHalfBytes + (kk & 3) * 32) >> 4), id_s, kk > 0);
+            tc_commit(s_full + 8 * i);
+          }
+          __syncwarp();
+        };
+        for (PfWalk w(a, *start); !w.done() && ok; w.advance()) {
+          const PfPiece pc(w);
+          if (!pc.any()) continue;
+          if (!wait(q_full, piece & 1)) break;
+          uint32_t ks = st % NS;
+          if (!wait(full + 8 * ks, (st / NS) & 1)) break;
+          tc_fence_after_sync();
+          for (int i = 0; i < 2; ++i)
+            if (pc.active(i)) issue_s(i, ks);
+          if (lane == 0) tc_commit(empty + 8 * ks);
+          if (pc.ka + 1 == pc.klast && lane == 0) tc_commit(q_empty);
+          ++st;
+          for (int k = pc.ka; k < pc.klast && ok; ++k) {
+            const uint32_t vs = st % NS;
+            if (!wait(full + 8 * vs, (st / NS) & 1)) break;
+            ++st;
+            if (!Sh::kWiden && (k + 1) * kPfTile > w.p.ctx && (w.p.ctx & 15)) {
+              // V rows behind the context in its last block: zero (whole blocks behind it were
+              // copied as zeros)
+              const int r0 = w.p.ctx - k * kPfTile, r1 = (r0 + 15) & ~15;
+              if (r0 >= 0) {
+                uint8_t* vt = smem + Sh::kRing + vs * Sh::kStageBytes;
+                for (int x = lane; x < (r1 - r0) * Sh::kHalves * 8; x += 32) {
+                  const int row = r0 + x / (Sh::kHalves * 8), ch = x % (Sh::kHalves * 8);
+                  *reinterpret_cast<uint4*>(vt + (ch >> 3) * Sh::kHalfBytes + row * 128 + (ch & 7) * 16) =
+                      make_uint4(0u, 0u, 0u, 0u);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+              }
+            }
+            const bool more = k + 1 < pc.klast;
+            if (more) {
+              ks = st % NS;
+              if (!wait(full + 8 * ks, (st / NS) & 1)) break;
+              ++st;
+            }
+            for (int i = 0; i < 2; ++i) {
+              if (k >= pc.kb[i]) continue;
+              if (!wait(p_ready + 8 * i, cnt[i] & 1)) break;
+              ++cnt[i];
+              tc_fence_after_sync();
+              if (lane == 0) {
+                const uint64_t vb = dv + ((vs * Sh::kStageBytes) >> 4);
+#pragma unroll
+                for (int kk = 0; kk < kPfTile / 16; ++kk)
+                  tc_mma_f16_ts(tmem + kPfOCol + 128 * i, tmem + kPfSCol + 128 * i + kk * 8, vb + ((kk * 2048) >> 4),
+                                id_o, (kk > 0 || k > pc.ka) ? 1u : 0u);
+                tc_commit(o_done + 8 * i);
+              }
+              __syncwarp();
+              if (k + 1 < pc.kb[i]) issue_s(i, ks);
+            }
+            if (!ok) break;
+            if (lane == 0) {
+              tc_commit(empty + 8 * vs);
+              if (more) tc_commit(empty + 8 * ks);
+              if (k + 2 == pc.klast) tc_commit(q_empty);   // the last scores are issued
+            }
+          }
+          ++piece;
+        }
+        if (!ok) {
+          ctl->abort = 1;
+          if (lane == 0 && a.status) atomicOr(a.status, kDevTimeout);
+        }
+        // Every product issued completes before the tensor memory is released.
+        if (lane == 0) {
+          tc_commit(final_bar);
+          mbar_wait(final_bar, 0);
+        }
+        __syncwarp();
+      } else if (warp == 9) {
+        // -------------------------------- copies ---------------------------------------
+        const int total_rows = a.num_blocks * a.num_kv_heads * kBlockSize;   // host guarantees < 2^31
+        uint32_t st = 0, piece = 0;
+        bool ok = true;
+        auto wait = [&](uint32_t bar, uint32_t parity) {
+          if (ok && !pf_wait(bar, parity, ctl)) ok = false;
+          ok = __all_sync(0xffffffffu, ok);
+          return ok;
+        };
+        for (PfWalk w(a, *start); !w.done() && ok; w.advance()) {
+          const PfPiece pc(w);
+          if (!pc.any()) continue;
+          if (piece > 0 && !wait(q_empty, (piece - 1) & 1)) break;
+          const int box_rows = a.box_tokens * a.group;
+          const int boxes = (pc.rows + box_rows - 1) / box_rows;
+          if (lane == 0) mbar_arrive_expect_tx(q_full, boxes * Sh::kHalves * box_rows * 128);
+          __syncwarp();
+          for (int x = lane; x < boxes * Sh::kHalves; x += 32) {
+            const int b = x / Sh::kHalves, hf = x % Sh::kHalves;
+            tma_load_3d_keep(base + hf * Sh::kQHalfBytes + b * box_rows * 128, &tm_q, 64 * hf, w.p.h * a.group,
+                             w.p.qb + pc.j0 + b * a.box_tokens, q_full);
+          }
+          ++piece;
+          if constexpr (!Sh::kWiden) {
+            const int32_t* bt = a.block_tables + static_cast<size_t>(w.p.s) * a.max_blocks_per_seq;
+            // lane = (block of the tile, half)
+            constexpr int NB = kPfTile / kBlockSize;
+            const int blk = lane / Sh::kHalves, hf = lane % Sh::kHalves;
+            for (int k = pc.ka; k < pc.klast && ok; ++k) {
+              int row = total_rows;   // wholly past the end: the copy fills zeros
+              if (blk < NB) {
+                const int p = k * kPfTile + blk * kBlockSize;
+                if (p < w.p.ctx) {
+                  const int id = bt[p >> 4];
+                  if (static_cast<unsigned>(id) < static_cast<unsigned>(a.num_blocks))
+                    row = (id * a.num_kv_heads + w.p.h) * kBlockSize;
+                  else if (a.status) atomicOr(a.status, kDevBadBlock);
+                }
+              }
+              for (int v = 0; v < 2; ++v, ++st) {
+                const uint32_t stage = st % NS, round = st / NS;
+                if (round > 0 && !wait(empty + 8 * stage, (round - 1) & 1)) break;
+                if (lane == 0) mbar_arrive_expect_tx(full + 8 * stage, Sh::kStageBytes);
+                __syncwarp();
+                if (blk < NB) {
+                  const CUtensorMap* tm = v ? (hf ? &tm_v1 : &tm_v0) : (hf ? &tm_k1 : &tm_k0);
+                  tma_load_2d_keep(base + Sh::kRing + stage * Sh::kStageBytes + hf * Sh::kHalfBytes +
+                                       blk * (kBlockSize * 128), tm, 0, row, full + 8 * stage);
+                }
+              }
+            }
+          }
+        }
+        if (!ok) {
+          ctl->abort = 1;
+          if (lane == 0 && a.status) atomicOr(a.status, kDevTimeout);
+        }
+        // Drain: every copy issued into this CTA's shared memory lands before exit.
+        if (lane == 0) {
+          if (piece > 0) mbar_wait(q_full, (piece - 1) & 1);
+          if (!Sh::kWiden)
+            for (uint32_t k = st > NS ? st - NS : 0; k < st; ++k) mbar_wait(full + 8 * (k % NS), (k / NS) & 1);
+        }
+        __syncwarp();
+      }
+    }
+  }
+
+  // Teardown: every role is done with the tensor memory.
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+}  // namespace pkv

@@ -1,0 +1,221 @@
+// How a prefill call's work is cut into the CTAs' shares.
+//
+// A unit is a (sequence, KV head, row tile): up to 256 query rows (a row is one query
+// token and one of the G query heads of the KV head; whole tokens, token-major) against
+// the positions its last token sees. Units lie on a line in the order sequence, KV head,
+// tile; a unit is kUnitCost positions (its query load and output) plus the positions its
+// last row sees. Every CTA takes an equal stretch of the line; tile k of a unit (positions
+// 128k .. 128k + 127) belongs to the CTA whose stretch holds its first position. A unit
+// cut by a stretch's end becomes pieces that are merged by the last to finish.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "pkv_internal.h"
+#include "prefill_row.cuh"
+
+namespace pkv {
+
+constexpr int kPfRows = 256;          // query rows of a unit: two tiles of the MMA's M
+constexpr int kPfTile = 128;          // positions of a KV tile
+constexpr int kPfUnitCost = 128;      // a unit's fixed cost, in positions
+constexpr int kPfMinShare = 2 * kPfTile + kPfUnitCost;   // at least one whole tile a piece
+
+// Tokens of one TMA box of query rows, and of a unit (whole boxes). Boxes start on the
+// swizzle's 8-row atoms, 32 rows or the next possible number each, so that a short unit
+// copies little; where such boxes leave more than a quarter of the rows empty (a large
+// odd group), one box of as many tokens as fit.
+struct PfBox {
+  int tokens, unit;
+};
+inline PfBox pf_box(int group) {
+  int atom = 1;
+  while (atom * group % 8 != 0) ++atom;
+  int bt = atom;
+  while ((bt + atom) * group <= 32) bt += atom;
+  const int most = kPfRows / group, unit = most / bt * bt;
+  if (4 * unit < 3 * most) return {most, most};
+  return {bt, unit};
+}
+
+// Shared description of a CTA's stretch, written by pf_plan.
+struct PfStart {
+  long long b0, b1, share, ub;
+  int s, h, t, any;
+};
+
+// A place on the walk: the current unit and its sequence.
+struct PfPos {
+  long long ub;              // line position of the unit
+  int s, h, t;
+  int n, qb, ctx;            // of sequence s
+};
+
+struct PfWalk {
+  const PrefillArgs& a;
+  const PfStart& st;
+  PfPos p;
+
+  __device__ PfWalk(const PrefillArgs& args, const PfStart& start) : a(args), st(start) {
+    p.ub = st.ub;
+    p.s = st.s;
+    p.h = st.h;
+    p.t = st.t;
+    load();
+  }
+  __device__ void load() {
+    const PrefillSeq q = prefill_seq(a, p.s);
+    p.n = q.n;
+    p.qb = q.qb;
+    p.ctx = q.ctx;
+  }
+  __device__ bool done() const { return p.ub >= st.b1; }
+  __device__ int past() const { return p.ctx - p.n; }
+  __device__ int pastp() const { return max(past(), 0); }
+  __device__ int len() const { return pastp() + min((p.t + 1) * a.unit_tokens, p.n); }
+  __device__ void advance() {
+    p.ub += kPfUnitCost + len();
+    if (++p.t * a.unit_tokens < p.n) return;
+    p.t = 0;
+    if (++p.h < a.num_kv_heads) return;
+    p.h = 0;
+    if (p.ub >= st.b1) return;
+    do {
+      ++p.s;
+      load();
+    } while (p.n == 0);   // ub < b1 <= the line's end: another sequence with rows follows
+  }
+  __device__ int owner(int k) const {
+    return static_cast<int>((p.ub + kPfUnitCost + static_cast<long long>(kPfTile) * k) / st.share);
+  }
+  // Keep the place in shared memory (of this warp) while a long loop needs the registers.
+  __device__ void save(volatile PfPos* to) const {
+    if ((threadIdx.x & 31) == 0) {
+      to->ub = p.ub;
+      to->s = p.s;
+      to->h = p.h;
+      to->t = p.t;
+      to->n = p.n;
+      to->qb = p.qb;
+      to->ctx = p.ctx;
+    }
+    __syncwarp();
+  }
+  __device__ void restore(const volatile PfPos* from) {
+    p.ub = from->ub;
+    p.s = from->s;
+    p.h = from->h;
+    p.t = from->t;
+    p.n = from->n;
+    p.qb = from->qb;
+    p.ctx = from->ctx;
+    __syncwarp();
+  }
+};
+
+// This CTA's piece of the walk's current unit.
+struct PfPiece {
+  int j0, rows;              // first query token, rows of the unit
+  int ka, kb[2];             // KV tiles [ka, kb[i]) of row tile i (empty: kb <= ka)
+  int kend[2];               // tiles of the whole unit row tile i needs
+  int klast;                 // max of kb
+
+  __device__ PfPiece(const PfWalk& w) {
+    const int G = w.a.group, qt = w.a.unit_tokens;
+    j0 = w.p.t * qt;
+    rows = min(qt, w.p.n - j0) * G;
+    const int k_all = (w.len() + kPfTile - 1) / kPfTile;
+    const long long x0 = w.st.b0 - w.p.ub - kPfUnitCost, x1 = w.st.b1 - w.p.ub - kPfUnitCost;
+    ka = x0 <= 0 ? 0 : static_cast<int>((x0 + kPfTile - 1) / kPfTile);
+    const int kx = x1 <= 0 ? 0 : static_cast<int>(min((x1 + kPfTile - 1) / kPfTile, static_cast<long long>(k_all)));
+    if (rows > 128) {
+      kend[0] = (w.pastp() + j0 + 127 / G + 1 + kPfTile - 1) / kPfTile;
+      kend[1] = k_all;
+    } else {
+      kend[0] = k_all;
+      kend[1] = 0;
+    }
+    kb[0] = min(kx, kend[0]);
+    kb[1] = min(kx, kend[1]);
+    klast = max(kb[0], kb[1]);
+  }
+  __device__ bool active(int i) const { return ka < kb[i]; }
+  __device__ bool any() const { return ka < klast; }
+  __device__ bool whole(int i) const { return ka == 0 && kb[i] == kend[i]; }
+};
+
+// Line length of one KV head of a sequence: T units of cost + pastp + min((t+1) qt, n).
+__device__ __forceinline__ long long pf_head_len(int n, int pastp, int qt) {
+  if (n == 0) return 0;
+  const long long T = (n + qt - 1) / qt;
+  return T * (kPfUnitCost + pastp) + static_cast<long long>(qt) * ((T - 1) * T / 2) + n;
+}
+
+// The CTA's start on the line. Every thread of the CTA takes part; scratch: one long long a
+// warp. CTA 0 flags the sequences that break a rule. Ends with a barrier.
+__device__ inline void pf_plan(const PrefillArgs& a, long long* scratch, PfStart* st) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
+  const int per = (a.num_seqs + blockDim.x - 1) / blockDim.x;
+  const int s0 = tid * per, s1 = min(s0 + per, a.num_seqs);
+  if (tid == 0) st->any = 0;
+  long long mine = 0;
+  bool bad = false;
+  for (int s = s0; s < s1; ++s) {
+    const PrefillSeq p = prefill_seq(a, s);
+    bad |= p.bad;
+    mine += a.num_kv_heads * pf_head_len(p.n, max(p.past(), 0), a.unit_tokens);
+  }
+  if (bad && blockIdx.x == 0 && a.status) atomicOr(a.status, kDevBadCtx);
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) scratch[warp] = incl;
+  __syncthreads();
+  long long total = 0, excl = incl - mine;
+  for (int w = 0; w < nw; ++w) {
+    if (w < warp) excl += scratch[w];
+    total += scratch[w];
+  }
+  long long share = (total + gridDim.x - 1) / gridDim.x;
+  if (share < kPfMinShare) share = kPfMinShare;
+  const long long b0 = static_cast<long long>(blockIdx.x) * share;
+  if (b0 < total && excl <= b0 && b0 < excl + mine) {
+    long long at = excl;
+    for (int s = s0; s < s1; ++s) {
+      const PrefillSeq p = prefill_seq(a, s);
+      const int pastp = max(p.past(), 0), qt = a.unit_tokens;
+      const long long head = pf_head_len(p.n, pastp, qt);
+      if (b0 >= at + a.num_kv_heads * head) {
+        at += a.num_kv_heads * head;
+        continue;
+      }
+      const int h = static_cast<int>((b0 - at) / head);
+      const long long rem = b0 - at - h * head;
+      // the unit that holds position rem: units before t take t (cost + pastp) + qt t (t + 1) / 2
+      const long long c = kPfUnitCost + pastp;
+      int lo = 0, hi = (p.n + qt - 1) / qt - 1;
+      while (lo < hi) {
+        const long long t = (lo + hi + 1) / 2;
+        if (t * c + qt * (t * (t + 1) / 2) <= rem) lo = static_cast<int>(t);
+        else hi = static_cast<int>(t) - 1;
+      }
+      st->b0 = b0;
+      st->b1 = min(b0 + share, total);
+      st->share = share;
+      st->ub = at + h * head + lo * c + static_cast<long long>(qt) * (static_cast<long long>(lo) * (lo + 1) / 2);
+      st->s = s;
+      st->h = h;
+      st->t = lo;
+      st->any = 1;
+      break;
+    }
+  }
+  __syncthreads();
+}
+
+}  // namespace pkv

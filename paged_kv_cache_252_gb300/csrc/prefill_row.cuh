@@ -30,6 +30,11 @@ struct PrefillArgs {
   int32_t q_rows, num_seqs, num_q_heads, num_kv_heads, group;
   int32_t max_blocks_per_seq, num_blocks;
   float scale_log2;            // softmax scale * log2(e)
+  int32_t box_tokens, unit_tokens;     // query tokens of a TMA box and of a unit (prefill_plan.cuh)
+  unsigned long long* piece_counts;    // [2 grid]: (call epoch << 32) | pieces of a cut row tile finished
+  float* partials;                     // [2 grid][row tiles] slots of pf_slot_floats
+  int32_t slot_tiles;                  // row tiles of a slot (1 or 2)
+  uint32_t epoch;                      // distinct for every call (tags the piece counters)
 };
 
 // A sequence's query rows and lengths, with everything out of range made harmless:
@@ -91,15 +96,14 @@ __device__ __forceinline__ float load1(const void* cache, size_t e) {
 
 // Row `row` (token qb + j) of query head hq of sequence s; limit = visible positions. The
 // warp's lanes take 32 positions at a time for the scores, then D/32 dimensions each
-// for the sum. qs: D floats of shared memory of this warp.
+// for the sum.
 template <int KV, int D>
-__device__ __forceinline__ void prefill_row(const PrefillArgs& a, int s, int row, int hq, int limit, float* qs) {
+__device__ __forceinline__ void prefill_row(const PrefillArgs& a, int s, int row, int hq, int limit) {
   constexpr int E = D / 32;
   const int lane = threadIdx.x & 31;
   const int h = hq / a.group;
   const size_t qo = (static_cast<size_t>(row) * a.num_q_heads + hq) * D;
-  for (int d = lane; d < D; d += 32) qs[d] = load1<KV == kKvBf16 ? kKvBf16 : kKvF16>(a.q, qo + d);
-  __syncwarp();
+  constexpr int Q = KV == kKvBf16 ? kKvBf16 : kKvF16;
   const int32_t* bt = a.block_tables + static_cast<size_t>(s) * a.max_blocks_per_seq;
   float m = -INFINITY, l = 0.f, o[E];
 #pragma unroll
@@ -115,10 +119,11 @@ __device__ __forceinline__ void prefill_row(const PrefillArgs& a, int s, int row
         crow = (static_cast<long long>(b) * a.num_kv_heads + h) * kBlockSize + (p & 15);
 #pragma unroll 4
         for (int c = 0; c < D / 8; ++c) {
-          float k[8];
+          float q[8], k[8];
+          load8<Q>(a.q, qo + 8 * c, q);   // the same for every lane
           load8<KV>(a.k_cache, static_cast<size_t>(crow) * D + 8 * c, k);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) dot = fmaf(qs[8 * c + i], k[i], dot);
+          for (int i = 0; i < 8; ++i) dot = fmaf(q[i], k[i], dot);
         }
         if constexpr (KV == kKvInt8) {
           dot *= a.scales[(crow >> 4) * 32 + (crow & 15)];
@@ -166,7 +171,6 @@ __device__ __forceinline__ void prefill_row(const PrefillArgs& a, int s, int row
     if constexpr (KV == kKvBf16) dst[e] = __bfloat16_as_ushort(__float2bfloat16_rn(y));
     else dst[e] = __half_as_ushort(__float2half_rn(y));
   }
-  __syncwarp();
 }
 
 }  // namespace pkv
