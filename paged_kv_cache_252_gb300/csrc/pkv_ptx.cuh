@@ -239,6 +239,13 @@ __device__ __forceinline__ float fast_exp2(float x) {
   return y;
 }
 
+// The largest of three (NaN operands lose, as with fmaxf).
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // {lo, hi} -> packed pair, round to nearest even.
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t d;

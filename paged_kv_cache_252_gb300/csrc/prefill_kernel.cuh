@@ -13,7 +13,7 @@
 //
 // Warps: 0..3 and 4..7 the softmax of row tiles 0 and 1, warp 8 issues the products, warp 9
 // the copies (queries; for 16-bit caches also the K and V tiles: 16-token boxes through the
-// block table into the swizzled operand layout). One-byte caches add warps 12..15, which
+// block table into the swizzled operand layout), warp 10 clears V rows behind the context. One-byte caches add warps 12..15, which
 // load the tiles, widen them to fp16 and write the operand layout themselves.
 //
 // Masks. Only tiles that reach past some row's last position compare positions; a masked
@@ -70,7 +70,7 @@ struct PfShape {
   static constexpr uint32_t kRing = kQBytes;
   static constexpr uint32_t kScales = kRing + kStages * kStageBytes;   // INT8: [kScaleRing][K, V][128] floats
   static constexpr uint32_t kBars = kScales + (KV == kKvInt8 ? kScaleRing * 2 * kPfTile * 4 : 0);
-  static constexpr uint32_t kMisc = kBars + (2 * kStages + 9 + kScaleRing) * 8;
+  static constexpr uint32_t kMisc = kBars + (4 * kStages + 9 + kScaleRing) * 8;
   static constexpr uint32_t kPos = kMisc + 256 + sizeof(PfStart);   // PfPos of each softmax warp
   static constexpr uint32_t kSmem = kPos + 8 * sizeof(PfPos) + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory of one CTA");
@@ -160,9 +160,12 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
   const uint32_t q_full = empty + 8 * NS, q_empty = q_full + 8;
   const uint32_t s_full = q_empty + 8;      // [2] scores of row tile i written
   const uint32_t p_ready = s_full + 16;     // [2] weights of row tile i written, O_i rescaled
-  const uint32_t o_done = p_ready + 16;     // [2] P V product of row tile i complete
+  const uint32_t o_done = p_ready + 16;     // [2] last P V product of a piece's row tile i complete
   const uint32_t final_bar = o_done + 16;
-  const uint32_t sc_full = final_bar + 8;   // [kScaleRing] row scales of a tile written (INT8)
+  // Per stage, so that a use is never more than one phase ahead of its waiter:
+  const uint32_t v_tail = final_bar + 8;    // [NS] V rows behind the context zeroed
+  const uint32_t v_sent = v_tail + 8 * NS;  // [NS] copies of such a tile issued
+  const uint32_t sc_full = v_sent + 8 * NS; // [kScaleRing] row scales of a tile written (INT8)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Sh::kMisc);
   PfCtl* ctl = reinterpret_cast<PfCtl*>(smem + Sh::kMisc + 8);
   volatile int* last_piece = reinterpret_cast<volatile int*>(smem + Sh::kMisc + 16);   // [2]
@@ -174,6 +177,8 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
     for (int k = 0; k < NS; ++k) {
       mbar_init(full + 8 * k, Sh::kWiden ? 128 : 1);
       mbar_init(empty + 8 * k, 1);
+      mbar_init(v_tail + 8 * k, 1);
+      mbar_init(v_sent + 8 * k, 1);
     }
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
@@ -215,7 +220,7 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
       const uint32_t bar_s = s_full + 8 * i, bar_p = p_ready + 8 * i, bar_o = o_done + 8 * i;
       const float c = a.scale_log2;
       bool alive = true;
-      uint32_t cnt = 0;                             // tiles of this row tile so far
+      uint32_t cnt = 0, done = 0;                   // tiles and pieces of this row tile so far
       uint32_t seen = 0;                            // KV tiles of the CTA so far (INT8 scale ring)
       auto wait = [&](uint32_t bar, uint32_t parity) {
         if (!alive) return;
@@ -275,14 +280,25 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
               for (int e = 0; e < 32; ++e) sv[g][e] = 32 * g + e < vis ? sv[g][e] : 0xFF800000u;
             }
           }
-          float mx4[4];
+          // eight chains of three-operand maxima
+          float mx8[8];
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
-            mx4[g] = __uint_as_float(sv[g][0]);
-#pragma unroll
-            for (int e = 1; e < 32; ++e) mx4[g] = fmaxf(mx4[g], __uint_as_float(sv[g][e]));
+            mx8[2 * g] = __uint_as_float(sv[g][0]);
+            mx8[2 * g + 1] = __uint_as_float(sv[g][1]);
           }
-          float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+#pragma unroll
+          for (int e = 2; e < 30; e += 4) {
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+              mx8[2 * g] = max3(mx8[2 * g], __uint_as_float(sv[g][e]), __uint_as_float(sv[g][e + 1]));
+              mx8[2 * g + 1] = max3(mx8[2 * g + 1], __uint_as_float(sv[g][e + 2]), __uint_as_float(sv[g][e + 3]));
+            }
+          }
+#pragma unroll
+          for (int g = 0; g < 4; ++g)
+            mx8[2 * g] = max3(mx8[2 * g], __uint_as_float(sv[g][30]), __uint_as_float(sv[g][31]));
+          float mx = max3(max3(mx8[0], mx8[1], mx8[2]), max3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7]));
           mx *= c;
           const bool need = mx > m + Sh::kSlack;
           if (__any_sync(0xffffffffu, need)) {
@@ -291,17 +307,14 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
             m = mn;
             l *= alpha;
             if (!first) {
-              wait(bar_o, (cnt - 1) & 1);
-              if (alive) {
-                tc_fence_after_sync();
+              // Products complete in issue order: these scores were issued behind the last P V.
 #pragma unroll 1
-                for (int e = 0; e < D; e += 32) {
-                  uint32_t ov[32];
-                  tmem_ld32(o_col + e, ov);
+              for (int e = 0; e < D; e += 32) {
+                uint32_t ov[32];
+                tmem_ld32(o_col + e, ov);
 #pragma unroll
-                  for (int x = 0; x < 32; ++x) ov[x] = __float_as_uint(__uint_as_float(ov[x]) * alpha);
-                  tmem_st32(o_col + e, ov);
-                }
+                for (int x = 0; x < 32; ++x) ov[x] = __float_as_uint(__uint_as_float(ov[x]) * alpha);
+                tmem_st32(o_col + e, ov);
               }
             }
           }
@@ -346,7 +359,7 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
         const PfPiece pc(w);
         const int ru = 128 * i + r, j = pc.j0 + ru / a.group;
         const bool real = ru < pc.rows;
-        wait(bar_o, (cnt - 1) & 1);
+        wait(bar_o, done++ & 1);
         if (alive) tc_fence_after_sync();
         uint16_t* dst = static_cast<uint16_t*>(a.out) +
                         (static_cast<size_t>(w.p.qb + j) * a.num_q_heads + w.p.h * a.group + ru % a.group) * D;
@@ -556,15 +569,17 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
         const uint64_t dq = smem_desc_sw128(base, 0, 1024);
         const uint64_t dk = smem_desc_sw128(base + Sh::kRing, 0, 1024);
         const uint64_t dv = smem_desc_sw128(base + Sh::kRing, Sh::kHalfBytes, 1024);
-        uint32_t st = 0, cnt[2] = {0, 0}, piece = 0;
-        bool ok = true;
-        auto wait = [&](uint32_t bar, uint32_t parity) {
-          if (ok && !pf_wait(bar, parity, ctl)) ok = false;
-          ok = __all_sync(0xffffffffu, ok);
-          return ok;
-        };
-        auto issue_s = [&](int i, uint32_t stage) {
-          if (lane == 0) {
+        // One thread does all of it: the tensor pipe accepts a product only when the one before
+        // has nearly run, so what this thread does between products is idle time there, and
+        // warp-wide steps cost it about as much as a product.
+        if (lane == 0) {
+          uint32_t st = 0, cnt[2] = {0, 0}, piece = 0, tails = 0;
+          bool ok = true;
+          auto wait = [&](uint32_t bar, uint32_t parity) {
+            if (!pf_wait(bar, parity, ctl)) ok = false;
+            return ok;
+          };
+          auto issue_s = [&](int i, uint32_t stage) {
             const uint64_t qa = dq + ((static_cast<uint32_t>(i) * 128 * 128) >> 4);
             const uint64_t kb = dk + ((stage * Sh::kStageBytes) >> 4);
 #pragma unroll
@@ -572,79 +587,97 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
               tc_mma_f16_ss(tmem + kPfSCol + 128 * i, qa + (((kk >> 2) * Sh::kQHalfBytes + (kk & 3) * 32) >> 4),
                             kb + (((kk >> 2) * Sh::kHalfBytes + (kk & 3) * 32) >> 4), id_s, kk > 0);
             tc_commit(s_full + 8 * i);
-          }
-          __syncwarp();
-        };
-        for (PfWalk w(a, *start); !w.done() && ok; w.advance()) {
-          const PfPiece pc(w);
-          if (!pc.any()) continue;
-          if (!wait(q_full, piece & 1)) break;
-          uint32_t ks = st % NS;
-          if (!wait(full + 8 * ks, (st / NS) & 1)) break;
-          tc_fence_after_sync();
-          for (int i = 0; i < 2; ++i)
-            if (pc.active(i)) issue_s(i, ks);
-          if (lane == 0) tc_commit(empty + 8 * ks);
-          if (pc.ka + 1 == pc.klast && lane == 0) tc_commit(q_empty);
-          ++st;
-          for (int k = pc.ka; k < pc.klast && ok; ++k) {
-            const uint32_t vs = st % NS;
-            if (!wait(full + 8 * vs, (st / NS) & 1)) break;
+          };
+          for (PfWalk w(a, *start); !w.done() && ok; w.advance()) {
+            const PfPiece pc(w);
+            if (!pc.any()) continue;
+            const int tail = !Sh::kWiden && (w.p.ctx & 15) ? w.p.ctx / kPfTile : -1;   // see warp 10
+            if (!wait(q_full, piece & 1)) break;
+            uint32_t ks = st % NS;
+            if (!wait(full + 8 * ks, (st / NS) & 1)) break;
+            tc_fence_after_sync();
+            for (int i = 0; i < 2; ++i)
+              if (pc.active(i)) issue_s(i, ks);
+            tc_commit(empty + 8 * ks);
+            if (pc.ka + 1 == pc.klast) tc_commit(q_empty);
             ++st;
-            if (!Sh::kWiden && (k + 1) * kPfTile > w.p.ctx && (w.p.ctx & 15)) {
-              // V rows behind the context in its last block: zero (whole blocks behind it were
-              // copied as zeros)
-              const int r0 = w.p.ctx - k * kPfTile, r1 = (r0 + 15) & ~15;
-              if (r0 >= 0) {
-                uint8_t* vt = smem + Sh::kRing + vs * Sh::kStageBytes;
-                for (int x = lane; x < (r1 - r0) * Sh::kHalves * 8; x += 32) {
-                  const int row = r0 + x / (Sh::kHalves * 8), ch = x % (Sh::kHalves * 8);
-                  *reinterpret_cast<uint4*>(vt + (ch >> 3) * Sh::kHalfBytes + row * 128 + (ch & 7) * 16) =
-                      make_uint4(0u, 0u, 0u, 0u);
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
+            for (int k = pc.ka; k < pc.klast; ++k) {
+              const uint32_t vs = st % NS;
+              if (!wait(full + 8 * vs, (st / NS) & 1)) break;
+              if (k == tail) {
+                if (!wait(v_tail + 8 * vs, (tails >> vs) & 1)) break;
+                tails ^= 1u << vs;
               }
-            }
-            const bool more = k + 1 < pc.klast;
-            if (more) {
-              ks = st % NS;
-              if (!wait(full + 8 * ks, (st / NS) & 1)) break;
               ++st;
-            }
-            for (int i = 0; i < 2; ++i) {
-              if (k >= pc.kb[i]) continue;
-              if (!wait(p_ready + 8 * i, cnt[i] & 1)) break;
-              ++cnt[i];
-              tc_fence_after_sync();
-              if (lane == 0) {
-                const uint64_t vb = dv + ((vs * Sh::kStageBytes) >> 4);
+              const bool more = k + 1 < pc.klast;
+              if (more) {
+                ks = st % NS;
+                if (!wait(full + 8 * ks, (st / NS) & 1)) break;
+                ++st;
+              }
+              const uint64_t vb = dv + ((vs * Sh::kStageBytes) >> 4);
+              const uint32_t acc = k > pc.ka ? 1u : 0u;
+              for (int i = 0; i < 2; ++i) {
+                if (k >= pc.kb[i]) continue;
+                if (!wait(p_ready + 8 * i, cnt[i] & 1)) break;
+                ++cnt[i];
+                tc_fence_after_sync();
 #pragma unroll
                 for (int kk = 0; kk < kPfTile / 16; ++kk)
                   tc_mma_f16_ts(tmem + kPfOCol + 128 * i, tmem + kPfSCol + 128 * i + kk * 8, vb + ((kk * 2048) >> 4),
-                                id_o, (kk > 0 || k > pc.ka) ? 1u : 0u);
-                tc_commit(o_done + 8 * i);
+                                id_o, kk > 0 ? 1u : acc);
+                if (k + 1 < pc.kb[i]) issue_s(i, ks);
+                else tc_commit(o_done + 8 * i);   // else the next scores' barrier tells of it
               }
-              __syncwarp();
-              if (k + 1 < pc.kb[i]) issue_s(i, ks);
-            }
-            if (!ok) break;
-            if (lane == 0) {
+              if (!ok) break;
               tc_commit(empty + 8 * vs);
               if (more) tc_commit(empty + 8 * ks);
               if (k + 2 == pc.klast) tc_commit(q_empty);   // the last scores are issued
             }
+            ++piece;
           }
-          ++piece;
-        }
-        if (!ok) {
-          ctl->abort = 1;
-          if (lane == 0 && a.status) atomicOr(a.status, kDevTimeout);
-        }
-        // Every product issued completes before the tensor memory is released.
-        if (lane == 0) {
+          if (!ok) {
+            ctl->abort = 1;
+            if (a.status) atomicOr(a.status, kDevTimeout);
+          }
+          // Every product issued completes before the tensor memory is released.
           tc_commit(final_bar);
           mbar_wait(final_bar, 0);
+        }
+        __syncwarp();
+      } else if (warp == 10 && !Sh::kWiden) {
+        // ---------------- V rows behind the context in its last block: zeros --------------
+        // (Whole blocks behind it are copied as zeros.) A piece that ends in such a block has the
+        // product wait for this warp once.
+        uint32_t st = 0, sent = 0;
+        bool ok = true;
+        for (PfWalk w(a, *start); !w.done() && ok; w.advance()) {
+          const PfPiece pc(w);
+          if (!pc.any()) continue;
+          const int tail = w.p.ctx & 15 ? w.p.ctx / kPfTile : -1;
+          if (tail >= pc.ka && tail < pc.klast) {
+            const uint32_t vst = st + 2 * (tail - pc.ka) + 1, vs = vst % NS;
+            // Once this use's copies are issued, the stage's barrier is in this use's phase.
+            ok = pf_wait(v_sent + 8 * vs, (sent >> vs) & 1, ctl) && pf_wait(full + 8 * vs, (vst / NS) & 1, ctl);
+            sent ^= 1u << vs;
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            const int r0 = w.p.ctx - tail * kPfTile, r1 = (r0 + 15) & ~15;
+            uint8_t* vt = smem + Sh::kRing + vs * Sh::kStageBytes;
+            for (int x = lane; x < (r1 - r0) * Sh::kHalves * 8; x += 32) {
+              const int row = r0 + x / (Sh::kHalves * 8), ch = x % (Sh::kHalves * 8);
+              *reinterpret_cast<uint4*>(vt + (ch >> 3) * Sh::kHalfBytes + row * 128 + (ch & 7) * 16) =
+                  make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(v_tail + 8 * vs);
+          }
+          st += 2 * (pc.klast - pc.ka);
+        }
+        if (!ok && lane == 0) {
+          ctl->abort = 1;
+          if (a.status) atomicOr(a.status, kDevTimeout);
         }
         __syncwarp();
       } else if (warp == 9) {
@@ -675,6 +708,7 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
             const int32_t* bt = a.block_tables + static_cast<size_t>(w.p.s) * a.max_blocks_per_seq;
             // lane = (block of the tile, half)
             constexpr int NB = kPfTile / kBlockSize;
+            const int tail = w.p.ctx & 15 ? w.p.ctx / kPfTile : -1;   // see warp 10
             const int blk = lane / Sh::kHalves, hf = lane % Sh::kHalves;
             for (int k = pc.ka; k < pc.klast && ok; ++k) {
               int row = total_rows;   // wholly past the end: the copy fills zeros
@@ -696,6 +730,10 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
                   const CUtensorMap* tm = v ? (hf ? &tm_v1 : &tm_v0) : (hf ? &tm_k1 : &tm_k0);
                   tma_load_2d_keep(base + Sh::kRing + stage * Sh::kStageBytes + hf * Sh::kHalfBytes +
                                        blk * (kBlockSize * 128), tm, 0, row, full + 8 * stage);
+                }
+                if (v && k == tail) {
+                  __syncwarp();
+                  if (lane == 0) mbar_arrive(v_sent + 8 * stage);
                 }
               }
             }
