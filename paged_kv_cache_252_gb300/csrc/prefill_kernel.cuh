@@ -11,8 +11,8 @@
 // columns) takes the place of the first half of S_i, which its own threads have read; the
 // next S_i is issued behind the P V product that reads P_i (products execute in issue order).
 //
-// Warps: 0..3 and 4..7 the softmax of row tiles 0 and 1, warp 8 issues the products, warp 9
-// the copies (queries; for 16-bit caches also the K and V tiles: 16-token boxes through the
+// Warps: 0..3 and 4..7 the softmax of row tiles 0 and 1, warps 8 and 11 issue their products,
+// warp 9 the copies (queries; for 16-bit caches also the K and V tiles: 16-token boxes through the
 // block table into the swizzled operand layout), warp 10 clears V rows behind the context. One-byte caches add warps 12..15, which
 // load the tiles, widen them to fp16 and write the operand layout themselves.
 //
@@ -70,7 +70,7 @@ struct PfShape {
   static constexpr uint32_t kRing = kQBytes;
   static constexpr uint32_t kScales = kRing + kStages * kStageBytes;   // INT8: [kScaleRing][K, V][128] floats
   static constexpr uint32_t kBars = kScales + (KV == kKvInt8 ? kScaleRing * 2 * kPfTile * 4 : 0);
-  static constexpr uint32_t kMisc = kBars + (4 * kStages + 9 + kScaleRing) * 8;
+  static constexpr uint32_t kMisc = kBars + (4 * kStages + 11 + kScaleRing) * 8;
   static constexpr uint32_t kPos = kMisc + 256 + sizeof(PfStart);   // PfPos of each softmax warp
   static constexpr uint32_t kSmem = kPos + 8 * sizeof(PfPos) + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory of one CTA");
@@ -161,7 +161,8 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
   const uint32_t s_full = q_empty + 8;      // [2] scores of row tile i written
   const uint32_t p_ready = s_full + 16;     // [2] weights of row tile i written, O_i rescaled
   const uint32_t o_done = p_ready + 16;     // [2] last P V product of a piece's row tile i complete
-  const uint32_t final_bar = o_done + 16;
+  const uint32_t turn = o_done + 16;        // [2] row tile i's products may be issued
+  const uint32_t final_bar = turn + 16;
   // Per stage, so that a use is never more than one phase ahead of its waiter:
   const uint32_t v_tail = final_bar + 8;    // [NS] V rows behind the context zeroed
   const uint32_t v_sent = v_tail + 8 * NS;  // [NS] copies of such a tile issued
@@ -176,22 +177,24 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
   if (tid == 0) {
     for (int k = 0; k < NS; ++k) {
       mbar_init(full + 8 * k, Sh::kWiden ? 128 : 1);
-      mbar_init(empty + 8 * k, 1);
+      mbar_init(empty + 8 * k, 2);
       mbar_init(v_tail + 8 * k, 1);
       mbar_init(v_sent + 8 * k, 1);
     }
     mbar_init(q_full, 1);
-    mbar_init(q_empty, 1);
+    mbar_init(q_empty, 2);
     for (int i = 0; i < 2; ++i) {
       mbar_init(s_full + 8 * i, 1);
       mbar_init(p_ready + 8 * i, 4);
       mbar_init(o_done + 8 * i, 1);
+      mbar_init(turn + 8 * i, 1);
     }
     for (int i = 0; i < Sh::kScaleRing; ++i) mbar_init(sc_full + 8 * i, 128);
-    mbar_init(final_bar, 1);
+    mbar_init(final_bar, 2);
     ctl->abort = 0;
     ctl->busy = 0;
     fence_barrier_init();
+    mbar_arrive(turn);   // row tile 0 begins
   }
   if (warp == 8) {
     tmem_alloc(smem_addr(tmem_slot), 512);
@@ -560,81 +563,111 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
       }
     } else {
       regs_shrink<Sh::kIssueRegs>();
-      if (warp == 8) {
+      if (warp == 8 || warp == 11) {
         // ----------------------------- product issue ----------------------------------
-        constexpr uint32_t id_s = idesc_kind_f16(128, 128, Sh::kBf16, 0, 0);   // Q (K-major) x K^T (K-major)
-        constexpr uint32_t id_o = idesc_kind_f16(128, D, Sh::kBf16, 0, 1);     // P (TMEM) x V (dimensions contiguous)
-        // An operand's later atoms: its first descriptor with the address field advanced
-        // (16-byte units; shared-memory addresses stay below 2^18, so it never carries).
-        const uint64_t dq = smem_desc_sw128(base, 0, 1024);
-        const uint64_t dk = smem_desc_sw128(base + Sh::kRing, 0, 1024);
-        const uint64_t dv = smem_desc_sw128(base + Sh::kRing, Sh::kHalfBytes, 1024);
-        // One thread does all of it: the tensor pipe accepts a product only when the one before
-        // has nearly run, so what this thread does between products is idle time there, and
-        // warp-wide steps cost it about as much as a product.
+        // One thread for each row tile. The tensor pipe accepts a product only when the one
+        // before has nearly run, so a single thread's waits, commits and bookkeeping (some 700
+        // cycles of a KV tile's 3550) were idle time there; with two, one thread's fall into the
+        // other's products. They take strict turns, a row tile's products of one KV tile each:
+        // left to themselves both row tiles fall into step and their softmax leaves the pipe idle
+        // (8192-token prompt: 577 us). The turn passes two products before a thread's last.
         if (lane == 0) {
-          uint32_t st = 0, cnt[2] = {0, 0}, piece = 0, tails = 0;
+          const int i = warp == 8 ? 0 : 1;
+          constexpr uint32_t id_s = idesc_kind_f16(128, 128, Sh::kBf16, 0, 0);   // Q (K-major) x K^T (K-major)
+          constexpr uint32_t id_o = idesc_kind_f16(128, D, Sh::kBf16, 0, 1);     // P (TMEM) x V (dimensions contiguous)
+          // An operand's later atoms: its first descriptor with the address field advanced
+          // (16-byte units; shared-memory addresses stay below 2^18, so it never carries).
+          const uint64_t dq = smem_desc_sw128(base + i * 128 * 128, 0, 1024);
+          const uint64_t dk = smem_desc_sw128(base + Sh::kRing, 0, 1024);
+          const uint64_t dv = smem_desc_sw128(base + Sh::kRing, Sh::kHalfBytes, 1024);
+          const uint32_t t_s = tmem + kPfSCol + 128 * i, t_o = tmem + kPfOCol + 128 * i;
+          uint32_t stage = 0, round = 0, cnt = 0, piece = 0, tails = 0;
           bool ok = true;
           auto wait = [&](uint32_t bar, uint32_t parity) {
             if (!pf_wait(bar, parity, ctl)) ok = false;
             return ok;
           };
-          auto issue_s = [&](int i, uint32_t stage) {
-            const uint64_t qa = dq + ((static_cast<uint32_t>(i) * 128 * 128) >> 4);
-            const uint64_t kb = dk + ((stage * Sh::kStageBytes) >> 4);
+          auto next_stage = [&] {
+            if (++stage == NS) {
+              stage = 0;
+              round ^= 1;
+            }
+          };
+          const uint32_t my_turn = turn + 8 * i, other_turn = turn + 8 * (1 - i);
+          uint32_t turns = 0;
+          auto issue_s = [&](uint32_t at) {
+            const uint64_t kb = dk + ((at * Sh::kStageBytes) >> 4);
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-              tc_mma_f16_ss(tmem + kPfSCol + 128 * i, qa + (((kk >> 2) * Sh::kQHalfBytes + (kk & 3) * 32) >> 4),
+            for (int kk = 0; kk < D / 16; ++kk) {
+              if (kk == D / 16 - 2) mbar_arrive(other_turn);
+              tc_mma_f16_ss(t_s, dq + (((kk >> 2) * Sh::kQHalfBytes + (kk & 3) * 32) >> 4),
                             kb + (((kk >> 2) * Sh::kHalfBytes + (kk & 3) * 32) >> 4), id_s, kk > 0);
+            }
             tc_commit(s_full + 8 * i);
           };
+          // Stages (and the queries) are released by both threads: behind the products that
+          // read them, or at once where this row tile has none.
           for (PfWalk w(a, *start); !w.done() && ok; w.advance()) {
             const PfPiece pc(w);
             if (!pc.any()) continue;
             const int tail = !Sh::kWiden && (w.p.ctx & 15) ? w.p.ctx / kPfTile : -1;   // see warp 10
+            const int kb = pc.kb[i], klast = pc.klast;
+            int k = pc.ka;
             if (!wait(q_full, piece & 1)) break;
-            uint32_t ks = st % NS;
-            if (!wait(full + 8 * ks, (st / NS) & 1)) break;
-            tc_fence_after_sync();
-            for (int i = 0; i < 2; ++i)
-              if (pc.active(i)) issue_s(i, ks);
-            tc_commit(empty + 8 * ks);
-            if (pc.ka + 1 == pc.klast) tc_commit(q_empty);
-            ++st;
-            for (int k = pc.ka; k < pc.klast; ++k) {
-              const uint32_t vs = st % NS;
-              if (!wait(full + 8 * vs, (st / NS) & 1)) break;
+            ++piece;
+            if (!wait(full + 8 * stage, round)) break;
+            if (!wait(my_turn, turns++ & 1)) break;
+            if (k < kb) {
+              tc_fence_after_sync();
+              issue_s(stage);
+              tc_commit(empty + 8 * stage);
+              if (k + 1 == kb) tc_commit(q_empty);
+            } else {
+              mbar_arrive(other_turn);
+              mbar_arrive(empty + 8 * stage);
+              mbar_arrive(q_empty);
+            }
+            next_stage();
+            for (bool first = true; k < klast; ++k, first = false) {
+              const uint32_t vs = stage;
+              if (!wait(full + 8 * vs, round)) break;
+              next_stage();
+              const uint32_t ks = stage;
+              if (k + 1 < klast) {
+                if (!wait(full + 8 * ks, round)) break;
+                next_stage();
+              }
               if (k == tail) {
-                if (!wait(v_tail + 8 * vs, (tails >> vs) & 1)) break;
+                if (k < kb && !wait(v_tail + 8 * vs, (tails >> vs) & 1)) break;
                 tails ^= 1u << vs;
               }
-              ++st;
-              const bool more = k + 1 < pc.klast;
-              if (more) {
-                ks = st % NS;
-                if (!wait(full + 8 * ks, (st / NS) & 1)) break;
-                ++st;
-              }
-              const uint64_t vb = dv + ((vs * Sh::kStageBytes) >> 4);
-              const uint32_t acc = k > pc.ka ? 1u : 0u;
-              for (int i = 0; i < 2; ++i) {
-                if (k >= pc.kb[i]) continue;
-                if (!wait(p_ready + 8 * i, cnt[i] & 1)) break;
-                ++cnt[i];
+              if (k < kb) {
+                const uint64_t vb = dv + ((vs * Sh::kStageBytes) >> 4);
+                if (!wait(p_ready + 8 * i, cnt & 1) || !wait(my_turn, turns++ & 1)) break;
+                ++cnt;
                 tc_fence_after_sync();
+                const bool more = k + 1 < kb;
 #pragma unroll
-                for (int kk = 0; kk < kPfTile / 16; ++kk)
-                  tc_mma_f16_ts(tmem + kPfOCol + 128 * i, tmem + kPfSCol + 128 * i + kk * 8, vb + ((kk * 2048) >> 4),
-                                id_o, kk > 0 ? 1u : acc);
-                if (k + 1 < pc.kb[i]) issue_s(i, ks);
-                else tc_commit(o_done + 8 * i);   // else the next scores' barrier tells of it
+                for (int kk = 0; kk < kPfTile / 16; ++kk) {
+                  if (kk == kPfTile / 16 - 2 && !more) mbar_arrive(other_turn);
+                  tc_mma_f16_ts(t_o, t_s + kk * 8, vb + ((kk * 2048) >> 4), id_o, kk > 0 || !first);
+                }
+                if (more) {
+                  issue_s(ks);
+                  tc_commit(empty + 8 * ks);
+                  if (k + 2 == kb) tc_commit(q_empty);   // the last scores are issued
+                } else {
+                  tc_commit(o_done + 8 * i);   // else the next scores' barrier tells of it
+                  if (k + 1 < klast) mbar_arrive(empty + 8 * ks);
+                }
+                tc_commit(empty + 8 * vs);
+              } else {
+                if (!wait(my_turn, turns++ & 1)) break;
+                mbar_arrive(other_turn);
+                mbar_arrive(empty + 8 * vs);
+                if (k + 1 < klast) mbar_arrive(empty + 8 * ks);
               }
-              if (!ok) break;
-              tc_commit(empty + 8 * vs);
-              if (more) tc_commit(empty + 8 * ks);
-              if (k + 2 == pc.klast) tc_commit(q_empty);   // the last scores are issued
             }
-            ++piece;
           }
           if (!ok) {
             ctl->abort = 1;
