@@ -142,23 +142,27 @@ int pkv_paged_attention_prefill(void* out, const void* q, const int32_t* cu_q_le
   a.epoch = next_call_epoch();
 
   // Query rows as [token][head][dimension]: boxes of 64 dimensions x the group's heads x tokens.
-  CUtensorMap tq, tk0, tv0, tk1, tv1;
+  CUtensorMap tq, tk0, tk1, tv;
   const uint64_t dims[3] = {static_cast<uint64_t>(d), static_cast<uint64_t>(num_q_heads),
                             static_cast<uint64_t>(num_q_rows)};
   const uint64_t strides[2] = {static_cast<uint64_t>(d) * 2, static_cast<uint64_t>(d) * 2 * num_q_heads};
   const uint32_t qbox[3] = {64, static_cast<uint32_t>(a.group), static_cast<uint32_t>(box.tokens)};
   if (int rc = encode_map_16bit(&tq, q, 3, dims, strides, qbox)) return rc;
-  tk0 = tv0 = tk1 = tv1 = tq;
+  tk0 = tk1 = tv = tq;
   if (!v.widen) {
     const long long rows = static_cast<long long>(cache->num_blocks) * cache->num_kv_heads * kBlockSize;
     if (int rc = encode_tile_map(&tk0, k_cache, kv, d, rows, 0)) return rc;
-    if (int rc = encode_tile_map(&tv0, v_cache, kv, d, rows, 0)) return rc;
     if (d == 128) {
       if (int rc = encode_tile_map(&tk1, k_cache, kv, d, rows, 1)) return rc;
-      if (int rc = encode_tile_map(&tv1, v_cache, kv, d, rows, 1)) return rc;
     }
+    // V: [half][token row][64 dimensions], a block's halves in one box.
+    const uint32_t halves = static_cast<uint32_t>(d) / 64;
+    const uint64_t vdims[3] = {64, static_cast<uint64_t>(rows), halves};
+    const uint64_t vstrides[2] = {static_cast<uint64_t>(d) * 2, 128};
+    const uint32_t vbox[3] = {64, kBlockSize, halves};
+    if (int rc = encode_map_16bit(&tv, v_cache, 3, vdims, vstrides, vbox)) return rc;
   }
-  void* args[6] = {&tq, &tk0, &tv0, &tk1, &tv1, &a};
+  void* args[5] = {&tq, &tk0, &tk1, &tv, &a};
   return launch_overlapped(v.fn, dim3(static_cast<unsigned>(sms)), dim3(v.threads), v.smem, stream, args);
 }
 

@@ -11,10 +11,11 @@
 // columns) takes the place of the first half of S_i, which its own threads have read; the
 // next S_i is issued behind the P V product that reads P_i (products execute in issue order).
 //
-// Warps: 0..3 and 4..7 the softmax of row tiles 0 and 1, warps 8 and 11 issue their products,
-// warp 9 the copies (queries; for 16-bit caches also the K and V tiles: 16-token boxes through the
-// block table into the swizzled operand layout), warp 10 clears V rows behind the context. One-byte caches add warps 12..15, which
-// load the tiles, widen them to fp16 and write the operand layout themselves.
+// Warps: 0..3 and 4..7 the softmax of row tiles 0 and 1; warps 8 and 11 issue their products;
+// warps 12..15 bring the K and V tiles: of a 16-bit cache as copies of 16-token boxes through the
+// block table into the swizzled operand layout (and the queries; warp 10 clears V rows behind
+// the context), of a one-byte cache through registers, widened to fp16 (warp 9 copies the
+// queries).
 //
 // Masks. Only tiles that reach past some row's last position compare positions; a masked
 // score is -inf, its weight 0. V rows behind the context are zeroed (a stale NaN times
@@ -48,16 +49,21 @@ struct PfShape {
   static constexpr bool kWiden = KV == kKvE5m2 || KV == kKvInt8;
   static constexpr bool kBf16 = KV == kKvBf16;
   static constexpr int kHalves = D / 64;
-  static constexpr int kThreads = kWiden ? 512 : 384;
-  // Register budgets (per thread of a warpgroup); their sum is the launch's total:
-  // 384 x 168 = 128 (200 + 200 + 104), 512 x 128 = 128 (184 + 184 + 56 + 88).
-  static constexpr int kLaunchRegs = kWiden ? 128 : 168;
-  static constexpr int kSoftmaxRegs = kWiden ? 184 : 200;
-  static constexpr int kIssueRegs = kWiden ? 56 : 104;
-  static constexpr int kWidenRegs = 88;
+  static constexpr int kThreads = 512;
+  // Register budgets (per thread of a warpgroup); twice the first and the others make the
+  // launch's 512 x 128.
+  static constexpr int kLaunchRegs = 128;
+  static constexpr int kSoftmaxRegs = kWiden ? 184 : 192;
+  static constexpr int kIssueRegs = kWiden ? 56 : 72;
+  static constexpr int kLoadRegs = kWiden ? 88 : 56;
+  static_assert(2 * kSoftmaxRegs + kIssueRegs + kLoadRegs == 4 * kLaunchRegs, "register split");
   static constexpr int kStages = kWiden ? (D == 128 ? 4 : 8) : (D == 128 ? 5 : 10);
   static constexpr uint32_t kHalfBytes = kPfTile * 128;             // 64 dimensions of a KV tile
   static constexpr uint32_t kStageBytes = kHalves * kHalfBytes;
+  // V as the products read it: by block for 16-bit caches (a block's halves adjacent, as one
+  // copy writes them), by half for widened tiles.
+  static constexpr uint32_t kVBlockBytes = kWiden ? kBlockSize * 128 : kHalves * kBlockSize * 128;
+  static constexpr uint32_t kVHalfStep = kWiden ? kHalfBytes : kBlockSize * 128;
   static constexpr uint32_t kQHalfBytes = kPfRows * 128;
   static constexpr uint32_t kQBytes = kHalves * kQHalfBytes;
   static constexpr float kSlack = KV == kKvInt8 ? 0.f : 8.f;
@@ -145,11 +151,26 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return BF16 ? pack_bf16x2(lo, hi) : pack_f16x2(lo, hi);
 }
 
+// Boxes first, first + step, ... of a unit's query rows, one thread: box b holds tokens
+// b * box_tokens .. of the unit; each 64-dimension half goes to its own half of the buffer.
+template <int D>
+__device__ __forceinline__ void pf_load_q(const PrefillArgs& a, const CUtensorMap* tm, uint32_t dst, uint32_t bar,
+                                          int head, int token, int boxes, int first, int step) {
+  const int rows = a.box_tokens * a.group;
+  const int mine = boxes > first ? (boxes - first + step - 1) / step : 0;
+  mbar_arrive_expect_tx(bar, mine * (D / 64) * rows * 128);
+  for (int b = first; b < boxes; b += step) {
+#pragma unroll
+    for (int hf = 0; hf < D / 64; ++hf)
+      tma_load_3d_keep(dst + hf * (kPfRows * 128) + b * rows * 128, tm, 64 * hf, head, token + b * a.box_tokens, bar);
+  }
+}
+
 template <int KV, int D>
 __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k0,
-                   const __grid_constant__ CUtensorMap tm_v0, const __grid_constant__ CUtensorMap tm_k1,
-                   const __grid_constant__ CUtensorMap tm_v1, const __grid_constant__ PrefillArgs a) {
+                   const __grid_constant__ CUtensorMap tm_k1, const __grid_constant__ CUtensorMap tm_v,
+                   const __grid_constant__ PrefillArgs a) {
   using Sh = PfShape<KV, D>;
   constexpr int NS = Sh::kStages;
   extern __shared__ uint8_t smem_raw[];
@@ -176,12 +197,12 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int k = 0; k < NS; ++k) {
-      mbar_init(full + 8 * k, Sh::kWiden ? 128 : 1);
+      mbar_init(full + 8 * k, Sh::kWiden ? 128 : 4);
       mbar_init(empty + 8 * k, 2);
       mbar_init(v_tail + 8 * k, 1);
       mbar_init(v_sent + 8 * k, 1);
     }
-    mbar_init(q_full, 1);
+    mbar_init(q_full, Sh::kWiden ? 1 : 4);
     mbar_init(q_empty, 2);
     for (int i = 0; i < 2; ++i) {
       mbar_init(s_full + 8 * i, 1);
@@ -203,7 +224,7 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
   if (warp == 9 && lane == 0) {
     prefetch_tensormap(&tm_q);
     prefetch_tensormap(&tm_k0);
-    prefetch_tensormap(&tm_v0);
+    prefetch_tensormap(&tm_v);
   }
   tc_fence_before_sync();
   pdl_wait_prior_grid();
@@ -485,10 +506,92 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
         if (again) pf_redo<KV, D>(a, again, w.p.s, w.p.qb, w.past(), pc.j0, 128 * i + 32 * (warp & 3), w.p.h, ctl);
         tc_fence_before_sync();   // O_i is read before the next piece's product overwrites it
       }
-    } else if (Sh::kWiden && warp >= 12) {
-      // ------------------------- widening loader (one-byte caches) --------------------
-      regs_shrink<Sh::kWidenRegs>();
-      if constexpr (Sh::kWiden) {
+    } else if (warp >= 12) {
+      regs_shrink<Sh::kLoadRegs>();
+      if constexpr (!Sh::kWiden) {
+        // -------------------- copies of queries and tiles (16-bit caches) ----------------
+        // Four warps, one issuing lane each: a lane takes some 75 cycles over a copy, and a
+        // 128-position K and V tile is 24 of them (one lane alone bounded the kernel). Warp x
+        // copies blocks 2x and 2x + 1 of a tile: two 2 KB boxes (64 dimensions each) of K,
+        // and for V, whose layout lets a block's halves lie together, one 4 KB box.
+        const int x = warp - 12;
+        const int total_rows = a.num_blocks * a.num_kv_heads * kBlockSize;   // host guarantees < 2^31
+        uint32_t st = 0, stage = 0, round = 0, piece = 0;
+        bool ok = true;
+        for (PfWalk w(a, *start); !w.done() && ok; w.advance()) {
+          const PfPiece pc(w);
+          if (!pc.any()) continue;
+          const int32_t* bt = a.block_tables + static_cast<size_t>(w.p.s) * a.max_blocks_per_seq;
+          const int tail = w.p.ctx & 15 ? w.p.ctx / kPfTile : -1;   // see warp 10
+          for (int k = pc.ka; k < pc.klast; ++k) {
+            // Rows of both blocks: lanes 0 and 1 look them up.
+            int mine = total_rows;   // wholly past the end: the copy fills zeros
+            if (lane < 2) {
+              const int p = k * kPfTile + (2 * x + lane) * kBlockSize;
+              if (p < w.p.ctx) {
+                const int id = bt[p >> 4];
+                if (static_cast<unsigned>(id) < static_cast<unsigned>(a.num_blocks))
+                  mine = (id * a.num_kv_heads + w.p.h) * kBlockSize;
+                else if (a.status) atomicOr(a.status, kDevBadBlock);
+              }
+            }
+            const int row0 = __shfl_sync(0xffffffffu, mine, 0), row1 = __shfl_sync(0xffffffffu, mine, 1);
+            if (lane == 0) {
+              if (k == pc.ka) {
+                ok = piece == 0 || pf_wait(q_empty, (piece - 1) & 1, ctl);
+                if (ok) {
+                  const int boxes = (pc.rows + a.box_tokens * a.group - 1) / (a.box_tokens * a.group);
+                  pf_load_q<D>(a, &tm_q, base, q_full, w.p.h * a.group, w.p.qb + pc.j0, boxes, x, 4);
+                }
+              }
+              for (int v = 0; v < 2 && ok; ++v) {
+                if (st >= NS && !pf_wait(empty + 8 * stage, round ^ 1, ctl)) {
+                  ok = false;
+                  break;
+                }
+                const uint32_t bar = full + 8 * stage;
+                const uint32_t dst = base + Sh::kRing + stage * Sh::kStageBytes;
+                mbar_arrive_expect_tx(bar, Sh::kStageBytes / 4);
+                if (v == 0) {
+                  const uint32_t d = dst + 2 * x * (kBlockSize * 128);
+                  tma_load_2d_keep(d, &tm_k0, 0, row0, bar);
+                  tma_load_2d_keep(d + kBlockSize * 128, &tm_k0, 0, row1, bar);
+                  if constexpr (Sh::kHalves == 2) {
+                    tma_load_2d_keep(d + Sh::kHalfBytes, &tm_k1, 0, row0, bar);
+                    tma_load_2d_keep(d + Sh::kHalfBytes + kBlockSize * 128, &tm_k1, 0, row1, bar);
+                  }
+                } else {
+                  const uint32_t d = dst + 2 * x * Sh::kVBlockBytes;
+                  tma_load_3d_keep(d, &tm_v, 0, row0, 0, bar);
+                  tma_load_3d_keep(d + Sh::kVBlockBytes, &tm_v, 0, row1, 0, bar);
+                  if (x == 0 && k == tail) mbar_arrive(v_sent + 8 * stage);
+                }
+                ++st;
+                if (++stage == NS) {
+                  stage = 0;
+                  round ^= 1;
+                }
+              }
+            }
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (!ok) break;
+          }
+          ++piece;
+        }
+        if (lane == 0) {
+          if (!ok) {
+            ctl->abort = 1;
+            if (a.status) atomicOr(a.status, kDevTimeout);
+          }
+          // Drain: every copy issued into this CTA's shared memory lands before exit. (Where a role
+          // gave up a barrier may stay incomplete; the first such wait outlasts any copy.)
+          bool landed = piece == 0 || mbar_wait(q_full, (piece - 1) & 1);
+          for (uint32_t k = st > NS ? st - NS : 0; k < st && landed; ++k)
+            landed = mbar_wait(full + 8 * (k % NS), (k / NS) & 1);
+        }
+        __syncwarp();
+      } else {
+        // ------------------------- widening loader (one-byte caches) --------------------
         constexpr int LPR = D / 16;               // lanes of a row (16 bytes each)
         constexpr int RPW = 32 / LPR;             // rows of a warp's load
         constexpr int NL = kPfTile / (4 * RPW);   // loads of a thread per tile
@@ -579,7 +682,7 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
           // (16-byte units; shared-memory addresses stay below 2^18, so it never carries).
           const uint64_t dq = smem_desc_sw128(base + i * 128 * 128, 0, 1024);
           const uint64_t dk = smem_desc_sw128(base + Sh::kRing, 0, 1024);
-          const uint64_t dv = smem_desc_sw128(base + Sh::kRing, Sh::kHalfBytes, 1024);
+          const uint64_t dv = smem_desc_sw128(base + Sh::kRing, Sh::kVHalfStep, 1024);
           const uint32_t t_s = tmem + kPfSCol + 128 * i, t_o = tmem + kPfOCol + 128 * i;
           uint32_t stage = 0, round = 0, cnt = 0, piece = 0, tails = 0;
           bool ok = true;
@@ -650,7 +753,7 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
 #pragma unroll
                 for (int kk = 0; kk < kPfTile / 16; ++kk) {
                   if (kk == kPfTile / 16 - 2 && !more) mbar_arrive(other_turn);
-                  tc_mma_f16_ts(t_o, t_s + kk * 8, vb + ((kk * 2048) >> 4), id_o, kk > 0 || !first);
+                  tc_mma_f16_ts(t_o, t_s + kk * 8, vb + ((kk * Sh::kVBlockBytes) >> 4), id_o, kk > 0 || !first);
                 }
                 if (more) {
                   issue_s(ks);
@@ -699,8 +802,8 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
             uint8_t* vt = smem + Sh::kRing + vs * Sh::kStageBytes;
             for (int x = lane; x < (r1 - r0) * Sh::kHalves * 8; x += 32) {
               const int row = r0 + x / (Sh::kHalves * 8), ch = x % (Sh::kHalves * 8);
-              *reinterpret_cast<uint4*>(vt + (ch >> 3) * Sh::kHalfBytes + row * 128 + (ch & 7) * 16) =
-                  make_uint4(0u, 0u, 0u, 0u);
+              *reinterpret_cast<uint4*>(vt + (row >> 4) * Sh::kVBlockBytes + (ch >> 3) * Sh::kVHalfStep +
+                                        (row & 15) * 128 + (ch & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -713,74 +816,27 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
           if (a.status) atomicOr(a.status, kDevTimeout);
         }
         __syncwarp();
-      } else if (warp == 9) {
-        // -------------------------------- copies ---------------------------------------
-        const int total_rows = a.num_blocks * a.num_kv_heads * kBlockSize;   // host guarantees < 2^31
-        uint32_t st = 0, piece = 0;
-        bool ok = true;
-        auto wait = [&](uint32_t bar, uint32_t parity) {
-          if (ok && !pf_wait(bar, parity, ctl)) ok = false;
-          ok = __all_sync(0xffffffffu, ok);
-          return ok;
-        };
-        for (PfWalk w(a, *start); !w.done() && ok; w.advance()) {
-          const PfPiece pc(w);
-          if (!pc.any()) continue;
-          if (piece > 0 && !wait(q_empty, (piece - 1) & 1)) break;
-          const int box_rows = a.box_tokens * a.group;
-          const int boxes = (pc.rows + box_rows - 1) / box_rows;
-          if (lane == 0) mbar_arrive_expect_tx(q_full, boxes * Sh::kHalves * box_rows * 128);
-          __syncwarp();
-          for (int x = lane; x < boxes * Sh::kHalves; x += 32) {
-            const int b = x / Sh::kHalves, hf = x % Sh::kHalves;
-            tma_load_3d_keep(base + hf * Sh::kQHalfBytes + b * box_rows * 128, &tm_q, 64 * hf, w.p.h * a.group,
-                             w.p.qb + pc.j0 + b * a.box_tokens, q_full);
-          }
-          ++piece;
-          if constexpr (!Sh::kWiden) {
-            const int32_t* bt = a.block_tables + static_cast<size_t>(w.p.s) * a.max_blocks_per_seq;
-            // lane = (block of the tile, half)
-            constexpr int NB = kPfTile / kBlockSize;
-            const int tail = w.p.ctx & 15 ? w.p.ctx / kPfTile : -1;   // see warp 10
-            const int blk = lane / Sh::kHalves, hf = lane % Sh::kHalves;
-            for (int k = pc.ka; k < pc.klast && ok; ++k) {
-              int row = total_rows;   // wholly past the end: the copy fills zeros
-              if (blk < NB) {
-                const int p = k * kPfTile + blk * kBlockSize;
-                if (p < w.p.ctx) {
-                  const int id = bt[p >> 4];
-                  if (static_cast<unsigned>(id) < static_cast<unsigned>(a.num_blocks))
-                    row = (id * a.num_kv_heads + w.p.h) * kBlockSize;
-                  else if (a.status) atomicOr(a.status, kDevBadBlock);
-                }
-              }
-              for (int v = 0; v < 2; ++v, ++st) {
-                const uint32_t stage = st % NS, round = st / NS;
-                if (round > 0 && !wait(empty + 8 * stage, (round - 1) & 1)) break;
-                if (lane == 0) mbar_arrive_expect_tx(full + 8 * stage, Sh::kStageBytes);
-                __syncwarp();
-                if (blk < NB) {
-                  const CUtensorMap* tm = v ? (hf ? &tm_v1 : &tm_v0) : (hf ? &tm_k1 : &tm_k0);
-                  tma_load_2d_keep(base + Sh::kRing + stage * Sh::kStageBytes + hf * Sh::kHalfBytes +
-                                       blk * (kBlockSize * 128), tm, 0, row, full + 8 * stage);
-                }
-                if (v && k == tail) {
-                  __syncwarp();
-                  if (lane == 0) mbar_arrive(v_sent + 8 * stage);
-                }
-              }
-            }
-          }
-        }
-        if (!ok) {
-          ctl->abort = 1;
-          if (lane == 0 && a.status) atomicOr(a.status, kDevTimeout);
-        }
-        // Drain: every copy issued into this CTA's shared memory lands before exit.
+      } else if (warp == 9 && Sh::kWiden) {
+        // --------------------------- query copies (one-byte caches) ------------------------
         if (lane == 0) {
-          if (piece > 0) mbar_wait(q_full, (piece - 1) & 1);
-          if (!Sh::kWiden)
-            for (uint32_t k = st > NS ? st - NS : 0; k < st; ++k) mbar_wait(full + 8 * (k % NS), (k / NS) & 1);
+          uint32_t piece = 0;
+          bool ok = true;
+          for (PfWalk w(a, *start); !w.done(); w.advance()) {
+            const PfPiece pc(w);
+            if (!pc.any()) continue;
+            if (piece > 0 && !pf_wait(q_empty, (piece - 1) & 1, ctl)) {
+              ok = false;
+              break;
+            }
+            const int boxes = (pc.rows + a.box_tokens * a.group - 1) / (a.box_tokens * a.group);
+            pf_load_q<D>(a, &tm_q, base, q_full, w.p.h * a.group, w.p.qb + pc.j0, boxes, 0, 1);
+            ++piece;
+          }
+          if (!ok) {
+            ctl->abort = 1;
+            if (a.status) atomicOr(a.status, kDevTimeout);
+          }
+          if (piece > 0) mbar_wait(q_full, (piece - 1) & 1);   // the last copies land before exit
         }
         __syncwarp();
       }
