@@ -23,11 +23,11 @@
 // meets weight 0 of the rows before it: an output row with a non-finite element is
 // computed again by prefill_row, which reads only what the row sees.
 //
-// The running maximum moves only when a score exceeds it by more than kSlack (base 2), so
-// that O is rescaled a few times a row, not every tile. fp16 weights carry a shift of 2^7:
-// with the slack of 8 they stay below 2^15, and weights down to 2^-21 of the largest
-// keep full precision. An INT8 cache's V scale enters the weight with it (at most 516, so
-// slack 0 and shift 6); its K scale multiplies the scores.
+// The running maximum moves only when a score exceeds it by more than kSlack (base 2) or a
+// tile's weights sum to more than 2^kSlack, so that O is rescaled a few times a row, not every
+// tile. fp16 weights carry a shift of 2^7: they stay at or below 2^15, and weights down to 2^-21
+// of the largest keep full precision. An INT8 cache's V scale enters the weight with it (at
+// most 516, so slack 0 and shift 6); its K scale multiplies the scores.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -68,6 +68,7 @@ struct PfShape {
   static constexpr uint32_t kQBytes = kHalves * kQHalfBytes;
   static constexpr float kSlack = KV == kKvInt8 ? 0.f : 8.f;
   static constexpr float kShift = KV == kKvBf16 ? 0.f : (KV == kKvInt8 ? 6.f : 7.f);
+  static constexpr float kMostSum = KV == kKvBf16 ? 256.f : 32768.f;   // 2^(slack + shift)
   // Row scales of an INT8 cache's tiles: tile t + kScaleRing is written once the K stage of
   // tile t + kScaleRing - kStages / 2 is released, which is after the softmax of the tile before
   // that one, so tile t's are no longer read when kScaleRing > kStages / 2.
@@ -280,98 +281,114 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
           if constexpr (KV == kKvInt8) wait(sc_full + 8 * slot, (nth / Sh::kScaleRing) & 1);
           if (!alive) continue;
           tc_fence_after_sync();
-          uint32_t sv[4][32];   // 32 scores each
-          tmem_ld128(s_col, sv[0], sv[1], sv[2], sv[3]);
-          if constexpr (KV == kKvInt8) {
-            const float4* ks = reinterpret_cast<const float4*>(smem + Sh::kScales) + slot * 64;
+          // Weights against the running maximum as it stands. Whether it may stand is seen from
+          // their sum: a score over it by more than the slack shows as a sum over 2^slack (a tile's
+          // 128 weights of at most 1 never do), and a row with no maximum yet is known. Then, in a
+          // second round from the same scores, the maximum is found and moves. (Finding it first in
+          // every tile cost 300 to 400 of the 1350 cycles between a tile's scores and weights.)
+          uint32_t pw[4][16];
+          bool settle = first || KV == kKvInt8;
+          const bool live = limit > p0;   // the row sees positions of this tile
+          float ls;
+          for (;;) {
+            uint32_t sv[4][32];   // 32 scores each
+            tmem_ld128(s_col, sv[0], sv[1], sv[2], sv[3]);
+            if constexpr (KV == kKvInt8) {
+              const float4* ks = reinterpret_cast<const float4*>(smem + Sh::kScales) + slot * 64;
+#pragma unroll
+              for (int g = 0; g < 4; ++g) {
+#pragma unroll
+                for (int e = 0; e < 32; e += 4) {
+                  const float4 f = ks[8 * g + e / 4];
+                  sv[g][e] = __float_as_uint(__uint_as_float(sv[g][e]) * f.x);
+                  sv[g][e + 1] = __float_as_uint(__uint_as_float(sv[g][e + 1]) * f.y);
+                  sv[g][e + 2] = __float_as_uint(__uint_as_float(sv[g][e + 2]) * f.z);
+                  sv[g][e + 3] = __float_as_uint(__uint_as_float(sv[g][e + 3]) * f.w);
+                }
+              }
+            }
+            if (p0 + kPfTile > limit0) {
+              const int vis = limit - p0;
+#pragma unroll
+              for (int g = 0; g < 4; ++g) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) sv[g][e] = 32 * g + e < vis ? sv[g][e] : 0xFF800000u;
+              }
+            }
+            if (settle) {
+              // eight chains of three-operand maxima
+              float mx8[8];
+#pragma unroll
+              for (int g = 0; g < 4; ++g) {
+                mx8[2 * g] = __uint_as_float(sv[g][0]);
+                mx8[2 * g + 1] = __uint_as_float(sv[g][1]);
+              }
+#pragma unroll
+              for (int e = 2; e < 30; e += 4) {
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                  mx8[2 * g] = max3(mx8[2 * g], __uint_as_float(sv[g][e]), __uint_as_float(sv[g][e + 1]));
+                  mx8[2 * g + 1] = max3(mx8[2 * g + 1], __uint_as_float(sv[g][e + 2]), __uint_as_float(sv[g][e + 3]));
+                }
+              }
+#pragma unroll
+              for (int g = 0; g < 4; ++g)
+                mx8[2 * g] = max3(mx8[2 * g], __uint_as_float(sv[g][30]), __uint_as_float(sv[g][31]));
+              const float mx = c * max3(max3(mx8[0], mx8[1], mx8[2]), max3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7]));
+              const bool need = mx > m + Sh::kSlack;
+              if (__any_sync(0xffffffffu, need)) {
+                const float mn = need ? mx : m;
+                const float alpha = need ? fast_exp2(m - mn) : 1.f;   // 0 from -inf
+                m = mn;
+                l *= alpha;
+                if (!first) {
+                  // Products complete in issue order: these scores were issued behind the last P V.
+#pragma unroll 1
+                  for (int e = 0; e < D; e += 16) {
+                    uint32_t ov[16];
+                    tmem_ld16(o_col + e, ov);
+#pragma unroll
+                    for (int x = 0; x < 16; ++x) ov[x] = __float_as_uint(__uint_as_float(ov[x]) * alpha);
+                    tmem_st16(o_col + e, ov);
+                  }
+                }
+              }
+            }
+            const float sub = Sh::kShift - (m == -INFINITY ? 0.f : m);
+            const uint64_t c2 = f32x2(c, c), sub2 = f32x2(sub, sub);
+            uint64_t l2 = f32x2(0.f, 0.f), l3 = l2;
+            const float4* vs = reinterpret_cast<const float4*>(smem + Sh::kScales) + slot * 64 + 32;
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
 #pragma unroll
               for (int e = 0; e < 32; e += 4) {
-                const float4 f = ks[8 * g + e / 4];
-                sv[g][e] = __float_as_uint(__uint_as_float(sv[g][e]) * f.x);
-                sv[g][e + 1] = __float_as_uint(__uint_as_float(sv[g][e + 1]) * f.y);
-                sv[g][e + 2] = __float_as_uint(__uint_as_float(sv[g][e + 2]) * f.z);
-                sv[g][e + 3] = __float_as_uint(__uint_as_float(sv[g][e + 3]) * f.w);
+                const float2 x0 = f32x2_parts(
+                    f32x2_fma(f32x2(__uint_as_float(sv[g][e]), __uint_as_float(sv[g][e + 1])), c2, sub2));
+                const float2 x1 = f32x2_parts(
+                    f32x2_fma(f32x2(__uint_as_float(sv[g][e + 2]), __uint_as_float(sv[g][e + 3])), c2, sub2));
+                float q0 = fast_exp2(x0.x), q1 = fast_exp2(x0.y), q2 = fast_exp2(x1.x), q3 = fast_exp2(x1.y);
+                l2 = f32x2_add(l2, f32x2(q0, q1));
+                l3 = f32x2_add(l3, f32x2(q2, q3));
+                if constexpr (KV == kKvInt8) {
+                  const float4 f = vs[8 * g + e / 4];
+                  q0 *= f.x;
+                  q1 *= f.y;
+                  q2 *= f.z;
+                  q3 *= f.w;
+                }
+                pw[g][e / 2] = pack2<Sh::kBf16>(q0, q1);
+                pw[g][e / 2 + 1] = pack2<Sh::kBf16>(q2, q3);
               }
             }
+            const float2 lp = f32x2_parts(f32x2_add(l2, l3));
+            ls = lp.x + lp.y;
+            if (settle) break;
+            settle = __any_sync(0xffffffffu, live && (!(ls <= Sh::kMostSum) || m == -INFINITY));
+            if (!settle) break;
           }
-          if (p0 + kPfTile > limit0) {
-            const int vis = limit - p0;
+          l += ls;
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-#pragma unroll
-              for (int e = 0; e < 32; ++e) sv[g][e] = 32 * g + e < vis ? sv[g][e] : 0xFF800000u;
-            }
-          }
-          // eight chains of three-operand maxima
-          float mx8[8];
-#pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            mx8[2 * g] = __uint_as_float(sv[g][0]);
-            mx8[2 * g + 1] = __uint_as_float(sv[g][1]);
-          }
-#pragma unroll
-          for (int e = 2; e < 30; e += 4) {
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-              mx8[2 * g] = max3(mx8[2 * g], __uint_as_float(sv[g][e]), __uint_as_float(sv[g][e + 1]));
-              mx8[2 * g + 1] = max3(mx8[2 * g + 1], __uint_as_float(sv[g][e + 2]), __uint_as_float(sv[g][e + 3]));
-            }
-          }
-#pragma unroll
-          for (int g = 0; g < 4; ++g)
-            mx8[2 * g] = max3(mx8[2 * g], __uint_as_float(sv[g][30]), __uint_as_float(sv[g][31]));
-          float mx = max3(max3(mx8[0], mx8[1], mx8[2]), max3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7]));
-          mx *= c;
-          const bool need = mx > m + Sh::kSlack;
-          if (__any_sync(0xffffffffu, need)) {
-            const float mn = need ? mx : m;
-            const float alpha = need ? fast_exp2(m - mn) : 1.f;   // 0 from -inf
-            m = mn;
-            l *= alpha;
-            if (!first) {
-              // Products complete in issue order: these scores were issued behind the last P V.
-#pragma unroll 1
-              for (int e = 0; e < D; e += 32) {
-                uint32_t ov[32];
-                tmem_ld32(o_col + e, ov);
-#pragma unroll
-                for (int x = 0; x < 32; ++x) ov[x] = __float_as_uint(__uint_as_float(ov[x]) * alpha);
-                tmem_st32(o_col + e, ov);
-              }
-            }
-          }
-          const float sub = Sh::kShift - (m == -INFINITY ? 0.f : m);
-          const uint64_t c2 = f32x2(c, c), sub2 = f32x2(sub, sub);
-          uint64_t l2 = f32x2(0.f, 0.f), l3 = l2;
-          const float4* vs = reinterpret_cast<const float4*>(smem + Sh::kScales) + slot * 64 + 32;
-#pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            uint32_t pw[16];
-#pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              const float2 x0 = f32x2_parts(
-                  f32x2_fma(f32x2(__uint_as_float(sv[g][e]), __uint_as_float(sv[g][e + 1])), c2, sub2));
-              const float2 x1 = f32x2_parts(
-                  f32x2_fma(f32x2(__uint_as_float(sv[g][e + 2]), __uint_as_float(sv[g][e + 3])), c2, sub2));
-              float q0 = fast_exp2(x0.x), q1 = fast_exp2(x0.y), q2 = fast_exp2(x1.x), q3 = fast_exp2(x1.y);
-              l2 = f32x2_add(l2, f32x2(q0, q1));
-              l3 = f32x2_add(l3, f32x2(q2, q3));
-              if constexpr (KV == kKvInt8) {
-                const float4 f = vs[8 * g + e / 4];
-                q0 *= f.x;
-                q1 *= f.y;
-                q2 *= f.z;
-                q3 *= f.w;
-              }
-              pw[e / 2] = pack2<Sh::kBf16>(q0, q1);
-              pw[e / 2 + 1] = pack2<Sh::kBf16>(q2, q3);
-            }
-            tmem_st16_async(s_col + 16 * g, pw);
-          }
-          const float2 ls = f32x2_parts(f32x2_add(l2, l3));
-          l += ls.x + ls.y;
+          for (int g = 0; g < 4; ++g) tmem_st16_async(s_col + 16 * g, pw[g]);
           tmem_st_wait();
           tc_fence_before_sync();
           __syncwarp();
