@@ -152,6 +152,71 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return BF16 ? pack_bf16x2(lo, hi) : pack_f16x2(lo, hi);
 }
 
+// Scores of positions vis and up: -inf.
+__device__ __forceinline__ void pf_mask(uint32_t (&sv)[4][32], int vis) {
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+#pragma unroll
+    for (int e = 0; e < 32; ++e) sv[g][e] = 32 * g + e < vis ? sv[g][e] : 0xFF800000u;
+  }
+}
+
+// The largest of 128 scores: eight chains of three-operand maxima.
+__device__ __forceinline__ float pf_max(const uint32_t (&sv)[4][32]) {
+  float mx[8];
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    mx[2 * g] = __uint_as_float(sv[g][0]);
+    mx[2 * g + 1] = __uint_as_float(sv[g][1]);
+  }
+#pragma unroll
+  for (int e = 2; e < 30; e += 4) {
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      mx[2 * g] = max3(mx[2 * g], __uint_as_float(sv[g][e]), __uint_as_float(sv[g][e + 1]));
+      mx[2 * g + 1] = max3(mx[2 * g + 1], __uint_as_float(sv[g][e + 2]), __uint_as_float(sv[g][e + 3]));
+    }
+  }
+#pragma unroll
+  for (int g = 0; g < 4; ++g) mx[2 * g] = max3(mx[2 * g], __uint_as_float(sv[g][30]), __uint_as_float(sv[g][31]));
+  return max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
+}
+
+// Weights 2^(s c + sub) of 128 scores, packed in pairs, and their sum; an INT8 cache's are
+// packed times its V scales. FMAs and sums go two to an instruction (alone on its scheduler a
+// warp is quicker with scalar ones, whose operands need no aligned pairs, 737 against 1137
+// cycles a tile; beside the products the fewer instructions win: 16384-token prompt 1542 us
+// against 1622).
+template <int KV>
+__device__ __forceinline__ float pf_weights(const uint32_t (&sv)[4][32], uint32_t (&pw)[4][16], float c, float sub,
+                                            const float4* v_scales) {
+  const uint64_t c2 = f32x2(c, c), sub2 = f32x2(sub, sub);
+  uint64_t l2 = f32x2(0.f, 0.f), l3 = l2;
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+#pragma unroll
+    for (int e = 0; e < 32; e += 4) {
+      const float2 x0 = f32x2_parts(f32x2_fma(f32x2(__uint_as_float(sv[g][e]), __uint_as_float(sv[g][e + 1])), c2, sub2));
+      const float2 x1 =
+          f32x2_parts(f32x2_fma(f32x2(__uint_as_float(sv[g][e + 2]), __uint_as_float(sv[g][e + 3])), c2, sub2));
+      float q0 = fast_exp2(x0.x), q1 = fast_exp2(x0.y), q2 = fast_exp2(x1.x), q3 = fast_exp2(x1.y);
+      l2 = f32x2_add(l2, f32x2(q0, q1));
+      l3 = f32x2_add(l3, f32x2(q2, q3));
+      if constexpr (KV == kKvInt8) {
+        const float4 f = v_scales[8 * g + e / 4];
+        q0 *= f.x;
+        q1 *= f.y;
+        q2 *= f.z;
+        q3 *= f.w;
+      }
+      pw[g][e / 2] = pack2<KV == kKvBf16>(q0, q1);
+      pw[g][e / 2 + 1] = pack2<KV == kKvBf16>(q2, q3);
+    }
+  }
+  const float2 l = f32x2_parts(f32x2_add(l2, l3));
+  return l.x + l.y;
+}
+
 // Boxes first, first + step, ... of a unit's query rows, one thread: box b holds tokens
 // b * box_tokens .. of the unit; each 64-dimension half goes to its own half of the buffer.
 template <int D>
@@ -287,19 +352,30 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
           // second round from the same scores, the maximum is found and moves. (Finding it first in
           // every tile cost 300 to 400 of the 1350 cycles between a tile's scores and weights.)
           uint32_t pw[4][16];
-          bool settle = first || KV == kKvInt8;
           const bool live = limit > p0;   // the row sees positions of this tile
-          float ls;
-          for (;;) {
+          const bool masked = p0 + kPfTile > limit0;
+          const float4* scales4 = reinterpret_cast<const float4*>(smem + Sh::kScales) + slot * 64;
+          float ls = 0.f;
+          bool settle = true;
+          if (KV != kKvInt8 && !first) {
             uint32_t sv[4][32];   // 32 scores each
             tmem_ld128(s_col, sv[0], sv[1], sv[2], sv[3]);
+            if (__builtin_expect(masked, 0)) {
+              __syncwarp();   // keeps this a branch: as predicated selects it would run in every tile
+              pf_mask(sv, limit - p0);
+            }
+            ls = pf_weights<KV>(sv, pw, c, Sh::kShift - (m == -INFINITY ? 0.f : m), scales4 + 32);
+            settle = __any_sync(0xffffffffu, live && (!(ls <= Sh::kMostSum) || m == -INFINITY));
+          }
+          if (__builtin_expect(settle, KV == kKvInt8)) {
+            uint32_t sv[4][32];
+            tmem_ld128(s_col, sv[0], sv[1], sv[2], sv[3]);
             if constexpr (KV == kKvInt8) {
-              const float4* ks = reinterpret_cast<const float4*>(smem + Sh::kScales) + slot * 64;
 #pragma unroll
               for (int g = 0; g < 4; ++g) {
 #pragma unroll
                 for (int e = 0; e < 32; e += 4) {
-                  const float4 f = ks[8 * g + e / 4];
+                  const float4 f = scales4[8 * g + e / 4];
                   sv[g][e] = __float_as_uint(__uint_as_float(sv[g][e]) * f.x);
                   sv[g][e + 1] = __float_as_uint(__uint_as_float(sv[g][e + 1]) * f.y);
                   sv[g][e + 2] = __float_as_uint(__uint_as_float(sv[g][e + 2]) * f.z);
@@ -307,84 +383,30 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
                 }
               }
             }
-            if (p0 + kPfTile > limit0) {
-              const int vis = limit - p0;
-#pragma unroll
-              for (int g = 0; g < 4; ++g) {
-#pragma unroll
-                for (int e = 0; e < 32; ++e) sv[g][e] = 32 * g + e < vis ? sv[g][e] : 0xFF800000u;
-              }
+            if (masked) {
+              __syncwarp();
+              pf_mask(sv, limit - p0);
             }
-            if (settle) {
-              // eight chains of three-operand maxima
-              float mx8[8];
-#pragma unroll
-              for (int g = 0; g < 4; ++g) {
-                mx8[2 * g] = __uint_as_float(sv[g][0]);
-                mx8[2 * g + 1] = __uint_as_float(sv[g][1]);
-              }
-#pragma unroll
-              for (int e = 2; e < 30; e += 4) {
-#pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                  mx8[2 * g] = max3(mx8[2 * g], __uint_as_float(sv[g][e]), __uint_as_float(sv[g][e + 1]));
-                  mx8[2 * g + 1] = max3(mx8[2 * g + 1], __uint_as_float(sv[g][e + 2]), __uint_as_float(sv[g][e + 3]));
-                }
-              }
-#pragma unroll
-              for (int g = 0; g < 4; ++g)
-                mx8[2 * g] = max3(mx8[2 * g], __uint_as_float(sv[g][30]), __uint_as_float(sv[g][31]));
-              const float mx = c * max3(max3(mx8[0], mx8[1], mx8[2]), max3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7]));
-              const bool need = mx > m + Sh::kSlack;
-              if (__any_sync(0xffffffffu, need)) {
-                const float mn = need ? mx : m;
-                const float alpha = need ? fast_exp2(m - mn) : 1.f;   // 0 from -inf
-                m = mn;
-                l *= alpha;
-                if (!first) {
-                  // Products complete in issue order: these scores were issued behind the last P V.
+            const float mx = c * pf_max(sv);
+            const bool need = mx > m + Sh::kSlack;
+            if (__any_sync(0xffffffffu, need)) {
+              const float mn = need ? mx : m;
+              const float alpha = need ? fast_exp2(m - mn) : 1.f;   // 0 from -inf
+              m = mn;
+              l *= alpha;
+              if (!first) {
+                // Products complete in issue order: these scores were issued behind the last P V.
 #pragma unroll 1
-                  for (int e = 0; e < D; e += 16) {
-                    uint32_t ov[16];
-                    tmem_ld16(o_col + e, ov);
+                for (int e = 0; e < D; e += 16) {
+                  uint32_t ov[16];
+                  tmem_ld16(o_col + e, ov);
 #pragma unroll
-                    for (int x = 0; x < 16; ++x) ov[x] = __float_as_uint(__uint_as_float(ov[x]) * alpha);
-                    tmem_st16(o_col + e, ov);
-                  }
+                  for (int x = 0; x < 16; ++x) ov[x] = __float_as_uint(__uint_as_float(ov[x]) * alpha);
+                  tmem_st16(o_col + e, ov);
                 }
               }
             }
-            const float sub = Sh::kShift - (m == -INFINITY ? 0.f : m);
-            const uint64_t c2 = f32x2(c, c), sub2 = f32x2(sub, sub);
-            uint64_t l2 = f32x2(0.f, 0.f), l3 = l2;
-            const float4* vs = reinterpret_cast<const float4*>(smem + Sh::kScales) + slot * 64 + 32;
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-#pragma unroll
-              for (int e = 0; e < 32; e += 4) {
-                const float2 x0 = f32x2_parts(
-                    f32x2_fma(f32x2(__uint_as_float(sv[g][e]), __uint_as_float(sv[g][e + 1])), c2, sub2));
-                const float2 x1 = f32x2_parts(
-                    f32x2_fma(f32x2(__uint_as_float(sv[g][e + 2]), __uint_as_float(sv[g][e + 3])), c2, sub2));
-                float q0 = fast_exp2(x0.x), q1 = fast_exp2(x0.y), q2 = fast_exp2(x1.x), q3 = fast_exp2(x1.y);
-                l2 = f32x2_add(l2, f32x2(q0, q1));
-                l3 = f32x2_add(l3, f32x2(q2, q3));
-                if constexpr (KV == kKvInt8) {
-                  const float4 f = vs[8 * g + e / 4];
-                  q0 *= f.x;
-                  q1 *= f.y;
-                  q2 *= f.z;
-                  q3 *= f.w;
-                }
-                pw[g][e / 2] = pack2<Sh::kBf16>(q0, q1);
-                pw[g][e / 2 + 1] = pack2<Sh::kBf16>(q2, q3);
-              }
-            }
-            const float2 lp = f32x2_parts(f32x2_add(l2, l3));
-            ls = lp.x + lp.y;
-            if (settle) break;
-            settle = __any_sync(0xffffffffu, live && (!(ls <= Sh::kMostSum) || m == -INFINITY));
-            if (!settle) break;
+            ls = pf_weights<KV>(sv, pw, c, Sh::kShift - (m == -INFINITY ? 0.f : m), scales4 + 32);
           }
           l += ls;
 #pragma unroll
