@@ -287,30 +287,15 @@ __device__ __forceinline__ void prefetch_l2(const void* p) {
 }
 
 // ---- pairs of floats (one instruction for two) ------------------------------------
-__device__ __forceinline__ uint64_t f32x2(float lo, float hi) {
-  uint64_t d;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
-  return d;
+// (x, y) = (a, b) * c + d
+__device__ __forceinline__ void fma_pair(float& x, float& y, float a, float b, float c, float d) {
+  asm("{.reg .b64 A, B, C, D;\n mov.b64 A, {%2, %3};\n mov.b64 B, {%4, %4};\n mov.b64 C, {%5, %5};\n"
+      " fma.rn.f32x2 D, A, B, C;\n mov.b64 {%0, %1}, D;}" : "=f"(x), "=f"(y) : "f"(a), "f"(b), "f"(c), "f"(d));
 }
-__device__ __forceinline__ float2 f32x2_parts(uint64_t a) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
-  return r;
-}
-__device__ __forceinline__ uint64_t f32x2_fma(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t f32x2_mul(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ uint64_t f32x2_add(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
+// (x, y) += (a, b)
+__device__ __forceinline__ void add_pair(float& x, float& y, float a, float b) {
+  asm("{.reg .b64 A, B, D;\n mov.b64 A, {%0, %1};\n mov.b64 B, {%2, %3};\n"
+      " add.rn.f32x2 D, A, B;\n mov.b64 {%0, %1}, D;}" : "+f"(x), "+f"(y) : "f"(a), "f"(b));
 }
 
 // ---- register budgets of warp groups -----------------------------------------------

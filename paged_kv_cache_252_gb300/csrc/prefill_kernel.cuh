@@ -183,38 +183,37 @@ __device__ __forceinline__ float pf_max(const uint32_t (&sv)[4][32]) {
 }
 
 // Weights 2^(s c + sub) of 128 scores, packed in pairs, and their sum; an INT8 cache's are
-// packed times its V scales. FMAs and sums go two to an instruction (alone on its scheduler a
-// warp is quicker with scalar ones, whose operands need no aligned pairs, 737 against 1137
-// cycles a tile; beside the products the fewer instructions win: 16384-token prompt 1542 us
-// against 1622).
+// packed times its V scales. FMAs and sums go two to an instruction: alone on its scheduler a
+// warp is quicker with scalar ones (787 against 963 cycles a tile), but every instruction saved
+// beside the products counts (16384-token prompt 1511 us against 1620, with either in pairs
+// 1544 and 1563).
 template <int KV>
 __device__ __forceinline__ float pf_weights(const uint32_t (&sv)[4][32], uint32_t (&pw)[4][16], float c, float sub,
                                             const float4* v_scales) {
-  const uint64_t c2 = f32x2(c, c), sub2 = f32x2(sub, sub);
-  uint64_t l2 = f32x2(0.f, 0.f), l3 = l2;
+  float l[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int g = 0; g < 4; ++g) {
 #pragma unroll
     for (int e = 0; e < 32; e += 4) {
-      const float2 x0 = f32x2_parts(f32x2_fma(f32x2(__uint_as_float(sv[g][e]), __uint_as_float(sv[g][e + 1])), c2, sub2));
-      const float2 x1 =
-          f32x2_parts(f32x2_fma(f32x2(__uint_as_float(sv[g][e + 2]), __uint_as_float(sv[g][e + 3])), c2, sub2));
-      float q0 = fast_exp2(x0.x), q1 = fast_exp2(x0.y), q2 = fast_exp2(x1.x), q3 = fast_exp2(x1.y);
-      l2 = f32x2_add(l2, f32x2(q0, q1));
-      l3 = f32x2_add(l3, f32x2(q2, q3));
+      float q[4];
+      fma_pair(q[0], q[1], __uint_as_float(sv[g][e]), __uint_as_float(sv[g][e + 1]), c, sub);
+      fma_pair(q[2], q[3], __uint_as_float(sv[g][e + 2]), __uint_as_float(sv[g][e + 3]), c, sub);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) q[x] = fast_exp2(q[x]);
+      add_pair(l[0], l[1], q[0], q[1]);
+      add_pair(l[2], l[3], q[2], q[3]);
       if constexpr (KV == kKvInt8) {
         const float4 f = v_scales[8 * g + e / 4];
-        q0 *= f.x;
-        q1 *= f.y;
-        q2 *= f.z;
-        q3 *= f.w;
+        q[0] *= f.x;
+        q[1] *= f.y;
+        q[2] *= f.z;
+        q[3] *= f.w;
       }
-      pw[g][e / 2] = pack2<KV == kKvBf16>(q0, q1);
-      pw[g][e / 2 + 1] = pack2<KV == kKvBf16>(q2, q3);
+      pw[g][e / 2] = pack2<KV == kKvBf16>(q[0], q[1]);
+      pw[g][e / 2 + 1] = pack2<KV == kKvBf16>(q[2], q[3]);
     }
   }
-  const float2 l = f32x2_parts(f32x2_add(l2, l3));
-  return l.x + l.y;
+  return (l[0] + l[1]) + (l[2] + l[3]);
 }
 
 // Boxes first, first + step, ... of a unit's query rows, one thread: box b holds tokens
