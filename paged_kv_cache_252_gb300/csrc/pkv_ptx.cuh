@@ -298,6 +298,20 @@ __device__ __forceinline__ void add_pair(float& x, float& y, float a, float b) {
       " add.rn.f32x2 D, A, B;\n mov.b64 {%0, %1}, D;}" : "+f"(x), "+f"(y) : "f"(a), "f"(b));
 }
 
+// True in one lane of a converged warp. Unlike a test of the lane number it tells the compiler
+// that one thread runs what follows, so operands of tensor instructions stay in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile(
+      "{\n"
+      "  .reg .pred p;\n"
+      "  elect.sync _|p, 0xffffffff;\n"
+      "  selp.u32 %0, 1, 0, p;\n"
+      "}\n"
+      : "=r"(ok));
+  return ok != 0;
+}
+
 // ---- register budgets of warp groups -----------------------------------------------
 // Called by all four warps of a warpgroup; the sum over the block must not exceed the
 // registers it was launched with.

@@ -14,8 +14,8 @@
 // Warps: 0..3 and 4..7 the softmax of row tiles 0 and 1; warps 8 and 11 issue their products;
 // warps 12..15 bring the K and V tiles: of a 16-bit cache as copies of 16-token boxes through the
 // block table into the swizzled operand layout (and the queries; warp 10 clears V rows behind
-// the context), of a one-byte cache through registers, widened to fp16 (warp 9 copies the
-// queries).
+// the context), of a one-byte cache through registers, widened to fp16 (warp 10 copies the
+// queries). Warp 9 works out the pieces.
 //
 // Masks. Only tiles that reach past some row's last position compare positions; a masked
 // score is -inf, its weight 0. V rows behind the context are zeroed (a stale NaN times
@@ -44,12 +44,16 @@
 
 namespace pkv {
 
+constexpr int kPfRing = 4;   // pieces worked out ahead
+
 template <int KV, int D>
 struct PfShape {
   static constexpr bool kWiden = KV == kKvE5m2 || KV == kKvInt8;
   static constexpr bool kBf16 = KV == kKvBf16;
   static constexpr int kHalves = D / 64;
   static constexpr int kThreads = 512;
+  // Warps that read the pieces: eight softmax, two issuing, four loading, one more (warp 10).
+  static constexpr int kReaders = 15;
   // Register budgets (per thread of a warpgroup); twice the first and the others make the
   // launch's 512 x 128.
   static constexpr int kLaunchRegs = 128;
@@ -77,9 +81,9 @@ struct PfShape {
   static constexpr uint32_t kRing = kQBytes;
   static constexpr uint32_t kScales = kRing + kStages * kStageBytes;   // INT8: [kScaleRing][K, V][128] floats
   static constexpr uint32_t kBars = kScales + (KV == kKvInt8 ? kScaleRing * 2 * kPfTile * 4 : 0);
-  static constexpr uint32_t kMisc = kBars + (4 * kStages + 11 + kScaleRing) * 8;
-  static constexpr uint32_t kPos = kMisc + 256 + sizeof(PfStart);   // PfPos of each softmax warp
-  static constexpr uint32_t kSmem = kPos + 8 * sizeof(PfPos) + 1024;
+  static constexpr uint32_t kMisc = kBars + (4 * kStages + 11 + 2 * kPfRing + kScaleRing) * 8;
+  static constexpr uint32_t kPieces = kMisc + 256 + sizeof(PfStart);   // ring of kPfRing
+  static constexpr uint32_t kSmem = kPieces + kPfRing * sizeof(PfPiece) + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory of one CTA");
 };
 
@@ -252,7 +256,9 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
   // Per stage, so that a use is never more than one phase ahead of its waiter:
   const uint32_t v_tail = final_bar + 8;    // [NS] V rows behind the context zeroed
   const uint32_t v_sent = v_tail + 8 * NS;  // [NS] copies of such a tile issued
-  const uint32_t sc_full = v_sent + 8 * NS; // [kScaleRing] row scales of a tile written (INT8)
+  const uint32_t pc_full = v_sent + 8 * NS; // [kPfRing] piece worked out
+  const uint32_t pc_empty = pc_full + 8 * kPfRing;   // [kPfRing] piece no longer read
+  const uint32_t sc_full = pc_empty + 8 * kPfRing;   // [kScaleRing] row scales of a tile written (INT8)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Sh::kMisc);
   PfCtl* ctl = reinterpret_cast<PfCtl*>(smem + Sh::kMisc + 8);
   volatile int* last_piece = reinterpret_cast<volatile int*>(smem + Sh::kMisc + 16);   // [2]
@@ -277,6 +283,10 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
     }
     for (int i = 0; i < Sh::kScaleRing; ++i) mbar_init(sc_full + 8 * i, 128);
     mbar_init(final_bar, 2);
+    for (int i = 0; i < kPfRing; ++i) {
+      mbar_init(pc_full + 8 * i, 1);
+      mbar_init(pc_empty + 8 * i, Sh::kReaders);
+    }
     ctl->abort = 0;
     ctl->busy = 0;
     fence_barrier_init();
@@ -297,6 +307,9 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
   tc_fence_after_sync();
   pdl_launch_dependents();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
+  volatile PfPiece* ring = reinterpret_cast<volatile PfPiece*>(smem + Sh::kPieces);
+  auto piece_ready = [&](uint32_t n) { return pf_wait(pc_full + 8 * (n % kPfRing), (n / kPfRing) & 1, ctl); };
+  auto piece_done = [&](uint32_t n) { mbar_arrive(pc_empty + 8 * (n % kPfRing)); };
 
   if (start->any) {
     if (warp < 8) {
@@ -320,23 +333,26 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
           if (lane == 0 && a.status) atomicOr(a.status, kDevTimeout);
         }
       };
-      volatile PfPos* keep = reinterpret_cast<volatile PfPos*>(smem + Sh::kPos) + warp;
-      for (PfWalk w(a, *start); !w.done(); w.advance()) {
+      // The unit's row is fixed: query token tok behind the unit's first, query head hd of the group.
+      const int ru = 128 * i + r, tok = ru / a.group, hd = ru - tok * a.group, tok0 = 128 * i / a.group;
+      for (uint32_t np = 0;; ++np) {
+        // All four warps go on or stop together (they meet at barriers).
+        bool none = !alive || !piece_ready(np);
+        if (bar_red_or(1 + i, 128, none)) break;
+        const volatile PfPiece* pc = ring + np % kPfRing;
+        if (pc->end) break;
         uint32_t nth = seen;                        // KV tile of the CTA
-        int k, kb, limit, limit0;
-        {
-          const PfPiece pc(w);
-          if (!pc.any()) continue;
-          seen += pc.klast - pc.ka;
-          if (!pc.active(i)) continue;
-          const int ru = 128 * i + r;               // row of the unit
-          k = pc.ka;
-          kb = pc.kb[i];
-          // visible positions of this row and of the tile's first (<= 0: none)
-          limit = ru < pc.rows ? w.past() + pc.j0 + ru / a.group + 1 : 0;
-          limit0 = w.past() + pc.j0 + 128 * i / a.group + 1;
+        int k = pc->ka;
+        const int kb = pc->kb[i];
+        seen += pc->klast - k;
+        if (k >= kb) {
+          __syncwarp();
+          if (lane == 0) piece_done(np);
+          continue;
         }
-        w.save(keep);
+        // visible positions of this row and of the tile's first (<= 0: none)
+        const int limit = ru < pc->rows ? pc->past + pc->j0 + tok + 1 : 0;
+        const int limit0 = pc->past + pc->j0 + tok0 + 1;
         float m = -INFINITY, l = 0.f;
         for (bool first = true; k < kb; ++k, ++cnt, ++nth, first = false) {
           const int p0 = k * kPfTile;
@@ -417,16 +433,14 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
         }
 
         // ---- end of the piece ----
-        w.restore(keep);
-        const PfPiece pc(w);
-        const int ru = 128 * i + r, j = pc.j0 + ru / a.group;
-        const bool real = ru < pc.rows;
         wait(bar_o, done++ & 1);
         if (alive) tc_fence_after_sync();
+        const bool real = ru < pc->rows;
         uint16_t* dst = static_cast<uint16_t*>(a.out) +
-                        (static_cast<size_t>(w.p.qb + j) * a.num_q_heads + w.p.h * a.group + ru % a.group) * D;
+                        (static_cast<size_t>(pc->qb + pc->j0 + tok) * a.num_q_heads + pc->h * a.group + hd) * D;
         bool odd = false;   // a real row whose result is not finite
-        if (pc.whole(i)) {
+        const int pieces = pc->pieces[i];
+        if (pieces == 1) {
           if (alive) {
             const float inv = l > 0.f ? 1.f / l : 0.f;
             float bad = l == 0.f && limit > 0 ? NAN : 0.f;
@@ -452,7 +466,7 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
         } else {
           // A cut unit: this piece's m, l and O to its slot; the last of the row tile's pieces
           // to finish adds them up in the order of their CTAs.
-          const int first = w.owner(0), pieces = w.owner(pc.kend[i] - 1) - first + 1;
+          const int first = pc->first[i];
           const size_t slot_sz = pf_slot_floats(D);
           auto slot_of = [&](int p) {
             return a.partials + (static_cast<size_t>(2 * (first + p) + (p == 0 ? 1 : 0)) * a.slot_tiles + i) * slot_sz;
@@ -500,9 +514,11 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
             fence_acq_rel_gpu();
             if (real) {
               float M = -INFINITY;
+              #pragma unroll 1
               for (int p = 0; p < pieces; ++p) M = fmaxf(M, __ldcg(slot_of(p) + r));
               const float mu = M == -INFINITY ? 0.f : M;
               float L = 0.f;
+#pragma unroll 1
               for (int p = 0; p < pieces; ++p)
                 L += __ldcg(slot_of(p) + 128 + r) * fast_exp2(__ldcg(slot_of(p) + r) - mu);
               const float inv = L > 0.f ? 1.f / L : 0.f;
@@ -512,6 +528,7 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
                 float o[16];
 #pragma unroll
                 for (int x = 0; x < 16; ++x) o[x] = 0.f;
+#pragma unroll 1
                 for (int p = 0; p < pieces; ++p) {
                   const float* sl = slot_of(p);
                   const float wp = fast_exp2(__ldcg(sl + r) - mu);
@@ -541,8 +558,10 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
         }
         __syncwarp();
         const unsigned again = __ballot_sync(0xffffffffu, odd);
-        if (again) pf_redo<KV, D>(a, again, w.p.s, w.p.qb, w.past(), pc.j0, 128 * i + 32 * (warp & 3), w.p.h, ctl);
+        if (again) pf_redo<KV, D>(a, again, pc->s, pc->qb, pc->past, pc->j0, 128 * i + 32 * (warp & 3), pc->h, ctl);
         tc_fence_before_sync();   // O_i is read before the next piece's product overwrites it
+        __syncwarp();
+        if (lane == 0) piece_done(np);
       }
     } else if (warp >= 12) {
       regs_shrink<Sh::kLoadRegs>();
@@ -556,31 +575,33 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
         const int total_rows = a.num_blocks * a.num_kv_heads * kBlockSize;   // host guarantees < 2^31
         uint32_t st = 0, stage = 0, round = 0, piece = 0;
         bool ok = true;
-        for (PfWalk w(a, *start); !w.done() && ok; w.advance()) {
-          const PfPiece pc(w);
-          if (!pc.any()) continue;
-          const int32_t* bt = a.block_tables + static_cast<size_t>(w.p.s) * a.max_blocks_per_seq;
-          const int tail = w.p.ctx & 15 ? w.p.ctx / kPfTile : -1;   // see warp 10
-          for (int k = pc.ka; k < pc.klast; ++k) {
+        for (;; ++piece) {
+          ok = __all_sync(0xffffffffu, piece_ready(piece));
+          const volatile PfPiece* pc = ring + piece % kPfRing;
+          if (!ok || pc->end) break;
+          const int32_t* bt = a.block_tables + static_cast<size_t>(pc->s) * a.max_blocks_per_seq;
+          const int ctx = pc->ctx, h = pc->h, ka = pc->ka, klast = pc->klast, tail = pc->tail;
+          const int boxes = (pc->rows + a.box_tokens * a.group - 1) / (a.box_tokens * a.group);
+          const int token = pc->qb + pc->j0;
+          __syncwarp();
+          if (lane == 0) piece_done(piece);
+          for (int k = ka; k < klast; ++k) {
             // Rows of both blocks: lanes 0 and 1 look them up.
             int mine = total_rows;   // wholly past the end: the copy fills zeros
             if (lane < 2) {
               const int p = k * kPfTile + (2 * x + lane) * kBlockSize;
-              if (p < w.p.ctx) {
+              if (p < ctx) {
                 const int id = bt[p >> 4];
                 if (static_cast<unsigned>(id) < static_cast<unsigned>(a.num_blocks))
-                  mine = (id * a.num_kv_heads + w.p.h) * kBlockSize;
+                  mine = (id * a.num_kv_heads + h) * kBlockSize;
                 else if (a.status) atomicOr(a.status, kDevBadBlock);
               }
             }
             const int row0 = __shfl_sync(0xffffffffu, mine, 0), row1 = __shfl_sync(0xffffffffu, mine, 1);
-            if (lane == 0) {
-              if (k == pc.ka) {
+            if (elect_one()) {
+              if (k == ka) {
                 ok = piece == 0 || pf_wait(q_empty, (piece - 1) & 1, ctl);
-                if (ok) {
-                  const int boxes = (pc.rows + a.box_tokens * a.group - 1) / (a.box_tokens * a.group);
-                  pf_load_q<D>(a, &tm_q, base, q_full, w.p.h * a.group, w.p.qb + pc.j0, boxes, x, 4);
-                }
+                if (ok) pf_load_q<D>(a, &tm_q, base, q_full, h * a.group, token, boxes, x, 4);
               }
               for (int v = 0; v < 2 && ok; ++v) {
                 if (st >= NS && !pf_wait(empty + 8 * stage, round ^ 1, ctl)) {
@@ -611,11 +632,12 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
                 }
               }
             }
-            ok = __shfl_sync(0xffffffffu, ok, 0);
+            ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
           }
-          ++piece;
+          if (!ok) break;
         }
+        st = __reduce_max_sync(0xffffffffu, st);   // of the lane that counted
         if (lane == 0) {
           if (!ok) {
             ctl->abort = 1;
@@ -638,10 +660,15 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
         uint32_t st = 0;
         uint32_t tiles = 0;
         bool alive = true;
-        for (PfWalk w(a, *start); !w.done() && alive; w.advance()) {
-          const PfPiece pc(w);
-          const int32_t* bt = a.block_tables + static_cast<size_t>(w.p.s) * a.max_blocks_per_seq;
-          for (int k = pc.ka; k < pc.klast && alive; ++k, ++tiles) {
+        for (uint32_t np = 0; alive; ++np) {
+          alive = __all_sync(0xffffffffu, piece_ready(np));
+          const volatile PfPiece* pc = ring + np % kPfRing;
+          if (!alive || pc->end) break;
+          const int32_t* bt = a.block_tables + static_cast<size_t>(pc->s) * a.max_blocks_per_seq;
+          const int ctx = pc->ctx, h = pc->h, ka = pc->ka, klast = pc->klast;
+          __syncwarp();
+          if (lane == 0) piece_done(np);
+          for (int k = ka; k < klast && alive; ++k, ++tiles) {
 #pragma unroll 1
             for (int v = 0; v < 2; ++v, ++st) {
               const uint8_t* cache = static_cast<const uint8_t*>(v ? a.v_cache : a.k_cache);
@@ -652,21 +679,21 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
                 const int p = k * kPfTile + row;
                 x[q] = make_uint4(0u, 0u, 0u, 0u);
                 if constexpr (KV == kKvInt8) x[q] = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
-                if (p < w.p.ctx) {
+                if (p < ctx) {
                   const int b = bt[p >> 4];
                   if (static_cast<unsigned>(b) < static_cast<unsigned>(a.num_blocks))
                     x[q] = __ldg(reinterpret_cast<const uint4*>(
-                        cache + ((static_cast<size_t>(b) * a.num_kv_heads + w.p.h) * kBlockSize + (p & 15)) * D + 16 * cc));
+                        cache + ((static_cast<size_t>(b) * a.num_kv_heads + h) * kBlockSize + (p & 15)) * D + 16 * cc));
                   else if (a.status) atomicOr(a.status, kDevBadBlock);
                 }
               }
               float scale = 0.f;
               if constexpr (KV == kKvInt8) {
                 const int p = k * kPfTile + wt;
-                if (p < w.p.ctx) {
+                if (p < ctx) {
                   const int b = bt[p >> 4];
                   if (static_cast<unsigned>(b) < static_cast<unsigned>(a.num_blocks))
-                    scale = a.scales[(static_cast<size_t>(b) * a.num_kv_heads + w.p.h) * 32 + 16 * v + (p & 15)];
+                    scale = a.scales[(static_cast<size_t>(b) * a.num_kv_heads + h) * 32 + 16 * v + (p & 15)];
                 }
               }
               const uint32_t stage = st % NS, round = st / NS;
@@ -711,8 +738,8 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
         // cycles of a KV tile's 3550) were idle time there; with two, one thread's fall into the
         // other's products. They take strict turns, a row tile's products of one KV tile each:
         // left to themselves both row tiles fall into step and their softmax leaves the pipe idle
-        // (8192-token prompt: 577 us). The turn passes two products before a thread's last.
-        if (lane == 0) {
+        // (8192-token prompt: 577 us). The turn passes before a thread's last product.
+        if (elect_one()) {
           const int i = warp == 8 ? 0 : 1;
           constexpr uint32_t id_s = idesc_kind_f16(128, 128, Sh::kBf16, 0, 0);   // Q (K-major) x K^T (K-major)
           constexpr uint32_t id_o = idesc_kind_f16(128, D, Sh::kBf16, 0, 1);     // P (TMEM) x V (dimensions contiguous)
@@ -740,7 +767,7 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
             const uint64_t kb = dk + ((at * Sh::kStageBytes) >> 4);
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
-              if (kk == D / 16 - 2) mbar_arrive(other_turn);
+              if (kk == D / 16 - 1) mbar_arrive(other_turn);
               tc_mma_f16_ss(t_s, dq + (((kk >> 2) * Sh::kQHalfBytes + (kk & 3) * 32) >> 4),
                             kb + (((kk >> 2) * Sh::kHalfBytes + (kk & 3) * 32) >> 4), id_s, kk > 0);
             }
@@ -748,14 +775,18 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
           };
           // Stages (and the queries) are released by both threads: behind the products that
           // read them, or at once where this row tile has none.
-          for (PfWalk w(a, *start); !w.done() && ok; w.advance()) {
-            const PfPiece pc(w);
-            if (!pc.any()) continue;
-            const int tail = !Sh::kWiden && (w.p.ctx & 15) ? w.p.ctx / kPfTile : -1;   // see warp 10
-            const int kb = pc.kb[i], klast = pc.klast;
-            int k = pc.ka;
+          for (;; ++piece) {
+            if (!piece_ready(piece)) {
+              ok = false;
+              break;
+            }
+            const volatile PfPiece* pc = ring + piece % kPfRing;
+            if (pc->end) break;
+            const int tail = Sh::kWiden ? -1 : pc->tail;   // see warp 10
+            const int kb = pc->kb[i], klast = pc->klast;
+            int k = pc->ka;
+            piece_done(piece);
             if (!wait(q_full, piece & 1)) break;
-            ++piece;
             if (!wait(full + 8 * stage, round)) break;
             if (!wait(my_turn, turns++ & 1)) break;
             if (k < kb) {
@@ -790,7 +821,7 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
                 const bool more = k + 1 < kb;
 #pragma unroll
                 for (int kk = 0; kk < kPfTile / 16; ++kk) {
-                  if (kk == kPfTile / 16 - 2 && !more) mbar_arrive(other_turn);
+                  if (kk == kPfTile / 16 - 1 && !more) mbar_arrive(other_turn);
                   tc_mma_f16_ts(t_o, t_s + kk * 8, vb + ((kk * Sh::kVBlockBytes) >> 4), id_o, kk > 0 || !first);
                 }
                 if (more) {
@@ -809,6 +840,7 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
                 if (k + 1 < klast) mbar_arrive(empty + 8 * ks);
               }
             }
+            if (!ok) break;
           }
           if (!ok) {
             ctl->abort = 1;
@@ -825,18 +857,21 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
         // product wait for this warp once.
         uint32_t st = 0, sent = 0;
         bool ok = true;
-        for (PfWalk w(a, *start); !w.done() && ok; w.advance()) {
-          const PfPiece pc(w);
-          if (!pc.any()) continue;
-          const int tail = w.p.ctx & 15 ? w.p.ctx / kPfTile : -1;
-          if (tail >= pc.ka && tail < pc.klast) {
-            const uint32_t vst = st + 2 * (tail - pc.ka) + 1, vs = vst % NS;
+        for (uint32_t np = 0;; ++np) {
+          ok = __all_sync(0xffffffffu, piece_ready(np));
+          const volatile PfPiece* pc = ring + np % kPfRing;
+          if (!ok || pc->end) break;
+          const int ctx = pc->ctx, ka = pc->ka, klast = pc->klast, tail = pc->tail;
+          __syncwarp();
+          if (lane == 0) piece_done(np);
+          if (tail >= ka && tail < klast) {
+            const uint32_t vst = st + 2 * (tail - ka) + 1, vs = vst % NS;
             // Once this use's copies are issued, the stage's barrier is in this use's phase.
             ok = pf_wait(v_sent + 8 * vs, (sent >> vs) & 1, ctl) && pf_wait(full + 8 * vs, (vst / NS) & 1, ctl);
             sent ^= 1u << vs;
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
-            const int r0 = w.p.ctx - tail * kPfTile, r1 = (r0 + 15) & ~15;
+            const int r0 = ctx - tail * kPfTile, r1 = (r0 + 15) & ~15;
             uint8_t* vt = smem + Sh::kRing + vs * Sh::kStageBytes;
             for (int x = lane; x < (r1 - r0) * Sh::kHalves * 8; x += 32) {
               const int row = r0 + x / (Sh::kHalves * 8), ch = x % (Sh::kHalves * 8);
@@ -847,34 +882,56 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(v_tail + 8 * vs);
           }
-          st += 2 * (pc.klast - pc.ka);
+          st += 2 * (klast - ka);
         }
         if (!ok && lane == 0) {
           ctl->abort = 1;
           if (a.status) atomicOr(a.status, kDevTimeout);
         }
         __syncwarp();
-      } else if (warp == 9 && Sh::kWiden) {
+      } else if (warp == 10) {
         // --------------------------- query copies (one-byte caches) ------------------------
         if (lane == 0) {
           uint32_t piece = 0;
           bool ok = true;
-          for (PfWalk w(a, *start); !w.done(); w.advance()) {
-            const PfPiece pc(w);
-            if (!pc.any()) continue;
-            if (piece > 0 && !pf_wait(q_empty, (piece - 1) & 1, ctl)) {
-              ok = false;
-              break;
-            }
-            const int boxes = (pc.rows + a.box_tokens * a.group - 1) / (a.box_tokens * a.group);
-            pf_load_q<D>(a, &tm_q, base, q_full, w.p.h * a.group, w.p.qb + pc.j0, boxes, 0, 1);
-            ++piece;
+          for (;; ++piece) {
+            ok = piece_ready(piece);
+            const volatile PfPiece* pc = ring + piece % kPfRing;
+            if (!ok || pc->end) break;
+            const int boxes = (pc->rows + a.box_tokens * a.group - 1) / (a.box_tokens * a.group);
+            const int head = pc->h * a.group, token = pc->qb + pc->j0;
+            piece_done(piece);
+            ok = piece == 0 || pf_wait(q_empty, (piece - 1) & 1, ctl);
+            if (!ok) break;
+            pf_load_q<D>(a, &tm_q, base, q_full, head, token, boxes, 0, 1);
           }
           if (!ok) {
             ctl->abort = 1;
             if (a.status) atomicOr(a.status, kDevTimeout);
           }
           if (piece > 0) mbar_wait(q_full, (piece - 1) & 1);   // the last copies land before exit
+        }
+        __syncwarp();
+      } else if (warp == 9) {
+        // ------------------------------- pieces ---------------------------------------------
+        if (lane == 0) {
+          uint32_t np = 0;
+          auto room = [&] { return np < kPfRing || pf_wait(pc_empty + 8 * (np % kPfRing), (np / kPfRing - 1) & 1, ctl); };
+          bool ok = true;
+          for (PfWalk w(a, *start); !w.done(); w.advance()) {
+            if (!(ok = room())) break;
+            if (!pf_piece(w, ring + np % kPfRing)) continue;
+            mbar_arrive(pc_full + 8 * (np % kPfRing));
+            ++np;
+          }
+          if (ok && (ok = room())) {
+            ring[np % kPfRing].end = 1;
+            mbar_arrive(pc_full + 8 * (np % kPfRing));
+          }
+          if (!ok) {
+            ctl->abort = 1;
+            if (a.status) atomicOr(a.status, kDevTimeout);
+          }
         }
         __syncwarp();
       }

@@ -90,61 +90,58 @@ struct PfWalk {
   __device__ int owner(int k) const {
     return static_cast<int>((p.ub + kPfUnitCost + static_cast<long long>(kPfTile) * k) / st.share);
   }
-  // Keep the place in shared memory (of this warp) while a long loop needs the registers.
-  __device__ void save(volatile PfPos* to) const {
-    if ((threadIdx.x & 31) == 0) {
-      to->ub = p.ub;
-      to->s = p.s;
-      to->h = p.h;
-      to->t = p.t;
-      to->n = p.n;
-      to->qb = p.qb;
-      to->ctx = p.ctx;
-    }
-    __syncwarp();
-  }
-  __device__ void restore(const volatile PfPos* from) {
-    p.ub = from->ub;
-    p.s = from->s;
-    p.h = from->h;
-    p.t = from->t;
-    p.n = from->n;
-    p.qb = from->qb;
-    p.ctx = from->ctx;
-    __syncwarp();
-  }
 };
 
-// This CTA's piece of the walk's current unit.
+// This CTA's piece of a unit, as one warp works it out and the others read it from shared
+// memory: the walk's 64-bit arithmetic, run by every role, was a good part of the kernel's code,
+// and what runs once a piece finds its code evicted by the loops.
 struct PfPiece {
-  int j0, rows;              // first query token, rows of the unit
-  int ka, kb[2];             // KV tiles [ka, kb[i]) of row tile i (empty: kb <= ka)
-  int kend[2];               // tiles of the whole unit row tile i needs
-  int klast;                 // max of kb
-
-  __device__ PfPiece(const PfWalk& w) {
-    const int G = w.a.group, qt = w.a.unit_tokens;
-    j0 = w.p.t * qt;
-    rows = min(qt, w.p.n - j0) * G;
-    const int k_all = (w.len() + kPfTile - 1) / kPfTile;
-    const long long x0 = w.st.b0 - w.p.ub - kPfUnitCost, x1 = w.st.b1 - w.p.ub - kPfUnitCost;
-    ka = x0 <= 0 ? 0 : static_cast<int>((x0 + kPfTile - 1) / kPfTile);
-    const int kx = x1 <= 0 ? 0 : static_cast<int>(min((x1 + kPfTile - 1) / kPfTile, static_cast<long long>(k_all)));
-    if (rows > 128) {
-      kend[0] = (w.pastp() + j0 + 127 / G + 1 + kPfTile - 1) / kPfTile;
-      kend[1] = k_all;
-    } else {
-      kend[0] = k_all;
-      kend[1] = 0;
-    }
-    kb[0] = min(kx, kend[0]);
-    kb[1] = min(kx, kend[1]);
-    klast = max(kb[0], kb[1]);
-  }
-  __device__ bool active(int i) const { return ka < kb[i]; }
-  __device__ bool any() const { return ka < klast; }
-  __device__ bool whole(int i) const { return ka == 0 && kb[i] == kend[i]; }
+  int end;                   // no further piece
+  int s, h;                  // sequence, KV head
+  int qb, past, ctx;         // first query row, positions before the first query token (may be < 0), context
+  int j0, rows;              // first query token of the unit, its rows
+  int ka, klast;             // KV tiles [ka, klast) ...
+  int kb[2];                 // ... of which row tile i takes those below kb[i] (none: kb <= ka)
+  int tail;                  // the tile whose V rows end behind the context inside a block, else -1
+  int first[2], pieces[2];   // of a row tile cut by a stretch's end: its first CTA, its pieces (1: not cut)
 };
+
+// False if the CTA has no tile of the unit.
+__device__ inline bool pf_piece(const PfWalk& w, volatile PfPiece* to) {
+  const int G = w.a.group, qt = w.a.unit_tokens;
+  const int j0 = w.p.t * qt, rows = min(qt, w.p.n - j0) * G;
+  const int k_all = (w.len() + kPfTile - 1) / kPfTile;
+  const long long x0 = w.st.b0 - w.p.ub - kPfUnitCost, x1 = w.st.b1 - w.p.ub - kPfUnitCost;
+  const int ka = x0 <= 0 ? 0 : static_cast<int>((x0 + kPfTile - 1) / kPfTile);
+  const int kx = x1 <= 0 ? 0 : static_cast<int>(min((x1 + kPfTile - 1) / kPfTile, static_cast<long long>(k_all)));
+  int kend[2] = {k_all, 0};   // tiles of the whole unit row tile i needs
+  if (rows > 128) {
+    kend[0] = (w.pastp() + j0 + 127 / G + 1 + kPfTile - 1) / kPfTile;
+    kend[1] = k_all;
+  }
+  const int klast = min(kx, k_all);
+  if (ka >= klast) return false;
+  to->end = 0;
+  to->s = w.p.s;
+  to->h = w.p.h;
+  to->qb = w.p.qb;
+  to->past = w.past();
+  to->ctx = w.p.ctx;
+  to->j0 = j0;
+  to->rows = rows;
+  to->ka = ka;
+  to->klast = klast;
+  to->tail = w.p.ctx & 15 ? w.p.ctx / kPfTile : -1;
+#pragma unroll 1
+  for (int i = 0; i < 2; ++i) {
+    to->kb[i] = min(kx, kend[i]);
+    const bool whole = ka == 0 && kx >= kend[i];
+    const int first = whole || kend[i] == 0 ? 0 : w.owner(0);
+    to->first[i] = first;
+    to->pieces[i] = whole || kend[i] == 0 ? 1 : w.owner(kend[i] - 1) - first + 1;
+  }
+  return true;
+}
 
 // Line length of one KV head of a sequence: T units of cost + pastp + min((t+1) qt, n).
 __device__ __forceinline__ long long pf_head_len(int n, int pastp, int qt) {

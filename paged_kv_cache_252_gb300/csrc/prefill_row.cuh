@@ -117,7 +117,7 @@ __device__ __forceinline__ void prefill_row(const PrefillArgs& a, int s, int row
       float dot = 0.f;
       if (static_cast<unsigned>(b) < static_cast<unsigned>(a.num_blocks)) {
         crow = (static_cast<long long>(b) * a.num_kv_heads + h) * kBlockSize + (p & 15);
-#pragma unroll 4
+#pragma unroll 1
         for (int c = 0; c < D / 8; ++c) {
           float q[8], k[8];
           load8<Q>(a.q, qo + 8 * c, q);   // the same for every lane
@@ -151,7 +151,7 @@ __device__ __forceinline__ void prefill_row(const PrefillArgs& a, int s, int row
     for (int e = 0; e < E; ++e) o[e] *= alpha;
     const float wv = w * sv;
     const int cnt = limit - p0 < 32 ? limit - p0 : 32;
-#pragma unroll 4
+#pragma unroll 1
     for (int t = 0; t < cnt; ++t) {
       const float wt = __shfl_sync(0xffffffffu, wv, t);
       const long long rt = __shfl_sync(0xffffffffu, crow, t);
