@@ -287,10 +287,17 @@ __device__ __forceinline__ void prefetch_l2(const void* p) {
 }
 
 // ---- pairs of floats (one instruction for two) ------------------------------------
-// (x, y) = (a, b) * c + d
-__device__ __forceinline__ void fma_pair(float& x, float& y, float a, float b, float c, float d) {
-  asm("{.reg .b64 A, B, C, D;\n mov.b64 A, {%2, %3};\n mov.b64 B, {%4, %4};\n mov.b64 C, {%5, %5};\n"
-      " fma.rn.f32x2 D, A, B, C;\n mov.b64 {%0, %1}, D;}" : "=f"(x), "=f"(y) : "f"(a), "f"(b), "f"(c), "f"(d));
+// (x, y) = (a * c, b * d) + e
+__device__ __forceinline__ void fma_pair(float& x, float& y, float a, float b, float c, float d, float e) {
+  asm("{.reg .b64 A, B, C, D;\n mov.b64 A, {%2, %3};\n mov.b64 B, {%4, %5};\n mov.b64 C, {%6, %6};\n"
+      " fma.rn.f32x2 D, A, B, C;\n mov.b64 {%0, %1}, D;}"
+      : "=f"(x), "=f"(y)
+      : "f"(a), "f"(b), "f"(c), "f"(d), "f"(e));
+}
+// (x, y) *= (a, b)
+__device__ __forceinline__ void mul_pair(float& x, float& y, float a, float b) {
+  asm("{.reg .b64 A, B, D;\n mov.b64 A, {%0, %1};\n mov.b64 B, {%2, %3};\n"
+      " mul.rn.f32x2 D, A, B;\n mov.b64 {%0, %1}, D;}" : "+f"(x), "+f"(y) : "f"(a), "f"(b));
 }
 // (x, y) += (a, b)
 __device__ __forceinline__ void add_pair(float& x, float& y, float a, float b) {

@@ -27,7 +27,8 @@
 // tile's weights sum to more than 2^kSlack, so that O is rescaled a few times a row, not every
 // tile. fp16 weights carry a shift of 2^7: they stay at or below 2^15, and weights down to 2^-21
 // of the largest keep full precision. An INT8 cache's V scale enters the weight with it (at
-// most 516, so slack 0 and shift 6); its K scale multiplies the scores.
+// most 516, so the shift is 6, and a maximum that moves moves to the largest score); its K scale
+// multiplies the scores.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -165,59 +166,82 @@ __device__ __forceinline__ void pf_mask(uint32_t (&sv)[4][32], int vis) {
   }
 }
 
-// The largest of 128 scores: eight chains of three-operand maxima.
-__device__ __forceinline__ float pf_max(const uint32_t (&sv)[4][32]) {
+// The largest of 128 scores times c (an INT8 cache's: times their K scales, which hold c):
+// eight chains.
+template <int KV>
+__device__ __forceinline__ float pf_max(const uint32_t (&sv)[4][32], float c, const float4* k_scales) {
   float mx[8];
+  if constexpr (KV == kKvInt8) {
 #pragma unroll
-  for (int g = 0; g < 4; ++g) {
-    mx[2 * g] = __uint_as_float(sv[g][0]);
-    mx[2 * g + 1] = __uint_as_float(sv[g][1]);
-  }
-#pragma unroll
-  for (int e = 2; e < 30; e += 4) {
+    for (int x = 0; x < 8; ++x) mx[x] = -INFINITY;
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
-      mx[2 * g] = max3(mx[2 * g], __uint_as_float(sv[g][e]), __uint_as_float(sv[g][e + 1]));
-      mx[2 * g + 1] = max3(mx[2 * g + 1], __uint_as_float(sv[g][e + 2]), __uint_as_float(sv[g][e + 3]));
-    }
-  }
 #pragma unroll
-  for (int g = 0; g < 4; ++g) mx[2 * g] = max3(mx[2 * g], __uint_as_float(sv[g][30]), __uint_as_float(sv[g][31]));
-  return max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
+      for (int e = 0; e < 32; e += 4) {
+        const float4 f = k_scales[8 * g + e / 4];
+        const float x = __uint_as_float(sv[g][e]) * f.x, y = __uint_as_float(sv[g][e + 1]) * f.y;
+        const float z = __uint_as_float(sv[g][e + 2]) * f.z, w = __uint_as_float(sv[g][e + 3]) * f.w;
+        mx[2 * g] = max3(mx[2 * g], x, y);
+        mx[2 * g + 1] = max3(mx[2 * g + 1], z, w);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      mx[2 * g] = __uint_as_float(sv[g][0]);
+      mx[2 * g + 1] = __uint_as_float(sv[g][1]);
+    }
+#pragma unroll
+    for (int e = 2; e < 30; e += 4) {
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        mx[2 * g] = max3(mx[2 * g], __uint_as_float(sv[g][e]), __uint_as_float(sv[g][e + 1]));
+        mx[2 * g + 1] = max3(mx[2 * g + 1], __uint_as_float(sv[g][e + 2]), __uint_as_float(sv[g][e + 3]));
+      }
+    }
+#pragma unroll
+    for (int g = 0; g < 4; ++g) mx[2 * g] = max3(mx[2 * g], __uint_as_float(sv[g][30]), __uint_as_float(sv[g][31]));
+  }
+  const float m = max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
+  return KV == kKvInt8 ? m : m * c;
 }
 
-// Weights 2^(s c + sub) of 128 scores, packed in pairs, and their sum; an INT8 cache's are
-// packed times its V scales. FMAs and sums go two to an instruction: alone on its scheduler a
-// warp is quicker with scalar ones (787 against 963 cycles a tile), but every instruction saved
-// beside the products counts (16384-token prompt 1511 us against 1620, with either in pairs
-// 1544 and 1563).
+// Weights 2^(s c + sub) of 128 scores, packed in pairs, their sum l and the sum `packed` of
+// what was packed: the same, or an INT8 cache's weights times its V scales (its K scales, which
+// hold c, multiply the scores). FMAs and sums go two to an instruction: alone on its scheduler
+// a warp is quicker with scalar ones (787 against 963 cycles a tile), but every instruction
+// saved beside the products counts (16384-token prompt 1511 us against 1620, with either in
+// pairs 1544 and 1563).
 template <int KV>
-__device__ __forceinline__ float pf_weights(const uint32_t (&sv)[4][32], uint32_t (&pw)[4][16], float c, float sub,
-                                            const float4* v_scales) {
-  float l[4] = {0.f, 0.f, 0.f, 0.f};
+__device__ __forceinline__ void pf_weights(const uint32_t (&sv)[4][32], uint32_t (&pw)[4][16], float c, float sub,
+                                           const float4* k_scales, const float4* v_scales, float& sum, float& packed) {
+  float l[4] = {0.f, 0.f, 0.f, 0.f}, t[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int g = 0; g < 4; ++g) {
 #pragma unroll
     for (int e = 0; e < 32; e += 4) {
+      float4 kc = make_float4(c, c, c, c);
+      if constexpr (KV == kKvInt8) kc = k_scales[8 * g + e / 4];
       float q[4];
-      fma_pair(q[0], q[1], __uint_as_float(sv[g][e]), __uint_as_float(sv[g][e + 1]), c, sub);
-      fma_pair(q[2], q[3], __uint_as_float(sv[g][e + 2]), __uint_as_float(sv[g][e + 3]), c, sub);
+      fma_pair(q[0], q[1], __uint_as_float(sv[g][e]), __uint_as_float(sv[g][e + 1]), kc.x, kc.y, sub);
+      fma_pair(q[2], q[3], __uint_as_float(sv[g][e + 2]), __uint_as_float(sv[g][e + 3]), kc.z, kc.w, sub);
 #pragma unroll
       for (int x = 0; x < 4; ++x) q[x] = fast_exp2(q[x]);
       add_pair(l[0], l[1], q[0], q[1]);
       add_pair(l[2], l[3], q[2], q[3]);
       if constexpr (KV == kKvInt8) {
         const float4 f = v_scales[8 * g + e / 4];
-        q[0] *= f.x;
-        q[1] *= f.y;
-        q[2] *= f.z;
-        q[3] *= f.w;
+        mul_pair(q[0], q[1], f.x, f.y);
+        mul_pair(q[2], q[3], f.z, f.w);
+        add_pair(t[0], t[1], q[0], q[1]);
+        add_pair(t[2], t[3], q[2], q[3]);
       }
       pw[g][e / 2] = pack2<KV == kKvBf16>(q[0], q[1]);
       pw[g][e / 2 + 1] = pack2<KV == kKvBf16>(q[2], q[3]);
     }
   }
-  return (l[0] + l[1]) + (l[2] + l[3]);
+  sum = (l[0] + l[1]) + (l[2] + l[3]);
+  packed = KV == kKvInt8 ? (t[0] + t[1]) + (t[2] + t[3]) : sum;
 }
 
 // Boxes first, first + step, ... of a unit's query rows, one thread: box b holds tokens
@@ -228,6 +252,7 @@ __device__ __forceinline__ void pf_load_q(const PrefillArgs& a, const CUtensorMa
   const int rows = a.box_tokens * a.group;
   const int mine = boxes > first ? (boxes - first + step - 1) / step : 0;
   mbar_arrive_expect_tx(bar, mine * (D / 64) * rows * 128);
+#pragma unroll 1
   for (int b = first; b < boxes; b += step) {
 #pragma unroll
     for (int hf = 0; hf < D / 64; ++hf)
@@ -262,11 +287,13 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Sh::kMisc);
   PfCtl* ctl = reinterpret_cast<PfCtl*>(smem + Sh::kMisc + 8);
   volatile int* last_piece = reinterpret_cast<volatile int*>(smem + Sh::kMisc + 16);   // [2]
+  volatile unsigned* row_bad = reinterpret_cast<volatile unsigned*>(smem + Sh::kMisc + 160);   // [8] merged rows
   long long* scratch = reinterpret_cast<long long*>(smem + Sh::kMisc + 32);            // [16]
   PfStart* start = reinterpret_cast<PfStart*>(smem + Sh::kMisc + 256);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
+#pragma unroll 1
     for (int k = 0; k < NS; ++k) {
       mbar_init(full + 8 * k, Sh::kWiden ? 128 : 4);
       mbar_init(empty + 8 * k, 2);
@@ -281,8 +308,10 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
       mbar_init(o_done + 8 * i, 1);
       mbar_init(turn + 8 * i, 1);
     }
+#pragma unroll 1
     for (int i = 0; i < Sh::kScaleRing; ++i) mbar_init(sc_full + 8 * i, 128);
     mbar_init(final_bar, 2);
+#pragma unroll 1
     for (int i = 0; i < kPfRing; ++i) {
       mbar_init(pc_full + 8 * i, 1);
       mbar_init(pc_empty + 8 * i, Sh::kReaders);
@@ -354,7 +383,10 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
         const int limit = ru < pc->rows ? pc->past + pc->j0 + tok + 1 : 0;
         const int limit0 = pc->past + pc->j0 + tok0 + 1;
         float m = -INFINITY, l = 0.f;
-        for (bool first = true; k < kb; ++k, ++cnt, ++nth, first = false) {
+        int fresh = 1;   // 1 in the piece's first tile; opaque, or the loop body is compiled twice
+        for (; k < kb; ++k, ++cnt, ++nth, fresh = 0) {
+          asm volatile("" : "+r"(fresh));
+          const bool first = fresh != 0;
           const int p0 = k * kPfTile;
           wait(bar_s, cnt & 1);
           const uint32_t slot = nth % Sh::kScaleRing;
@@ -363,65 +395,62 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
           tc_fence_after_sync();
           // Weights against the running maximum as it stands. Whether it may stand is seen from
           // their sum: a score over it by more than the slack shows as a sum over 2^slack (a tile's
-          // 128 weights of at most 1 never do), and a row with no maximum yet is known. Then, in a
-          // second round from the same scores, the maximum is found and moves. (Finding it first in
-          // every tile cost 300 to 400 of the 1350 cycles between a tile's scores and weights.)
-          uint32_t pw[4][16];
-          const bool live = limit > p0;   // the row sees positions of this tile
+          // 128 weights of at most 1 never do; of an INT8 cache the packed products must stay in
+          // fp16's range), and a row with no maximum yet is known. Then, in a second round from the
+          // same scores, the maximum is found and moves. (Finding it first in every tile cost 300
+          // to 400 of the 1350 cycles between a tile's scores and weights.)
+          const float4* k_scales = reinterpret_cast<const float4*>(smem + Sh::kScales) + slot * 64;
           const bool masked = p0 + kPfTile > limit0;
-          const float4* scales4 = reinterpret_cast<const float4*>(smem + Sh::kScales) + slot * 64;
-          float ls = 0.f;
-          bool settle = true;
-          if (KV != kKvInt8 && !first) {
+          uint32_t pw[4][16];
+          float ls, packed;
+          auto round = [&](bool settle) {
             uint32_t sv[4][32];   // 32 scores each
             tmem_ld128(s_col, sv[0], sv[1], sv[2], sv[3]);
             if (__builtin_expect(masked, 0)) {
               __syncwarp();   // keeps this a branch: as predicated selects it would run in every tile
               pf_mask(sv, limit - p0);
             }
-            ls = pf_weights<KV>(sv, pw, c, Sh::kShift - (m == -INFINITY ? 0.f : m), scales4 + 32);
-            settle = __any_sync(0xffffffffu, live && (!(ls <= Sh::kMostSum) || m == -INFINITY));
-          }
-          if (__builtin_expect(settle, KV == kKvInt8)) {
-            uint32_t sv[4][32];
-            tmem_ld128(s_col, sv[0], sv[1], sv[2], sv[3]);
-            if constexpr (KV == kKvInt8) {
-#pragma unroll
-              for (int g = 0; g < 4; ++g) {
-#pragma unroll
-                for (int e = 0; e < 32; e += 4) {
-                  const float4 f = scales4[8 * g + e / 4];
-                  sv[g][e] = __float_as_uint(__uint_as_float(sv[g][e]) * f.x);
-                  sv[g][e + 1] = __float_as_uint(__uint_as_float(sv[g][e + 1]) * f.y);
-                  sv[g][e + 2] = __float_as_uint(__uint_as_float(sv[g][e + 2]) * f.z);
-                  sv[g][e + 3] = __float_as_uint(__uint_as_float(sv[g][e + 3]) * f.w);
-                }
-              }
-            }
-            if (masked) {
-              __syncwarp();
-              pf_mask(sv, limit - p0);
-            }
-            const float mx = c * pf_max(sv);
-            const bool need = mx > m + Sh::kSlack;
-            if (__any_sync(0xffffffffu, need)) {
-              const float mn = need ? mx : m;
-              const float alpha = need ? fast_exp2(m - mn) : 1.f;   // 0 from -inf
-              m = mn;
-              l *= alpha;
-              if (!first) {
-                // Products complete in issue order: these scores were issued behind the last P V.
+            if (__builtin_expect(settle, 0)) {
+              const float mx = pf_max<KV>(sv, c, k_scales);
+              const bool need = mx > m + Sh::kSlack;
+              if (__any_sync(0xffffffffu, need)) {
+                const float mn = need ? mx : m;
+                const float alpha = need ? fast_exp2(m - mn) : 1.f;   // 0 from -inf
+                m = mn;
+                l *= alpha;
+                if (!first) {
+                  // Products complete in issue order: these scores were issued behind the last P V.
 #pragma unroll 1
-                for (int e = 0; e < D; e += 16) {
-                  uint32_t ov[16];
-                  tmem_ld16(o_col + e, ov);
+                  for (int e = 0; e < D; e += 16) {
+                    uint32_t ov[16];
+                    tmem_ld16(o_col + e, ov);
 #pragma unroll
-                  for (int x = 0; x < 16; ++x) ov[x] = __float_as_uint(__uint_as_float(ov[x]) * alpha);
-                  tmem_st16(o_col + e, ov);
+                    for (int x = 0; x < 16; ++x) ov[x] = __float_as_uint(__uint_as_float(ov[x]) * alpha);
+                    tmem_st16(o_col + e, ov);
+                  }
                 }
               }
             }
-            ls = pf_weights<KV>(sv, pw, c, Sh::kShift - (m == -INFINITY ? 0.f : m), scales4 + 32);
+            pf_weights<KV>(sv, pw, c, Sh::kShift - (m == -INFINITY ? 0.f : m), k_scales, k_scales + 32, ls, packed);
+          };
+          // (only rows that see positions of this tile ask for a second round)
+          auto moves = [&] {
+            return __any_sync(0xffffffffu, limit > p0 && (!(packed <= Sh::kMostSum) || m == -INFINITY)) != 0;
+          };
+          if constexpr (KV == kKvInt8) {
+            // one copy of the code: two of this longer one spill registers
+            for (int again = fresh;; again = 1) {
+              asm volatile("" : "+r"(again));
+              round(again != 0);
+              if (again || !moves()) break;
+            }
+          } else {
+            bool settle = true;
+            if (!first) {
+              round(false);
+              settle = moves();
+            }
+            if (__builtin_expect(settle, 0)) round(true);
           }
           l += ls;
 #pragma unroll
@@ -511,49 +540,80 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
           const bool mine = last_piece[i] != 0 && alive;
           named_bar_sync(1 + i, 128);   // read before the next piece's flag
           if (mine) {
+            // Items of 8 dimensions of one row, all real rows of the tile, spread over the 128
+            // threads (a unit of few rows is spread too). A trip to L2 per item is what it costs, so
+            // two items and four pieces go at a time.
             fence_acq_rel_gpu();
-            if (real) {
-              float M = -INFINITY;
-              #pragma unroll 1
-              for (int p = 0; p < pieces; ++p) M = fmaxf(M, __ldcg(slot_of(p) + r));
-              const float mu = M == -INFINITY ? 0.f : M;
-              float L = 0.f;
+            const int rows = min(pc->rows - 128 * i, 128), items = rows * (D / 8);
+            if (r < 4) row_bad[4 * i + r] = 0;
+            named_bar_sync(1 + i, 128);
+            const size_t step = 2 * static_cast<size_t>(a.slot_tiles) * slot_sz;
+            const float* s0 = slot_of(0);
+            const float* s1 = slot_of(1);   // pieces 1, 2, ... are `step` apart
+            const int row0 = pc->qb + pc->j0, head0 = pc->h * a.group;
 #pragma unroll 1
-              for (int p = 0; p < pieces; ++p)
-                L += __ldcg(slot_of(p) + 128 + r) * fast_exp2(__ldcg(slot_of(p) + r) - mu);
-              const float inv = L > 0.f ? 1.f / L : 0.f;
-              float bad = L == 0.f && limit > 0 ? NAN : 0.f;
+            for (int it = r; it < items; it += 256) {
+              float M[2] = {-INFINITY, -INFINITY}, L[2] = {0.f, 0.f}, o[2][8] = {};
 #pragma unroll 1
-              for (int e = 0; e < D; e += 16) {
-                float o[16];
+              for (int p0 = 0; p0 < pieces; p0 += 4) {
+                float m4[2][4], l4[2][4];
+                float4 f[2][4][2];
 #pragma unroll
-                for (int x = 0; x < 16; ++x) o[x] = 0.f;
-#pragma unroll 1
-                for (int p = 0; p < pieces; ++p) {
-                  const float* sl = slot_of(p);
-                  const float wp = fast_exp2(__ldcg(sl + r) - mu);
-                  const float4* src0 = reinterpret_cast<const float4*>(sl + 256 + (e / 8 * 128 + r) * 8);
-                  const float4* src1 = src0 + 256;
-                  const float4 f[4] = {__ldcg(src0), __ldcg(src0 + 1), __ldcg(src1), __ldcg(src1 + 1)};
+                for (int q = 0; q < 2; ++q) {
+                  const int id = min(it + 128 * q, items - 1), ch = id / rows, rr = id - ch * rows;
 #pragma unroll
-                  for (int x = 0; x < 4; ++x) {
-                    o[4 * x] = fmaf(wp, f[x].x, o[4 * x]);
-                    o[4 * x + 1] = fmaf(wp, f[x].y, o[4 * x + 1]);
-                    o[4 * x + 2] = fmaf(wp, f[x].z, o[4 * x + 2]);
-                    o[4 * x + 3] = fmaf(wp, f[x].w, o[4 * x + 3]);
+                  for (int p = 0; p < 4; ++p) {
+                    const int pp = min(p0 + p, pieces - 1);   // past the last: read again, weight 0
+                    const float* sl = pp == 0 ? s0 : s1 + (pp - 1) * step;
+                    const float4* src = reinterpret_cast<const float4*>(sl + 256 + (ch * 128 + rr) * 8);
+                    m4[q][p] = p0 + p < pieces ? sl[rr] : -INFINITY;
+                    l4[q][p] = p0 + p < pieces ? sl[128 + rr] : 0.f;
+                    f[q][p][0] = src[0];
+                    f[q][p][1] = src[1];
                   }
                 }
-                uint32_t y[8];
 #pragma unroll
-                for (int x = 0; x < 16; x += 2) {
-                  bad = fmaf(o[x], 0.f, fmaf(o[x + 1], 0.f, bad));
-                  y[x / 2] = pack2<Sh::kBf16>(o[x] * inv, o[x + 1] * inv);
+                for (int q = 0; q < 2; ++q) {
+                  const float Mn = fmaxf(M[q], fmaxf(fmaxf(m4[q][0], m4[q][1]), fmaxf(m4[q][2], m4[q][3])));
+                  const float mu = Mn == -INFINITY ? 0.f : Mn;
+                  const float al = fast_exp2(M[q] - mu);
+                  M[q] = Mn;
+                  L[q] *= al;
+#pragma unroll
+                  for (int x = 0; x < 8; ++x) o[q][x] *= al;
+#pragma unroll
+                  for (int p = 0; p < 4; ++p) {
+                    if (p0 + p >= pieces) break;
+                    const float wp = fast_exp2(m4[q][p] - mu);
+                    L[q] = fmaf(l4[q][p], wp, L[q]);
+                    const float* fv = reinterpret_cast<const float*>(f[q][p]);
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) o[q][x] = fmaf(wp, fv[x], o[q][x]);
+                  }
                 }
-                *reinterpret_cast<uint4*>(dst + e) = make_uint4(y[0], y[1], y[2], y[3]);
-                *reinterpret_cast<uint4*>(dst + e + 8) = make_uint4(y[4], y[5], y[6], y[7]);
               }
-              odd = !(bad == 0.f && L < INFINITY);
+#pragma unroll
+              for (int q = 0; q < 2; ++q) {
+                const int id = it + 128 * q, ch = id / rows, rr = id - ch * rows;
+                if (id >= items) break;
+                const float inv = L[q] > 0.f ? 1.f / L[q] : 0.f;
+                const int u = 128 * i + rr, j = u / a.group;
+                float bad = L[q] == 0.f && pc->past + pc->j0 + j >= 0 ? NAN : L[q] - L[q];
+                uint32_t y[4];
+#pragma unroll
+                for (int x = 0; x < 8; x += 2) {
+                  bad = fmaf(o[q][x], 0.f, fmaf(o[q][x + 1], 0.f, bad));
+                  y[x / 2] = pack2<Sh::kBf16>(o[q][x] * inv, o[q][x + 1] * inv);
+                }
+                if (bad != 0.f) atomicOr(const_cast<unsigned*>(row_bad) + 4 * i + (rr >> 5), 1u << (rr & 31));
+                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) +
+                                          (static_cast<size_t>(row0 + j) * a.num_q_heads + head0 + u - j * a.group) * D +
+                                          8 * ch) = make_uint4(y[0], y[1], y[2], y[3]);
+              }
             }
+            __threadfence_block();
+            named_bar_sync(1 + i, 128);
+            odd = (row_bad[4 * i + (warp & 3)] >> lane) & 1u;
           }
         }
         __syncwarp();
@@ -585,6 +645,7 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
           const int token = pc->qb + pc->j0;
           __syncwarp();
           if (lane == 0) piece_done(piece);
+#pragma unroll 1
           for (int k = ka; k < klast; ++k) {
             // Rows of both blocks: lanes 0 and 1 look them up.
             int mine = total_rows;   // wholly past the end: the copy fills zeros
@@ -603,6 +664,7 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
                 ok = piece == 0 || pf_wait(q_empty, (piece - 1) & 1, ctl);
                 if (ok) pf_load_q<D>(a, &tm_q, base, q_full, h * a.group, token, boxes, x, 4);
               }
+#pragma unroll 1
               for (int v = 0; v < 2 && ok; ++v) {
                 if (st >= NS && !pf_wait(empty + 8 * stage, round ^ 1, ctl)) {
                   ok = false;
@@ -646,6 +708,7 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
           // Drain: every copy issued into this CTA's shared memory lands before exit. (Where a role
           // gave up a barrier may stay incomplete; the first such wait outlasts any copy.)
           bool landed = piece == 0 || mbar_wait(q_full, (piece - 1) & 1);
+#pragma unroll 1
           for (uint32_t k = st > NS ? st - NS : 0; k < st && landed; ++k)
             landed = mbar_wait(full + 8 * (k % NS), (k / NS) & 1);
         }
@@ -687,13 +750,16 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
                   else if (a.status) atomicOr(a.status, kDevBadBlock);
                 }
               }
-              float scale = 0.f;
+              float scale = v ? 0.f : 1.f;
               if constexpr (KV == kKvInt8) {
                 const int p = k * kPfTile + wt;
                 if (p < ctx) {
                   const int b = bt[p >> 4];
                   if (static_cast<unsigned>(b) < static_cast<unsigned>(a.num_blocks))
-                    scale = a.scales[(static_cast<size_t>(b) * a.num_kv_heads + h) * 32 + 16 * v + (p & 15)];
+                    scale = a.scales[(static_cast<size_t>(b) * a.num_kv_heads + h) * 32 + 16 * v + (p & 15)] *
+                            (v ? 1.f : a.scale_log2);
+                  // a masked score, -inf, must stay that times an all-zero row's K scale
+                  if (v == 0 && scale == 0.f) scale = 1e-30f;
                 }
               }
               const uint32_t stage = st % NS, round = st / NS;
@@ -800,7 +866,11 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
               mbar_arrive(q_empty);
             }
             next_stage();
-            for (bool first = true; k < klast; ++k, first = false) {
+            int fresh = 1;   // 1 at the piece's first tile; opaque, or the loop body is compiled twice
+#pragma unroll 1
+            for (; k < klast; ++k, fresh = 0) {
+              asm volatile("" : "+r"(fresh));
+              const bool first = fresh != 0;
               const uint32_t vs = stage;
               if (!wait(full + 8 * vs, round)) break;
               next_stage();
@@ -873,6 +943,7 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
             if (!ok) break;
             const int r0 = ctx - tail * kPfTile, r1 = (r0 + 15) & ~15;
             uint8_t* vt = smem + Sh::kRing + vs * Sh::kStageBytes;
+#pragma unroll 1
             for (int x = lane; x < (r1 - r0) * Sh::kHalves * 8; x += 32) {
               const int row = r0 + x / (Sh::kHalves * 8), ch = x % (Sh::kHalves * 8);
               *reinterpret_cast<uint4*>(vt + (row >> 4) * Sh::kVBlockBytes + (ch >> 3) * Sh::kVHalfStep +

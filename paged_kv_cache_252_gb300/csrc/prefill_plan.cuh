@@ -6,7 +6,10 @@
 // tile; a unit is kUnitCost positions (its query load and output) plus the positions its
 // last row sees. Every CTA takes an equal stretch of the line; tile k of a unit (positions
 // 128k .. 128k + 127) belongs to the CTA whose stretch holds its first position. A unit
-// cut by a stretch's end becomes pieces that are merged by the last to finish.
+// cut by a stretch's end becomes pieces that are merged by the last to finish. While stretches
+// are short (kPfWholeShare) a unit of at most kPfWhole positions is not cut: all of it belongs
+// to the CTA whose stretch holds its start, since writing and merging pieces takes as long as some
+// five tiles (eight prompts of 512 tokens: 45 us against 59).
 #pragma once
 
 #include <cuda_runtime.h>
@@ -20,8 +23,11 @@ namespace pkv {
 
 constexpr int kPfRows = 256;          // query rows of a unit: two tiles of the MMA's M
 constexpr int kPfTile = 128;          // positions of a KV tile
-constexpr int kPfUnitCost = 128;      // a unit's fixed cost, in positions
-constexpr int kPfMinShare = 2 * kPfTile + kPfUnitCost;   // at least one whole tile a piece
+// A unit's fixed cost, in positions (128 / 256 / 384 / 512 gave an 8192-token bf16 prompt 437 /
+// 405 / 378 / 383 us).
+constexpr int kPfUnitCost = 384;
+constexpr int kPfWhole = 8 * kPfTile, kPfWholeShare = 2400;
+constexpr int kPfMinShare = 3 * kPfTile + kPfUnitCost;   // where units are cut: at least one whole tile a piece
 
 // Tokens of one TMA box of query rows, and of a unit (whole boxes). Boxes start on the
 // swizzle's 8-row atoms, 32 rows or the next possible number each, so that a short unit
@@ -112,8 +118,12 @@ __device__ inline bool pf_piece(const PfWalk& w, volatile PfPiece* to) {
   const int j0 = w.p.t * qt, rows = min(qt, w.p.n - j0) * G;
   const int k_all = (w.len() + kPfTile - 1) / kPfTile;
   const long long x0 = w.st.b0 - w.p.ub - kPfUnitCost, x1 = w.st.b1 - w.p.ub - kPfUnitCost;
-  const int ka = x0 <= 0 ? 0 : static_cast<int>((x0 + kPfTile - 1) / kPfTile);
-  const int kx = x1 <= 0 ? 0 : static_cast<int>(min((x1 + kPfTile - 1) / kPfTile, static_cast<long long>(k_all)));
+  int ka = x0 <= 0 ? 0 : static_cast<int>((x0 + kPfTile - 1) / kPfTile);
+  int kx = x1 <= 0 ? 0 : static_cast<int>(min((x1 + kPfTile - 1) / kPfTile, static_cast<long long>(k_all)));
+  if (w.len() <= kPfWhole && w.st.share < kPfWholeShare) {
+    ka = 0;
+    kx = w.p.ub >= w.st.b0 ? k_all : 0;   // (the walk passes no unit that starts behind the stretch)
+  }
   int kend[2] = {k_all, 0};   // tiles of the whole unit row tile i needs
   if (rows > 128) {
     kend[0] = (w.pastp() + j0 + 127 / G + 1 + kPfTile - 1) / kPfTile;
@@ -158,31 +168,35 @@ __device__ inline void pf_plan(const PrefillArgs& a, long long* scratch, PfStart
   const int s0 = tid * per, s1 = min(s0 + per, a.num_seqs);
   if (tid == 0) st->any = 0;
   long long mine = 0;
-  bool bad = false;
+  bool bad = false, cut = false;
+#pragma unroll 1
   for (int s = s0; s < s1; ++s) {
     const PrefillSeq p = prefill_seq(a, s);
     bad |= p.bad;
+    cut |= p.n > 0 && max(p.ctx, p.n) > kPfWhole;   // its longest unit
     mine += a.num_kv_heads * pf_head_len(p.n, max(p.past(), 0), a.unit_tokens);
   }
   if (bad && blockIdx.x == 0 && a.status) atomicOr(a.status, kDevBadCtx);
   long long incl = mine;
-#pragma unroll
+#pragma unroll 1
   for (int o = 1; o < 32; o <<= 1) {
     const long long v = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += v;
   }
   if (lane == 31) scratch[warp] = incl;
-  __syncthreads();
+  cut = __syncthreads_or(cut);
   long long total = 0, excl = incl - mine;
+#pragma unroll 1
   for (int w = 0; w < nw; ++w) {
     if (w < warp) excl += scratch[w];
     total += scratch[w];
   }
   long long share = (total + gridDim.x - 1) / gridDim.x;
-  if (share < kPfMinShare) share = kPfMinShare;
+  if (cut && share < kPfMinShare) share = kPfMinShare;
   const long long b0 = static_cast<long long>(blockIdx.x) * share;
   if (b0 < total && excl <= b0 && b0 < excl + mine) {
     long long at = excl;
+#pragma unroll 1
     for (int s = s0; s < s1; ++s) {
       const PrefillSeq p = prefill_seq(a, s);
       const int pastp = max(p.past(), 0), qt = a.unit_tokens;
@@ -196,6 +210,7 @@ __device__ inline void pf_plan(const PrefillArgs& a, long long* scratch, PfStart
       // the unit that holds position rem: units before t take t (cost + pastp) + qt t (t + 1) / 2
       const long long c = kPfUnitCost + pastp;
       int lo = 0, hi = (p.n + qt - 1) / qt - 1;
+#pragma unroll 1
       while (lo < hi) {
         const long long t = (lo + hi + 1) / 2;
         if (t * c + qt * (t * (t + 1) / 2) <= rem) lo = static_cast<int>(t);

@@ -108,6 +108,7 @@ __device__ __forceinline__ void prefill_row(const PrefillArgs& a, int s, int row
   float m = -INFINITY, l = 0.f, o[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.f;
+#pragma unroll 1
   for (int p0 = 0; p0 < limit; p0 += 32) {
     const int p = p0 + lane;
     float x = -INFINITY, sv = 1.f;
@@ -136,7 +137,7 @@ __device__ __forceinline__ void prefill_row(const PrefillArgs& a, int s, int row
     }
     float mx = x;
     bool nan = x != x;
-#pragma unroll
+#pragma unroll 1
     for (int k = 16; k > 0; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
     nan = __any_sync(0xffffffffu, nan);
     const float mn = fmaxf(m, mx);
@@ -144,7 +145,7 @@ __device__ __forceinline__ void prefill_row(const PrefillArgs& a, int s, int row
     const float alpha = exp2f(m - mu), w = p < limit ? exp2f(x - mu) : 0.f;
     m = mn;
     float sum = w;
-#pragma unroll
+#pragma unroll 1
     for (int k = 16; k > 0; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
     l = l * alpha + sum;
 #pragma unroll
