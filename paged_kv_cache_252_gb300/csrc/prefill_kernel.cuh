@@ -80,7 +80,8 @@ struct PfShape {
   static constexpr int kScaleRing = kStages;
   // Shared memory from a 1024-aligned base.
   static constexpr uint32_t kRing = kQBytes;
-  static constexpr uint32_t kScales = kRing + kStages * kStageBytes;   // INT8: [kScaleRing][K, V][128] floats
+  static constexpr uint32_t kRaw = kRing + kStages * kStageBytes;      // one-byte caches: three parts
+  static constexpr uint32_t kScales = kRaw + (kWiden ? 3 * 8192 : 0);   // INT8: [kScaleRing][K, V][128] floats
   static constexpr uint32_t kBars = kScales + (KV == kKvInt8 ? kScaleRing * 2 * kPfTile * 4 : 0);
   static constexpr uint32_t kMisc = kBars + (4 * kStages + 11 + 2 * kPfRing + kScaleRing) * 8;
   static constexpr uint32_t kPieces = kMisc + 256 + sizeof(PfStart);   // ring of kPfRing
@@ -715,13 +716,30 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
         __syncwarp();
       } else {
         // ------------------------- widening loader (one-byte caches) --------------------
+        // Parts of 8 KB (half a tile of head size 128, a tile of 64) go through a ring of three raw
+        // buffers, copied asynchronously; each thread copies what it converts itself, so the
+        // ring needs no barrier and a part in flight no registers. A thread's rows are the
+        // same in every block, so its addresses are constants beside the block's.
         constexpr int LPR = D / 16;               // lanes of a row (16 bytes each)
-        constexpr int RPW = 32 / LPR;             // rows of a warp's load
-        constexpr int NL = kPfTile / (4 * RPW);   // loads of a thread per tile
+        constexpr int RPW = 32 / LPR;             // rows of a warp's copy
+        constexpr int NL = 4;                     // copies of a thread per part
+        constexpr int kParts = D / 64;            // parts of a tile's K or V
+        constexpr int BPC = RPW * 4 / kBlockSize; // blocks the four warps cover in one copy
         const int wi = warp - 12, wt = tid - 384;
-        const int cc = lane % LPR;
-        uint32_t st = 0;
-        uint32_t tiles = 0;
+        const int cc = lane % LPR, rw = wi * RPW + lane / LPR;
+        const int blk0 = rw / kBlockSize, rb = rw % kBlockSize;   // block of a copy, row of the block
+        const uint8_t* k_base = static_cast<const uint8_t*>(a.k_cache) + rb * D + 16 * cc;
+        const uint8_t* v_base = static_cast<const uint8_t*>(a.v_cache) + rb * D + 16 * cc;
+        uint8_t* raw = smem + Sh::kRaw + wt * 16;
+        const uint32_t raw_s = smem_addr(raw);
+        // Elements 16 cc .. 16 cc + 15: chunks 2 (cc % 4), + 1 of half cc / 4. The upper half's
+        // lanes write their second chunk first, so that a row's eight lanes cover eight chunks
+        // (all banks) in each store.
+        const bool upper = (cc >> 2) != 0;
+        const int c0 = 2 * (cc & 3) + (cc >> 2), c1 = 2 * (cc & 3) + 1 - (cc >> 2);
+        uint8_t* out0 = smem + Sh::kRing + (cc >> 2) * Sh::kHalfBytes + rw * 128;
+        const int o0 = (c0 ^ (rw & 7)) << 4, o1 = (c1 ^ (rw & 7)) << 4;
+        uint32_t stage = 0, round = 0, uses = 0, tiles = 0, put_slot = 0, get_slot = 0;
         bool alive = true;
         for (uint32_t np = 0; alive; ++np) {
           alive = __all_sync(0xffffffffu, piece_ready(np));
@@ -731,68 +749,110 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
           const int ctx = pc->ctx, h = pc->h, ka = pc->ka, klast = pc->klast;
           __syncwarp();
           if (lane == 0) piece_done(np);
-          for (int k = ka; k < klast && alive; ++k, ++tiles) {
-#pragma unroll 1
-            for (int v = 0; v < 2; ++v, ++st) {
-              const uint8_t* cache = static_cast<const uint8_t*>(v ? a.v_cache : a.k_cache);
-              uint4 x[NL];
+          // Lane b < 8: the id of block b of tile k (-1 behind the context), and what it names as a
+          // (block, head) tile, -1 where it is out of range and reads as zeros. The id is looked at
+          // a tile after it was asked for.
+          auto id_of = [&](int k) {
+            const int p = k * kPfTile + lane * kBlockSize;
+            return lane < kPfTile / kBlockSize && p < ctx && k < klast ? bt[p >> 4] : -1;
+          };
+          auto tile_of = [&](int id, int k) {
+            if (static_cast<unsigned>(id) < static_cast<unsigned>(a.num_blocks)) return id * a.num_kv_heads + h;
+            if (lane < kPfTile / kBlockSize && k * kPfTile + lane * kBlockSize < ctx && k < klast && a.status)
+              atomicOr(a.status, kDevBadBlock);
+            return -1;
+          };
+          // fetch() copies the parts in order (tile, K then V, part), nothing past the end, so that
+          // groups count alike. It runs kAhead parts ahead, block ids a tile ahead of it.
+          int ids = tile_of(id_of(ka), ka), id_next = id_of(ka + 1);
+          int fk = ka, fv = 0, fp = 0;
+          float scale_k = 0.f, scale_v = 0.f;
+          auto fetch = [&] {
+            if (fk < klast) {
+              const uint8_t* cache = fv ? v_base : k_base;
+              const uint32_t dst = raw_s + put_slot * 8192;
 #pragma unroll
               for (int q = 0; q < NL; ++q) {
-                const int row = (q * 4 + wi) * RPW + lane / LPR;
-                const int p = k * kPfTile + row;
-                x[q] = make_uint4(0u, 0u, 0u, 0u);
-                if constexpr (KV == kKvInt8) x[q] = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
-                if (p < ctx) {
-                  const int b = bt[p >> 4];
-                  if (static_cast<unsigned>(b) < static_cast<unsigned>(a.num_blocks))
-                    x[q] = __ldg(reinterpret_cast<const uint4*>(
-                        cache + ((static_cast<size_t>(b) * a.num_kv_heads + h) * kBlockSize + (p & 15)) * D + 16 * cc));
-                  else if (a.status) atomicOr(a.status, kDevBadBlock);
-                }
+                const int b = (fp * NL + q) * BPC + blk0;
+                const int t = __shfl_sync(0xffffffffu, ids, b);
+                const bool real = t >= 0 && fk * kPfTile + b * kBlockSize + rb < ctx;
+                cp_async_16(dst + q * 2048, cache + (real ? static_cast<size_t>(t) * (kBlockSize * D) : 0),
+                            real ? 16u : 0u);
               }
-              float scale = v ? 0.f : 1.f;
               if constexpr (KV == kKvInt8) {
-                const int p = k * kPfTile + wt;
-                if (p < ctx) {
-                  const int b = bt[p >> 4];
-                  if (static_cast<unsigned>(b) < static_cast<unsigned>(a.num_blocks))
-                    scale = a.scales[(static_cast<size_t>(b) * a.num_kv_heads + h) * 32 + 16 * v + (p & 15)] *
-                            (v ? 1.f : a.scale_log2);
-                  // a masked score, -inf, must stay that times an all-zero row's K scale
-                  if (v == 0 && scale == 0.f) scale = 1e-30f;
+                if (fp == 0) {
+                  // (a tile's K scale is written before the next tile's is fetched, V's likewise)
+                  const int t = __shfl_sync(0xffffffffu, ids, wt >> 4);
+                  float f = 0.f;
+                  if (t >= 0 && fk * kPfTile + wt < ctx)
+                    f = a.scales[static_cast<size_t>(t) * 32 + 16 * fv + (wt & 15)] * (fv ? 1.f : a.scale_log2);
+                  if (fv) scale_v = f;
+                  else scale_k = f;
                 }
               }
-              const uint32_t stage = st % NS, round = st / NS;
-              if (round > 0) {
-                const bool ok = pf_wait(empty + 8 * stage, (round - 1) & 1, ctl);
-                if (!__all_sync(0xffffffffu, ok)) {
-                  alive = false;
-                  ctl->abort = 1;
-                  if (lane == 0 && a.status) atomicOr(a.status, kDevTimeout);
-                  break;
+              if (++put_slot == 3) put_slot = 0;
+              if (++fp == kParts) {
+                fp = 0;
+                fv ^= 1;
+                if (fv == 0) {
+                  ++fk;
+                  ids = tile_of(id_next, fk);
+                  id_next = id_of(fk + 1);
                 }
               }
-              uint8_t* dst = smem + Sh::kRing + stage * Sh::kStageBytes;
+            }
+            cp_async_commit();
+          };
+          constexpr int kAhead = KV == kKvInt8 && kParts == 1 ? 2 : 3;
+#pragma unroll 1
+          for (int n = 0; n < kAhead; ++n) fetch();
+#pragma unroll 1
+          for (int n = 2 * kParts * ka; n < 2 * kParts * klast; ++n) {
+            const int part = n & (kParts - 1), v = (n / kParts) & 1;
+            if (part == 0 && uses >= NS) {
+              const bool ok = pf_wait(empty + 8 * stage, round ^ 1, ctl);
+              if (!__all_sync(0xffffffffu, ok)) {
+                alive = false;
+                ctl->abort = 1;
+                if (lane == 0 && a.status) atomicOr(a.status, kDevTimeout);
+                break;
+              }
+            }
+            cp_async_wait<kAhead - 1>();
+            const uint8_t* src = raw + get_slot * 8192;
+            uint8_t* dst = out0 + stage * Sh::kStageBytes + part * (kPfTile / kParts) * 128;
+            uint4 x[NL];
 #pragma unroll
-              for (int q = 0; q < NL; ++q) {
-                const int row = (q * 4 + wi) * RPW + lane / LPR;
-                uint4 lo, hi;
-                widen16<KV>(x[q], lo, hi);
-                // Elements 16 cc .. 16 cc + 15: chunks 2 (cc % 4), + 1 of half cc / 4. The upper
-                // half's lanes write their second chunk first, so that a row's eight lanes
-                // cover eight chunks (all banks) in each store.
-                uint8_t* d = dst + (cc >> 2) * Sh::kHalfBytes + row * 128;
-                const int c0 = 2 * (cc & 3) + (cc >> 2), c1 = 2 * (cc & 3) + 1 - (cc >> 2);
-                *reinterpret_cast<uint4*>(d + ((c0 ^ (row & 7)) << 4)) = (cc >> 2) ? hi : lo;
-                *reinterpret_cast<uint4*>(d + ((c1 ^ (row & 7)) << 4)) = (cc >> 2) ? lo : hi;
+            for (int q = 0; q < NL; ++q) x[q] = *reinterpret_cast<const uint4*>(src + q * 2048);
+#pragma unroll
+            for (int q = 0; q < NL; ++q) {
+              uint4 lo, hi;
+              widen16<KV>(x[q], lo, hi);
+              *reinterpret_cast<uint4*>(dst + q * (4 * RPW * 128) + o0) = upper ? hi : lo;
+              *reinterpret_cast<uint4*>(dst + q * (4 * RPW * 128) + o1) = upper ? lo : hi;
+            }
+            if (++get_slot == 3) get_slot = 0;
+            if (part == kParts - 1) {
+              if constexpr (KV == kKvInt8) {
+                // a masked score, -inf, must stay that times an all-zero row's K scale
+                const float f = v ? scale_v : (scale_k == 0.f ? 1e-30f : scale_k);
+                reinterpret_cast<float*>(smem + Sh::kScales)[tiles % Sh::kScaleRing * 2 * kPfTile + v * kPfTile + wt] = f;
               }
-              if constexpr (KV == kKvInt8)
-                reinterpret_cast<float*>(smem + Sh::kScales)[tiles % Sh::kScaleRing * 2 * kPfTile + v * kPfTile + wt] = scale;
               fence_proxy_async_smem();
               mbar_arrive(full + 8 * stage);
-              if (KV == kKvInt8 && v == 1) mbar_arrive(sc_full + 8 * (tiles % Sh::kScaleRing));
+              if (v == 1) {
+                if (KV == kKvInt8) mbar_arrive(sc_full + 8 * (tiles % Sh::kScaleRing));
+                ++tiles;
+              }
+              ++uses;
+              if (++stage == NS) {
+                stage = 0;
+                round ^= 1;
+              }
             }
+            fetch();
           }
+          cp_async_wait<0>();
         }
       }
     } else {
