@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import math
 import os
 import threading
 
@@ -659,10 +660,16 @@ def rotary_inv_freq(rotary_dim: int, base: float = 10000.0, *, scaling: str | No
     return torch.from_numpy(inv).to(device=device or "cuda"), attn
 
 
-def _same_device(ref, tensors):
-    for n, t in tensors:
-        if t is not None and t.device != ref.device:
-            raise PagedKVError(f"{n} is on {t.device}, not on {ref.device}")
+def _placed(names, tensors) -> int:
+    """The CUDA device that all of the tensors (None: not given) lie on, contiguous. The calls
+    that serve single steps check placement, types and shapes in few attribute reads each: on
+    the host they cost as much as the kernels."""
+    dev = tensors[0].get_device()
+    for n, t in zip(names, tensors):
+        if t is not None and (t.get_device() != dev or dev < 0 or not t.is_contiguous()):
+            _need_cuda_contig(n, t)
+            raise PagedKVError(f"{n} is on {t.device}, not on {tensors[0].device}")
+    return dev
 
 
 def _status_word(status):
@@ -670,37 +677,82 @@ def _status_word(status):
         raise PagedKVError("device_status must be an int32 tensor")
 
 
-def _head_rows(name, t, heads=None, head_size=None) -> int:
-    """Token stride of a [tokens, heads, head_size] tensor whose tokens hold contiguous heads."""
-    if not t.is_cuda:
-        raise PagedKVError(f"{name} must be a CUDA tensor")
-    if t.dim() != 3 or (heads is not None and int(t.shape[1]) != heads) or \
-            (head_size is not None and int(t.shape[2]) != head_size):
+def _head_rows(name, t, dev, heads, head_size) -> int:
+    """Token stride of a [tokens, heads, head_size] tensor whose tokens hold contiguous heads
+    (None: any size)."""
+    if t.get_device() != dev or dev < 0:
+        raise PagedKVError(f"{name} must be a CUDA tensor on the inputs' device")
+    shape = t.shape
+    if len(shape) != 3 or (heads is not None and shape[1] != heads) or \
+            (head_size is not None and shape[2] != head_size):
         raise PagedKVError(f"{name} must be [tokens, {heads or 'heads'}, {head_size or 'head_size'}], "
-                           f"got {tuple(t.shape)}")
-    H, D = int(t.shape[1]), int(t.shape[2])
-    if t.stride(2) != 1 or (H > 1 and t.stride(1) != D):
+                           f"got {tuple(shape)}")
+    T, H, D = shape
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (H > 1 and s1 != D):
         raise PagedKVError(f"the heads of a token of {name} must be contiguous")
-    stride = int(t.stride(0)) if int(t.shape[0]) > 1 else H * D
-    if stride < H * D or stride % 8:
+    if T <= 1:
+        return H * D
+    if s0 < H * D or s0 % 8:
         raise PagedKVError(f"the tokens of {name} must be at least a row apart, in multiples of 8 elements")
-    return stride
+    return s0
 
 
-def _rotary_inputs(x, positions, inv_freq, attn_factor):
-    for n, t in (("positions", positions), ("inv_freq", inv_freq)):
-        _need_cuda_contig(n, t)
-    if positions.dtype not in (torch.int32, torch.int64) or positions.dim() != 1 or \
-            int(positions.shape[0]) != int(x.shape[0]):
+_descs: dict = {}
+
+
+def _desc_of(k_cache, v_cache):
+    """A descriptor of the cache pair for the library (kept by its sizes), its KV heads and head size."""
+    shape = k_cache.shape
+    if v_cache.shape != shape or v_cache.dtype != k_cache.dtype:
+        raise PagedKVError("k_cache and v_cache must have the same shape and dtype")
+    if len(shape) != 4 or shape[2] != BLOCK_SIZE:
+        raise PagedKVError(f"cache must be [num_blocks, num_kv_heads, 16, head_size], got {tuple(shape)}")
+    nb, hkv, _, d = shape
+    ref = _descs.get((nb, hkv, d))
+    if ref is None:
+        if len(_descs) > 256:
+            _descs.clear()
+        ref = _descs[(nb, hkv, d)] = ctypes.byref(_CacheDesc(nb, BLOCK_SIZE, hkv, d))
+    return ref, hkv, d
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_of(stream, dev: int) -> int:
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(dev)
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+def _at(dev: int):
+    """The device context of a call: entered only when dev is not the current device."""
+    return _NOWHERE if torch.cuda.current_device() == dev else torch.cuda.device(dev)
+
+
+_NOWHERE = contextlib.nullcontext()
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _rotary_inputs(T, D, positions, inv_freq, attn_factor):
+    """Rotary dimension and bytes of a position, checked."""
+    pt = positions.dtype
+    if (pt is not torch.int64 and pt is not torch.int32) or positions.shape != (T,):
         raise PagedKVError("positions must be int32 or int64, one per token")
-    if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1:
+    if inv_freq.dtype is not torch.float64 or inv_freq.dim() != 1:
         raise PagedKVError("inv_freq must be float64 [rotary_dim / 2]")
-    if not np.isfinite(attn_factor):
+    if not math.isfinite(attn_factor):
         raise PagedKVError("attn_factor must be finite")
-    rd = 2 * int(inv_freq.shape[0])
-    if rd < 16 or rd % 16 or rd > int(x.shape[2]):
-        raise PagedKVError(f"rotary_dim = {rd} must be a multiple of 16, at most the head size {int(x.shape[2])}")
-    return rd, positions.element_size()
+    rd = 2 * inv_freq.shape[0]
+    if rd < 16 or rd % 16 or rd > D:
+        raise PagedKVError(f"rotary_dim = {rd} must be a multiple of 16, at most the head size {D}")
+    return rd, 8 if pt is torch.int64 else 4
 
 
 def rotary_embed(out, x, positions, inv_freq, *, interleaved: bool = False, attn_factor: float = 1.0,
@@ -708,18 +760,25 @@ def rotary_embed(out, x, positions, inv_freq, *, interleaved: bool = False, attn
     """Turn the first 2 * len(inv_freq) dimensions of x [T, H, D] (fp16 or bf16) by
     positions[t] * inv_freq[i], pairs (i, i + half) or (2i, 2i + 1), times attn_factor; the rest is
     copied. out may be x. ``inverse`` turns back (the gradient of the forward call)."""
-    xs, os_ = _head_rows("x", x), _head_rows("out", out, int(x.shape[1]), int(x.shape[2]))
-    if int(out.shape[0]) != int(x.shape[0]) or out.dtype != x.dtype:
+    dev = _placed(("positions", "inv_freq"), (positions, inv_freq))
+    xs = _head_rows("x", x, dev, None, None)
+    T, H, D = x.shape
+    os_ = _head_rows("out", out, dev, H, D)
+    if out.shape[0] != T or out.dtype is not x.dtype:
         raise PagedKVError("out must have the shape and dtype of x")
-    rd, pb = _rotary_inputs(x, positions, inv_freq, attn_factor)
-    _same_device(x, (("out", out), ("positions", positions), ("inv_freq", inv_freq)))
-    with _on_device(x.device):
-        rc = load_library().pkv_rotary_embed(
-            _ptr(out), os_, _ptr(x), xs, _src_code(x), int(x.shape[0]), int(x.shape[1]), int(x.shape[2]),
-            _ptr(positions), pb, _ptr(inv_freq), rd, int(bool(interleaved)), float(attn_factor),
-            int(bool(inverse)), _stream_handle(stream, x.device))
-    _check(rc, "rotary_embed")
+    rd, pb = _rotary_inputs(T, D, positions, inv_freq, attn_factor)
+    lib = _lib or load_library()
+    with _at(dev):
+        rc = lib.pkv_rotary_embed(
+            out.data_ptr(), os_, x.data_ptr(), xs, _src_code(x), T, H, D, positions.data_ptr(), pb,
+            inv_freq.data_ptr(), rd, 1 if interleaved else 0, attn_factor, 1 if inverse else 0,
+            _stream_of(stream, dev))
+    if rc:
+        _check(rc, "rotary_embed")
     return out
+
+
+_WRITE_NAMES = ("slot_mapping", "positions", "inv_freq", "k_cache", "v_cache", "scales", "device_status")
 
 
 def rotary_write(q_out, q, key, value, positions, slot_mapping, k_cache, v_cache, inv_freq, kv_dtype=None, *,
@@ -728,56 +787,54 @@ def rotary_write(q_out, q, key, value, positions, slot_mapping, k_cache, v_cache
     (which may be q), key [T, Hkv, D] turned and written with value to the slots of the cache.
     The inputs may be views of one packed QKV tensor (token strides of any multiple of 8).
     An INT8 cache takes its row scales."""
-    qs = _head_rows("q", q)
-    d = _pair(k_cache, v_cache)
-    Hkv, D = int(k_cache.shape[1]), int(k_cache.shape[3])
-    qos = _head_rows("q_out", q_out, int(q.shape[1]), D)
-    ks, vs = _head_rows("key", key, Hkv, D), _head_rows("value", value, Hkv, D)
-    for n, t in (("slot_mapping", slot_mapping), ("k_cache", k_cache), ("v_cache", v_cache)):
-        _need_cuda_contig(n, t)
-    T = int(q.shape[0])
-    if int(q.shape[2]) != D or any(int(t.shape[0]) != T for t in (q_out, key, value)):
-        raise PagedKVError("q, q_out, key and value must hold the same tokens at the cache's head size")
-    if not q.dtype == q_out.dtype == key.dtype == value.dtype:
+    dev = _placed(_WRITE_NAMES, (slot_mapping, positions, inv_freq, k_cache, v_cache, scales, device_status))
+    desc, Hkv, D = _desc_of(k_cache, v_cache)
+    qs = _head_rows("q", q, dev, None, D)
+    T, Hq, _ = q.shape
+    qos = _head_rows("q_out", q_out, dev, Hq, D)
+    ks, vs = _head_rows("key", key, dev, Hkv, D), _head_rows("value", value, dev, Hkv, D)
+    if q_out.shape[0] != T or key.shape[0] != T or value.shape[0] != T:
+        raise PagedKVError("q, q_out, key and value must hold the same tokens")
+    dt = q.dtype
+    if q_out.dtype is not dt or key.dtype is not dt or value.dtype is not dt:
         raise PagedKVError("q, q_out, key and value must share a dtype")
-    if slot_mapping.dtype != torch.int32 or slot_mapping.dim() != 1 or int(slot_mapping.shape[0]) != T:
+    if slot_mapping.dtype is not torch.int32 or slot_mapping.shape != (T,):
         raise PagedKVError("slot_mapping must be int32 with one slot per token")
-    rd, pb = _rotary_inputs(q, positions, inv_freq, attn_factor)
+    rd, pb = _rotary_inputs(T, D, positions, inv_freq, attn_factor)
     code = _kv_code(kv_dtype, k_cache)
     _int8_scales(code, k_cache, scales)
     _status_word(device_status)
-    _same_device(q, (("q_out", q_out), ("key", key), ("value", value), ("positions", positions),
-                     ("slot_mapping", slot_mapping), ("k_cache", k_cache), ("v_cache", v_cache),
-                     ("inv_freq", inv_freq), ("scales", scales), ("device_status", device_status)))
-    with _on_device(q.device):
-        rc = load_library().pkv_rotary_write(
-            _ptr(q_out), qos, _ptr(q), qs, _ptr(key), ks, _ptr(value), vs, _src_code(q), T, int(q.shape[1]),
-            _ptr(positions), pb, _ptr(slot_mapping), _ptr(inv_freq), rd, int(bool(interleaved)),
-            float(attn_factor), _ptr(k_cache), _ptr(v_cache), _ptr(scales), code, ctypes.byref(d),
-            _ptr(device_status), _stream_handle(stream, q.device))
-    _check(rc, "rotary_write")
+    lib = _lib or load_library()
+    with _at(dev):
+        rc = lib.pkv_rotary_write(
+            q_out.data_ptr(), qos, q.data_ptr(), qs, key.data_ptr(), ks, value.data_ptr(), vs, _src_code(q), T, Hq,
+            positions.data_ptr(), pb, slot_mapping.data_ptr(), inv_freq.data_ptr(), rd, 1 if interleaved else 0,
+            attn_factor, k_cache.data_ptr(), v_cache.data_ptr(), _addr(scales), code, desc, _addr(device_status),
+            _stream_of(stream, dev))
+    if rc:
+        _check(rc, "rotary_write")
     return q_out
 
 
 _prefill_workspaces: dict = {}
+_prefill_ws_bytes: dict = {}
 _PREFILL_COUNTER_BYTES = 4096   # the start of the workspace, where the split counters are
 
 
-def _prefill_workspace(nbytes: int, device, stream) -> torch.Tensor:
+def _prefill_workspace(nbytes: int, dev: int, stream) -> torch.Tensor:
     """Scratch of a prefill call: one buffer per (device, stream the call runs on), grown as
     needed. A call that is being captured gets a buffer of its own from the graph's memory
     pool (its counters cleared by a captured fill), so two graphs, or a graph and eager calls,
     never share one and a later growth takes nothing away from a captured graph."""
-    on = contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
-    with on:
+    with _NOWHERE if stream is None else torch.cuda.stream(stream):
         if torch.cuda.is_current_stream_capturing():
-            ws = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+            ws = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
             ws[:_PREFILL_COUNTER_BYTES].zero_()
             return ws
-        key = (str(device), torch.cuda.current_stream(device).cuda_stream)
+        key = (dev, _stream_of(stream, dev))
         ws = _prefill_workspaces.get(key)
-        if ws is None or ws.numel() < nbytes:
-            ws = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
+        if ws is None or ws.shape[0] < nbytes:
+            ws = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=dev)
             _prefill_workspaces[key] = ws
         return ws
 
@@ -790,6 +847,10 @@ def prefill_workspace_bytes(num_q_rows: int, num_seqs: int, num_q_heads: int, k_
                                                               ctypes.byref(d)))
 
 
+_PREFILL_NAMES = ("q", "out", "cu_q_lens", "k_cache", "v_cache", "block_tables", "context_lens", "scales", "workspace",
+                  "device_status")
+
+
 def paged_attention_prefill(out, q, cu_q_lens, k_cache, v_cache, block_tables, context_lens, scale: float,
                             kv_dtype=None, *, scales=None, workspace=None, device_status=None, stream=None):
     """Causal attention of every sequence's newest tokens over its blocks: whole prompts,
@@ -797,37 +858,54 @@ def paged_attention_prefill(out, q, cu_q_lens, k_cache, v_cache, block_tables, c
     owns rows cu_q_lens[s]..cu_q_lens[s+1]-1 of q/out [rows, Hq, D] (int32, on the device; any
     count from 0) and its token j sees positions <= context_lens[s] - n_s + j. An INT8 cache
     takes its row scales."""
-    for nm, t in (("out", out), ("q", q), ("cu_q_lens", cu_q_lens), ("k_cache", k_cache), ("v_cache", v_cache),
-                  ("block_tables", block_tables), ("context_lens", context_lens)):
-        _need_cuda_contig(nm, t)
-    if (block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32
-            or cu_q_lens.dtype != torch.int32):
+    dev = _placed(_PREFILL_NAMES, (q, out, cu_q_lens, k_cache, v_cache, block_tables, context_lens, scales, workspace,
+                                   device_status))
+    i32 = torch.int32
+    if block_tables.dtype is not i32 or context_lens.dtype is not i32 or cu_q_lens.dtype is not i32:
         raise PagedKVError("block_tables, context_lens and cu_q_lens must be int32")
-    d, S = _decode_shapes(out, q, k_cache, v_cache, block_tables, context_lens)
+    desc, Hkv, D = _desc_of(k_cache, v_cache)
+    shape = q.shape
+    if len(shape) != 3 or out.shape != shape or shape[2] != D:
+        raise PagedKVError(f"q and out must both be [rows, num_q_heads, {D}], got {tuple(shape)} and "
+                           f"{tuple(out.shape)}")
+    R, Hq, _ = shape
+    if context_lens.dim() != 1:
+        raise PagedKVError("context_lens must be 1-D [num_seqs]")
+    S = context_lens.shape[0]
+    tables = block_tables.shape
+    if len(tables) != 2 or tables[0] < S:
+        raise PagedKVError(f"block_tables must be [num_seqs, max_blocks_per_seq], got {tuple(tables)}")
+    if cu_q_lens.shape != (S + 1,):
+        raise PagedKVError("cu_q_lens must have num_seqs + 1 entries")
     code = _kv_code(kv_dtype, k_cache)
     want = torch.bfloat16 if code == KV_BF16 else torch.float16
-    if q.dtype != want or out.dtype != want:
+    if q.dtype is not want or out.dtype is not want:
         raise PagedKVError(f"q and out must be {want} over this cache")
-    if cu_q_lens.dim() != 1 or int(cu_q_lens.shape[0]) != S + 1:
-        raise PagedKVError("cu_q_lens must have num_seqs + 1 entries")
     _int8_scales(code, k_cache, scales)
     _status_word(device_status)
-    _same_device(q, (("out", out), ("cu_q_lens", cu_q_lens), ("k_cache", k_cache), ("v_cache", v_cache),
-                     ("block_tables", block_tables), ("context_lens", context_lens), ("scales", scales),
-                     ("workspace", workspace), ("device_status", device_status)))
-    R, Hq = int(q.shape[0]), int(q.shape[1])
-    lib = load_library()
-    with _on_device(q.device):
+    lib = _lib or load_library()
+    with _at(dev):
         if workspace is None:
-            need = int(lib.pkv_prefill_workspace_bytes(R, S, Hq, ctypes.byref(d)))
-            workspace = _prefill_workspace(need, q.device, stream)
+            # The size goes by the device, the head size and whether a unit may hold over 128 rows.
+            key = (dev, D, R * Hq > 128 * Hkv)
+            need = _prefill_ws_bytes.get(key)
+            if need is None:
+                need = int(lib.pkv_prefill_workspace_bytes(R, S, Hq, desc))
+                if need:
+                    _prefill_ws_bytes[key] = need
+            workspace = _prefill_workspace(need, dev, stream)
         rc = lib.pkv_paged_attention_prefill(
-            _ptr(out), _ptr(q), _ptr(cu_q_lens), R, S, Hq, _ptr(k_cache), _ptr(v_cache), _ptr(scales), code,
-            ctypes.byref(d), _ptr(block_tables), int(block_tables.shape[1]), _ptr(context_lens), float(scale),
-            _ptr(workspace), int(workspace.numel() * workspace.element_size()), _ptr(device_status),
-            _stream_handle(stream, q.device))
-    _check(rc, "paged_attention_prefill")
+            out.data_ptr(), q.data_ptr(), cu_q_lens.data_ptr(), R, S, Hq, k_cache.data_ptr(), v_cache.data_ptr(),
+            _addr(scales), code, desc, block_tables.data_ptr(), tables[1], context_lens.data_ptr(), scale,
+            workspace.data_ptr(), workspace.numel() * workspace.element_size(), _addr(device_status),
+            _stream_of(stream, dev))
+    if rc:
+        _check(rc, "paged_attention_prefill")
     return out
+
+
+_ACCEPT_NAMES = ("k_cache", "v_cache", "block_tables", "context_lens", "accepted", "num_accepted", "new_context_lens",
+                 "cu_q_lens", "scales", "device_status")
 
 
 def kv_cache_accept(k_cache, v_cache, block_tables, context_lens, accepted, num_accepted, new_context_lens,
@@ -838,41 +916,36 @@ def kv_cache_accept(k_cache, v_cache, block_tables, context_lens, accepted, num_
     rows read before any is written) and new_context_lens[s] = base + num_accepted[s]. n_s is
     max_q_per_seq, or from cu_q_lens. accepted: int32 [num_seqs, max_accepted]; new_context_lens
     may be None. An INT8 cache's row scales move along."""
-    for nm, t in (("k_cache", k_cache), ("v_cache", v_cache), ("block_tables", block_tables),
-                  ("context_lens", context_lens), ("accepted", accepted), ("num_accepted", num_accepted),
-                  ("new_context_lens", new_context_lens), ("cu_q_lens", cu_q_lens)):
-        if t is None and nm in ("new_context_lens", "cu_q_lens"):
-            continue
-        _need_cuda_contig(nm, t)
-        if nm not in ("k_cache", "v_cache") and t.dtype != torch.int32:
+    dev = _placed(_ACCEPT_NAMES, (k_cache, v_cache, block_tables, context_lens, accepted, num_accepted,
+                                  new_context_lens, cu_q_lens, scales, device_status))
+    for nm, t in (("block_tables", block_tables), ("context_lens", context_lens), ("accepted", accepted),
+                  ("num_accepted", num_accepted), ("new_context_lens", new_context_lens), ("cu_q_lens", cu_q_lens)):
+        if t is not None and t.dtype is not torch.int32:
             raise PagedKVError(f"{nm} must be int32")
-    d = _pair(k_cache, v_cache)
+    desc, _, _ = _desc_of(k_cache, v_cache)
     if context_lens.dim() != 1:
         raise PagedKVError("context_lens must be 1-D [num_seqs]")
-    S = int(context_lens.shape[0])
-    if block_tables.dim() != 2 or int(block_tables.shape[0]) < S:
-        raise PagedKVError(f"block_tables must be [num_seqs, max_blocks_per_seq], got {tuple(block_tables.shape)}")
-    if accepted.dim() != 2 or int(accepted.shape[0]) != S or num_accepted.dim() != 1 or \
-            int(num_accepted.shape[0]) != S:
+    S = context_lens.shape[0]
+    tables, acc = block_tables.shape, accepted.shape
+    if len(tables) != 2 or tables[0] < S:
+        raise PagedKVError(f"block_tables must be [num_seqs, max_blocks_per_seq], got {tuple(tables)}")
+    if len(acc) != 2 or acc[0] != S or num_accepted.shape != (S,):
         raise PagedKVError("accepted must be [num_seqs, max_accepted] and num_accepted [num_seqs]")
-    if new_context_lens is not None and (new_context_lens.dim() != 1 or int(new_context_lens.shape[0]) != S):
+    if new_context_lens is not None and new_context_lens.shape != (S,):
         raise PagedKVError("new_context_lens must be [num_seqs]")
-    if cu_q_lens is not None and (cu_q_lens.dim() != 1 or int(cu_q_lens.shape[0]) != S + 1):
+    if cu_q_lens is not None and cu_q_lens.shape != (S + 1,):
         raise PagedKVError("cu_q_lens must have num_seqs + 1 entries")
     code = _kv_code(kv_dtype, k_cache)
     _int8_scales(code, k_cache, scales)
     _status_word(device_status)
-    _same_device(k_cache, (("v_cache", v_cache), ("block_tables", block_tables), ("context_lens", context_lens),
-                           ("accepted", accepted), ("num_accepted", num_accepted),
-                           ("new_context_lens", new_context_lens), ("cu_q_lens", cu_q_lens), ("scales", scales),
-                           ("device_status", device_status)))
-    with _on_device(k_cache.device):
-        rc = load_library().pkv_kv_cache_accept(
-            _ptr(k_cache), _ptr(v_cache), _ptr(scales), code, ctypes.byref(d), _ptr(block_tables),
-            int(block_tables.shape[1]), _ptr(context_lens), _ptr(cu_q_lens), S, int(max_q_per_seq), _ptr(accepted),
-            int(accepted.shape[1]), _ptr(num_accepted), _ptr(new_context_lens), _ptr(device_status),
-            _stream_handle(stream, k_cache.device))
-    _check(rc, "kv_cache_accept")
+    lib = _lib or load_library()
+    with _at(dev):
+        rc = lib.pkv_kv_cache_accept(
+            k_cache.data_ptr(), v_cache.data_ptr(), _addr(scales), code, desc, block_tables.data_ptr(), tables[1],
+            context_lens.data_ptr(), _addr(cu_q_lens), S, int(max_q_per_seq), accepted.data_ptr(), acc[1],
+            num_accepted.data_ptr(), _addr(new_context_lens), _addr(device_status), _stream_of(stream, dev))
+    if rc:
+        _check(rc, "kv_cache_accept")
     return new_context_lens
 
 

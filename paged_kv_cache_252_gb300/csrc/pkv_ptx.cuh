@@ -199,6 +199,13 @@ __device__ __forceinline__ float lds_f32_early(uint32_t addr) {
   return v;
 }
 
+// The same for four floats at a 16-byte aligned address.
+__device__ __forceinline__ float4 lds_f4_early(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
+  return v;
+}
+
 // ---- warp-level matrix data movement ---------------------------------------------
 __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t& r0, uint32_t& r1, uint32_t& r2,
                                         uint32_t& r3) {

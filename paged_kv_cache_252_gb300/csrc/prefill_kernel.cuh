@@ -222,7 +222,8 @@ __device__ __forceinline__ void pf_weights(const uint32_t (&sv)[4][32], uint32_t
 #pragma unroll
     for (int e = 0; e < 32; e += 4) {
       float4 kc = make_float4(c, c, c, c);
-      if constexpr (KV == kKvInt8) kc = k_scales[8 * g + e / 4];
+      // (read where they are used: hoisted, the scales' registers spill)
+      if constexpr (KV == kKvInt8) kc = lds_f4_early(smem_addr(k_scales + 8 * g + e / 4));
       float q[4];
       fma_pair(q[0], q[1], __uint_as_float(sv[g][e]), __uint_as_float(sv[g][e + 1]), kc.x, kc.y, sub);
       fma_pair(q[2], q[3], __uint_as_float(sv[g][e + 2]), __uint_as_float(sv[g][e + 3]), kc.z, kc.w, sub);
@@ -231,7 +232,7 @@ __device__ __forceinline__ void pf_weights(const uint32_t (&sv)[4][32], uint32_t
       add_pair(l[0], l[1], q[0], q[1]);
       add_pair(l[2], l[3], q[2], q[3]);
       if constexpr (KV == kKvInt8) {
-        const float4 f = v_scales[8 * g + e / 4];
+        const float4 f = lds_f4_early(smem_addr(v_scales + 8 * g + e / 4));
         mul_pair(q[0], q[1], f.x, f.y);
         mul_pair(q[2], q[3], f.z, f.w);
         add_pair(t[0], t[1], q[0], q[1]);

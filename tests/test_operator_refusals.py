@@ -115,15 +115,14 @@ class _Reached(Exception):
 
 @pytest.fixture
 def stub(monkeypatch):
-    monkeypatch.setattr(api, "_need_cuda_contig", lambda name, t: None)
-    real = api._head_rows
-
+    """Host tensors stand in for CUDA ones, and the library is never reached."""
     class Cuda(torch.Tensor):
-        is_cuda = True
-
-    def rows(name, t, heads=None, head_size=None):
-        return real(name, t.as_subclass(Cuda), heads, head_size)
-    monkeypatch.setattr(api, "_head_rows", rows)
+        def get_device(self):
+            return 0
+    real = api._head_rows
+    monkeypatch.setattr(api, "_placed", lambda names, tensors: 0)
+    monkeypatch.setattr(api, "_head_rows", lambda n, t, dev, h, d: real(n, t.as_subclass(Cuda), dev, h, d))
+    monkeypatch.setattr(api, "_lib", None)
 
     def no_library():
         raise _Reached()
