@@ -93,24 +93,39 @@ template <int KV>
 __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const RotaryArgs a) {
   constexpr bool BF16 = KV == kKvBf16;
   __shared__ unsigned long long step[kRotaryMaxPairs];
-  __shared__ float2 cs[kRotaryMaxTokens * kRotaryMaxPairs];
+  __shared__ float2 cs2[2][kRotaryMaxTokens * kRotaryMaxPairs];
   const int tid = threadIdx.x, lane = tid & 31;
   const int pairs = a.rot_items * 8;
   pdl_wait_prior_grid();
-  // inv_freq / 2 pi modulo one turn, as a 64-bit fraction. (Both products round to 2^-53
-  // of their value, as an fp64 angle would.)
-  if (tid < pairs) {
-    const double turns = a.inv_freq[tid] * 0.15915494309189533577;
-    step[tid] = __double2ull_rn((turns - floor(turns)) * 18446744073709551616.0);
-  }
   const int heads = a.num_q_heads + 2 * a.num_kv_heads;
   const int per_token = heads << a.log_items_row;
   const int D = a.items_row * 16;
   const int second = a.interleaved ? 8 : a.rot_items * 8;   // distance of an item's second chunk
-  for (long long t0 = static_cast<long long>(blockIdx.x) * a.tile; t0 < a.num_tokens;
-       t0 += static_cast<long long>(gridDim.x) * a.tile) {
-    const int nt = static_cast<int>(a.num_tokens - t0 < a.tile ? a.num_tokens - t0 : a.tile);
-    __syncthreads();   // steps written; the last tile's cosines read
+  const long long stride = static_cast<long long>(gridDim.x) * a.tile;
+  auto tile_tokens = [&](long long t0) { return static_cast<int>(a.num_tokens - t0 < a.tile ? a.num_tokens - t0 : a.tile); };
+  // Items i0, i0 + 256, ... of the tile at t0: both chunks of each.
+  uint4 va[kRotaryBatch], vb[kRotaryBatch];
+  auto load = [&](long long t0, int total, int i0) {
+#pragma unroll
+    for (int b = 0; b < kRotaryBatch; ++b) {
+      const int i = i0 + b * kRotaryThreads;
+      if (i >= total) break;
+      const int row = i >> a.log_items_row, c = i & (a.items_row - 1);
+      const int t = row / heads, h = row - t * heads;
+      const uint16_t* src;
+      if (h < a.num_q_heads) src = a.q + (t0 + t) * a.q_stride + h * D;
+      else if (h < a.num_q_heads + a.num_kv_heads) src = a.key + (t0 + t) * a.key_stride + (h - a.num_q_heads) * D;
+      else src = a.value + (t0 + t) * a.value_stride + (h - a.num_q_heads - a.num_kv_heads) * D;
+      const bool turn = c < a.rot_items && h < a.num_q_heads + a.num_kv_heads;
+      const int o1 = turn && !a.interleaved ? 8 * c : 16 * c;
+      const int o2 = o1 + (turn ? second : 8);
+      va[b] = *reinterpret_cast<const uint4*>(src + o1);
+      vb[b] = *reinterpret_cast<const uint4*>(src + o2);
+    }
+  };
+  // The cosines and sines of the tile at t0.
+  auto angles = [&](long long t0, float2* cs) {
+    const int nt = tile_tokens(t0);
     for (int i = tid; i < nt * pairs; i += kRotaryThreads) {
       const int t = i / pairs, j = i - t * pairs;
       const long long p = a.pos64 ? static_cast<const long long*>(a.positions)[t0 + t]
@@ -120,26 +135,27 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const RotaryArgs
       sincospif(__ll2float_rn(phase) * 1.0842021724855044e-19f, &s, &c);   // 2^-63: half turns in [-1, 1]
       cs[t * pairs + j] = make_float2(c * a.factor, s * a.factor * a.sign);
     }
-    __syncthreads();
-    const int total = nt * per_token;
+  };
+  long long t0 = static_cast<long long>(blockIdx.x) * a.tile;
+  // A tile's first rows are under way while angles are worked out: the first tile's its own, a
+  // later one's the tile's behind it.
+  if (t0 < a.num_tokens) load(t0, tile_tokens(t0) * per_token, tid);
+  // inv_freq / 2 pi modulo one turn, as a 64-bit fraction. (Both products round to 2^-53
+  // of their value, as an fp64 angle would.)
+  if (tid < pairs) {
+    const double turns = a.inv_freq[tid] * 0.15915494309189533577;
+    step[tid] = __double2ull_rn((turns - floor(turns)) * 18446744073709551616.0);
+  }
+  __syncthreads();
+  int buf = 0;
+  if (t0 < a.num_tokens) angles(t0, cs2[0]);
+  for (; t0 < a.num_tokens; t0 += stride, buf ^= 1) {
+    __syncthreads();   // this tile's cosines are written, the last tile's read
+    if (t0 + stride < a.num_tokens) angles(t0 + stride, cs2[buf ^ 1]);
+    const float2* cs = cs2[buf];
+    const int total = tile_tokens(t0) * per_token;
     for (int i0 = tid; i0 < total; i0 += kRotaryThreads * kRotaryBatch) {
-      uint4 va[kRotaryBatch], vb[kRotaryBatch];
-#pragma unroll
-      for (int b = 0; b < kRotaryBatch; ++b) {
-        const int i = i0 + b * kRotaryThreads;
-        if (i >= total) break;
-        const int row = i >> a.log_items_row, c = i & (a.items_row - 1);
-        const int t = row / heads, h = row - t * heads;
-        const uint16_t* src;
-        if (h < a.num_q_heads) src = a.q + (t0 + t) * a.q_stride + h * D;
-        else if (h < a.num_q_heads + a.num_kv_heads) src = a.key + (t0 + t) * a.key_stride + (h - a.num_q_heads) * D;
-        else src = a.value + (t0 + t) * a.value_stride + (h - a.num_q_heads - a.num_kv_heads) * D;
-        const bool turn = c < a.rot_items && h < a.num_q_heads + a.num_kv_heads;
-        const int o1 = turn && !a.interleaved ? 8 * c : 16 * c;
-        const int o2 = o1 + (turn ? second : 8);
-        va[b] = *reinterpret_cast<const uint4*>(src + o1);
-        vb[b] = *reinterpret_cast<const uint4*>(src + o2);
-      }
+      if (i0 != tid) load(t0, total, i0);
 #pragma unroll
       for (int b = 0; b < kRotaryBatch; ++b) {
         const int i = i0 + b * kRotaryThreads;
@@ -235,6 +251,7 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const RotaryArgs
         }
       }
     }
+    if (t0 + stride < a.num_tokens) load(t0 + stride, tile_tokens(t0 + stride) * per_token, tid);
   }
   pdl_launch_dependents();
 }
@@ -279,16 +296,16 @@ int rotary_launch(RotaryArgs& a, const void* fn, void* stream) {
   if (int rc = device_sm_count(&sms)) return rc;
   const long long heads = a.num_q_heads + 2ll * a.num_kv_heads;
   if (heads * a.items_row * kRotaryMaxTokens >= (1ll << 31)) return PKV_ERR_UNSUPPORTED;
-  // Tokens of a tile: about four items a thread, but no fewer tiles than the GPU holds CTAs.
+  // Tokens of a tile: about six items a thread, but no fewer tiles than the GPU holds CTAs.
   const long long per_token = heads * a.items_row;
-  long long tile = (4ll * kRotaryThreads + per_token - 1) / per_token;
+  long long tile = (6ll * kRotaryThreads + per_token - 1) / per_token;
   const long long even = a.num_tokens / (sms * 4ll);
   if (tile > even) tile = even;
   if (tile > kRotaryMaxTokens) tile = kRotaryMaxTokens;
   if (tile < 1) tile = 1;
   a.tile = static_cast<int32_t>(tile);
   long long blocks = (a.num_tokens + tile - 1) / tile;
-  if (blocks > sms * 6ll) blocks = sms * 6ll;
+  if (blocks > sms * 4ll) blocks = sms * 4ll;
   void* args[1] = {&a};
   return launch_overlapped(fn, dim3(static_cast<unsigned>(blocks)), dim3(kRotaryThreads), 0, stream, args);
 }
