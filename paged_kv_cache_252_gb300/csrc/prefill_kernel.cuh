@@ -365,6 +365,7 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
         }
       };
       // The unit's row is fixed: query token tok behind the unit's first, query head hd of the group.
+      const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
       const int ru = 128 * i + r, tok = ru / a.group, hd = ru - tok * a.group, tok0 = 128 * i / a.group;
       for (uint32_t np = 0;; ++np) {
         // All four warps go on or stop together (they meet at barriers).
@@ -470,15 +471,162 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
         uint16_t* dst = static_cast<uint16_t*>(a.out) +
                         (static_cast<size_t>(pc->qb + pc->j0 + tok) * a.num_q_heads + pc->h * a.group + hd) * D;
         bool odd = false;   // a real row whose result is not finite
-        const int pieces = pc->pieces[i];
-        if (pieces == 1) {
-          if (alive) {
-            const float inv = l > 0.f ? 1.f / l : 0.f;
-            float bad = l == 0.f && limit > 0 ? NAN : 0.f;
+        // The row's result is the sum over its unit's pieces p of w_p O_p, in their order, over that
+        // of w_p l_p: this piece's O from tensor memory, others' (of a cut unit, for the last
+        // to finish) from their slots.
+        const int pieces = pc->pieces[i], first_cta = pc->first[i], own = pieces > 1 ? blockIdx.x - first_cta : 0;
+        const size_t slot_sz = pf_slot_floats(D);
+        auto slot_of = [&](int p) {
+          return a.partials + (static_cast<size_t>(2 * (first_cta + p) + (p == 0 ? 1 : 0)) * a.slot_tiles + i) * slot_sz;
+        };
+        bool write = alive;
+        float mu = m == -INFINITY ? 0.f : m, L = l;   // w_p = 2^(m_p - mu)
+        if (pieces > 1) {
+          const int rows = min(pc->rows - 128 * i, 128);
+          const bool few = rows <= 32;
+          unsigned long long* ctr = a.piece_counts + 2 * first_cta + i;
+          if (r == 0) {
+            // If every other piece is counted, this one is the last and need not be published (the
+            // first piece of a unit, at the end of its CTA's stretch, usually is).
+            const unsigned long long all = (static_cast<unsigned long long>(a.epoch) << 32) | (pieces - 1);
+            last_piece[i] = !few && *reinterpret_cast<volatile unsigned long long*>(ctr) == all &&
+                            atomicCAS(ctr, all, 0ull) == all;   // 0: clear for a replay
+            if (last_piece[i]) fence_acq_rel_gpu();   // the others' slots, for the threads behind the barrier
+          }
+          named_bar_sync(1 + i, 128);
+          bool last = last_piece[i] != 0;
+          if (!last) {
+            if (alive) {
+              float* sl = slot_of(own);
+              if (real) {
+                sl[r] = m;
+                sl[128 + r] = l;
+              }
 #pragma unroll 1
-            for (int e = 0; e < D; e += 32) {
-              uint32_t ov[32];
-              tmem_ld32(o_col + e, ov);
+              for (int e = 0; e < D; e += 32) {
+                uint32_t ov[32];
+                tmem_ld32(o_col + e, ov);
+                if (real) {
+#pragma unroll
+                  for (int x = 0; x < 32; x += 4)
+                    *reinterpret_cast<uint4*>(sl + 256 + ((e + x) / 8 * 128 + r) * 8 + x % 8) =
+                        make_uint4(ov[x], ov[x + 1], ov[x + 2], ov[x + 3]);
+                }
+              }
+            }
+            named_bar_sync(1 + i, 128);
+            if (r == 0) {
+              fence_acq_rel_gpu();   // releases what the barrier ordered before it
+              const unsigned long long tag = static_cast<unsigned long long>(a.epoch) << 32;
+              unsigned long long old = *reinterpret_cast<volatile unsigned long long*>(ctr), want;
+              for (;;) {
+                const unsigned counted = (old >> 32) == a.epoch ? static_cast<unsigned>(old) : 0u;
+                want = static_cast<int>(counted + 1) == pieces ? 0ull : tag | (counted + 1);
+                const unsigned long long got = atomicCAS(ctr, old, want);
+                if (got == old) break;
+                old = got;
+              }
+              last_piece[i] = want == 0ull;
+              fence_acq_rel_gpu();
+            }
+            named_bar_sync(1 + i, 128);
+            last = last_piece[i] != 0;
+          }
+          named_bar_sync(1 + i, 128);   // read before the next piece's flag
+          write = alive && last && !few;
+          if (write && real) {
+            float M = m;
+            for (int p = 0; p < pieces; ++p) M = fmaxf(M, p == own ? m : slot_of(p)[r]);
+            mu = M == -INFINITY ? 0.f : M;
+            L = 0.f;
+            for (int p = 0; p < pieces; ++p)
+              L = p == own ? fmaf(l, fast_exp2(m - mu), L) : fmaf(slot_of(p)[128 + r], fast_exp2(slot_of(p)[r] - mu), L);
+          }
+          if (last && alive && few) {
+            // Few rows (single decode rows over a long context): items of 8 dimensions of one row,
+            // spread over the 128 threads, all pieces from their slots.
+            if (r < 4) row_bad[4 * i + r] = 0;
+            named_bar_sync(1 + i, 128);
+            const int items = rows * (D / 8);
+#pragma unroll 1
+            for (int it = r; it < items; it += 128) {
+              const int ch = it / rows, rr = it - ch * rows;
+              float M = -INFINITY;
+#pragma unroll 4
+              for (int p = 0; p < pieces; ++p) M = fmaxf(M, slot_of(p)[rr]);
+              const float mr = M == -INFINITY ? 0.f : M;
+              float Lr = 0.f, o[8] = {};
+#pragma unroll 2
+              for (int p = 0; p < pieces; ++p) {
+                const float* sl = slot_of(p);
+                const float wp = fast_exp2(sl[rr] - mr);
+                const float4* src = reinterpret_cast<const float4*>(sl + 256 + (ch * 128 + rr) * 8);
+                const float4 f0 = src[0], f1 = src[1];
+                Lr = fmaf(sl[128 + rr], wp, Lr);
+                o[0] = fmaf(wp, f0.x, o[0]);
+                o[1] = fmaf(wp, f0.y, o[1]);
+                o[2] = fmaf(wp, f0.z, o[2]);
+                o[3] = fmaf(wp, f0.w, o[3]);
+                o[4] = fmaf(wp, f1.x, o[4]);
+                o[5] = fmaf(wp, f1.y, o[5]);
+                o[6] = fmaf(wp, f1.z, o[6]);
+                o[7] = fmaf(wp, f1.w, o[7]);
+              }
+              const float inv = Lr > 0.f ? 1.f / Lr : 0.f;
+              const int u = 128 * i + rr, j = u / a.group;
+              float bad = Lr == 0.f && pc->past + pc->j0 + j >= 0 ? NAN : Lr - Lr;
+              uint32_t y[4];
+#pragma unroll
+              for (int x = 0; x < 8; x += 2) {
+                bad = fmaf(o[x], 0.f, fmaf(o[x + 1], 0.f, bad));
+                y[x / 2] = pack2<Sh::kBf16>(o[x] * inv, o[x + 1] * inv);
+              }
+              if (bad != 0.f) atomicOr(const_cast<unsigned*>(row_bad) + 4 * i + (rr >> 5), 1u << (rr & 31));
+              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) +
+                                        (static_cast<size_t>(pc->qb + pc->j0 + j) * a.num_q_heads + pc->h * a.group + u -
+                                         j * a.group) * D + 8 * ch) = make_uint4(y[0], y[1], y[2], y[3]);
+            }
+            __threadfence_block();
+            named_bar_sync(1 + i, 128);
+            odd = (row_bad[4 * i + (warp & 3)] >> lane) & 1u;
+          }
+        }
+        if (write) {
+          const float inv = L > 0.f ? 1.f / L : 0.f, w_own = pieces > 1 ? fast_exp2(m - mu) : 1.f;
+          float bad = L == 0.f && limit > 0 ? NAN : 0.f;
+#pragma unroll 1
+          for (int e = 0; e < D; e += 32) {
+            uint32_t ov[32];
+            tmem_ld32(o_col + e, ov);
+            if (real) {
+              if (pieces > 1) {
+                float acc[32];
+#pragma unroll
+                for (int x = 0; x < 32; ++x) acc[x] = 0.f;
+#pragma unroll 1
+                for (int p = 0; p < pieces; ++p) {
+                  if (p == own) {
+#pragma unroll
+                    for (int x = 0; x < 32; ++x) acc[x] = fmaf(w_own, __uint_as_float(ov[x]), acc[x]);
+                  } else {
+                    const float* sl = slot_of(p);
+                    const float wp = fast_exp2(sl[r] - mu);
+                    float4 f[8];
+#pragma unroll
+                    for (int x = 0; x < 8; ++x)
+                      f[x] = *reinterpret_cast<const float4*>(sl + 256 + ((e / 8 + x / 2) * 128 + r) * 8 + 4 * (x & 1));
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) {
+                      acc[4 * x] = fmaf(wp, f[x].x, acc[4 * x]);
+                      acc[4 * x + 1] = fmaf(wp, f[x].y, acc[4 * x + 1]);
+                      acc[4 * x + 2] = fmaf(wp, f[x].z, acc[4 * x + 2]);
+                      acc[4 * x + 3] = fmaf(wp, f[x].w, acc[4 * x + 3]);
+                    }
+                  }
+                }
+#pragma unroll
+                for (int x = 0; x < 32; ++x) ov[x] = __float_as_uint(acc[x]);
+              }
               uint32_t y[16];
 #pragma unroll
               for (int x = 0; x < 32; x += 2) {
@@ -486,137 +634,19 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
                 bad = fmaf(u, 0.f, fmaf(v, 0.f, bad));
                 y[x / 2] = pack2<Sh::kBf16>(u * inv, v * inv);
               }
-              if (real) {
+              // whole 32-byte sectors where the output's alignment allows: neighbouring threads
+              // write different rows
+              if (wide) {
+                st_global_v8(dst + e, y);
+                st_global_v8(dst + e + 16, y + 8);
+              } else {
 #pragma unroll
                 for (int x = 0; x < 4; ++x)
                   *reinterpret_cast<uint4*>(dst + e + 8 * x) = make_uint4(y[4 * x], y[4 * x + 1], y[4 * x + 2], y[4 * x + 3]);
               }
             }
-            odd = real && !(bad == 0.f && l < INFINITY);
           }
-        } else {
-          // A cut unit: this piece's m, l and O to its slot; the last of the row tile's pieces
-          // to finish adds them up in the order of their CTAs.
-          const int first = pc->first[i];
-          const size_t slot_sz = pf_slot_floats(D);
-          auto slot_of = [&](int p) {
-            return a.partials + (static_cast<size_t>(2 * (first + p) + (p == 0 ? 1 : 0)) * a.slot_tiles + i) * slot_sz;
-          };
-          if (alive) {
-            float* sl = slot_of(blockIdx.x - first);
-            if (real) {
-              sl[r] = m;
-              sl[128 + r] = l;
-            }
-#pragma unroll 1
-            for (int e = 0; e < D; e += 32) {
-              uint32_t ov[32];
-              tmem_ld32(o_col + e, ov);
-              if (real) {
-#pragma unroll
-                for (int x = 0; x < 32; x += 4)
-                  *reinterpret_cast<uint4*>(sl + 256 + ((e + x) / 8 * 128 + r) * 8 + x % 8) =
-                      make_uint4(ov[x], ov[x + 1], ov[x + 2], ov[x + 3]);
-              }
-            }
-            tc_fence_before_sync();
-          }
-          fence_acq_rel_gpu();
-          named_bar_sync(1 + i, 128);
-          if (r == 0) {
-            unsigned long long* ctr = a.piece_counts + 2 * first + i;
-            const unsigned long long tag = static_cast<unsigned long long>(a.epoch) << 32;
-            unsigned long long old = *reinterpret_cast<volatile unsigned long long*>(ctr), want;
-            for (;;) {
-              const unsigned done = (old >> 32) == a.epoch ? static_cast<unsigned>(old) : 0u;
-              want = tag | (done + 1);
-              const unsigned long long got = atomicCAS(ctr, old, want);
-              if (got == old) break;
-              old = got;
-            }
-            const bool fin = static_cast<int>(static_cast<unsigned>(want)) == pieces;
-            if (fin) *reinterpret_cast<volatile unsigned long long*>(ctr) = 0ull;   // clear for a replay
-            last_piece[i] = fin;
-          }
-          named_bar_sync(1 + i, 128);
-          const bool mine = last_piece[i] != 0 && alive;
-          named_bar_sync(1 + i, 128);   // read before the next piece's flag
-          if (mine) {
-            // Items of 8 dimensions of one row, all real rows of the tile, spread over the 128
-            // threads (a unit of few rows is spread too). A trip to L2 per item is what it costs, so
-            // two items and four pieces go at a time.
-            fence_acq_rel_gpu();
-            const int rows = min(pc->rows - 128 * i, 128), items = rows * (D / 8);
-            if (r < 4) row_bad[4 * i + r] = 0;
-            named_bar_sync(1 + i, 128);
-            const size_t step = 2 * static_cast<size_t>(a.slot_tiles) * slot_sz;
-            const float* s0 = slot_of(0);
-            const float* s1 = slot_of(1);   // pieces 1, 2, ... are `step` apart
-            const int row0 = pc->qb + pc->j0, head0 = pc->h * a.group;
-#pragma unroll 1
-            for (int it = r; it < items; it += 256) {
-              float M[2] = {-INFINITY, -INFINITY}, L[2] = {0.f, 0.f}, o[2][8] = {};
-#pragma unroll 1
-              for (int p0 = 0; p0 < pieces; p0 += 4) {
-                float m4[2][4], l4[2][4];
-                float4 f[2][4][2];
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                  const int id = min(it + 128 * q, items - 1), ch = id / rows, rr = id - ch * rows;
-#pragma unroll
-                  for (int p = 0; p < 4; ++p) {
-                    const int pp = min(p0 + p, pieces - 1);   // past the last: read again, weight 0
-                    const float* sl = pp == 0 ? s0 : s1 + (pp - 1) * step;
-                    const float4* src = reinterpret_cast<const float4*>(sl + 256 + (ch * 128 + rr) * 8);
-                    m4[q][p] = p0 + p < pieces ? sl[rr] : -INFINITY;
-                    l4[q][p] = p0 + p < pieces ? sl[128 + rr] : 0.f;
-                    f[q][p][0] = src[0];
-                    f[q][p][1] = src[1];
-                  }
-                }
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                  const float Mn = fmaxf(M[q], fmaxf(fmaxf(m4[q][0], m4[q][1]), fmaxf(m4[q][2], m4[q][3])));
-                  const float mu = Mn == -INFINITY ? 0.f : Mn;
-                  const float al = fast_exp2(M[q] - mu);
-                  M[q] = Mn;
-                  L[q] *= al;
-#pragma unroll
-                  for (int x = 0; x < 8; ++x) o[q][x] *= al;
-#pragma unroll
-                  for (int p = 0; p < 4; ++p) {
-                    if (p0 + p >= pieces) break;
-                    const float wp = fast_exp2(m4[q][p] - mu);
-                    L[q] = fmaf(l4[q][p], wp, L[q]);
-                    const float* fv = reinterpret_cast<const float*>(f[q][p]);
-#pragma unroll
-                    for (int x = 0; x < 8; ++x) o[q][x] = fmaf(wp, fv[x], o[q][x]);
-                  }
-                }
-              }
-#pragma unroll
-              for (int q = 0; q < 2; ++q) {
-                const int id = it + 128 * q, ch = id / rows, rr = id - ch * rows;
-                if (id >= items) break;
-                const float inv = L[q] > 0.f ? 1.f / L[q] : 0.f;
-                const int u = 128 * i + rr, j = u / a.group;
-                float bad = L[q] == 0.f && pc->past + pc->j0 + j >= 0 ? NAN : L[q] - L[q];
-                uint32_t y[4];
-#pragma unroll
-                for (int x = 0; x < 8; x += 2) {
-                  bad = fmaf(o[q][x], 0.f, fmaf(o[q][x + 1], 0.f, bad));
-                  y[x / 2] = pack2<Sh::kBf16>(o[q][x] * inv, o[q][x + 1] * inv);
-                }
-                if (bad != 0.f) atomicOr(const_cast<unsigned*>(row_bad) + 4 * i + (rr >> 5), 1u << (rr & 31));
-                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) +
-                                          (static_cast<size_t>(row0 + j) * a.num_q_heads + head0 + u - j * a.group) * D +
-                                          8 * ch) = make_uint4(y[0], y[1], y[2], y[3]);
-              }
-            }
-            __threadfence_block();
-            named_bar_sync(1 + i, 128);
-            odd = (row_bad[4 * i + (warp & 3)] >> lane) & 1u;
-          }
+          odd = real && !(bad == 0.f && L < INFINITY);
         }
         __syncwarp();
         const unsigned again = __ballot_sync(0xffffffffu, odd);
