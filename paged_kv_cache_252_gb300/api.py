@@ -325,11 +325,15 @@ def kv_cache_write(key, value, slot_mapping, k_cache, v_cache, kv_dtype=None, *,
         _need_cuda_contig(n, t)
     if slot_mapping.dtype != torch.int32:
         raise PagedKVError("slot_mapping must be int32")
-    d = _write_shapes(key, value, slot_mapping, k_cache, v_cache)
+    d, hkv, head = _desc_of(k_cache, v_cache)
+    shape = key.shape
+    if len(shape) != 3 or shape[1] != hkv or shape[2] != head or value.shape != shape or \
+            slot_mapping.shape != shape[:1]:
+        _write_shapes(key, value, slot_mapping, k_cache, v_cache)
     rc = load_library().pkv_kv_cache_write(
-        _ptr(key), _ptr(value), _src_code(key), int(key.shape[0]), _ptr(slot_mapping),
-        _ptr(k_cache), _ptr(v_cache), _kv_code(kv_dtype, k_cache), ctypes.byref(d),
-        _ptr(device_status), _stream_handle(stream, key.device))
+        key.data_ptr(), value.data_ptr(), _src_code(key), shape[0], slot_mapping.data_ptr(),
+        k_cache.data_ptr(), v_cache.data_ptr(), _kv_code(kv_dtype, k_cache), d,
+        _addr(device_status), _stream_of(stream, key.get_device()))
     _check(rc, "kv_cache_write")
 
 
