@@ -485,12 +485,13 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
           const int rows = min(pc->rows - 128 * i, 128);
           const bool few = rows <= 32;
           unsigned long long* ctr = a.piece_counts + 2 * first_cta + i;
+          unsigned long long old = 0;   // (thread 0's) the counter as last seen
           if (r == 0) {
             // If every other piece is counted, this one is the last and need not be published (the
             // first piece of a unit, at the end of its CTA's stretch, usually is).
             const unsigned long long all = (static_cast<unsigned long long>(a.epoch) << 32) | (pieces - 1);
-            last_piece[i] = !few && *reinterpret_cast<volatile unsigned long long*>(ctr) == all &&
-                            atomicCAS(ctr, all, 0ull) == all;   // 0: clear for a replay
+            old = *reinterpret_cast<volatile unsigned long long*>(ctr);
+            last_piece[i] = !few && old == all && atomicCAS(ctr, all, 0ull) == all;   // 0: clear for a replay
             if (last_piece[i]) fence_acq_rel_gpu();   // the others' slots, for the threads behind the barrier
           }
           named_bar_sync(1 + i, 128);
@@ -508,9 +509,7 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
                 tmem_ld32(o_col + e, ov);
                 if (real) {
 #pragma unroll
-                  for (int x = 0; x < 32; x += 4)
-                    *reinterpret_cast<uint4*>(sl + 256 + ((e + x) / 8 * 128 + r) * 8 + x % 8) =
-                        make_uint4(ov[x], ov[x + 1], ov[x + 2], ov[x + 3]);
+                  for (int x = 0; x < 32; x += 8) st_global_v8(sl + 256 + ((e + x) / 8 * 128 + r) * 8, ov + x);
                 }
               }
             }
@@ -518,7 +517,7 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
             if (r == 0) {
               fence_acq_rel_gpu();   // releases what the barrier ordered before it
               const unsigned long long tag = static_cast<unsigned long long>(a.epoch) << 32;
-              unsigned long long old = *reinterpret_cast<volatile unsigned long long*>(ctr), want;
+              unsigned long long want;
               for (;;) {
                 const unsigned counted = (old >> 32) == a.epoch ? static_cast<unsigned>(old) : 0u;
                 want = static_cast<int>(counted + 1) == pieces ? 0ull : tag | (counted + 1);
@@ -527,7 +526,7 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
                 old = got;
               }
               last_piece[i] = want == 0ull;
-              fence_acq_rel_gpu();
+              if (want == 0ull) fence_acq_rel_gpu();
             }
             named_bar_sync(1 + i, 128);
             last = last_piece[i] != 0;
@@ -536,9 +535,11 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
           write = alive && last && !few;
           if (write && real) {
             float M = m;
+#pragma unroll 4
             for (int p = 0; p < pieces; ++p) M = fmaxf(M, p == own ? m : slot_of(p)[r]);
             mu = M == -INFINITY ? 0.f : M;
             L = 0.f;
+#pragma unroll 4
             for (int p = 0; p < pieces; ++p)
               L = p == own ? fmaf(l, fast_exp2(m - mu), L) : fmaf(slot_of(p)[128 + r], fast_exp2(slot_of(p)[r] - mu), L);
           }
@@ -611,17 +612,11 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
                   } else {
                     const float* sl = slot_of(p);
                     const float wp = fast_exp2(sl[r] - mu);
-                    float4 f[8];
+                    uint32_t f[32];
 #pragma unroll
-                    for (int x = 0; x < 8; ++x)
-                      f[x] = *reinterpret_cast<const float4*>(sl + 256 + ((e / 8 + x / 2) * 128 + r) * 8 + 4 * (x & 1));
+                    for (int x = 0; x < 32; x += 8) ld_global_v8(sl + 256 + ((e + x) / 8 * 128 + r) * 8, f + x);
 #pragma unroll
-                    for (int x = 0; x < 8; ++x) {
-                      acc[4 * x] = fmaf(wp, f[x].x, acc[4 * x]);
-                      acc[4 * x + 1] = fmaf(wp, f[x].y, acc[4 * x + 1]);
-                      acc[4 * x + 2] = fmaf(wp, f[x].z, acc[4 * x + 2]);
-                      acc[4 * x + 3] = fmaf(wp, f[x].w, acc[4 * x + 3]);
-                    }
+                    for (int x = 0; x < 32; ++x) acc[x] = fmaf(wp, __uint_as_float(f[x]), acc[x]);
                   }
                 }
 #pragma unroll
