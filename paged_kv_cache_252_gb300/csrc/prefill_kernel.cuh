@@ -479,169 +479,197 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
         auto slot_of = [&](int p) {
           return a.partials + (static_cast<size_t>(2 * (first_cta + p) + (p == 0 ? 1 : 0)) * a.slot_tiles + i) * slot_sz;
         };
-        bool write = alive;
-        float mu = m == -INFINITY ? 0.f : m, L = l;   // w_p = 2^(m_p - mu)
-        if (pieces > 1) {
-          const int rows = min(pc->rows - 128 * i, 128);
-          const bool few = rows <= 32;
-          unsigned long long* ctr = a.piece_counts + 2 * first_cta + i;
-          unsigned long long old = 0;   // (thread 0's) the counter as last seen
-          if (r == 0) {
-            // If every other piece is counted, this one is the last and need not be published (the
-            // first piece of a unit, at the end of its CTA's stretch, usually is).
-            const unsigned long long all = (static_cast<unsigned long long>(a.epoch) << 32) | (pieces - 1);
-            old = *reinterpret_cast<volatile unsigned long long*>(ctr);
-            last_piece[i] = !few && old == all && atomicCAS(ctr, all, 0ull) == all;   // 0: clear for a replay
-            if (last_piece[i]) fence_acq_rel_gpu();   // the others' slots, for the threads behind the barrier
-          }
-          named_bar_sync(1 + i, 128);
-          bool last = last_piece[i] != 0;
-          if (!last) {
-            if (alive) {
-              float* sl = slot_of(own);
-              if (real) {
-                sl[r] = m;
-                sl[128 + r] = l;
-              }
+        const int rows = min(pc->rows - 128 * i, 128);
+        const bool few = rows <= 32;
+        // One CTA adds up the pieces lo + step y, y < n, of which its own is the x-th: all of them,
+        // or, of more than kPfJoin, first those of every group of g neighbours, then the groups' sums.
+        int lo = 0, step = 1, n = pieces, x = own, g = 0;
+        if (pieces > kPfJoin && !few) {
+          for (g = 3; g * g < pieces;) ++g;
+          lo = own / g * g;
+          n = min(g, pieces - lo);
+          x = own - lo;
+        }
 #pragma unroll 1
-              for (int e = 0; e < D; e += 32) {
-                uint32_t ov[32];
-                tmem_ld32(o_col + e, ov);
-                if (real) {
-#pragma unroll
-                  for (int x = 0; x < 32; x += 8) st_global_v8(sl + 256 + ((e + x) / 8 * 128 + r) * 8, ov + x);
-                }
-              }
-            }
-            named_bar_sync(1 + i, 128);
+        for (;;) {
+          bool write = alive, last = true;
+          float M = m, mu = m == -INFINITY ? 0.f : m, L = l;   // w_p = 2^(m_p - mu)
+          if (n > 1) {
+            // (A group's count is at its first CTA, the first group's at the next one: no other unit
+            // begins at either.)
+            unsigned long long* ctr = a.piece_counts + 2 * (first_cta + (g && lo == 0 ? 1 : lo)) + i;
+            unsigned long long old = 0;   // (thread 0's) the counter as last seen
             if (r == 0) {
-              fence_acq_rel_gpu();   // releases what the barrier ordered before it
-              const unsigned long long tag = static_cast<unsigned long long>(a.epoch) << 32;
-              unsigned long long want;
-              for (;;) {
-                const unsigned counted = (old >> 32) == a.epoch ? static_cast<unsigned>(old) : 0u;
-                want = static_cast<int>(counted + 1) == pieces ? 0ull : tag | (counted + 1);
-                const unsigned long long got = atomicCAS(ctr, old, want);
-                if (got == old) break;
-                old = got;
-              }
-              last_piece[i] = want == 0ull;
-              if (want == 0ull) fence_acq_rel_gpu();
+              // If every other piece is counted, this one is the last and need not be published (the
+              // first piece of a unit, at the end of its CTA's stretch, usually is).
+              const unsigned long long all = (static_cast<unsigned long long>(a.epoch) << 32) | (n - 1);
+              old = *reinterpret_cast<volatile unsigned long long*>(ctr);
+              last_piece[i] = !few && old == all && atomicCAS(ctr, all, 0ull) == all;   // 0: clear for a replay
+              if (last_piece[i]) fence_acq_rel_gpu();   // the others' slots, for the threads behind the barrier
             }
             named_bar_sync(1 + i, 128);
             last = last_piece[i] != 0;
-          }
-          named_bar_sync(1 + i, 128);   // read before the next piece's flag
-          write = alive && last && !few;
-          if (write && real) {
-            float M = m;
-#pragma unroll 4
-            for (int p = 0; p < pieces; ++p) M = fmaxf(M, p == own ? m : slot_of(p)[r]);
-            mu = M == -INFINITY ? 0.f : M;
-            L = 0.f;
-#pragma unroll 4
-            for (int p = 0; p < pieces; ++p)
-              L = p == own ? fmaf(l, fast_exp2(m - mu), L) : fmaf(slot_of(p)[128 + r], fast_exp2(slot_of(p)[r] - mu), L);
-          }
-          if (last && alive && few) {
-            // Few rows (single decode rows over a long context): items of 8 dimensions of one row,
-            // spread over the 128 threads, all pieces from their slots.
-            if (r < 4) row_bad[4 * i + r] = 0;
-            named_bar_sync(1 + i, 128);
-            const int items = rows * (D / 8);
+            if (!last) {
+              if (alive) {
+                float* sl = slot_of(lo + step * x);
+                if (real) {
+                  sl[r] = m;
+                  sl[128 + r] = l;
+                }
 #pragma unroll 1
-            for (int it = r; it < items; it += 128) {
-              const int ch = it / rows, rr = it - ch * rows;
-              float M = -INFINITY;
-#pragma unroll 4
-              for (int p = 0; p < pieces; ++p) M = fmaxf(M, slot_of(p)[rr]);
-              const float mr = M == -INFINITY ? 0.f : M;
-              float Lr = 0.f, o[8] = {};
-#pragma unroll 2
-              for (int p = 0; p < pieces; ++p) {
-                const float* sl = slot_of(p);
-                const float wp = fast_exp2(sl[rr] - mr);
-                const float4* src = reinterpret_cast<const float4*>(sl + 256 + (ch * 128 + rr) * 8);
-                const float4 f0 = src[0], f1 = src[1];
-                Lr = fmaf(sl[128 + rr], wp, Lr);
-                o[0] = fmaf(wp, f0.x, o[0]);
-                o[1] = fmaf(wp, f0.y, o[1]);
-                o[2] = fmaf(wp, f0.z, o[2]);
-                o[3] = fmaf(wp, f0.w, o[3]);
-                o[4] = fmaf(wp, f1.x, o[4]);
-                o[5] = fmaf(wp, f1.y, o[5]);
-                o[6] = fmaf(wp, f1.z, o[6]);
-                o[7] = fmaf(wp, f1.w, o[7]);
-              }
-              const float inv = Lr > 0.f ? 1.f / Lr : 0.f;
-              const int u = 128 * i + rr, j = u / a.group;
-              float bad = Lr == 0.f && pc->past + pc->j0 + j >= 0 ? NAN : Lr - Lr;
-              uint32_t y[4];
+                for (int e = 0; e < D; e += 32) {
+                  uint32_t ov[32];
+                  tmem_ld32(o_col + e, ov);
+                  if (real) {
 #pragma unroll
-              for (int x = 0; x < 8; x += 2) {
-                bad = fmaf(o[x], 0.f, fmaf(o[x + 1], 0.f, bad));
-                y[x / 2] = pack2<Sh::kBf16>(o[x] * inv, o[x + 1] * inv);
-              }
-              if (bad != 0.f) atomicOr(const_cast<unsigned*>(row_bad) + 4 * i + (rr >> 5), 1u << (rr & 31));
-              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) +
-                                        (static_cast<size_t>(pc->qb + pc->j0 + j) * a.num_q_heads + pc->h * a.group + u -
-                                         j * a.group) * D + 8 * ch) = make_uint4(y[0], y[1], y[2], y[3]);
-            }
-            __threadfence_block();
-            named_bar_sync(1 + i, 128);
-            odd = (row_bad[4 * i + (warp & 3)] >> lane) & 1u;
-          }
-        }
-        if (write) {
-          const float inv = L > 0.f ? 1.f / L : 0.f, w_own = pieces > 1 ? fast_exp2(m - mu) : 1.f;
-          float bad = L == 0.f && limit > 0 ? NAN : 0.f;
-#pragma unroll 1
-          for (int e = 0; e < D; e += 32) {
-            uint32_t ov[32];
-            tmem_ld32(o_col + e, ov);
-            if (real) {
-              if (pieces > 1) {
-                float acc[32];
-#pragma unroll
-                for (int x = 0; x < 32; ++x) acc[x] = 0.f;
-#pragma unroll 1
-                for (int p = 0; p < pieces; ++p) {
-                  if (p == own) {
-#pragma unroll
-                    for (int x = 0; x < 32; ++x) acc[x] = fmaf(w_own, __uint_as_float(ov[x]), acc[x]);
-                  } else {
-                    const float* sl = slot_of(p);
-                    const float wp = fast_exp2(sl[r] - mu);
-                    uint32_t f[32];
-#pragma unroll
-                    for (int x = 0; x < 32; x += 8) ld_global_v8(sl + 256 + ((e + x) / 8 * 128 + r) * 8, f + x);
-#pragma unroll
-                    for (int x = 0; x < 32; ++x) acc[x] = fmaf(wp, __uint_as_float(f[x]), acc[x]);
+                    for (int x = 0; x < 32; x += 8) st_global_v8(sl + 256 + ((e + x) / 8 * 128 + r) * 8, ov + x);
                   }
                 }
-#pragma unroll
-                for (int x = 0; x < 32; ++x) ov[x] = __float_as_uint(acc[x]);
               }
-              uint32_t y[16];
-#pragma unroll
-              for (int x = 0; x < 32; x += 2) {
-                const float u = __uint_as_float(ov[x]), v = __uint_as_float(ov[x + 1]);
-                bad = fmaf(u, 0.f, fmaf(v, 0.f, bad));
-                y[x / 2] = pack2<Sh::kBf16>(u * inv, v * inv);
+              named_bar_sync(1 + i, 128);
+              if (r == 0) {
+                fence_acq_rel_gpu();   // releases what the barrier ordered before it
+                const unsigned long long tag = static_cast<unsigned long long>(a.epoch) << 32;
+                unsigned long long want;
+                for (;;) {
+                  const unsigned counted = (old >> 32) == a.epoch ? static_cast<unsigned>(old) : 0u;
+                  want = static_cast<int>(counted + 1) == n ? 0ull : tag | (counted + 1);
+                  const unsigned long long got = atomicCAS(ctr, old, want);
+                  if (got == old) break;
+                  old = got;
+                }
+                last_piece[i] = want == 0ull;
+                if (want == 0ull) fence_acq_rel_gpu();
               }
-              // whole 32-byte sectors where the output's alignment allows: neighbouring threads
-              // write different rows
-              if (wide) {
-                st_global_v8(dst + e, y);
-                st_global_v8(dst + e + 16, y + 8);
-              } else {
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-                  *reinterpret_cast<uint4*>(dst + e + 8 * x) = make_uint4(y[4 * x], y[4 * x + 1], y[4 * x + 2], y[4 * x + 3]);
+              named_bar_sync(1 + i, 128);
+              last = last_piece[i] != 0;
+            }
+            named_bar_sync(1 + i, 128);   // read before the next piece's flag
+            write = alive && last && !few;
+            if (write && real) {
+#pragma unroll 4
+              for (int y = 0; y < n; ++y) M = fmaxf(M, y == x ? m : slot_of(lo + step * y)[r]);
+              mu = M == -INFINITY ? 0.f : M;
+              L = 0.f;
+#pragma unroll 4
+              for (int y = 0; y < n; ++y) {
+                const float* sl = slot_of(lo + step * y);
+                L = y == x ? fmaf(l, fast_exp2(m - mu), L) : fmaf(sl[128 + r], fast_exp2(sl[r] - mu), L);
               }
             }
+            if (last && alive && few) {
+              // Few rows (single decode rows over a long context): items of 8 dimensions of one row,
+              // spread over the 128 threads, all pieces from their slots.
+              if (r < 4) row_bad[4 * i + r] = 0;
+              named_bar_sync(1 + i, 128);
+              const int items = rows * (D / 8);
+#pragma unroll 1
+              for (int it = r; it < items; it += 128) {
+                const int ch = it / rows, rr = it - ch * rows;
+                float M = -INFINITY;
+#pragma unroll 4
+                for (int p = 0; p < pieces; ++p) M = fmaxf(M, slot_of(p)[rr]);
+                const float mr = M == -INFINITY ? 0.f : M;
+                float Lr = 0.f, o[8] = {};
+#pragma unroll 2
+                for (int p = 0; p < pieces; ++p) {
+                  const float* sl = slot_of(p);
+                  const float wp = fast_exp2(sl[rr] - mr);
+                  const float4* src = reinterpret_cast<const float4*>(sl + 256 + (ch * 128 + rr) * 8);
+                  const float4 f0 = src[0], f1 = src[1];
+                  Lr = fmaf(sl[128 + rr], wp, Lr);
+                  o[0] = fmaf(wp, f0.x, o[0]);
+                  o[1] = fmaf(wp, f0.y, o[1]);
+                  o[2] = fmaf(wp, f0.z, o[2]);
+                  o[3] = fmaf(wp, f0.w, o[3]);
+                  o[4] = fmaf(wp, f1.x, o[4]);
+                  o[5] = fmaf(wp, f1.y, o[5]);
+                  o[6] = fmaf(wp, f1.z, o[6]);
+                  o[7] = fmaf(wp, f1.w, o[7]);
+                }
+                const float inv = Lr > 0.f ? 1.f / Lr : 0.f;
+                const int u = 128 * i + rr, j = u / a.group;
+                float bad = Lr == 0.f && pc->past + pc->j0 + j >= 0 ? NAN : Lr - Lr;
+                uint32_t y[4];
+#pragma unroll
+                for (int x = 0; x < 8; x += 2) {
+                  bad = fmaf(o[x], 0.f, fmaf(o[x + 1], 0.f, bad));
+                  y[x / 2] = pack2<Sh::kBf16>(o[x] * inv, o[x + 1] * inv);
+                }
+                if (bad != 0.f) atomicOr(const_cast<unsigned*>(row_bad) + 4 * i + (rr >> 5), 1u << (rr & 31));
+                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) +
+                                          (static_cast<size_t>(pc->qb + pc->j0 + j) * a.num_q_heads + pc->h * a.group + u -
+                                           j * a.group) * D + 8 * ch) = make_uint4(y[0], y[1], y[2], y[3]);
+              }
+              __threadfence_block();
+              named_bar_sync(1 + i, 128);
+              odd = (row_bad[4 * i + (warp & 3)] >> lane) & 1u;
+            }
           }
-          odd = real && !(bad == 0.f && L < INFINITY);
+          if (write && !(g && n == 1)) {
+            const float inv = L > 0.f ? 1.f / L : 0.f, w_own = n > 1 ? fast_exp2(m - mu) : 1.f;
+            float bad = L == 0.f && limit > 0 ? NAN : 0.f;
+#pragma unroll 1
+            for (int e = 0; e < D; e += 32) {
+              uint32_t ov[32];
+              tmem_ld32(o_col + e, ov);
+              if (real) {
+                if (n > 1) {
+                  float acc[32];
+#pragma unroll
+                  for (int x = 0; x < 32; ++x) acc[x] = 0.f;
+#pragma unroll 1
+                  for (int y = 0; y < n; ++y) {
+                    if (y == x) {
+#pragma unroll
+                      for (int x = 0; x < 32; ++x) acc[x] = fmaf(w_own, __uint_as_float(ov[x]), acc[x]);
+                    } else {
+                      const float* sl = slot_of(lo + step * y);
+                      const float wp = fast_exp2(sl[r] - mu);
+                      uint32_t f[32];
+#pragma unroll
+                      for (int x = 0; x < 32; x += 8) ld_global_v8(sl + 256 + ((e + x) / 8 * 128 + r) * 8, f + x);
+#pragma unroll
+                      for (int x = 0; x < 32; ++x) acc[x] = fmaf(wp, __uint_as_float(f[x]), acc[x]);
+                    }
+                  }
+#pragma unroll
+                  for (int x = 0; x < 32; ++x) ov[x] = __float_as_uint(acc[x]);
+                }
+              }
+              if (g) {
+                tmem_st32(o_col + e, ov);
+              } else if (real) {
+                uint32_t y[16];
+#pragma unroll
+                for (int x = 0; x < 32; x += 2) {
+                  const float u = __uint_as_float(ov[x]), v = __uint_as_float(ov[x + 1]);
+                  bad = fmaf(u, 0.f, fmaf(v, 0.f, bad));
+                  y[x / 2] = pack2<Sh::kBf16>(u * inv, v * inv);
+                }
+                // whole 32-byte sectors where the output's alignment allows: neighbouring threads
+                // write different rows
+                if (wide) {
+                  st_global_v8(dst + e, y);
+                  st_global_v8(dst + e + 16, y + 8);
+                } else {
+#pragma unroll
+                  for (int x = 0; x < 4; ++x)
+                    *reinterpret_cast<uint4*>(dst + e + 8 * x) = make_uint4(y[4 * x], y[4 * x + 1], y[4 * x + 2], y[4 * x + 3]);
+                }
+              }
+            }
+            odd = real && g == 0 && !(bad == 0.f && L < INFINITY);
+            if (g) {
+              m = M;
+              l = L;
+            }
+          }
+          if (!last || g == 0) break;   // (the same for all: whatever `alive` says, barriers are met)
+          x = lo / g;
+          n = (pieces + g - 1) / g;
+          step = g;
+          lo = g = 0;
         }
         __syncwarp();
         const unsigned again = __ballot_sync(0xffffffffu, odd);

@@ -27,6 +27,7 @@ constexpr int kPfTile = 128;          // positions of a KV tile
 // 405 / 378 / 383 us).
 constexpr int kPfUnitCost = 384;
 constexpr int kPfWhole = 8 * kPfTile, kPfWholeShare = 2400;
+constexpr int kPfJoin = 6;
 constexpr int kPfMinShare = 3 * kPfTile + kPfUnitCost;   // where units are cut: at least one whole tile a piece
 
 // Tokens of one TMA box of query rows, and of a unit (whole boxes). Boxes start on the
