@@ -374,10 +374,10 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
         const volatile PfPiece* pc = ring + np % kPfRing;
         if (pc->end) break;
         uint32_t nth = seen;                        // KV tile of the CTA
-        int k = pc->ka;
-        const int kb = pc->kb[i];
-        seen += pc->klast - k;
-        if (k >= kb) {
+        const int ka = pc->ka, span = (pc->klast - ka) * kPfTile, pend = pc->klast * kPfTile;
+        int left = pc->kb[i] - ka, p0 = PfPiece::at(ka, pc->rot, ka, pc->klast) * kPfTile;
+        seen += pc->klast - ka;
+        if (left <= 0) {
           __syncwarp();
           if (lane == 0) piece_done(np);
           continue;
@@ -387,10 +387,9 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
         const int limit0 = pc->past + pc->j0 + tok0 + 1;
         float m = -INFINITY, l = 0.f;
         int fresh = 1;   // 1 in the piece's first tile; opaque, or the loop body is compiled twice
-        for (; k < kb; ++k, ++cnt, ++nth, fresh = 0) {
+        for (; left > 0; --left, ++cnt, ++nth, fresh = 0, p0 = p0 + kPfTile == pend ? pend - span : p0 + kPfTile) {
           asm volatile("" : "+r"(fresh));
           const bool first = fresh != 0;
-          const int p0 = k * kPfTile;
           wait(bar_s, cnt & 1);
           const uint32_t slot = nth % Sh::kScaleRing;
           if constexpr (KV == kKvInt8) wait(sc_full + 8 * slot, (nth / Sh::kScaleRing) & 1);
@@ -695,7 +694,7 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
           const volatile PfPiece* pc = ring + piece % kPfRing;
           if (!ok || pc->end) break;
           const int32_t* bt = a.block_tables + static_cast<size_t>(pc->s) * a.max_blocks_per_seq;
-          const int ctx = pc->ctx, h = pc->h, ka = pc->ka, klast = pc->klast, tail = pc->tail;
+          const int ctx = pc->ctx, h = pc->h, ka = pc->ka, klast = pc->klast, rot = pc->rot, tail = pc->tail;
           const int boxes = (pc->rows + a.box_tokens * a.group - 1) / (a.box_tokens * a.group);
           const int token = pc->qb + pc->j0;
           __syncwarp();
@@ -705,7 +704,7 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
             // Rows of both blocks: lanes 0 and 1 look them up.
             int mine = total_rows;   // wholly past the end: the copy fills zeros
             if (lane < 2) {
-              const int p = k * kPfTile + (2 * x + lane) * kBlockSize;
+              const int p = PfPiece::at(k, rot, ka, klast) * kPfTile + (2 * x + lane) * kBlockSize;
               if (p < ctx) {
                 const int id = bt[p >> 4];
                 if (static_cast<unsigned>(id) < static_cast<unsigned>(a.num_blocks))
@@ -800,19 +799,20 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
           const volatile PfPiece* pc = ring + np % kPfRing;
           if (!alive || pc->end) break;
           const int32_t* bt = a.block_tables + static_cast<size_t>(pc->s) * a.max_blocks_per_seq;
-          const int ctx = pc->ctx, h = pc->h, ka = pc->ka, klast = pc->klast;
+          const int ctx = pc->ctx, h = pc->h, ka = pc->ka, klast = pc->klast, rot = pc->rot;
           __syncwarp();
           if (lane == 0) piece_done(np);
-          // Lane b < 8: the id of block b of tile k (-1 behind the context), and what it names as a
+          // Lane b < 8: the id of block b of step k's tile (-1 behind the context), and what it names as a
           // (block, head) tile, -1 where it is out of range and reads as zeros. The id is looked at
           // a tile after it was asked for.
           auto id_of = [&](int k) {
-            const int p = k * kPfTile + lane * kBlockSize;
+            const int p = PfPiece::at(k, rot, ka, klast) * kPfTile + lane * kBlockSize;
             return lane < kPfTile / kBlockSize && p < ctx && k < klast ? bt[p >> 4] : -1;
           };
           auto tile_of = [&](int id, int k) {
             if (static_cast<unsigned>(id) < static_cast<unsigned>(a.num_blocks)) return id * a.num_kv_heads + h;
-            if (lane < kPfTile / kBlockSize && k * kPfTile + lane * kBlockSize < ctx && k < klast && a.status)
+            if (lane < kPfTile / kBlockSize && PfPiece::at(k, rot, ka, klast) * kPfTile + lane * kBlockSize < ctx &&
+                k < klast && a.status)
               atomicOr(a.status, kDevBadBlock);
             return -1;
           };
@@ -820,6 +820,7 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
           // groups count alike. It runs kAhead parts ahead, block ids a tile ahead of it.
           int ids = tile_of(id_of(ka), ka), id_next = id_of(ka + 1);
           int fk = ka, fv = 0, fp = 0;
+          int left = ctx - PfPiece::at(ka, rot, ka, klast) * kPfTile;   // positions from the fetched tile's first on
           float scale_k = 0.f, scale_v = 0.f;
           auto fetch = [&] {
             if (fk < klast) {
@@ -829,7 +830,7 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
               for (int q = 0; q < NL; ++q) {
                 const int b = (fp * NL + q) * BPC + blk0;
                 const int t = __shfl_sync(0xffffffffu, ids, b);
-                const bool real = t >= 0 && fk * kPfTile + b * kBlockSize + rb < ctx;
+                const bool real = t >= 0 && b * kBlockSize + rb < left;
                 cp_async_16(dst + q * 2048, cache + (real ? static_cast<size_t>(t) * (kBlockSize * D) : 0),
                             real ? 16u : 0u);
               }
@@ -838,7 +839,7 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
                   // (a tile's K scale is written before the next tile's is fetched, V's likewise)
                   const int t = __shfl_sync(0xffffffffu, ids, wt >> 4);
                   float f = 0.f;
-                  if (t >= 0 && fk * kPfTile + wt < ctx)
+                  if (t >= 0 && wt < left)
                     f = a.scales[static_cast<size_t>(t) * 32 + 16 * fv + (wt & 15)] * (fv ? 1.f : a.scale_log2);
                   if (fv) scale_v = f;
                   else scale_k = f;
@@ -850,6 +851,7 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
                 fv ^= 1;
                 if (fv == 0) {
                   ++fk;
+                  left = ctx - PfPiece::at(fk, rot, ka, klast) * kPfTile;
                   ids = tile_of(id_next, fk);
                   id_next = id_of(fk + 1);
                 }
@@ -1055,7 +1057,7 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
             sent ^= 1u << vs;
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
-            const int r0 = ctx - tail * kPfTile, r1 = (r0 + 15) & ~15;
+            const int r0 = ctx & (kPfTile - 1), r1 = (r0 + 15) & ~15;
             uint8_t* vt = smem + Sh::kRing + vs * Sh::kStageBytes;
 #pragma unroll 1
             for (int x = lane; x < (r1 - r0) * Sh::kHalves * 8; x += 32) {

@@ -27,6 +27,8 @@ constexpr int kPfTile = 128;          // positions of a KV tile
 // 405 / 378 / 383 us).
 constexpr int kPfUnitCost = 384;
 constexpr int kPfWhole = 8 * kPfTile, kPfWholeShare = 2400;
+// A unit of more pieces is joined in groups first: one CTA that adds up 19 pieces of two full row
+// tiles takes 30 us at the call's end (64 tokens over 131008: 141 us against 122; 4 to 9 alike).
 constexpr int kPfJoin = 6;
 constexpr int kPfMinShare = 3 * kPfTile + kPfUnitCost;   // where units are cut: at least one whole tile a piece
 
@@ -109,7 +111,13 @@ struct PfPiece {
   int j0, rows;              // first query token of the unit, its rows
   int ka, klast;             // KV tiles [ka, klast) ...
   int kb[2];                 // ... of which row tile i takes those below kb[i] (none: kb <= ka)
-  int tail;                  // the tile whose V rows end behind the context inside a block, else -1
+  int rot;                   // the tiles are taken from ka + rot on, then those from ka: step k takes tile at(k)
+  int tail;                  // the step whose tile's V rows end behind the context inside a block, else -1
+
+  __device__ static int at(int k, int rot, int ka, int klast) {
+    const int t = k + rot;
+    return t < klast ? t : t - (klast - ka);
+  }
   int first[2], pieces[2];   // of a row tile cut by a stretch's end: its first CTA, its pieces (1: not cut)
 };
 
@@ -142,7 +150,25 @@ __device__ inline bool pf_piece(const PfWalk& w, volatile PfPiece* to) {
   to->rows = rows;
   to->ka = ka;
   to->klast = klast;
-  to->tail = w.p.ctx & 15 ? w.p.ctx / kPfTile : -1;
+  // Several units of one head read the same tiles. So that they do so at about the same time, out
+  // of L2, the CTA begins a cut unit with the tile whose line length is its own elapsed one,
+  // modulo a stretch's (128 tokens over 130944: 204 us in rising order, where each unit reads the
+  // context from memory, against 194; of whole units too, a ragged E5M2 batch lost 9 %). Not
+  // where one row tile takes fewer of the tiles than the other.
+  int rot = 0;
+  bool level = w.p.n > qt && (ka > 0 || kx < k_all);
+  for (int i = 0; i < 2; ++i) level &= min(kx, kend[i]) <= ka || kend[i] >= klast;
+  if (level) {
+    const long long e0 = static_cast<long long>(kPfTile) * ka - x0;   // elapsed at the piece's start
+    const long long m = x0 > 0 ? (x0 + w.st.share - 1) / w.st.share : 0;
+    const long long k0 = (e0 + m * w.st.share + kPfTile - 1) / kPfTile;
+    if (k0 > ka && k0 < klast) rot = static_cast<int>(k0) - ka;
+  }
+  to->rot = rot;
+  int tail = w.p.ctx & 15 ? w.p.ctx / kPfTile : -1;
+  if (tail >= ka && tail < klast) tail = tail - rot < ka ? tail - rot + klast - ka : tail - rot;
+  else tail = -1;
+  to->tail = tail;
 #pragma unroll 1
   for (int i = 0; i < 2; ++i) {
     to->kb[i] = min(kx, kend[i]);

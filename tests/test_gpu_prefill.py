@@ -62,6 +62,8 @@ CASES = {
     "decode-rows": (128, 32, 8, [1] * 20, [700 + 31 * i for i in range(20)]),
     "mixed": (128, 16, 4, [1, 500, 4, 1, 0, 33, 1], [900, 1300, 64, 1, 0, 33, 2050]),
     "few-rows-long": (128, 8, 2, [3], [20011]),
+    "rows-long": (128, 8, 2, [40], [20011]),          # joined in groups; a row tile of few rows
+    "units-long": (64, 8, 2, [150, 1], [30005, 7]),    # units that share a long context
     "chunk-long": (128, 8, 2, [260], [9000]),
     "many": (64, 2, 1, [(7 * i) % 40 for i in range(150)], [(7 * i) % 40 + (13 * i) % 90 for i in range(150)]),
     "prompt": (128, 8, 2, [1100], [1100]),
