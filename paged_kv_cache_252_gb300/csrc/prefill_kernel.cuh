@@ -802,25 +802,24 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
           const int ctx = pc->ctx, h = pc->h, ka = pc->ka, klast = pc->klast, rot = pc->rot;
           __syncwarp();
           if (lane == 0) piece_done(np);
-          // Lane b < 8: the id of block b of step k's tile (-1 behind the context), and what it names as a
+          // Lane b < 8: the id of block b of tile t (-1 behind the context), and what it names as a
           // (block, head) tile, -1 where it is out of range and reads as zeros. The id is looked at
           // a tile after it was asked for.
-          auto id_of = [&](int k) {
-            const int p = PfPiece::at(k, rot, ka, klast) * kPfTile + lane * kBlockSize;
-            return lane < kPfTile / kBlockSize && p < ctx && k < klast ? bt[p >> 4] : -1;
+          auto id_of = [&](int t) {
+            const int p = t * kPfTile + lane * kBlockSize;
+            return lane < kPfTile / kBlockSize && p < ctx ? bt[p >> 4] : -1;
           };
-          auto tile_of = [&](int id, int k) {
+          auto tile_of = [&](int id, int t) {
             if (static_cast<unsigned>(id) < static_cast<unsigned>(a.num_blocks)) return id * a.num_kv_heads + h;
-            if (lane < kPfTile / kBlockSize && PfPiece::at(k, rot, ka, klast) * kPfTile + lane * kBlockSize < ctx &&
-                k < klast && a.status)
+            if (lane < kPfTile / kBlockSize && t * kPfTile + lane * kBlockSize < ctx && a.status)
               atomicOr(a.status, kDevBadBlock);
             return -1;
           };
+          auto next = [&](int t) { return t + 1 == klast ? ka : t + 1; };   // (behind the last step: unused)
           // fetch() copies the parts in order (tile, K then V, part), nothing past the end, so that
           // groups count alike. It runs kAhead parts ahead, block ids a tile ahead of it.
-          int ids = tile_of(id_of(ka), ka), id_next = id_of(ka + 1);
-          int fk = ka, fv = 0, fp = 0;
-          int left = ctx - PfPiece::at(ka, rot, ka, klast) * kPfTile;   // positions from the fetched tile's first on
+          int fk = ka, fv = 0, fp = 0, ft = PfPiece::at(ka, rot, ka, klast);   // step; K or V; part; tile
+          int ids = tile_of(id_of(ft), ft), id_next = id_of(next(ft));
           float scale_k = 0.f, scale_v = 0.f;
           auto fetch = [&] {
             if (fk < klast) {
@@ -830,7 +829,7 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
               for (int q = 0; q < NL; ++q) {
                 const int b = (fp * NL + q) * BPC + blk0;
                 const int t = __shfl_sync(0xffffffffu, ids, b);
-                const bool real = t >= 0 && b * kBlockSize + rb < left;
+                const bool real = t >= 0 && ft * kPfTile + b * kBlockSize + rb < ctx;
                 cp_async_16(dst + q * 2048, cache + (real ? static_cast<size_t>(t) * (kBlockSize * D) : 0),
                             real ? 16u : 0u);
               }
@@ -839,7 +838,7 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
                   // (a tile's K scale is written before the next tile's is fetched, V's likewise)
                   const int t = __shfl_sync(0xffffffffu, ids, wt >> 4);
                   float f = 0.f;
-                  if (t >= 0 && wt < left)
+                  if (t >= 0 && ft * kPfTile + wt < ctx)
                     f = a.scales[static_cast<size_t>(t) * 32 + 16 * fv + (wt & 15)] * (fv ? 1.f : a.scale_log2);
                   if (fv) scale_v = f;
                   else scale_k = f;
@@ -851,9 +850,9 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
                 fv ^= 1;
                 if (fv == 0) {
                   ++fk;
-                  left = ctx - PfPiece::at(fk, rot, ka, klast) * kPfTile;
-                  ids = tile_of(id_next, fk);
-                  id_next = id_of(fk + 1);
+                  ft = next(ft);
+                  ids = tile_of(id_next, ft);
+                  id_next = id_of(next(ft));
                 }
               }
             }

@@ -248,6 +248,15 @@ def test_same_bits_every_time_and_whatever_the_workspace_held(dev):
         assert torch.equal(b.out, ref)
 
 
+def test_same_bits_where_pieces_are_joined_in_groups(dev):
+    b = Batch(dev, "fp16", 128, 8, 2, [40, 90], [20011, 15000])
+    ref = b.run().clone()
+    b.check()
+    for _ in range(20):
+        b.out.fill_(7.5)
+        assert torch.equal(b.run(), ref)
+
+
 def test_graphs_replay_and_do_not_share_scratch(dev):
     """Two captured calls and eager calls, replayed on two streams at once."""
     a = Batch(dev, "fp16", 128, 8, 2, [130, 4], [6000, 9001], seed=1)
