@@ -161,6 +161,10 @@ int pkv_paged_attention_prefill(void* out, const void* q, const int32_t* cu_q_le
     const uint64_t vstrides[2] = {static_cast<uint64_t>(d) * 2, 128};
     const uint32_t vbox[3] = {64, kBlockSize, halves};
     if (int rc = encode_map_16bit(&tv, v_cache, 3, vdims, vstrides, vbox)) return rc;
+  } else {
+    const long long rows = static_cast<long long>(cache->num_blocks) * cache->num_kv_heads * kBlockSize;
+    if (int rc = encode_tile_map(&tk0, k_cache, kv, d, rows, 0)) return rc;
+    if (int rc = encode_tile_map(&tv, v_cache, kv, d, rows, 0)) return rc;
   }
   void* args[5] = {&tq, &tk0, &tk1, &tv, &a};
   return launch_overlapped(v.fn, dim3(static_cast<unsigned>(sms)), dim3(v.threads), v.smem, stream, args);

@@ -58,9 +58,9 @@ struct PfShape {
   // Register budgets (per thread of a warpgroup); twice the first and the others make the
   // launch's 512 x 128.
   static constexpr int kLaunchRegs = 128;
-  static constexpr int kSoftmaxRegs = kWiden ? 184 : 192;
+  static constexpr int kSoftmaxRegs = 192;
   static constexpr int kIssueRegs = kWiden ? 56 : 72;
-  static constexpr int kLoadRegs = kWiden ? 88 : 56;
+  static constexpr int kLoadRegs = kWiden ? 72 : 56;
   static_assert(2 * kSoftmaxRegs + kIssueRegs + kLoadRegs == 4 * kLaunchRegs, "register split");
   static constexpr int kStages = kWiden ? (D == 128 ? 4 : 8) : (D == 128 ? 5 : 10);
   static constexpr uint32_t kHalfBytes = kPfTile * 128;             // 64 dimensions of a KV tile
@@ -80,10 +80,11 @@ struct PfShape {
   static constexpr int kScaleRing = kStages;
   // Shared memory from a 1024-aligned base.
   static constexpr uint32_t kRing = kQBytes;
-  static constexpr uint32_t kRaw = kRing + kStages * kStageBytes;      // one-byte caches: three parts
-  static constexpr uint32_t kScales = kRaw + (kWiden ? 3 * 8192 : 0);   // INT8: [kScaleRing][K, V][128] floats
+  static constexpr int kRawRing = 3;                                   // one-byte caches: parts of 8 KB as they lie
+  static constexpr uint32_t kRaw = kRing + kStages * kStageBytes;
+  static constexpr uint32_t kScales = kRaw + (kWiden ? kRawRing * 8192 : 0);   // INT8: [kScaleRing][K, V][128] floats
   static constexpr uint32_t kBars = kScales + (KV == kKvInt8 ? kScaleRing * 2 * kPfTile * 4 : 0);
-  static constexpr uint32_t kMisc = kBars + (4 * kStages + 11 + 2 * kPfRing + kScaleRing) * 8;
+  static constexpr uint32_t kMisc = kBars + (4 * kStages + 11 + 2 * kPfRing + kScaleRing + 2 * kRawRing) * 8;
   static constexpr uint32_t kPieces = kMisc + 256 + sizeof(PfStart);   // ring of kPfRing
   static constexpr uint32_t kSmem = kPieces + kPfRing * sizeof(PfPiece) + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory of one CTA");
@@ -286,6 +287,8 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
   const uint32_t pc_full = v_sent + 8 * NS; // [kPfRing] piece worked out
   const uint32_t pc_empty = pc_full + 8 * kPfRing;   // [kPfRing] piece no longer read
   const uint32_t sc_full = pc_empty + 8 * kPfRing;   // [kScaleRing] row scales of a tile written (INT8)
+  const uint32_t raw_full = sc_full + 8 * Sh::kScaleRing;   // [kRawRing] part landed (one-byte caches)
+  const uint32_t raw_empty = raw_full + 8 * Sh::kRawRing;  // [kRawRing] part read
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Sh::kMisc);
   PfCtl* ctl = reinterpret_cast<PfCtl*>(smem + Sh::kMisc + 8);
   volatile int* last_piece = reinterpret_cast<volatile int*>(smem + Sh::kMisc + 16);   // [2]
@@ -297,7 +300,7 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
   if (tid == 0) {
 #pragma unroll 1
     for (int k = 0; k < NS; ++k) {
-      mbar_init(full + 8 * k, Sh::kWiden ? 128 : 4);
+      mbar_init(full + 8 * k, 4);
       mbar_init(empty + 8 * k, 2);
       mbar_init(v_tail + 8 * k, 1);
       mbar_init(v_sent + 8 * k, 1);
@@ -311,7 +314,12 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
       mbar_init(turn + 8 * i, 1);
     }
 #pragma unroll 1
-    for (int i = 0; i < Sh::kScaleRing; ++i) mbar_init(sc_full + 8 * i, 128);
+    for (int i = 0; i < Sh::kScaleRing; ++i) mbar_init(sc_full + 8 * i, 4);
+#pragma unroll 1
+    for (int i = 0; i < Sh::kRawRing; ++i) {
+      mbar_init(raw_full + 8 * i, 1);
+      mbar_init(raw_empty + 8 * i, 4);
+    }
     mbar_init(final_bar, 2);
 #pragma unroll 1
     for (int i = 0; i < kPfRing; ++i) {
@@ -769,22 +777,16 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
         __syncwarp();
       } else {
         // ------------------------- widening loader (one-byte caches) --------------------
-        // Parts of 8 KB (half a tile of head size 128, a tile of 64) go through a ring of three raw
-        // buffers, copied asynchronously; each thread copies what it converts itself, so the
-        // ring needs no barrier and a part in flight no registers. A thread's rows are the
-        // same in every block, so its addresses are constants beside the block's.
+        // Warp 10 copies parts of 8 KB (half a tile of head size 128, a tile of 64) into a ring of raw
+        // buffers; these four warps widen them into the stages the products read. A thread's rows
+        // are the same in every block, so its addresses are constants beside the part's.
         constexpr int LPR = D / 16;               // lanes of a row (16 bytes each)
-        constexpr int RPW = 32 / LPR;             // rows of a warp's copy
-        constexpr int NL = 4;                     // copies of a thread per part
+        constexpr int RPW = 32 / LPR;             // rows of a warp's 16-byte reads
+        constexpr int NL = 4;                     // reads of a thread per part
         constexpr int kParts = D / 64;            // parts of a tile's K or V
-        constexpr int BPC = RPW * 4 / kBlockSize; // blocks the four warps cover in one copy
         const int wi = warp - 12, wt = tid - 384;
         const int cc = lane % LPR, rw = wi * RPW + lane / LPR;
-        const int blk0 = rw / kBlockSize, rb = rw % kBlockSize;   // block of a copy, row of the block
-        const uint8_t* k_base = static_cast<const uint8_t*>(a.k_cache) + rb * D + 16 * cc;
-        const uint8_t* v_base = static_cast<const uint8_t*>(a.v_cache) + rb * D + 16 * cc;
-        uint8_t* raw = smem + Sh::kRaw + wt * 16;
-        const uint32_t raw_s = smem_addr(raw);
+        const uint8_t* raw = smem + Sh::kRaw + rw * D + ((cc ^ (D == 128 ? rw & 7 : (rw >> 1) & 3)) << 4);
         // Elements 16 cc .. 16 cc + 15: chunks 2 (cc % 4), + 1 of half cc / 4. The upper half's
         // lanes write their second chunk first, so that a row's eight lanes cover eight chunks
         // (all banks) in each store.
@@ -792,122 +794,100 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
         const int c0 = 2 * (cc & 3) + (cc >> 2), c1 = 2 * (cc & 3) + 1 - (cc >> 2);
         uint8_t* out0 = smem + Sh::kRing + (cc >> 2) * Sh::kHalfBytes + rw * 128;
         const int o0 = (c0 ^ (rw & 7)) << 4, o1 = (c1 ^ (rw & 7)) << 4;
-        uint32_t stage = 0, round = 0, uses = 0, tiles = 0, put_slot = 0, get_slot = 0;
+        uint32_t stage = 0, round = 0, uses = 0, tiles = 0, slot = 0, raw_round = 0;
         bool alive = true;
         for (uint32_t np = 0; alive; ++np) {
           alive = __all_sync(0xffffffffu, piece_ready(np));
           const volatile PfPiece* pc = ring + np % kPfRing;
           if (!alive || pc->end) break;
           const int32_t* bt = a.block_tables + static_cast<size_t>(pc->s) * a.max_blocks_per_seq;
-          const int ctx = pc->ctx, h = pc->h, ka = pc->ka, klast = pc->klast, rot = pc->rot;
+          const int ctx = pc->ctx, h = pc->h, ka = pc->ka, klast = pc->klast;
+          int t = PfPiece::at(ka, pc->rot, ka, klast);
           __syncwarp();
           if (lane == 0) piece_done(np);
-          // Lane b < 8: the id of block b of tile t (-1 behind the context), and what it names as a
-          // (block, head) tile, -1 where it is out of range and reads as zeros. The id is looked at
-          // a tile after it was asked for.
-          auto id_of = [&](int t) {
-            const int p = t * kPfTile + lane * kBlockSize;
-            return lane < kPfTile / kBlockSize && p < ctx ? bt[p >> 4] : -1;
+          auto next = [&](int x) { return x + 1 == klast ? ka : x + 1; };   // (behind the last step: unused)
+          // Row scales of an INT8 cache, a tile ahead; their blocks' ids another tile.
+          auto id_of = [&](int x) {
+            const int pos = x * kPfTile + wt;
+            return pos < ctx ? bt[pos >> 4] : -1;
           };
-          auto tile_of = [&](int id, int t) {
-            if (static_cast<unsigned>(id) < static_cast<unsigned>(a.num_blocks)) return id * a.num_kv_heads + h;
-            if (lane < kPfTile / kBlockSize && t * kPfTile + lane * kBlockSize < ctx && a.status)
-              atomicOr(a.status, kDevBadBlock);
-            return -1;
+          auto scales_of = [&](int id, float& k, float& v) {
+            k = v = 0.f;
+            if (static_cast<unsigned>(id) >= static_cast<unsigned>(a.num_blocks)) return;
+            const float* from = a.scales + (static_cast<size_t>(id) * a.num_kv_heads + h) * 32 + (wt & 15);
+            k = from[0] * a.scale_log2;
+            v = from[16];
           };
-          auto next = [&](int t) { return t + 1 == klast ? ka : t + 1; };   // (behind the last step: unused)
-          // fetch() copies the parts in order (tile, K then V, part), nothing past the end, so that
-          // groups count alike. It runs kAhead parts ahead, block ids a tile ahead of it.
-          int fk = ka, fv = 0, fp = 0, ft = PfPiece::at(ka, rot, ka, klast);   // step; K or V; part; tile
-          int ids = tile_of(id_of(ft), ft), id_next = id_of(next(ft));
-          float scale_k = 0.f, scale_v = 0.f;
-          auto fetch = [&] {
-            if (fk < klast) {
-              const uint8_t* cache = fv ? v_base : k_base;
-              const uint32_t dst = raw_s + put_slot * 8192;
-#pragma unroll
-              for (int q = 0; q < NL; ++q) {
-                const int b = (fp * NL + q) * BPC + blk0;
-                const int t = __shfl_sync(0xffffffffu, ids, b);
-                const bool real = t >= 0 && ft * kPfTile + b * kBlockSize + rb < ctx;
-                cp_async_16(dst + q * 2048, cache + (real ? static_cast<size_t>(t) * (kBlockSize * D) : 0),
-                            real ? 16u : 0u);
-              }
-              if constexpr (KV == kKvInt8) {
-                if (fp == 0) {
-                  // (a tile's K scale is written before the next tile's is fetched, V's likewise)
-                  const int t = __shfl_sync(0xffffffffu, ids, wt >> 4);
-                  float f = 0.f;
-                  if (t >= 0 && ft * kPfTile + wt < ctx)
-                    f = a.scales[static_cast<size_t>(t) * 32 + 16 * fv + (wt & 15)] * (fv ? 1.f : a.scale_log2);
-                  if (fv) scale_v = f;
-                  else scale_k = f;
-                }
-              }
-              if (++put_slot == 3) put_slot = 0;
-              if (++fp == kParts) {
-                fp = 0;
-                fv ^= 1;
-                if (fv == 0) {
-                  ++fk;
-                  ft = next(ft);
-                  ids = tile_of(id_next, ft);
-                  id_next = id_of(next(ft));
-                }
-              }
+          int id = -1;
+          float next_k = 0.f, next_v = 0.f;
+          if constexpr (KV == kKvInt8) {
+            scales_of(id_of(t), next_k, next_v);
+            id = id_of(next(t));
+          }
+#pragma unroll 1
+          for (int k = ka; k < klast; ++k, t = next(t)) {
+            const float scale_k = next_k, scale_v = next_v;
+            if constexpr (KV == kKvInt8) {
+              scales_of(id, next_k, next_v);
+              id = id_of(next(next(t)));
             }
-            cp_async_commit();
-          };
-          constexpr int kAhead = KV == kKvInt8 && kParts == 1 ? 2 : 3;
 #pragma unroll 1
-          for (int n = 0; n < kAhead; ++n) fetch();
-#pragma unroll 1
-          for (int n = 2 * kParts * ka; n < 2 * kParts * klast; ++n) {
-            const int part = n & (kParts - 1), v = (n / kParts) & 1;
-            if (part == 0 && uses >= NS) {
-              const bool ok = pf_wait(empty + 8 * stage, round ^ 1, ctl);
+            for (int n = 0; n < 2 * kParts; ++n) {
+              const int part = n & (kParts - 1), v = n / kParts;
+              bool ok = part != 0 || uses < NS || pf_wait(empty + 8 * stage, round ^ 1, ctl);
+              ok = ok && pf_wait(raw_full + 8 * slot, raw_round, ctl);
               if (!__all_sync(0xffffffffu, ok)) {
                 alive = false;
                 ctl->abort = 1;
                 if (lane == 0 && a.status) atomicOr(a.status, kDevTimeout);
                 break;
               }
-            }
-            cp_async_wait<kAhead - 1>();
-            const uint8_t* src = raw + get_slot * 8192;
-            uint8_t* dst = out0 + stage * Sh::kStageBytes + part * (kPfTile / kParts) * 128;
-            uint4 x[NL];
+              const uint8_t* src = raw + slot * 8192;
+              uint8_t* dst = out0 + stage * Sh::kStageBytes + part * (kPfTile / kParts) * 128;
+              uint4 x[NL];
 #pragma unroll
-            for (int q = 0; q < NL; ++q) x[q] = *reinterpret_cast<const uint4*>(src + q * 2048);
+              for (int q = 0; q < NL; ++q) x[q] = *reinterpret_cast<const uint4*>(src + q * 2048);
+              __syncwarp();
+              if (lane == 0) mbar_arrive(raw_empty + 8 * slot);
+              if (++slot == Sh::kRawRing) {
+                slot = 0;
+                raw_round ^= 1;
+              }
+              if (t * kPfTile + kPfTile > ctx) {   // rows behind the context: whatever the block holds
+                const int row = t * kPfTile + part * (kPfTile / kParts) + rw;
 #pragma unroll
-            for (int q = 0; q < NL; ++q) {
-              uint4 lo, hi;
-              widen16<KV>(x[q], lo, hi);
-              *reinterpret_cast<uint4*>(dst + q * (4 * RPW * 128) + o0) = upper ? hi : lo;
-              *reinterpret_cast<uint4*>(dst + q * (4 * RPW * 128) + o1) = upper ? lo : hi;
+                for (int q = 0; q < NL; ++q)
+                  if (row + q * (4 * RPW) >= ctx) x[q] = make_uint4(0u, 0u, 0u, 0u);
+              }
+#pragma unroll
+              for (int q = 0; q < NL; ++q) {
+                uint4 lo, hi;
+                widen16<KV>(upper ? make_uint4(x[q].z, x[q].w, x[q].x, x[q].y) : x[q], lo, hi);
+                *reinterpret_cast<uint4*>(dst + q * (4 * RPW * 128) + o0) = lo;
+                *reinterpret_cast<uint4*>(dst + q * (4 * RPW * 128) + o1) = hi;
+              }
+              if (part == kParts - 1) {
+                if constexpr (KV == kKvInt8) {
+                  // a masked score, -inf, must stay that times an all-zero row's K scale
+                  const float f = v ? scale_v : (scale_k == 0.f ? 1e-30f : scale_k);
+                  reinterpret_cast<float*>(smem + Sh::kScales)[tiles % Sh::kScaleRing * 2 * kPfTile + v * kPfTile + wt] = f;
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                  mbar_arrive(full + 8 * stage);
+                  if (KV == kKvInt8 && v == 1) mbar_arrive(sc_full + 8 * (tiles % Sh::kScaleRing));
+                }
+                tiles += v;
+                ++uses;
+                if (++stage == NS) {
+                  stage = 0;
+                  round ^= 1;
+                }
+              }
             }
-            if (++get_slot == 3) get_slot = 0;
-            if (part == kParts - 1) {
-              if constexpr (KV == kKvInt8) {
-                // a masked score, -inf, must stay that times an all-zero row's K scale
-                const float f = v ? scale_v : (scale_k == 0.f ? 1e-30f : scale_k);
-                reinterpret_cast<float*>(smem + Sh::kScales)[tiles % Sh::kScaleRing * 2 * kPfTile + v * kPfTile + wt] = f;
-              }
-              fence_proxy_async_smem();
-              mbar_arrive(full + 8 * stage);
-              if (v == 1) {
-                if (KV == kKvInt8) mbar_arrive(sc_full + 8 * (tiles % Sh::kScaleRing));
-                ++tiles;
-              }
-              ++uses;
-              if (++stage == NS) {
-                stage = 0;
-                round ^= 1;
-              }
-            }
-            fetch();
+            if (!alive) break;
           }
-          cp_async_wait<0>();
         }
       }
     } else {
@@ -1076,26 +1056,77 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
         }
         __syncwarp();
       } else if (warp == 10) {
-        // --------------------------- query copies (one-byte caches) ------------------------
-        if (lane == 0) {
-          uint32_t piece = 0;
-          bool ok = true;
-          for (;; ++piece) {
-            ok = piece_ready(piece);
-            const volatile PfPiece* pc = ring + piece % kPfRing;
-            if (!ok || pc->end) break;
-            const int boxes = (pc->rows + a.box_tokens * a.group - 1) / (a.box_tokens * a.group);
-            const int head = pc->h * a.group, token = pc->qb + pc->j0;
-            piece_done(piece);
-            ok = piece == 0 || pf_wait(q_empty, (piece - 1) & 1, ctl);
-            if (!ok) break;
-            pf_load_q<D>(a, &tm_q, base, q_full, head, token, boxes, 0, 1);
+        // ----------------- copies of queries and raw parts (one-byte caches) -----------------
+        // Lane b copies block b of a tile; its row is looked up a tile ahead. A piece's queries go
+        // behind its first K and V parts, which need not wait for the piece before to end.
+        constexpr int kParts = D / 64, kPer = kPfTile / kBlockSize / kParts;   // blocks of a part
+        const int total_rows = a.num_blocks * a.num_kv_heads * kBlockSize;   // host guarantees < 2^31
+        uint32_t parts = 0, slot = 0, round = 0, piece = 0;
+        bool ok = true;
+        for (;; ++piece) {
+          ok = __all_sync(0xffffffffu, piece_ready(piece));
+          const volatile PfPiece* pc = ring + piece % kPfRing;
+          if (!ok || pc->end) break;
+          const int32_t* bt = a.block_tables + static_cast<size_t>(pc->s) * a.max_blocks_per_seq;
+          const int ctx = pc->ctx, h = pc->h, ka = pc->ka, klast = pc->klast;
+          const int boxes = (pc->rows + a.box_tokens * a.group - 1) / (a.box_tokens * a.group);
+          const int token = pc->qb + pc->j0;
+          int t = PfPiece::at(ka, pc->rot, ka, klast);
+          __syncwarp();
+          if (lane == 0) piece_done(piece);
+          auto id_of = [&](int x) {
+            const int pos = x * kPfTile + lane * kBlockSize;
+            return lane < kPfTile / kBlockSize && pos < ctx ? bt[pos >> 4] : -1;
+          };
+          int id = id_of(t);
+          bool asked = false;
+#pragma unroll 1
+          for (int k = ka; k < klast && ok; ++k) {
+            int row = total_rows;   // wholly past the end: the copy fills zeros
+            if (static_cast<unsigned>(id) < static_cast<unsigned>(a.num_blocks))
+              row = (id * a.num_kv_heads + h) * kBlockSize;
+            else if (lane < kPfTile / kBlockSize && t * kPfTile + lane * kBlockSize < ctx && a.status)
+              atomicOr(a.status, kDevBadBlock);
+            t = t + 1 == klast ? ka : t + 1;
+            id = id_of(t);
+#pragma unroll 1
+            for (int n = 0; n < 2 * kParts; ++n) {
+              const int at = lane - (n & (kParts - 1)) * kPer;
+              ok = parts < Sh::kRawRing || pf_wait(raw_empty + 8 * slot, round ^ 1, ctl);
+              ok = __all_sync(0xffffffffu, ok);
+              if (!ok) break;
+              if (lane == 0) mbar_arrive_expect_tx(raw_full + 8 * slot, 8192);
+              __syncwarp();
+              if (at >= 0 && at < kPer)
+                tma_load_2d_keep(base + Sh::kRaw + slot * 8192 + at * (kBlockSize * D), n < kParts ? &tm_k0 : &tm_v, 0, row,
+                                 raw_full + 8 * slot);
+              ++parts;
+              if (++slot == Sh::kRawRing) {
+                slot = 0;
+                round ^= 1;
+              }
+              if (!asked && n == 1) {
+                asked = true;
+                ok = piece == 0 || pf_wait(q_empty, (piece - 1) & 1, ctl);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                if (lane == 0) pf_load_q<D>(a, &tm_q, base, q_full, h * a.group, token, boxes, 0, 1);
+                __syncwarp();
+              }
+            }
           }
+          if (!ok) break;
+        }
+        if (lane == 0) {
           if (!ok) {
             ctl->abort = 1;
             if (a.status) atomicOr(a.status, kDevTimeout);
           }
-          if (piece > 0) mbar_wait(q_full, (piece - 1) & 1);   // the last copies land before exit
+          // Every copy issued lands before exit (where a role gave up: within these bounded waits).
+          bool landed = piece == 0 || mbar_wait(q_full, (piece - 1) & 1);
+#pragma unroll 1
+          for (uint32_t n = parts > Sh::kRawRing ? parts - Sh::kRawRing : 0; n < parts && landed; ++n)
+            landed = mbar_wait(raw_full + 8 * (n % Sh::kRawRing), (n / Sh::kRawRing) & 1);
         }
         __syncwarp();
       } else if (warp == 9) {
