@@ -78,12 +78,13 @@ struct PfShape {
   // tile t + kScaleRing - kStages / 2 is released, which is after the softmax of the tile before
   // that one, so tile t's are no longer read when kScaleRing > kStages / 2.
   static constexpr int kScaleRing = kStages;
+  static constexpr int kScaleSlot = 2 * kPfTile + 4;   // K, V, and the loading warps' largest V scales
   // Shared memory from a 1024-aligned base.
   static constexpr uint32_t kRing = kQBytes;
   static constexpr int kRawRing = 3;                                   // one-byte caches: parts of 8 KB as they lie
   static constexpr uint32_t kRaw = kRing + kStages * kStageBytes;
-  static constexpr uint32_t kScales = kRaw + (kWiden ? kRawRing * 8192 : 0);   // INT8: [kScaleRing][K, V][128] floats
-  static constexpr uint32_t kBars = kScales + (KV == kKvInt8 ? kScaleRing * 2 * kPfTile * 4 : 0);
+  static constexpr uint32_t kScales = kRaw + (kWiden ? kRawRing * 8192 : 0);   // INT8: [kScaleRing][kScaleSlot] floats
+  static constexpr uint32_t kBars = kScales + (KV == kKvInt8 ? kScaleRing * kScaleSlot * 4 : 0);
   static constexpr uint32_t kMisc = kBars + (4 * kStages + 11 + 2 * kPfRing + kScaleRing + 2 * kRawRing) * 8;
   static constexpr uint32_t kPieces = kMisc + 256 + sizeof(PfStart);   // ring of kPfRing
   static constexpr uint32_t kSmem = kPieces + kPfRing * sizeof(PfPiece) + 1024;
@@ -208,16 +209,15 @@ __device__ __forceinline__ float pf_max(const uint32_t (&sv)[4][32], float c, co
   return KV == kKvInt8 ? m : m * c;
 }
 
-// Weights 2^(s c + sub) of 128 scores, packed in pairs, their sum l and the sum `packed` of
-// what was packed: the same, or an INT8 cache's weights times its V scales (its K scales, which
-// hold c, multiply the scores). FMAs and sums go two to an instruction: alone on its scheduler
+// Weights 2^(s c + sub) of 128 scores, packed in pairs, and their sum; an INT8 cache's are packed
+// times its V scales (its K scales, which hold c, multiply the scores). FMAs and sums go two to an instruction: alone on its scheduler
 // a warp is quicker with scalar ones (787 against 963 cycles a tile), but every instruction
 // saved beside the products counts (16384-token prompt 1511 us against 1620, with either in
 // pairs 1544 and 1563).
 template <int KV>
 __device__ __forceinline__ void pf_weights(const uint32_t (&sv)[4][32], uint32_t (&pw)[4][16], float c, float sub,
-                                           const float4* k_scales, const float4* v_scales, float& sum, float& packed) {
-  float l[4] = {0.f, 0.f, 0.f, 0.f}, t[4] = {0.f, 0.f, 0.f, 0.f};
+                                           const float4* k_scales, const float4* v_scales, float& sum) {
+  float l[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int g = 0; g < 4; ++g) {
 #pragma unroll
@@ -236,15 +236,12 @@ __device__ __forceinline__ void pf_weights(const uint32_t (&sv)[4][32], uint32_t
         const float4 f = lds_f4_early(smem_addr(v_scales + 8 * g + e / 4));
         mul_pair(q[0], q[1], f.x, f.y);
         mul_pair(q[2], q[3], f.z, f.w);
-        add_pair(t[0], t[1], q[0], q[1]);
-        add_pair(t[2], t[3], q[2], q[3]);
       }
       pw[g][e / 2] = pack2<KV == kKvBf16>(q[0], q[1]);
       pw[g][e / 2 + 1] = pack2<KV == kKvBf16>(q[2], q[3]);
     }
   }
   sum = (l[0] + l[1]) + (l[2] + l[3]);
-  packed = KV == kKvInt8 ? (t[0] + t[1]) + (t[2] + t[3]) : sum;
 }
 
 // Boxes first, first + step, ... of a unit's query rows, one thread: box b holds tokens
@@ -405,14 +402,19 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
           tc_fence_after_sync();
           // Weights against the running maximum as it stands. Whether it may stand is seen from
           // their sum: a score over it by more than the slack shows as a sum over 2^slack (a tile's
-          // 128 weights of at most 1 never do; of an INT8 cache the packed products must stay in
-          // fp16's range), and a row with no maximum yet is known. Then, in a second round from the
+          // 128 weights of at most 1 never do; of an INT8 cache the sum times the largest V scale, as the
+          // packed products must stay in fp16's range), and a row with no maximum yet is known. Then, in a second round from the
           // same scores, the maximum is found and moves. (Finding it first in every tile cost 300
           // to 400 of the 1350 cycles between a tile's scores and weights.)
-          const float4* k_scales = reinterpret_cast<const float4*>(smem + Sh::kScales) + slot * 64;
+          const float4* k_scales = reinterpret_cast<const float4*>(smem + Sh::kScales) + slot * (Sh::kScaleSlot / 4);
           const bool masked = p0 + kPfTile > limit0;
           uint32_t pw[4][16];
-          float ls, packed;
+          float ls, most = 1.f;   // a tile's sum of weights; its largest V scale
+          if constexpr (KV == kKvInt8) {
+            const float4 f = k_scales[kPfTile / 2];
+            most = __uint_as_float(max(max(__float_as_uint(f.x), __float_as_uint(f.y)),
+                                       max(__float_as_uint(f.z), __float_as_uint(f.w))));
+          }
           auto round = [&](bool settle) {
             uint32_t sv[4][32];   // 32 scores each
             tmem_ld128(s_col, sv[0], sv[1], sv[2], sv[3]);
@@ -441,11 +443,11 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
                 }
               }
             }
-            pf_weights<KV>(sv, pw, c, Sh::kShift - (m == -INFINITY ? 0.f : m), k_scales, k_scales + 32, ls, packed);
+            pf_weights<KV>(sv, pw, c, Sh::kShift - (m == -INFINITY ? 0.f : m), k_scales, k_scales + 32, ls);
           };
           // (only rows that see positions of this tile ask for a second round)
           auto moves = [&] {
-            return __any_sync(0xffffffffu, limit > p0 && (!(packed <= Sh::kMostSum) || m == -INFINITY)) != 0;
+            return __any_sync(0xffffffffu, limit > p0 && (!(ls * most <= Sh::kMostSum) || m == -INFINITY)) != 0;
           };
           if constexpr (KV == kKvInt8) {
             // one copy of the code: two of this longer one spill registers
@@ -870,7 +872,11 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
                 if constexpr (KV == kKvInt8) {
                   // a masked score, -inf, must stay that times an all-zero row's K scale
                   const float f = v ? scale_v : (scale_k == 0.f ? 1e-30f : scale_k);
-                  reinterpret_cast<float*>(smem + Sh::kScales)[tiles % Sh::kScaleRing * 2 * kPfTile + v * kPfTile + wt] = f;
+                  float* to = reinterpret_cast<float*>(smem + Sh::kScales) + tiles % Sh::kScaleRing * Sh::kScaleSlot;
+                  to[v * kPfTile + wt] = f;
+                  // (bits of positive floats are in their order, a NaN's above all)
+                  const unsigned most = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(f)));
+                  if (v && lane == 0) to[2 * kPfTile + wi] = __uint_as_float(most);
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
