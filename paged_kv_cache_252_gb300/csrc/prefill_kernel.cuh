@@ -449,21 +449,12 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
           auto moves = [&] {
             return __any_sync(0xffffffffu, limit > p0 && (!(ls * most <= Sh::kMostSum) || m == -INFINITY)) != 0;
           };
-          if constexpr (KV == kKvInt8) {
-            // one copy of the code: two of this longer one spill registers
-            for (int again = fresh;; again = 1) {
-              asm volatile("" : "+r"(again));
-              round(again != 0);
-              if (again || !moves()) break;
-            }
-          } else {
-            bool settle = true;
-            if (!first) {
-              round(false);
-              settle = moves();
-            }
-            if (__builtin_expect(settle, 0)) round(true);
+          bool settle = true;
+          if (!first) {
+            round(false);
+            settle = moves();
           }
+          if (__builtin_expect(settle, 0)) round(true);
           l += ls;
 #pragma unroll
           for (int g = 0; g < 4; ++g) tmem_st16_async(s_col + 16 * g, pw[g]);
