@@ -1,12 +1,20 @@
 """GB300-native paged decode attention over a blocked KV cache.
 
-Two calls, both hand-written CUDA for sm_103a behind a C ABI (``libpagedkv.so``):
+Hand-written CUDA for sm_103a behind a C ABI (``libpagedkv.so``), first of all:
 
 * :func:`kv_cache_write` scatters new key/value tokens into their physical
   cache slots (fp16/bf16 copy, or fp16 -> FP8 E5M2 cast).
 * :func:`paged_attention_decode` computes softmax(q K^T * scale) V for every
   sequence over its blocks, one CTA stream per KV head serving the whole GQA
   group, causal among a sequence's query tokens (speculative verify).
+
+Around them, what a serving step runs:
+
+* :func:`rotary_write` (and :func:`rotary_embed`) turns q and k by their positions and
+  writes the cache in the same pass; :func:`rotary_inv_freq` gives the frequencies.
+* :func:`paged_attention_prefill` is the attention of prompts and prompt chunks.
+* :func:`kv_cache_accept` keeps the accepted drafts of a speculative verify, and
+  :meth:`BlockAllocator.truncate` gives the dropped ones' blocks back.
 
 :class:`BlockAllocator` (host, C++) hands out the blocks: sequences, fork with
 copy-on-write (:func:`copy_blocks` performs the copies), and a prefix cache.

@@ -9,7 +9,7 @@
 // cut by a stretch's end becomes pieces that are merged by the last to finish. While stretches
 // are short (kPfWholeShare) a unit of at most kPfWhole positions is not cut: all of it belongs
 // to the CTA whose stretch holds its start, since writing and merging pieces takes as long as some
-// five tiles (eight prompts of 512 tokens: 45 us against 59).
+// five tiles (eight prompts of 512 tokens: 43 us; 49 with kPfWholeShare 1600, where they are cut).
 #pragma once
 
 #include <cuda_runtime.h>
@@ -23,8 +23,8 @@ namespace pkv {
 
 constexpr int kPfRows = 256;          // query rows of a unit: two tiles of the MMA's M
 constexpr int kPfTile = 128;          // positions of a KV tile
-// A unit's fixed cost, in positions (128 / 256 / 384 / 512 gave an 8192-token bf16 prompt 437 /
-// 405 / 378 / 383 us).
+// A unit's fixed cost, in positions (256 / 320 / 384 gave an 8192-token bf16 prompt 372 / 370 /
+// 360 us; 512 no less).
 constexpr int kPfUnitCost = 384;
 constexpr int kPfWhole = 8 * kPfTile, kPfWholeShare = 2400;
 // A unit of more pieces is joined in groups first: one CTA that adds up 19 pieces of two full row

@@ -20,7 +20,12 @@
 // whatever the layout. A CTA takes tiles of a few tokens: their cosines and sines go
 // through shared memory once, and the tile's items (all heads of q, key and value) are
 // spread over its threads. The D/16 lanes of one row are neighbours in a warp, which
-// gives the INT8 writer its row maximum by shuffles.
+// gives the INT8 writer its row maximum by shuffles. The next tile's angles are worked out while
+// this tile's rows are under way (8192 tokens 42 us without, 36.7 with).
+//
+// Bound by memory, a step of few tokens by its launch. Measured, 32 query and 8 KV heads of 128:
+// 8192 bf16 tokens 36.7 us, 5.5 TB/s (a copy reaches 6.77); 64 tokens 2.9 us. 2001 fp16 tokens of
+// 16 + 4 heads of 64, half of each rotated: 4.9 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
