@@ -16,6 +16,7 @@ using namespace pkv;
 
 constexpr int kMaxDevices = 64;
 constexpr size_t kCounterBytes = 4096;   // 2 per CTA: up to 256 multiprocessors
+constexpr uintptr_t kSlotAlign = 32;     // slots are read and written 32 bytes a thread; a workspace has 16
 
 struct Variant {
   const void* fn;
@@ -75,7 +76,7 @@ size_t pkv_prefill_workspace_bytes(int32_t num_q_rows, int32_t num_seqs, int32_t
   int sms = 0;
   if (device_sm_count(&sms)) return 0;
   const long long rows = static_cast<long long>(num_q_rows) * (num_q_heads / cache->num_kv_heads);
-  return kCounterBytes + static_cast<size_t>(2) * sms * prefill_slot_tiles(rows) * pf_slot_floats(cache->head_size) *
+  return kCounterBytes + kSlotAlign + static_cast<size_t>(2) * sms * prefill_slot_tiles(rows) * pf_slot_floats(cache->head_size) *
                              sizeof(float);
 }
 
@@ -137,7 +138,8 @@ int pkv_paged_attention_prefill(void* out, const void* q, const int32_t* cu_q_le
   a.unit_tokens = box.unit;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   a.piece_counts = reinterpret_cast<unsigned long long*>(ws);
-  a.partials = reinterpret_cast<float*>(ws + kCounterBytes);
+  a.partials = reinterpret_cast<float*>((reinterpret_cast<uintptr_t>(ws) + kCounterBytes + kSlotAlign - 1) &
+                                        ~(kSlotAlign - 1));
   a.slot_tiles = prefill_slot_tiles(static_cast<long long>(num_q_rows) * a.group);
   a.epoch = next_call_epoch();
 

@@ -248,6 +248,23 @@ def test_same_bits_every_time_and_whatever_the_workspace_held(dev):
         assert torch.equal(b.out, ref)
 
 
+@pytest.mark.parametrize("kv,D,ns,lens", [("bf16", 128, [300, 5], [300, 900]), ("fp16", 64, [40, 1], [20011, 9000]),
+                                          ("e5m2", 128, [90, 40], [3000, 20011])])
+def test_output_and_workspace_on_16_byte_boundaries(dev, kv, D, ns, lens):
+    """What the header asks for and no more: whole units, cut ones, joined groups, few rows."""
+    import paged_kv_cache_252_gb300 as pkv
+    b = Batch(dev, kv, D, 8, 2, ns, lens)
+    ref = b.run().clone()
+    need = pkv.prefill_workspace_bytes(b.q.shape[0], len(ns), 8, b.kc)
+    ws = torch.zeros(need + 16, dtype=torch.uint8, device=dev)[16:]
+    flat = torch.full((b.q.numel() + 16,), 7.5, dtype=b.q.dtype, device=dev)
+    out = flat[8:8 + b.q.numel()].view(b.q.shape)
+    assert ws.data_ptr() % 32 == 16 and out.data_ptr() % 32 == 16
+    pkv.paged_attention_prefill(out, b.q, b.cu, b.kc, b.vc, b.bt, b.cl, b.scale, workspace=ws)
+    assert torch.equal(out, ref)
+    assert (flat[:8] == 7.5).all() and (flat[-8:] == 7.5).all()
+
+
 def test_same_bits_where_pieces_are_joined_in_groups(dev):
     b = Batch(dev, "fp16", 128, 8, 2, [40, 90], [20011, 15000])
     ref = b.run().clone()
