@@ -248,6 +248,17 @@ def test_same_bits_every_time_and_whatever_the_workspace_held(dev):
         assert torch.equal(b.out, ref)
 
 
+@pytest.mark.parametrize("kv,D", [("fp16", 128), ("int8", 64)])
+def test_more_sequences_than_threads(dev, kv, D):
+    """The plan gives a thread several sequences; runs of empty ones at the start, inside and at the end."""
+    ns = [0] * 700 + [(5 * i) % 7 for i in range(900)] + [200] + [0] * 600 + [1, 3] + [0] * 40
+    lens = [n + (11 * i) % 50 for i, n in enumerate(ns)]
+    b = Batch(dev, kv, D, 4, 2, ns, lens, extra_rows=2)
+    b.run()
+    b.check("many sequences")
+    assert b.status.item() == 0
+
+
 @pytest.mark.parametrize("kv,D,ns,lens", [("bf16", 128, [300, 5], [300, 900]), ("fp16", 64, [40, 1], [20011, 9000]),
                                           ("e5m2", 128, [90, 40], [3000, 20011])])
 def test_output_and_workspace_on_16_byte_boundaries(dev, kv, D, ns, lens):
