@@ -3,7 +3,7 @@
 // A unit is a (sequence, KV head, row tile): up to 256 query rows (a row is one query
 // token and one of the G query heads of the KV head; whole tokens, token-major) against
 // the positions its last token sees. Units lie on a line in the order sequence, KV head,
-// tile; a unit is kUnitCost positions (its query load and output) plus the positions its
+// tile; a unit is kPfUnitCost positions (its query load and output) plus the positions its
 // last row sees. Every CTA takes an equal stretch of the line; tile k of a unit (positions
 // 128k .. 128k + 127) belongs to the CTA whose stretch holds its first position. A unit
 // cut by a stretch's end becomes pieces that are merged by the last to finish. While stretches
@@ -26,6 +26,14 @@ constexpr int kPfTile = 128;          // positions of a KV tile
 // A unit's fixed cost, in positions (256 / 320 / 384 gave an 8192-token bf16 prompt 372 / 370 /
 // 360 us; 512 no less).
 constexpr int kPfUnitCost = 384;
+// Of a sequence whose unit fills one row tile at most (single decode rows): its tiles and outputs
+// take less. (With the same cost a chunk's CTAs end at 109 us, those of 31 decode rows beside it at
+// 88. 0 / 128 / 256 / 384 gave that batch 133 / 117 / 118 / 120 us, two chunks of 512 and 30 decode
+// rows over INT8 139 / 124 / 130 / 131.)
+constexpr int kPfUnitCostFew = 128;
+__device__ __forceinline__ int pf_unit_cost(int n, int group) {
+  return n * group <= 128 ? kPfUnitCostFew : kPfUnitCost;   // (n < 2^31 / num_q_heads)
+}
 constexpr int kPfWhole = 8 * kPfTile, kPfWholeShare = 2400;
 // A unit of more pieces is joined in groups first: one CTA that adds up 19 pieces of two full row
 // tiles takes 30 us at the call's end (64 tokens over 131008: 141 us against 122; 4 to 9 alike).
@@ -84,8 +92,9 @@ struct PfWalk {
   __device__ int past() const { return p.ctx - p.n; }
   __device__ int pastp() const { return max(past(), 0); }
   __device__ int len() const { return pastp() + min((p.t + 1) * a.unit_tokens, p.n); }
+  __device__ int cost() const { return pf_unit_cost(p.n, a.group); }
   __device__ void advance() {
-    p.ub += kPfUnitCost + len();
+    p.ub += cost() + len();
     if (++p.t * a.unit_tokens < p.n) return;
     p.t = 0;
     if (++p.h < a.num_kv_heads) return;
@@ -97,7 +106,7 @@ struct PfWalk {
     } while (p.n == 0);   // ub < b1 <= the line's end: another sequence with rows follows
   }
   __device__ int owner(int k) const {
-    return static_cast<int>((p.ub + kPfUnitCost + static_cast<long long>(kPfTile) * k) / st.share);
+    return static_cast<int>((p.ub + cost() + static_cast<long long>(kPfTile) * k) / st.share);
   }
 };
 
@@ -126,7 +135,7 @@ __device__ inline bool pf_piece(const PfWalk& w, volatile PfPiece* to) {
   const int G = w.a.group, qt = w.a.unit_tokens;
   const int j0 = w.p.t * qt, rows = min(qt, w.p.n - j0) * G;
   const int k_all = (w.len() + kPfTile - 1) / kPfTile;
-  const long long x0 = w.st.b0 - w.p.ub - kPfUnitCost, x1 = w.st.b1 - w.p.ub - kPfUnitCost;
+  const long long x0 = w.st.b0 - w.p.ub - w.cost(), x1 = w.st.b1 - w.p.ub - w.cost();
   int ka = x0 <= 0 ? 0 : static_cast<int>((x0 + kPfTile - 1) / kPfTile);
   int kx = x1 <= 0 ? 0 : static_cast<int>(min((x1 + kPfTile - 1) / kPfTile, static_cast<long long>(k_all)));
   if (w.len() <= kPfWhole && w.st.share < kPfWholeShare) {
@@ -181,10 +190,10 @@ __device__ inline bool pf_piece(const PfWalk& w, volatile PfPiece* to) {
 }
 
 // Line length of one KV head of a sequence: T units of cost + pastp + min((t+1) qt, n).
-__device__ __forceinline__ long long pf_head_len(int n, int pastp, int qt) {
+__device__ __forceinline__ long long pf_head_len(int n, int pastp, int qt, int group) {
   if (n == 0) return 0;
   const long long T = (n + qt - 1) / qt;
-  return T * (kPfUnitCost + pastp) + static_cast<long long>(qt) * ((T - 1) * T / 2) + n;
+  return T * (pf_unit_cost(n, group) + pastp) + static_cast<long long>(qt) * ((T - 1) * T / 2) + n;
 }
 
 // The CTA's start on the line. Every thread of the CTA takes part; scratch: one long long a
@@ -201,7 +210,7 @@ __device__ inline void pf_plan(const PrefillArgs& a, long long* scratch, PfStart
     const PrefillSeq p = prefill_seq(a, s);
     bad |= p.bad;
     cut |= p.n > 0 && max(p.ctx, p.n) > kPfWhole;   // its longest unit
-    mine += a.num_kv_heads * pf_head_len(p.n, max(p.past(), 0), a.unit_tokens);
+    mine += a.num_kv_heads * pf_head_len(p.n, max(p.past(), 0), a.unit_tokens, a.group);
   }
   if (bad && blockIdx.x == 0 && a.status) atomicOr(a.status, kDevBadCtx);
   long long incl = mine;
@@ -227,7 +236,7 @@ __device__ inline void pf_plan(const PrefillArgs& a, long long* scratch, PfStart
     for (int s = s0; s < s1; ++s) {
       const PrefillSeq p = prefill_seq(a, s);
       const int pastp = max(p.past(), 0), qt = a.unit_tokens;
-      const long long head = pf_head_len(p.n, pastp, qt);
+      const long long head = pf_head_len(p.n, pastp, qt, a.group);
       if (b0 >= at + a.num_kv_heads * head) {
         at += a.num_kv_heads * head;
         continue;
@@ -235,7 +244,7 @@ __device__ inline void pf_plan(const PrefillArgs& a, long long* scratch, PfStart
       const int h = static_cast<int>((b0 - at) / head);
       const long long rem = b0 - at - h * head;
       // the unit that holds position rem: units before t take t (cost + pastp) + qt t (t + 1) / 2
-      const long long c = kPfUnitCost + pastp;
+      const long long c = pf_unit_cost(p.n, a.group) + pastp;
       int lo = 0, hi = (p.n + qt - 1) / qt - 1;
 #pragma unroll 1
       while (lo < hi) {
