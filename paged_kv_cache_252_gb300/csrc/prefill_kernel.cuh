@@ -308,39 +308,38 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
   PfStart* start = reinterpret_cast<PfStart*>(smem + Sh::kMisc + 256);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (tid == 0) {
-#pragma unroll 1
-    for (int k = 0; k < NS; ++k) {
-      mbar_init(full + 8 * k, 4);
-      mbar_init(empty + 8 * k, 2);
-      mbar_init(v_tail + 8 * k, 1);
-      mbar_init(v_sent + 8 * k, 1);
+  if (warp == 0) {   // a lane for each index (one thread for all: 10.2 us a tiny call against 9.7)
+    if (lane < NS) {
+      mbar_init(full + 8 * lane, 4);
+      mbar_init(empty + 8 * lane, 2);
+      mbar_init(v_tail + 8 * lane, 1);
+      mbar_init(v_sent + 8 * lane, 1);
     }
-    mbar_init(q_full, Sh::kWiden ? 1 : 4);
-    mbar_init(q_empty, 2);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(s_full + 8 * i, 1);
-      mbar_init(p_ready + 8 * i, 4);
-      mbar_init(o_done + 8 * i, 1);
-      mbar_init(turn + 8 * i, 1);
+    if (lane < 2) {
+      mbar_init(s_full + 8 * lane, 1);
+      mbar_init(p_ready + 8 * lane, 4);
+      mbar_init(o_done + 8 * lane, 1);
+      mbar_init(turn + 8 * lane, 1);
     }
-#pragma unroll 1
-    for (int i = 0; i < Sh::kScaleRing; ++i) mbar_init(sc_full + 8 * i, 4);
-#pragma unroll 1
-    for (int i = 0; i < Sh::kRawRing; ++i) {
-      mbar_init(raw_full + 8 * i, 1);
-      mbar_init(raw_empty + 8 * i, 4);
+    if (lane < Sh::kScaleRing) mbar_init(sc_full + 8 * lane, 4);
+    if (lane < Sh::kRawRing) {
+      mbar_init(raw_full + 8 * lane, 1);
+      mbar_init(raw_empty + 8 * lane, 4);
     }
-    mbar_init(final_bar, 2);
-#pragma unroll 1
-    for (int i = 0; i < kPfRing; ++i) {
-      mbar_init(pc_full + 8 * i, 1);
-      mbar_init(pc_empty + 8 * i, Sh::kReaders);
+    if (lane < kPfRing) {
+      mbar_init(pc_full + 8 * lane, 1);
+      mbar_init(pc_empty + 8 * lane, Sh::kReaders);
     }
-    ctl->abort = 0;
-    ctl->busy = 0;
+    if (lane == 0) {
+      mbar_init(q_full, Sh::kWiden ? 1 : 4);
+      mbar_init(q_empty, 2);
+      mbar_init(final_bar, 2);
+      ctl->abort = 0;
+      ctl->busy = 0;
+    }
     fence_barrier_init();
-    mbar_arrive(turn);   // row tile 0 begins
+    __syncwarp();
+    if (lane == 0) mbar_arrive(turn);   // row tile 0 begins
   }
   if (warp == 8) {
     tmem_alloc(smem_addr(tmem_slot), 512);
