@@ -183,13 +183,6 @@ __device__ __forceinline__ void cp_async_wait_all() {
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// Groups of cp.async: close one; wait until at most N of this thread's are still under way.
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 // A 32-bit shared-memory load issued where it stands in the instruction stream
 // (volatile: the compiler does not sink it towards its first use), so that its
 // latency overlaps the work in between.
