@@ -37,9 +37,9 @@
 //   8192-token prompt    bf16 361 us, 1522 TFLOP/s: the products' operands and the softmax's
 //                        chain from scores to weights share the SM (tensor pipe busy 65 %), and
 //                        25 us are the ends of pieces; 16384 tokens 1320 us, 1666 TFLOP/s.
-//                        E5M2 436 us: widening, a second pass through shared memory (410 without
-//                        its stores). INT8 520 us: its row scales, two 16-byte reads a thread for
-//                        every four scores.
+//                        E5M2 422 us: widening, a second pass through shared memory (its stores
+//                        alone are 20 us). INT8 507 us: its row scales, two 16-byte reads a thread
+//                        for every four scores.
 //   100 tokens over a context of 130972 (bf16)   193 us, 537 MB read once: 80 us of memory time,
 //                        113 of products; rows fill 400 of 512.
 //   one token            10 us: five of launch and planning, five of one chain through the CTA.
@@ -70,11 +70,14 @@ struct PfShape {
   // Warps that read the pieces: eight softmax, two issuing, four loading, one more (warp 10).
   static constexpr int kReaders = 15;
   // Register budgets (per thread of a warpgroup); twice the first and the others make the
-  // launch's 512 x 128.
+  // launch's 512 x 128. What spills decides: an 8192-token E5M2 prompt takes 422 us with 64 for the
+  // issuing warps and 433 with 56, an INT8 one 507 with 184 / 64 / 80, 521 with 192 / 56 / 72 and 540
+  // with 192 / 64 / 64 (head size 64: 418, 397, 409).
   static constexpr int kLaunchRegs = 128;
-  static constexpr int kSoftmaxRegs = 192;
-  static constexpr int kIssueRegs = kWiden ? 56 : 72;
-  static constexpr int kLoadRegs = kWiden ? 72 : 56;
+  static constexpr bool kInt8Wide = KV == kKvInt8 && D == 128, kInt8Narrow = KV == kKvInt8 && D == 64;
+  static constexpr int kSoftmaxRegs = kInt8Wide ? 184 : 192;
+  static constexpr int kIssueRegs = kInt8Narrow ? 56 : (kWiden ? 64 : 72);
+  static constexpr int kLoadRegs = kInt8Wide ? 80 : (kInt8Narrow ? 72 : (kWiden ? 64 : 56));
   static_assert(2 * kSoftmaxRegs + kIssueRegs + kLoadRegs == 4 * kLaunchRegs, "register split");
   static constexpr int kStages = kWiden ? (D == 128 ? 4 : 8) : (D == 128 ? 5 : 10);
   static constexpr uint32_t kHalfBytes = kPfTile * 128;             // 64 dimensions of a KV tile
