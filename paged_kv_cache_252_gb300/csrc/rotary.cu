@@ -11,7 +11,7 @@
 // Angles. p * inv_freq reaches 10^6 rad, where an fp32 product is off by 0.03 rad. One
 // turn is 2^64 here: each CTA converts inv_freq / 2 pi once to a 64-bit fraction of a turn
 // per position (fp64), and p times that step modulo 2^64 is the angle, the whole turns
-// gone exactly; its top bits as an fp32 number of half turns go to sincospif. The fp64 unit
+// gone exactly; quarter turns taken off, the rest as two fp32 numbers goes to sincospif. The fp64 unit
 // is left with rotary_dim / 2 operations a CTA instead of one chain per (token, pair).
 //
 // Work. A row of D dimensions is D/16 items: an item is one pair of 16-byte chunks, eight
@@ -21,11 +21,11 @@
 // through shared memory once, and the tile's items (all heads of q, key and value) are
 // spread over its threads. The D/16 lanes of one row are neighbours in a warp, which
 // gives the INT8 writer its row maximum by shuffles. The next tile's angles are worked out while
-// this tile's rows are under way (8192 tokens 42 us without, 36.7 with).
+// this tile's rows are under way (8192 tokens 42 us without, 37 with).
 //
 // Bound by memory, a step of few tokens by its launch. Measured, 32 query and 8 KV heads of 128:
-// 8192 bf16 tokens 36.7 us, 5.5 TB/s (a copy reaches 6.77); 64 tokens 2.9 us. 2001 fp16 tokens of
-// 16 + 4 heads of 64, half of each rotated: 4.9 us.
+// 8192 bf16 tokens 37 us, 5.4 TB/s (a copy reaches 6.77); 64 tokens 3 us. 2001 fp16 tokens of
+// 16 + 4 heads of 64, half of each rotated: 5 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -135,9 +135,26 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const RotaryArgs
       const int t = i / pairs, j = i - t * pairs;
       const long long p = a.pos64 ? static_cast<const long long*>(a.positions)[t0 + t]
                                   : static_cast<const int32_t*>(a.positions)[t0 + t];
-      const long long phase = static_cast<long long>(static_cast<unsigned long long>(p) * step[j]);
-      float s, c;
-      sincospif(__ll2float_rn(phase) * 1.0842021724855044e-19f, &s, &c);   // 2^-63: half turns in [-1, 1]
+      const unsigned long long phase = static_cast<unsigned long long>(p) * step[j];
+      // Quarter turns apart (exactly), the rest r within an eighth of a turn as hi + lo: rounded to
+      // one fp32 number, an angle near half a turn would be off by more than the fp32 cosine (of 15.7 M
+      // E5M2 keys 27 fell on the wrong side of a rounding border, 11 so; of fp64 cosines 12).
+      const unsigned quarter = static_cast<unsigned>((phase + (1ull << 61)) >> 62);
+      const long long rest = static_cast<long long>(phase - (static_cast<unsigned long long>(quarter) << 62));
+      const float hi = __ll2float_rn(rest), lo = __ll2float_rn(rest - __float2ll_rn(hi));
+      float s0, c0;
+      sincospif(hi * 1.0842021724855044e-19f, &s0, &c0);   // 2^-63: half turns in [-1/4, 1/4]
+      const float e = lo * 3.4061215800865545e-19f;        // 2^-63 pi: sin(r + e) = sin r + e cos r, e^2 below 2^-48
+      float s = fmaf(e, c0, s0), c = fmaf(-e, s0, c0);
+      if (quarter & 1) {
+        const float t = c;
+        c = -s;
+        s = t;
+      }
+      if (quarter & 2) {
+        c = -c;
+        s = -s;
+      }
       cs[t * pairs + j] = make_float2(c * a.factor, s * a.factor * a.sign);
     }
   };
