@@ -384,17 +384,18 @@ int pkv_paged_attention_decode_chunked(void* out, const void* q, const int32_t* 
  * pkv_kv_cache_write / _int8 do (slot -1 skips the cache write, not the query; other
  * out-of-range slots are skipped and flagged PKV_DEV_BAD_SLOT; two tokens on one slot
  * race). Allowed (src_dtype, kv_dtype): (FP16, FP16), (BF16, BF16), (FP16, FP8_E5M2),
- * (FP16, INT8; with `scales`, else NULL). A turned key goes from fp32 to the cache's type in
- * one rounding (a pkv_rotary_embed followed by a cache write rounds to 16 bits between). */
+ * (FP16, INT8; with `scales`, else NULL). A turned key goes to the cache's type in one
+ * rounding (a pkv_rotary_embed followed by a cache write rounds to 16 bits between): from fp32, an
+ * E5M2 key that fp32 cannot place beside a rounding border from fp64. */
 int pkv_rotary_embed(void* out, int64_t out_stride, const void* x, int64_t x_stride, pkv_dtype dtype,
                      int32_t num_tokens, int32_t num_heads, int32_t head_size, const void* positions,
                      int32_t position_bytes, const double* inv_freq, int32_t rotary_dim, int32_t interleaved,
-                     float attn_factor, int32_t inverse, void* stream);
+                     double attn_factor, int32_t inverse, void* stream);
 int pkv_rotary_write(void* q_out, int64_t q_out_stride, const void* q, int64_t q_stride, const void* key,
                      int64_t key_stride, const void* value, int64_t value_stride, pkv_dtype src_dtype,
                      int32_t num_tokens, int32_t num_q_heads, const void* positions, int32_t position_bytes,
                      const int32_t* slot_mapping, const double* inv_freq, int32_t rotary_dim, int32_t interleaved,
-                     float attn_factor, void* k_cache, void* v_cache, float* scales, pkv_dtype kv_dtype,
+                     double attn_factor, void* k_cache, void* v_cache, float* scales, pkv_dtype kv_dtype,
                      const pkv_cache_desc* cache, int32_t* device_status, void* stream);
 
 /* ==== Attention of a chunk of new tokens (prefill) ============================

@@ -128,10 +128,10 @@ def load_library(path: str | None = None):
             ctypes.c_size_t, vp, vp]
         lib.pkv_paged_attention_decode_chunked.restype = ctypes.c_int
         cint, f32 = ctypes.c_int, ctypes.c_float
-        lib.pkv_rotary_embed.argtypes = [vp, i64, vp, i64, cint, i32, i32, i32, vp, i32, vp, i32, i32, f32, i32, vp]
+        lib.pkv_rotary_embed.argtypes = [vp, i64, vp, i64, cint, i32, i32, i32, vp, i32, vp, i32, i32, ctypes.c_double, i32, vp]
         lib.pkv_rotary_embed.restype = cint
         lib.pkv_rotary_write.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, cint, i32, i32, vp, i32, vp, vp, i32,
-                                         i32, f32, vp, vp, vp, cint, P(_CacheDesc), vp, vp]
+                                         i32, ctypes.c_double, vp, vp, vp, cint, P(_CacheDesc), vp, vp]
         lib.pkv_rotary_write.restype = cint
         lib.pkv_prefill_workspace_bytes.argtypes = [i32, i32, i32, P(_CacheDesc)]
         lib.pkv_prefill_workspace_bytes.restype = ctypes.c_size_t

@@ -25,7 +25,8 @@
 //
 // Bound by memory, a step of few tokens by its launch. Measured, 32 query and 8 KV heads of 128:
 // 8192 bf16 tokens 37 us, 5.4 TB/s (a copy reaches 6.77); 64 tokens 3 us. 2001 fp16 tokens of
-// 16 + 4 heads of 64, half of each rotated: 5 us.
+// 16 + 4 heads of 64, half of each rotated: 5 us. 512 tokens of 64 + 8 heads to an E5M2 cache: 9.9
+// us, 6.9 with fp32 alone, which puts 11 of 15.7 M keys on the wrong side of a rounding border.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -66,6 +67,7 @@ struct RotaryArgs {
   int32_t tile;                // tokens of a CTA's tile
   int32_t pos64, interleaved;
   float factor, sign;          // sign -1 turns the other way
+  double factor64;
 };
 
 template <bool BF16>
@@ -93,9 +95,70 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// An item's E5M2 key bytes where fp32 leaves open on which side of a rounding border a value
+// lies: `low` and `high` are the bytes of the values less and plus fp32's error; pairs in which they
+// differ are turned again in fp64. Elements by their order in the item (first chunk, then second).
+__device__ __noinline__ uint4 rotary_e5m2_exact(uint4 va, uint4 vb, uint4 low, uint4 high, unsigned long long pos,
+                                                const unsigned long long* step, int interleaved, double factor,
+                                                double sign) {
+  const uint32_t src[8] = {va.x, va.y, va.z, va.w, vb.x, vb.y, vb.z, vb.w};
+  uint32_t w[4] = {low.x, low.y, low.z, low.w};
+  const uint32_t u[4] = {high.x, high.y, high.z, high.w};
+  auto value = [&](int e) {
+    return static_cast<double>(__half2float(__ushort_as_half(static_cast<unsigned short>(src[e >> 1] >> (16 * (e & 1))))));
+  };
+  auto differs = [&](int e) { return (((w[e >> 2] ^ u[e >> 2]) >> (8 * (e & 3))) & 0xFFu) != 0; };
+  auto put = [&](int e, double y) {
+    // fp64 -> fp32 with the dropped bits kept in the last one, so that the next rounding is the only one
+    float f = __double2float_rz(y);
+    if (static_cast<double>(f) != y) f = __uint_as_float(__float_as_uint(f) | 1u);
+    const uint32_t byte = e5m2x2_of_f32(f, 0.f) & 0xFFu;
+    w[e >> 2] = (w[e >> 2] & ~(0xFFu << (8 * (e & 3)))) | (byte << (8 * (e & 3)));
+  };
+#pragma unroll 1
+  for (int k = 0; k < 8; ++k) {
+    const int e0 = interleaved ? 2 * k : k, e1 = interleaved ? 2 * k + 1 : 8 + k;
+    if (!differs(e0) && !differs(e1)) continue;
+    // Quarter turns apart; of the rest z, at most pi / 4, the Taylor sums of sine to z^13 and cosine
+    // to z^14 (2 10^-14 off).
+    const unsigned long long phase = pos * step[k];
+    const unsigned quarter = static_cast<unsigned>((phase + (1ull << 61)) >> 62);
+    const double z = static_cast<double>(static_cast<long long>(phase - (static_cast<unsigned long long>(quarter) << 62))) *
+                     3.4061215800865545e-19;   // 2^-63 pi
+    const double zz = z * z;
+    double sn = 1.0 / 6227020800.0, cn = -1.0 / 87178291200.0;
+    sn = fma(sn, zz, -1.0 / 39916800.0);
+    cn = fma(cn, zz, 1.0 / 479001600.0);
+    sn = fma(sn, zz, 1.0 / 362880.0);
+    cn = fma(cn, zz, -1.0 / 3628800.0);
+    sn = fma(sn, zz, -1.0 / 5040.0);
+    cn = fma(cn, zz, 1.0 / 40320.0);
+    sn = fma(sn, zz, 1.0 / 120.0);
+    cn = fma(cn, zz, -1.0 / 720.0);
+    sn = fma(sn, zz, -1.0 / 6.0);
+    cn = fma(cn, zz, 1.0 / 24.0);
+    sn = fma(sn * zz, z, z);
+    cn = fma(fma(cn, zz, -0.5), zz, 1.0);
+    if (quarter & 1) {
+      const double t = cn;
+      cn = -sn;
+      sn = t;
+    }
+    if (quarter & 2) {
+      cn = -cn;
+      sn = -sn;
+    }
+    sn *= sign;
+    const double re = value(e0), im = value(e1);
+    put(e0, factor * (re * cn - im * sn));
+    put(e1, factor * (re * sn + im * cn));
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // KV: the cache's element type (kKvBf16 means bf16 rows everywhere, the others fp16 rows).
 template <int KV>
-__global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const RotaryArgs a) {
+__global__ void __launch_bounds__(kRotaryThreads, KV == kKvE5m2 ? 4 : 0) rotary_kernel(const RotaryArgs a) {
   constexpr bool BF16 = KV == kKvBf16;
   __shared__ unsigned long long step[kRotaryMaxPairs];
   __shared__ float2 cs2[2][kRotaryMaxTokens * kRotaryMaxPairs];
@@ -138,7 +201,7 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const RotaryArgs
       const unsigned long long phase = static_cast<unsigned long long>(p) * step[j];
       // Quarter turns apart (exactly), the rest r within an eighth of a turn as hi + lo: rounded to
       // one fp32 number, an angle near half a turn would be off by more than the fp32 cosine (of 15.7 M
-      // E5M2 keys 27 fell on the wrong side of a rounding border, 11 so; of fp64 cosines 12).
+      // keys rounded to E5M2 27 fell on the wrong side of a border, 11 so; of fp64 cosines 12).
       const unsigned quarter = static_cast<unsigned>((phase + (1ull << 61)) >> 62);
       const long long rest = static_cast<long long>(phase - (static_cast<unsigned long long>(quarter) << 62));
       const float hi = __ll2float_rn(rest), lo = __ll2float_rn(rest - __float2ll_rn(hi));
@@ -235,11 +298,43 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const RotaryArgs
           uint8_t* dst = static_cast<uint8_t*>(cache) + crow * D;
           uint2 w1, w2;
           if (turn) {
-            // from fp32 in one rounding
-            w1.x = e5m2x2_of_f32(x[0], x[1]) | (e5m2x2_of_f32(x[2], x[3]) << 16);
-            w1.y = e5m2x2_of_f32(x[4], x[5]) | (e5m2x2_of_f32(x[6], x[7]) << 16);
-            w2.x = e5m2x2_of_f32(y[0], y[1]) | (e5m2x2_of_f32(y[2], y[3]) << 16);
-            w2.y = e5m2x2_of_f32(y[4], y[5]) | (e5m2x2_of_f32(y[6], y[7]) << 16);
+            // From fp32 in one rounding where its error d does not reach a border; one of 10^5 elements
+            // does. d is 2^-22 (|re| + |im|): the cosine and sine are within 2^-24 (sincospif), their
+            // correction and the factor's three roundings add 3/2 of it, the products' and this sum's as much.
+            float ox[8], oy[8];
+            unpack8<BF16>(va[b], ox);
+            unpack8<BF16>(vb[b], oy);
+            const float eps = fabsf(a.factor) * 2.384185791015625e-7f;
+            uint32_t low[4], high[4];
+#pragma unroll
+            for (int k = 0; k < 8; k += 2) {
+              float dx[2], dy[2];
+              if (a.interleaved) {
+                dx[0] = dx[1] = (fabsf(ox[k]) + fabsf(ox[k + 1])) * eps;
+                dy[0] = dy[1] = (fabsf(oy[k]) + fabsf(oy[k + 1])) * eps;
+              } else {
+                dx[0] = dy[0] = (fabsf(ox[k]) + fabsf(oy[k])) * eps;
+                dx[1] = dy[1] = (fabsf(ox[k + 1]) + fabsf(oy[k + 1])) * eps;
+              }
+              const uint32_t lx = e5m2x2_of_f32(x[k] - dx[0], x[k + 1] - dx[1]);
+              const uint32_t hx = e5m2x2_of_f32(x[k] + dx[0], x[k + 1] + dx[1]);
+              const uint32_t ly = e5m2x2_of_f32(y[k] - dy[0], y[k + 1] - dy[1]);
+              const uint32_t hy = e5m2x2_of_f32(y[k] + dy[0], y[k + 1] + dy[1]);
+              const int at = k >> 2, sh = (k & 2) * 8;
+              low[at] = sh ? low[at] | (lx << 16) : lx;
+              high[at] = sh ? high[at] | (hx << 16) : hx;
+              low[2 + at] = sh ? low[2 + at] | (ly << 16) : ly;
+              high[2 + at] = sh ? high[2 + at] | (hy << 16) : hy;
+            }
+            uint4 w = make_uint4(low[0], low[1], low[2], low[3]);
+            if ((low[0] ^ high[0]) | (low[1] ^ high[1]) | (low[2] ^ high[2]) | (low[3] ^ high[3])) {
+              const long long p = a.pos64 ? static_cast<const long long*>(a.positions)[t0 + t]
+                                          : static_cast<const int32_t*>(a.positions)[t0 + t];
+              w = rotary_e5m2_exact(va[b], vb[b], w, make_uint4(high[0], high[1], high[2], high[3]),
+                                    static_cast<unsigned long long>(p), step + 8 * c, a.interleaved, a.factor64, a.sign);
+            }
+            w1 = make_uint2(w.x, w.y);
+            w2 = make_uint2(w.z, w.w);
           } else {
             w1 = make_uint2(e5m2x4(va[b].x, va[b].y), e5m2x4(va[b].z, va[b].w));
             w2 = make_uint2(e5m2x4(vb[b].x, vb[b].y), e5m2x4(vb[b].z, vb[b].w));
@@ -286,13 +381,13 @@ using namespace pkv;
 
 // Arguments both entry points share: types, sizes, alignment. Token strides are in elements.
 int rotary_common(RotaryArgs* a, pkv_dtype dtype, int32_t num_tokens, int32_t head_size, const void* positions,
-                  int32_t position_bytes, const double* inv_freq, int32_t rotary_dim, float attn_factor) {
+                  int32_t position_bytes, const double* inv_freq, int32_t rotary_dim, double attn_factor) {
   if (dtype != PKV_FP16 && dtype != PKV_BF16) return PKV_ERR_UNSUPPORTED;
   if (num_tokens < 0) return PKV_ERR_INVALID_ARGUMENT;
   if (head_size != 64 && head_size != 128) return PKV_ERR_UNSUPPORTED;
   if (rotary_dim < 16 || rotary_dim > head_size || rotary_dim % 16 != 0) return PKV_ERR_UNSUPPORTED;
   if (position_bytes != 4 && position_bytes != 8) return PKV_ERR_INVALID_ARGUMENT;
-  if (!std::isfinite(attn_factor)) return PKV_ERR_INVALID_ARGUMENT;
+  if (!std::isfinite(static_cast<float>(attn_factor))) return PKV_ERR_INVALID_ARGUMENT;
   if (num_tokens > 0 && (!positions || !inv_freq)) return PKV_ERR_INVALID_ARGUMENT;
   if (!aligned_to(positions, static_cast<uintptr_t>(position_bytes)) || !aligned_to(inv_freq, 8))
     return PKV_ERR_INVALID_ARGUMENT;
@@ -303,7 +398,8 @@ int rotary_common(RotaryArgs* a, pkv_dtype dtype, int32_t num_tokens, int32_t he
   a->items_row = head_size / 16;
   a->log_items_row = head_size == 128 ? 3 : 2;
   a->rot_items = rotary_dim / 16;
-  a->factor = attn_factor;
+  a->factor = static_cast<float>(attn_factor);
+  a->factor64 = attn_factor;
   a->sign = 1.f;
   return PKV_OK;
 }
@@ -339,7 +435,7 @@ extern "C" {
 int pkv_rotary_embed(void* out, int64_t out_stride, const void* x, int64_t x_stride, pkv_dtype dtype,
                      int32_t num_tokens, int32_t num_heads, int32_t head_size, const void* positions,
                      int32_t position_bytes, const double* inv_freq, int32_t rotary_dim, int32_t interleaved,
-                     float attn_factor, int32_t inverse, void* stream) {
+                     double attn_factor, int32_t inverse, void* stream) {
   RotaryArgs a{};
   if (int rc = rotary_common(&a, dtype, num_tokens, head_size, positions, position_bytes, inv_freq, rotary_dim,
                              attn_factor))
@@ -363,7 +459,7 @@ int pkv_rotary_write(void* q_out, int64_t q_out_stride, const void* q, int64_t q
                      int64_t key_stride, const void* value, int64_t value_stride, pkv_dtype src_dtype,
                      int32_t num_tokens, int32_t num_q_heads, const void* positions, int32_t position_bytes,
                      const int32_t* slot_mapping, const double* inv_freq, int32_t rotary_dim, int32_t interleaved,
-                     float attn_factor, void* k_cache, void* v_cache, float* scales, pkv_dtype kv_dtype,
+                     double attn_factor, void* k_cache, void* v_cache, float* scales, pkv_dtype kv_dtype,
                      const pkv_cache_desc* cache, int32_t* device_status, void* stream) {
   if (!cache_desc_ok(cache)) return PKV_ERR_INVALID_ARGUMENT;
   const bool pair_ok = (src_dtype == PKV_FP16 && (kv_dtype == PKV_FP16 || kv_dtype == PKV_FP8_E5M2 ||

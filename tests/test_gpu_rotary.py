@@ -186,6 +186,27 @@ def test_write_matches_64_bits(dev, kv, T, hq, hkv, D, rot, inter, packed):
     assert torch.equal(rows(kc)[rest], rows(k0)[rest])
 
 
+@pytest.mark.parametrize("inter", [False, True], ids=["halves", "pairs"])
+@pytest.mark.parametrize("scaling", [None, "ramp"])
+def test_e5m2_keys_are_the_nearest_to_the_64_bit_value(dev, inter, scaling):
+    """8.4 million keys, of which fp32 would place several on the wrong side of a rounding border: codes
+    equal those of the 64-bit value (its own error, 2^-53 of an angle of 2e4 rad, reaches a border
+    in fewer than one of 10^9)."""
+    import paged_kv_cache_252_gb300 as pkv
+    T, hkv, D = 8192, 8, 128
+    q, key, value, slots, kc, vc, _ = _write_case(dev, "e5m2", T, 1, hkv, D, 77)
+    inv, f = pkv.rotary_inv_freq(D, 10000.0, scaling=scaling, factor=4.0, original_context=4096, device=dev)
+    pos = torch.arange(16384, 16384 + T, device=dev, dtype=torch.int32)
+    pkv.rotary_write(torch.empty_like(q, memory_format=torch.contiguous_format), q, key, value, pos, slots, kc, vc, inv,
+                     interleaved=inter, attn_factor=f)
+    want = op.turn(key, pos, inv, inter, f)
+    # nearest E5M2 value: two fraction bits, steps of 2^-16 below 2^-14, at most 57344
+    step = torch.exp2(torch.frexp(want)[1].double().sub(3).clamp(min=-16))
+    want = (want / step).round().mul(step).clamp(-57344, 57344)
+    got = op.cache_rows(kc).transpose(1, 2).reshape(-1, hkv, D)[slots.long()]
+    assert int((got != want).sum()) == 0
+
+
 @pytest.mark.parametrize("kv", ["e5m2", "int8"])
 def test_zero_angle_writes_what_the_cache_write_writes(dev, kv):
     """At position 0 nothing turns: bit for bit the plain cache write, extreme values included."""
