@@ -423,8 +423,8 @@ int pkv_rotary_write(void* q_out, int64_t q_out_stride, const void* q, int64_t q
  *                 decode calls: contents need no initialisation, calls in flight at the
  *                 same time must not share one, and a captured call may be replayed.
  *   num_q_heads / num_kv_heads <= 64; num_q_rows * num_q_heads < 2^31.
- * Scores, softmax statistics and sums are fp32; the probabilities enter the P V product in
- * the query type. What lies behind a row's last visible position, in its blocks or in
+ * Scores, softmax statistics and sums are fp32; the probabilities (over an INT8 cache times
+ * their row's V scale) enter the P V product in the query type. What lies behind a row's last visible position, in its blocks or in
  * later tokens of its chunk, does not reach it, infinities and NaN included. */
 size_t pkv_prefill_workspace_bytes(int32_t num_q_rows, int32_t num_seqs, int32_t num_q_heads,
                                    const pkv_cache_desc* cache);

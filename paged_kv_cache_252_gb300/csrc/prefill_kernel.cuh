@@ -26,10 +26,14 @@
 // The running maximum moves only when a score exceeds it by more than kSlack (base 2) and a
 // tile's weights so sum to more than kMostSum = 2^(kSlack + kShift): O is rescaled a few times a
 // row, not every tile. fp16 weights carry a shift of 2^7: they stay at or below 2^15, and weights
-// down to 2^-21 of the largest keep full precision. An INT8 cache's V scale enters the weight
-// with it (at most 516, so the shift is 6, and a maximum that moves moves to the largest score);
-// its K scale multiplies the scores. The weights' rounding to 16 bits is the products' operand
-// type; scores, sums and O stay fp32.
+// down to 2^-21 of the largest keep full precision. An INT8 cache's K scale multiplies the scores,
+// its V scale the weight, and the product is what is rounded to fp16. So that these products keep full
+// precision down to 2^-18 of the largest whatever the scales' size, m there is the largest sum of a
+// score and its V scale's exponent, and l and O carry that factor. (Under the largest score alone, with
+// a shift for the largest scale an fp16 row gives, 516, values of at most 0.0025 left weights of 2^-12
+// of the largest no bits at all. The exponents cost an 8192-token prompt 1 %.) Their shift is 2^5: m has
+// no slack there, so products may come to 65504 before it moves. The weights' rounding to 16 bits is the products' operand type; scores,
+// sums and O stay fp32.
 //
 // Measured (32 query heads on 8 KV heads of 128 dimensions; a large library product of bf16
 // reaches 1895 TFLOP/s). A KV tile against two row tiles is 2050 cycles of products; it takes
@@ -71,13 +75,13 @@ struct PfShape {
   static constexpr int kReaders = 15;
   // Register budgets (per thread of a warpgroup); twice the first and the others make the
   // launch's 512 x 128. What spills decides: an 8192-token E5M2 prompt takes 422 us with 64 for the
-  // issuing warps and 433 with 56, an INT8 one 507 with 184 / 64 / 80, 521 with 192 / 56 / 72 and 540
-  // with 192 / 64 / 64 (head size 64: 418, 397, 409).
+  // issuing warps and 433 with 56, an INT8 one 511 with 184 / 64 / 80 and 527 with 192 / 48 / 80, of
+  // head size 64 426 and 405.
   static constexpr int kLaunchRegs = 128;
   static constexpr bool kInt8Wide = KV == kKvInt8 && D == 128, kInt8Narrow = KV == kKvInt8 && D == 64;
   static constexpr int kSoftmaxRegs = kInt8Wide ? 184 : 192;
-  static constexpr int kIssueRegs = kInt8Narrow ? 56 : (kWiden ? 64 : 72);
-  static constexpr int kLoadRegs = kInt8Wide ? 80 : (kInt8Narrow ? 72 : (kWiden ? 64 : 56));
+  static constexpr int kIssueRegs = kInt8Narrow ? 48 : (kWiden ? 64 : 72);
+  static constexpr int kLoadRegs = KV == kKvInt8 ? 80 : (kWiden ? 64 : 56);
   static_assert(2 * kSoftmaxRegs + kIssueRegs + kLoadRegs == 4 * kLaunchRegs, "register split");
   static constexpr int kStages = kWiden ? (D == 128 ? 4 : 8) : (D == 128 ? 5 : 10);
   static constexpr uint32_t kHalfBytes = kPfTile * 128;             // 64 dimensions of a KV tile
@@ -89,8 +93,9 @@ struct PfShape {
   static constexpr uint32_t kQHalfBytes = kPfRows * 128;
   static constexpr uint32_t kQBytes = kHalves * kQHalfBytes;
   static constexpr float kSlack = KV == kKvInt8 ? 0.f : 8.f;
-  static constexpr float kShift = KV == kKvBf16 ? 0.f : (KV == kKvInt8 ? 6.f : 7.f);
-  static constexpr float kMostSum = KV == kKvBf16 ? 256.f : 32768.f;   // 2^(slack + shift)
+  static constexpr float kShift = KV == kKvBf16 ? 0.f : (KV == kKvInt8 ? 5.f : 7.f);
+  // 2^(slack + shift); over INT8 the most the products may come to.
+  static constexpr float kMostSum = KV == kKvBf16 ? 256.f : (KV == kKvInt8 ? 65504.f : 32768.f);
   // Row scales of an INT8 cache's tiles: tile t + kScaleRing is written once the K stage of
   // tile t + kScaleRing - kStages / 2 is released, which is after the softmax of the tile before
   // that one, so tile t's are no longer read when kScaleRing > kStages / 2.
@@ -186,8 +191,14 @@ __device__ __forceinline__ void pf_mask(uint32_t (&sv)[4][32], int vis) {
   }
 }
 
-// The largest of 128 scores times c (an INT8 cache's: times their K scales, which hold c):
-// eight chains.
+// The exponent e of a V scale below 2^e (as a number of 2^23 plus its field); -31 at least: 127 times a
+// smaller one is half of the least step of an fp16 output.
+__device__ __forceinline__ float scale_exponent(float v) {
+  return __uint_as_float((__float_as_uint(fmaxf(v, 0x1p-32f)) >> 23) | 0x4B000000u) - (8388608.f + 126.f);
+}
+
+// The largest of 128 scores times c (an INT8 cache's: times their K scales, which hold c, plus their V
+// scales' exponents): eight chains.
 template <int KV>
 __device__ __forceinline__ float pf_max(const uint32_t (&sv)[4][32], float c, const float4* k_scales) {
   float mx[8];
@@ -198,9 +209,11 @@ __device__ __forceinline__ float pf_max(const uint32_t (&sv)[4][32], float c, co
     for (int g = 0; g < 4; ++g) {
 #pragma unroll
       for (int e = 0; e < 32; e += 4) {
-        const float4 f = k_scales[8 * g + e / 4];
-        const float x = __uint_as_float(sv[g][e]) * f.x, y = __uint_as_float(sv[g][e + 1]) * f.y;
-        const float z = __uint_as_float(sv[g][e + 2]) * f.z, w = __uint_as_float(sv[g][e + 3]) * f.w;
+        const float4 f = k_scales[8 * g + e / 4], v = k_scales[kPfTile / 4 + 8 * g + e / 4];
+        const float x = fmaf(__uint_as_float(sv[g][e]), f.x, scale_exponent(v.x));
+        const float y = fmaf(__uint_as_float(sv[g][e + 1]), f.y, scale_exponent(v.y));
+        const float z = fmaf(__uint_as_float(sv[g][e + 2]), f.z, scale_exponent(v.z));
+        const float w = fmaf(__uint_as_float(sv[g][e + 3]), f.w, scale_exponent(v.w));
         mx[2 * g] = max3(mx[2 * g], x, y);
         mx[2 * g + 1] = max3(mx[2 * g + 1], z, w);
       }
