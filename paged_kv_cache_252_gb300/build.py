@@ -8,7 +8,8 @@ the driver's tensor-map encoder is looked up at run time).
 A profiling variant, ``libpagedkv_timeline.so`` (objects under ``_build_timeline/``),
 is the same library compiled with ``-DPKV_TIMELINE``: its decode kernels record
 per-CTA event times (``csrc/pkv_timeline.cuh``; driven by ``timeline.py``). The
-product library never contains that code.
+product library never contains that code. ``libpagedkv_giveup.so`` (``-DPKV_GIVE_UP``) is the
+build in which a test has chosen warps of the prefill kernel give up a wait, as if its limit had run out.
 
 Usage: ``python -m paged_kv_cache_252_gb300.build [--verbose-ptxas] [--timeline]``
 """
@@ -31,6 +32,7 @@ VARIANTS = {  # name -> (object dir, library, extra nvcc flags)
     "": (OUT_DIR, LIB, []),
     "timeline": (os.path.join(HERE, "_build_timeline"), os.path.join(HERE, "libpagedkv_timeline.so"),
                  ["-DPKV_TIMELINE"]),
+    "giveup": (os.path.join(HERE, "_build_giveup"), os.path.join(HERE, "libpagedkv_giveup.so"), ["-DPKV_GIVE_UP"]),
 }
 
 SOURCES = ["capi.cu", "kv_cache_write.cu", "decode_f16.cu", "decode_bf16.cu", "decode_e5m2.cu",

@@ -389,14 +389,15 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
       bool alive = true;
       uint32_t cnt = 0, done = 0;                   // tiles and pieces of this row tile so far
       uint32_t seen = 0;                            // KV tiles of the CTA so far (INT8 scale ring)
+      auto give_up = [&] {
+        alive = false;
+        ctl->abort = 1;
+        if (lane == 0 && a.status) atomicOr(a.status, kDevTimeout);
+      };
       auto wait = [&](uint32_t bar, uint32_t parity) {
         if (!alive) return;
         const bool ok = pf_wait(bar, parity, ctl);
-        if (!__all_sync(0xffffffffu, ok)) {
-          alive = false;
-          ctl->abort = 1;
-          if (lane == 0 && a.status) atomicOr(a.status, kDevTimeout);
-        }
+        if (!__all_sync(0xffffffffu, ok)) give_up();
       };
       // The unit's row is fixed: query token tok behind the unit's first, query head hd of the group.
       const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
@@ -494,8 +495,19 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
         }
 
         // ---- end of the piece ----
+#ifdef PKV_GIVE_UP
+        // (the build that tests this path: status[1] names softmax warps whose wait here runs out)
+        if (a.status && (a.status[1] >> warp & 1)) give_up();
+#endif
         wait(bar_o, done++ & 1);
-        if (alive) tc_fence_after_sync();
+        const int pieces = pc->pieces[i], first_cta = pc->first[i], own = pieces > 1 ? blockIdx.x - first_cta : 0;
+        // A wait may have given up in one warp and not in its neighbour. Over a cut unit's piece they go
+        // on as one: the join meets at barriers, and a piece that is counted must have been stored whole.
+        if (pieces > 1 ? bar_red_or(1 + i, 128, !alive) : !alive) {
+          alive = false;
+          continue;   // to the barrier that ends it for all four
+        }
+        tc_fence_after_sync();
         const bool real = ru < pc->rows;
         uint16_t* dst = static_cast<uint16_t*>(a.out) +
                         (static_cast<size_t>(pc->qb + pc->j0 + tok) * a.num_q_heads + pc->h * a.group + hd) * D;
@@ -503,7 +515,6 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
         // The row's result is the sum over its unit's pieces p of w_p O_p, in their order, over that
         // of w_p l_p: this piece's O from tensor memory, others' (of a cut unit, for the last
         // to finish) from their slots.
-        const int pieces = pc->pieces[i], first_cta = pc->first[i], own = pieces > 1 ? blockIdx.x - first_cta : 0;
         const size_t slot_sz = pf_slot_floats(D);
         auto slot_of = [&](int p) {
           return a.partials + (static_cast<size_t>(2 * (first_cta + p) + (p == 0 ? 1 : 0)) * a.slot_tiles + i) * slot_sz;
@@ -521,7 +532,7 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
         }
 #pragma unroll 1
         for (;;) {
-          bool write = alive, last = true;
+          bool write = true, last = true;
           float M = m, mu = m == -INFINITY ? 0.f : m, L = l;   // w_p = 2^(m_p - mu)
           if (n > 1) {
             // (A group's count is at its first CTA, the first group's at the next one: no other unit
@@ -539,20 +550,18 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
             named_bar_sync(1 + i, 128);
             last = last_piece[i] != 0;
             if (!last) {
-              if (alive) {
-                float* sl = slot_of(lo + step * x);
-                if (real) {
-                  sl[r] = m;
-                  sl[128 + r] = l;
-                }
+              float* sl = slot_of(lo + step * x);
+              if (real) {
+                sl[r] = m;
+                sl[128 + r] = l;
+              }
 #pragma unroll 1
-                for (int e = 0; e < D; e += 32) {
-                  uint32_t ov[32];
-                  tmem_ld32(o_col + e, ov);
-                  if (real) {
+              for (int e = 0; e < D; e += 32) {
+                uint32_t ov[32];
+                tmem_ld32(o_col + e, ov);
+                if (real) {
 #pragma unroll
-                    for (int x = 0; x < 32; x += 8) st_global_v8(sl + 256 + ((e + x) / 8 * 128 + r) * 8, ov + x);
-                  }
+                  for (int x = 0; x < 32; x += 8) st_global_v8(sl + 256 + ((e + x) / 8 * 128 + r) * 8, ov + x);
                 }
               }
               named_bar_sync(1 + i, 128);
@@ -574,7 +583,7 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
               last = last_piece[i] != 0;
             }
             named_bar_sync(1 + i, 128);   // read before the next piece's flag
-            write = alive && last && !few;
+            write = last && !few;
             if (write && real) {
 #pragma unroll 4
               for (int y = 0; y < n; ++y) M = fmaxf(M, y == x ? m : slot_of(lo + step * y)[r]);
@@ -586,7 +595,7 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
                 L = y == x ? fmaf(l, fast_exp2(m - mu), L) : fmaf(sl[128 + r], fast_exp2(sl[r] - mu), L);
               }
             }
-            if (last && alive && few) {
+            if (last && few) {
               // Few rows (single decode rows over a long context): items of 8 dimensions of one row,
               // spread over the 128 threads, all pieces from their slots.
               if (r < 4) row_bad[4 * i + r] = 0;
@@ -694,7 +703,7 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
               l = L;
             }
           }
-          if (!last || g == 0) break;   // (the same for all: whatever `alive` says, barriers are met)
+          if (!last || g == 0) break;
           x = lo / g;
           n = (pieces + g - 1) / g;
           step = g;
@@ -717,7 +726,7 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
         // and for V, whose layout lets a block's halves lie together, one 4 KB box.
         const int x = warp - 12;
         const int total_rows = a.num_blocks * a.num_kv_heads * kBlockSize;   // host guarantees < 2^31
-        uint32_t st = 0, stage = 0, round = 0, piece = 0;
+        uint32_t st = 0, stage = 0, round = 0, piece = 0, queries = 0;   // queries: pieces whose queries were asked for
         bool ok = true;
         for (;; ++piece) {
           ok = __all_sync(0xffffffffu, piece_ready(piece));
@@ -746,7 +755,10 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
             if (elect_one()) {
               if (k == ka) {
                 ok = piece == 0 || pf_wait(q_empty, (piece - 1) & 1, ctl);
-                if (ok) pf_load_q<D>(a, &tm_q, base, q_full, h * a.group, token, boxes, x, 4);
+                if (ok) {
+                  pf_load_q<D>(a, &tm_q, base, q_full, h * a.group, token, boxes, x, 4);
+                  ++queries;
+                }
               }
 #pragma unroll 1
               for (int v = 0; v < 2 && ok; ++v) {
@@ -784,6 +796,7 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
           if (!ok) break;
         }
         st = __reduce_max_sync(0xffffffffu, st);   // of the lane that counted
+        queries = __reduce_max_sync(0xffffffffu, queries);
         if (lane == 0) {
           if (!ok) {
             ctl->abort = 1;
@@ -791,7 +804,7 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
           }
           // Drain: every copy issued into this CTA's shared memory lands before exit. (Where a role
           // gave up a barrier may stay incomplete; the first such wait outlasts any copy.)
-          bool landed = piece == 0 || mbar_wait(q_full, (piece - 1) & 1);
+          bool landed = queries == 0 || mbar_wait(q_full, (queries - 1) & 1);
 #pragma unroll 1
           for (uint32_t k = st > NS ? st - NS : 0; k < st && landed; ++k)
             landed = mbar_wait(full + 8 * (k % NS), (k / NS) & 1);
@@ -1087,7 +1100,7 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
         // behind its first K and V parts, which need not wait for the piece before to end.
         constexpr int kParts = D / 64, kPer = kPfTile / kBlockSize / kParts;   // blocks of a part
         const int total_rows = a.num_blocks * a.num_kv_heads * kBlockSize;   // host guarantees < 2^31
-        uint32_t parts = 0, slot = 0, round = 0, piece = 0;
+        uint32_t parts = 0, slot = 0, round = 0, piece = 0, queries = 0;
         bool ok = true;
         for (;; ++piece) {
           ok = __all_sync(0xffffffffu, piece_ready(piece));
@@ -1137,6 +1150,7 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 if (lane == 0) pf_load_q<D>(a, &tm_q, base, q_full, h * a.group, token, boxes, 0, 1);
+                ++queries;
                 __syncwarp();
               }
             }
@@ -1149,7 +1163,7 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
             if (a.status) atomicOr(a.status, kDevTimeout);
           }
           // Every copy issued lands before exit (where a role gave up: within these bounded waits).
-          bool landed = piece == 0 || mbar_wait(q_full, (piece - 1) & 1);
+          bool landed = queries == 0 || mbar_wait(q_full, (queries - 1) & 1);
 #pragma unroll 1
           for (uint32_t n = parts > Sh::kRawRing ? parts - Sh::kRawRing : 0; n < parts && landed; ++n)
             landed = mbar_wait(raw_full + 8 * (n % Sh::kRawRing), (n / Sh::kRawRing) & 1);
