@@ -7,6 +7,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
+#include <limits.h>
 #include <math.h>
 
 #include <cstdint>
@@ -94,6 +95,65 @@ __device__ __forceinline__ float load1(const void* cache, size_t e) {
   else return static_cast<float>(static_cast<int>(static_cast<const uint8_t*>(cache)[e]) - 128);
 }
 
+// Which of E neighbouring elements are (or hold, of several rows) NaN or an infinity, a bit each.
+struct NonFinite {
+  unsigned nan = 0, pos = 0, neg = 0;
+  template <int KV, int E>
+  __device__ __forceinline__ void add(const void* p) {
+    constexpr unsigned kInf = KV == kKvBf16 ? 0x7F80u : (KV == kKvE5m2 ? 0x7Cu : 0x7C00u);
+    constexpr unsigned kSign = KV == kKvE5m2 ? 0x80u : 0x8000u;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const unsigned x = KV == kKvE5m2 ? static_cast<const uint8_t*>(p)[e] : static_cast<const uint16_t*>(p)[e];
+      nan |= static_cast<unsigned>((x & (kSign - 1u)) > kInf) << e;
+      pos |= static_cast<unsigned>(x == kInf) << e;
+      neg |= static_cast<unsigned>(x == (kInf | kSign)) << e;
+    }
+  }
+};
+
+// The position (whole blocks, exclusive; INT_MAX: none below `end`) up to which a sequence's value rows of KV
+// head h account for what is not finite in outputs, by one warp: a NaN by a NaN or by infinities of
+// both signs in its dimension, an infinity by any of them. `out` has the lane's E = D / 32 dimensions. A value
+// of an INT8 cache is its code times its scale; a NaN K scale makes the whole row NaN.
+template <int KV, int D>
+__device__ __forceinline__ int accounted_for(const PrefillArgs& a, int s, int h, const NonFinite& out, int end) {
+  constexpr int E = D / 32;
+  const int lane = threadIdx.x & 31;
+  const int32_t* bt = a.block_tables + static_cast<size_t>(s) * a.max_blocks_per_seq;
+  NonFinite seen;
+#pragma unroll 1
+  for (int p = 0; p < end; p += kBlockSize) {
+    const int b = bt[p >> 4];
+    if (static_cast<unsigned>(b) < static_cast<unsigned>(a.num_blocks)) {
+      const size_t tile = static_cast<size_t>(b) * a.num_kv_heads + h;
+      constexpr int kBytes = KV == kKvE5m2 || KV == kKvInt8 ? 1 : 2;
+      const uint8_t* from = static_cast<const uint8_t*>(a.v_cache) + (tile * kBlockSize * D + lane * E) * kBytes;
+      if constexpr (KV == kKvInt8) {
+        const float f = a.scales[tile * 32 + lane];   // K scales, then V scales
+        if (__any_sync(0xffffffffu, f != f)) seen.nan = (1u << E) - 1u;
+        for (unsigned inf = __ballot_sync(0xffffffffu, fabsf(f) == INFINITY) >> 16; inf; inf &= inf - 1) {
+          const int t = __ffs(inf) - 1;
+          const bool minus = __shfl_sync(0xffffffffu, f, 16 + t) < 0.f;
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            const int code = static_cast<int>(from[t * D + e]) - 128;
+            seen.nan |= static_cast<unsigned>(code == 0) << e;
+            seen.pos |= static_cast<unsigned>(code != 0 && (code < 0) == minus) << e;
+            seen.neg |= static_cast<unsigned>(code != 0 && (code < 0) != minus) << e;
+          }
+        }
+      } else {
+#pragma unroll
+        for (int t = 0; t < kBlockSize; ++t) seen.add<KV, E>(from + t * D * kBytes);
+      }
+    }
+    const unsigned any = seen.nan | seen.pos | seen.neg, none = seen.nan | (seen.pos & seen.neg);
+    if (!__any_sync(0xffffffffu, (out.nan & ~none) | ((out.pos | out.neg) & ~any))) return p + kBlockSize;
+  }
+  return INT_MAX;
+}
+
 // Row `row` (token qb + j) of query head hq of sequence s; limit = visible positions. The
 // warp's lanes take 32 positions at a time for the scores, then D/32 dimensions each
 // for the sum.
@@ -118,7 +178,7 @@ __device__ __forceinline__ void prefill_row(const PrefillArgs& a, int s, int row
       float dot = 0.f;
       if (static_cast<unsigned>(b) < static_cast<unsigned>(a.num_blocks)) {
         crow = (static_cast<long long>(b) * a.num_kv_heads + h) * kBlockSize + (p & 15);
-#pragma unroll 1
+#pragma unroll
         for (int c = 0; c < D / 8; ++c) {
           float q[8], k[8];
           load8<Q>(a.q, qo + 8 * c, q);   // the same for every lane
@@ -153,12 +213,20 @@ __device__ __forceinline__ void prefill_row(const PrefillArgs& a, int s, int row
     const float wv = w * sv;
     const int cnt = limit - p0 < 32 ? limit - p0 : 32;
 #pragma unroll 1
-    for (int t = 0; t < cnt; ++t) {
-      const float wt = __shfl_sync(0xffffffffu, wv, t);
-      const long long rt = __shfl_sync(0xffffffffu, crow, t);
-      if (rt >= 0) {
+    for (int t0 = 0; t0 < cnt; t0 += 8) {   // eight rows' loads under way at once
+      float v[8][E];
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = fmaf(wt, load1<KV>(a.v_cache, static_cast<size_t>(rt) * D + lane * E + e), o[e]);
+      for (int t = 0; t < 8; ++t) {
+        const long long rt = __shfl_sync(0xffffffffu, crow, t0 + t);   // (-1 behind the limit)
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          v[t][e] = rt >= 0 ? load1<KV>(a.v_cache, static_cast<size_t>(rt) * D + lane * E + e) : 0.f;
+      }
+#pragma unroll
+      for (int t = 0; t < 8; ++t) {
+        const float wt = __shfl_sync(0xffffffffu, wv, t0 + t);
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = fmaf(wt, v[t][e], o[e]);
       }
     }
     if (nan || l != l) break;   // every element is NaN from here on
