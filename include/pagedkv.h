@@ -362,12 +362,12 @@ int pkv_paged_attention_decode_chunked(void* out, const void* q, const int32_t* 
  * `interleaved` is not 0, (2i, 2i + 1). At position p pair i turns by a = p * inv_freq[i]:
  *     y_re = attn_factor * (x_re cos a - x_im sin a)
  *     y_im = attn_factor * (x_re sin a + x_im cos a)
- * in fp32, rounded once; the other dimensions are copied. Angles are reduced exactly (a
- * position times a 64-bit fraction of a turn), so they hold at any position an int64
- * names, negative ones too.
+ * in fp32, rounded once; the other dimensions are copied. An angle is the position times a
+ * 64-bit fraction of a turn, off by at most |p| 2^-64 turns: less than half of an fp16 step
+ * up to |p| = 2^50, negative positions too.
  *
  *   positions       [num_tokens], int32 (position_bytes 4) or int64 (8).
- *   inv_freq        [rotary_dim / 2] double, device: radians per position. Scalings for
+ *   inv_freq        [rotary_dim / 2] double, device: radians per position, below 2^52. Scalings for
  *                   long contexts (interpolated or banded frequencies) are in these numbers.
  *   rotary_dim      a multiple of 16, at most the head size (64 or 128).
  *   attn_factor     finite; 1 unless a scaling asks for another.

@@ -10,9 +10,9 @@
 //
 // Angles. p * inv_freq reaches 10^6 rad, where an fp32 product is off by 0.03 rad. One
 // turn is 2^64 here: each CTA converts inv_freq / 2 pi once to a 64-bit fraction of a turn
-// per position (fp64), and p times that step modulo 2^64 is the angle, the whole turns
-// gone exactly; quarter turns taken off, the rest as two fp32 numbers goes to sincospif. The fp64 unit
-// is left with rotary_dim / 2 operations a CTA instead of one chain per (token, pair).
+// per position (in whole numbers: an fp64 product's error, 2^-53 of the angle, came to 0.003 rad at
+// position 2^45), and p times that step modulo 2^64 is the angle, the whole turns gone exactly;
+// quarter turns taken off, the rest as two fp32 numbers goes to sincospif. No angle needs the fp64 unit.
 //
 // Work. A row of D dimensions is D/16 items: an item is one pair of 16-byte chunks, eight
 // (re, im) pairs of the rotated part or sixteen plain dimensions (the unrotated tail, and
@@ -69,6 +69,20 @@ struct RotaryArgs {
   float factor, sign;          // sign -1 turns the other way
   double factor64;
 };
+
+// f / 2 pi modulo one turn in units of 2^-64, to the nearest (|f| below 2^52): a long multiplication of
+// f's 53 bits with 2^128 / 2 pi.
+__device__ __forceinline__ unsigned long long turn_fraction(double f) {
+  const unsigned long long bits = static_cast<unsigned long long>(__double_as_longlong(f));
+  const int field = static_cast<int>(bits >> 52) & 0x7FF;
+  const unsigned long long m = (bits & ((1ull << 52) - 1)) | (1ull << 52);
+  const int down = 1075 - field;   // f = m 2^-down; the product is m f 2^64 2^down
+  if (down < 0 || down > 127) return 0;
+  unsigned __int128 p = static_cast<unsigned __int128>(m) * 0x28BE60DB9391054Aull + __umul64hi(m, 0x7F09D5F47D4D3770ull);
+  if (down > 0) p = (p + (static_cast<unsigned __int128>(1) << (down - 1))) >> down;
+  const unsigned long long r = static_cast<unsigned long long>(p);
+  return (bits >> 63) ? 0ull - r : r;
+}
 
 template <bool BF16>
 __device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8]) {
@@ -225,12 +239,7 @@ __global__ void __launch_bounds__(kRotaryThreads, KV == kKvE5m2 ? 4 : 0) rotary_
   // A tile's first rows are under way while angles are worked out: the first tile's its own, a
   // later one's the tile's behind it.
   if (t0 < a.num_tokens) load(t0, tile_tokens(t0) * per_token, tid);
-  // inv_freq / 2 pi modulo one turn, as a 64-bit fraction. (Both products round to 2^-53
-  // of their value, as an fp64 angle would.)
-  if (tid < pairs) {
-    const double turns = a.inv_freq[tid] * 0.15915494309189533577;
-    step[tid] = __double2ull_rn((turns - floor(turns)) * 18446744073709551616.0);
-  }
+  if (tid < pairs) step[tid] = turn_fraction(a.inv_freq[tid]);
   __syncthreads();
   int buf = 0;
   if (t0 < a.num_tokens) angles(t0, cs2[0]);
