@@ -76,7 +76,7 @@ __device__ __forceinline__ unsigned long long turn_fraction(double f) {
   const unsigned long long bits = static_cast<unsigned long long>(__double_as_longlong(f));
   const int field = static_cast<int>(bits >> 52) & 0x7FF;
   const unsigned long long m = (bits & ((1ull << 52) - 1)) | (1ull << 52);
-  const int down = 1075 - field;   // f = m 2^-down; the product is m f 2^64 2^down
+  const int down = 1075 - field;   // f = m 2^-down, and p = m 2^64 / 2 pi
   if (down < 0 || down > 127) return 0;
   unsigned __int128 p = static_cast<unsigned __int128>(m) * 0x28BE60DB9391054Aull + __umul64hi(m, 0x7F09D5F47D4D3770ull);
   if (down > 0) p = (p + (static_cast<unsigned __int128>(1) << (down - 1))) >> down;
@@ -307,13 +307,14 @@ __global__ void __launch_bounds__(kRotaryThreads, KV == kKvE5m2 ? 4 : 0) rotary_
           uint8_t* dst = static_cast<uint8_t*>(cache) + crow * D;
           uint2 w1, w2;
           if (turn) {
-            // From fp32 in one rounding where its error d does not reach a border; one of 10^5 elements
-            // does. d is 2^-22 (|re| + |im|): the cosine and sine are within 2^-24 (sincospif), their
-            // correction and the factor's three roundings add 3/2 of it, the products' and this sum's as much.
+            // From fp32 in one rounding where its error d does not reach a border; two of 10^5 elements'
+            // does. d is 8 u factor (|re| + |im|), u = 2^-24: the cosine and sine are within 2 u (two ulp of
+            // sincospif below 1), their correction rounds by u / 2, the factor to fp32 by u, their product by
+            // u, of the two products with re and im one by u, the sum by u, x - d and x + d by u.
             float ox[8], oy[8];
             unpack8<BF16>(va[b], ox);
             unpack8<BF16>(vb[b], oy);
-            const float eps = fabsf(a.factor) * 2.384185791015625e-7f;
+            const float eps = fabsf(a.factor) * 4.76837158203125e-7f;
             uint32_t low[4], high[4];
 #pragma unroll
             for (int k = 0; k < 8; k += 2) {
