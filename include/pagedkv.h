@@ -449,7 +449,7 @@ int pkv_paged_attention_prefill(void* out, const void* q, const int32_t* cu_q_le
  *                 [0, max_q_per_seq]; NULL: n_s = max_q_per_seq. max_q_per_seq <= 64.
  *   accepted      [num_seqs][max_accepted] int32, device: draft indices in [0, n_s).
  *   num_accepted  [num_seqs] int32, device, in [0, min(max_accepted, n_s)].
- *   new_context_lens  [num_seqs] int32, device, or NULL; must not overlap context_lens.
+ *   new_context_lens  [num_seqs] int32, device, or NULL; must not overlap an input.
  * A sequence that breaks a rule on the device (an index or count out of range, context_lens
  * outside [n_s, max_blocks_per_seq * 16]: PKV_DEV_BAD_CTX; a block id out of range:
  * PKV_DEV_BAD_BLOCK) is left as it is, new_context_lens[s] = context_lens[s]. Blocks holding

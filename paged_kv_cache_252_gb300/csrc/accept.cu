@@ -131,8 +131,13 @@ extern "C" int pkv_kv_cache_accept(void* k_cache, void* v_cache, float* scales, 
       !aligned_to(context_lens, 4) || !aligned_to(cu_q_lens, 4) || !aligned_to(accepted, 4) ||
       !aligned_to(num_accepted, 4) || !aligned_to(new_context_lens, 4) || !aligned_to(device_status, 4))
     return PKV_ERR_INVALID_ARGUMENT;
-  // Every head's CTA reads the lengths that one of them would overwrite.
-  if (new_context_lens && new_context_lens < context_lens + num_seqs && context_lens < new_context_lens + num_seqs)
+  // Every head's CTA reads what one of them would overwrite.
+  auto written = [&](const int32_t* p, long long n) {
+    return new_context_lens && p && new_context_lens < p + n && p < new_context_lens + num_seqs;
+  };
+  const long long seqs = num_seqs;
+  if (written(context_lens, seqs) || written(num_accepted, seqs) || written(accepted, seqs * max_accepted) ||
+      written(cu_q_lens, seqs + 1) || written(block_tables, seqs * max_blocks_per_seq))
     return PKV_ERR_INVALID_ARGUMENT;
   AcceptArgs a{};
   a.k_cache = static_cast<uint4*>(k_cache);
