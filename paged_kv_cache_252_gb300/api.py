@@ -631,15 +631,19 @@ def rotary_inv_freq(rotary_dim: int, base: float = 10000.0, *, scaling: str | No
       attn_factor = 0.1 ln(factor) + 1.
     """
     rd = int(rotary_dim)
-    if rd < 2 or rd % 2 or not base > 0 or not factor > 0:
-        raise PagedKVError("rotary_dim must be even and positive, base and factor positive")
+    if rd < 2 or rd % 2 or not 0 < base < math.inf or not 0 < factor < math.inf:
+        raise PagedKVError("rotary_dim must be even and positive, base and factor positive and finite")
     if scaling not in (None, "linear", "base", "bands", "ramp"):
         raise PagedKVError(f"unknown rotary scaling {scaling!r}")
-    if scaling in ("bands", "ramp") and not (original_context and original_context > 0):
+    if scaling in ("bands", "ramp") and not (original_context and 0 < original_context < math.inf):
         raise PagedKVError(f"scaling {scaling!r} needs original_context")
+    if scaling == "ramp" and not base > 1:
+        raise PagedKVError("scaling 'ramp' needs base > 1: pairs that make fewer turns the higher their index")
     if scaling == "base":
         if rd == 2:
             raise PagedKVError("scaling 'base' needs rotary_dim > 2")
+        if math.log(base) + math.log(factor) * rd / (rd - 2) > 700.0:
+            raise PagedKVError("scaling 'base': base * factor^(rotary_dim / (rotary_dim - 2)) is out of range")
         base = base * factor ** (rd / (rd - 2))
     i = np.arange(rd // 2, dtype=np.float64)
     inv = base ** (-2.0 * i / rd)
@@ -648,7 +652,7 @@ def rotary_inv_freq(rotary_dim: int, base: float = 10000.0, *, scaling: str | No
         inv = inv / factor
     elif scaling in ("bands", "ramp"):
         high = (4.0 if scaling == "bands" else 32.0) if high is None else high
-        if not high > low > 0:
+        if not math.inf > high > low > 0:
             raise PagedKVError("the bands need high > low > 0")
         if scaling == "bands":
             keep = (original_context * inv / (2 * np.pi) - low) / (high - low)
