@@ -46,28 +46,33 @@ def row_bound(q, k, v, scale, v_scale=None):
     return o, tol + (2.0 ** -25 if q.dtype == torch.float16 else 0.0)
 
 
-def attention_rows(b, s):
-    """(rows of q/out, out, bound) of sequence s of a test batch: all its rows and heads, in 64 bits."""
-    a, e, ctx = b.cu_host[s], b.cu_host[s + 1], b.lens[s]
-    hq, d = b.q.shape[1:]
-    hkv = b.kc.shape[1]
+def seen_rows(b, s):
+    """(k, v, V scales or None) of a test batch's sequence s in 64 bits, [kv head][position][dimension]."""
+    ctx, hkv, d = b.lens[s], b.kc.shape[1], b.kc.shape[3]
     ids = b.bt[s, :-(-ctx // op.BLOCK)].long()
+    sc = None if b.sc is None else b.sc[ids]
 
     def rows(cache, which):
-        sc = None if b.sc is None else b.sc[ids]
-        x = op.cache_rows(cache[ids], sc, which)
-        return x.transpose(0, 1).reshape(hkv, -1, d)[:, :ctx]
-    k, v = rows(b.kc, 0), rows(b.vc, 1)
-    vs = None if b.sc is None else b.sc[ids][:, :, 1].transpose(0, 1).reshape(hkv, -1)[:, :ctx]
-    out = torch.empty((e - a, hq, d), dtype=torch.float64, device=b.q.device)
+        return op.cache_rows(cache[ids], sc, which).transpose(0, 1).reshape(hkv, -1, d)[:, :ctx]
+    return rows(b.kc, 0), rows(b.vc, 1), None if sc is None else sc[:, :, 1].transpose(0, 1).reshape(hkv, -1)[:, :ctx]
+
+
+def attention_rows(b, s, tokens=None):
+    """(rows of q/out, out, bound) of sequence s of a test batch: the given (default: all) new tokens, all
+    heads, in 64 bits."""
+    a, e, ctx = b.cu_host[s], b.cu_host[s + 1], b.lens[s]
+    hq, d = b.q.shape[1:]
+    k, v, vs = seen_rows(b, s)
+    at = list(range(e - a)) if tokens is None else list(tokens)
+    out = torch.empty((len(at), hq, d), dtype=torch.float64, device=b.q.device)
     tol = torch.empty_like(out)
-    for h in range(hq):
-        g = h // (hq // hkv)
-        for j in range(e - a):
-            n = ctx - (e - a) + j + 1
-            out[j, h], tol[j, h] = (x[0] for x in row_bound(b.q[a + j:a + j + 1, h], k[g, :n], v[g, :n], b.scale,
-                                                            None if vs is None else vs[g, :n]))
-    return slice(a, e), out, tol
+    group = hq // b.kc.shape[1]
+    for i, j in enumerate(at):
+        n = ctx - (e - a) + j + 1
+        for g in range(b.kc.shape[1]):
+            h = slice(g * group, (g + 1) * group)
+            out[i, h], tol[i, h] = row_bound(b.q[a + j, h], k[g, :n], v[g, :n], b.scale, None if vs is None else vs[g, :n])
+    return (slice(a, e) if tokens is None else [a + j for j in at]), out, tol
 
 
 def check_rows(b, what=""):
