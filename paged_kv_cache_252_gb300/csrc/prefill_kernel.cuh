@@ -537,14 +537,14 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
         };
         const int rows = min(pc->rows - 128 * i, 128);
         const bool few = rows <= 32;
-        // One CTA adds up the pieces lo + step y, y < n, of which its own is the x-th: all of them,
+        // One CTA adds up the pieces lo + step y, y < n, of which its own is the me-th: all of them,
         // or, of more than kPfJoin, first those of every group of g neighbours, then the groups' sums.
-        int lo = 0, step = 1, n = pieces, x = own, g = 0;
+        int lo = 0, step = 1, n = pieces, me = own, g = 0;
         if (pieces > kPfJoin && !few) {
           for (g = 3; g * g < pieces;) ++g;
           lo = own / g * g;
           n = min(g, pieces - lo);
-          x = own - lo;
+          me = own - lo;
         }
 #pragma unroll 1
         for (;;) {
@@ -566,7 +566,7 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
             named_bar_sync(1 + i, 128);
             last = last_piece[i] != 0;
             if (!last) {
-              float* sl = slot_of(lo + step * x);
+              float* sl = slot_of(lo + step * me);
               if (real) {
                 sl[r] = m;
                 sl[128 + r] = l;
@@ -602,13 +602,13 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
             write = last && !few;
             if (write && real) {
 #pragma unroll 4
-              for (int y = 0; y < n; ++y) M = fmaxf(M, y == x ? m : slot_of(lo + step * y)[r]);
+              for (int y = 0; y < n; ++y) M = fmaxf(M, y == me ? m : slot_of(lo + step * y)[r]);
               mu = M == -INFINITY ? 0.f : M;
               L = 0.f;
 #pragma unroll 4
               for (int y = 0; y < n; ++y) {
                 const float* sl = slot_of(lo + step * y);
-                L = y == x ? fmaf(l, fast_exp2(m - mu), L) : fmaf(sl[128 + r], fast_exp2(sl[r] - mu), L);
+                L = y == me ? fmaf(l, fast_exp2(m - mu), L) : fmaf(sl[128 + r], fast_exp2(sl[r] - mu), L);
               }
             }
             if (last && few) {
@@ -677,7 +677,7 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
                   for (int x = 0; x < 32; ++x) acc[x] = 0.f;
 #pragma unroll 1
                   for (int y = 0; y < n; ++y) {
-                    if (y == x) {
+                    if (y == me) {
 #pragma unroll
                       for (int x = 0; x < 32; ++x) acc[x] = fmaf(w_own, __uint_as_float(ov[x]), acc[x]);
                     } else {
@@ -723,7 +723,7 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
             }
           }
           if (!last || g == 0) break;
-          x = lo / g;
+          me = lo / g;
           n = (pieces + g - 1) / g;
           step = g;
           lo = g = 0;
