@@ -643,7 +643,8 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
                 }
                 const int u = 128 * i + rr, j = u / a.group;
                 // (a row that sees nothing is 0; one whose visible scores are all -inf, or not all numbers, NaN)
-                const float inv = Lr > 0.f ? 1.f / Lr : (Lr == 0.f && pc->past + pc->j0 + j < 0 ? 0.f : NAN);
+                const bool blind = pc->past + pc->j0 + j < 0;
+                const float inv = Lr > 0.f ? 1.f / Lr : (Lr == 0.f && blind ? 0.f : NAN);
                 // (an unseen NaN scale of an INT8 cache spoils the sum, nothing else does)
                 float bad = KV == kKvInt8 ? Lr - Lr : 0.f;
                 uint32_t y[4];
@@ -652,7 +653,7 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
                   bad = fmaf(o[x], 0.f, fmaf(o[x + 1], 0.f, bad));
                   y[x / 2] = pack2<Sh::kBf16>(o[x] * inv, o[x + 1] * inv);
                 }
-                if (bad != 0.f && (KV == kKvInt8 || Lr > 0.f)) atomicOr(const_cast<unsigned*>(row_bad) + 4 * i + (rr >> 5), 1u << (rr & 31));
+                if (bad != 0.f && (KV == kKvInt8 || Lr > 0.f || blind)) atomicOr(const_cast<unsigned*>(row_bad) + 4 * i + (rr >> 5), 1u << (rr & 31));
                 *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) +
                                           (static_cast<size_t>(pc->qb + pc->j0 + j) * a.num_q_heads + pc->h * a.group + u -
                                            j * a.group) * D + 8 * ch) = make_uint4(y[0], y[1], y[2], y[3]);
@@ -716,7 +717,7 @@ __global__ void __launch_bounds__(PfShape<KV, D>::kThreads, 1)
                 }
               }
             }
-            odd = real && g == 0 && (KV == kKvInt8 ? !(bad == 0.f && L < INFINITY) : bad != 0.f && L > 0.f);
+            odd = real && g == 0 && (KV == kKvInt8 ? !(bad == 0.f && L < INFINITY) : bad != 0.f && (L > 0.f || limit <= 0));
             if (g) {
               m = M;
               l = L;

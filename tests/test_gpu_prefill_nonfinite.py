@@ -86,6 +86,23 @@ def test_a_key_that_is_not_a_number(dev, kv, ns, lens):  # noqa: F811
     op.assert_within(b.out[:k], want[:k], tol[:k], "rows before it")
 
 
+@pytest.mark.parametrize("kv", ["fp16", "bf16", "e5m2", "int8"])
+@pytest.mark.parametrize("n,ctx", [(30, 11), (4, 3), (300, 290)])
+def test_rows_that_see_nothing_stay_zero(dev, kv, n, ctx):  # noqa: F811
+    """A context shorter than its new tokens, whose last token holds NaN: only the last row sees that."""
+    b = Batch(dev, kv, 64, 4, 2, [n], [n])
+    b.cl[0] = ctx
+    p = ctx - 1
+    if kv == "int8":
+        b.sc[int(b.bt[0, p // 16]), :, 1, p % 16] = float("nan")
+    else:
+        _plant(b, 0, p, [3, 40], "nan")
+    b.run()
+    torch.cuda.synchronize()
+    assert b.status.item() == 4
+    assert (b.out[:n - ctx] == 0).all() and torch.isfinite(b.out[:n - 1]).all() and torch.isnan(b.out[n - 1, :, 3]).all()
+
+
 def _time(b):
     for _ in range(2):
         b.run()
