@@ -210,7 +210,7 @@ __device__ __forceinline__ void pf_mask(uint32_t (&sv)[4][32], int vis) {
 // The exponent e of a V scale below 2^e (as a number of 2^23 plus its field); -31 at least: 127 times a
 // smaller one is half of the least step of an fp16 output.
 __device__ __forceinline__ float scale_exponent(float v) {
-  return __uint_as_float((__float_as_uint(fmaxf(v, 0x1p-32f)) >> 23) | 0x4B000000u) - (8388608.f + 126.f);
+  return __uint_as_float((__float_as_uint(fmaxf(fabsf(v), 0x1p-32f)) >> 23) | 0x4B000000u) - (8388608.f + 126.f);
 }
 
 // The largest of 128 scores times c (an INT8 cache's: times their K scales, which hold c, plus their V

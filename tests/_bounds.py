@@ -40,7 +40,7 @@ def row_bound(q, k, v, scale, v_scale=None):
     tol = u * o.abs() + u * big + pe @ v.abs() + o.abs() * pe.sum(-1, keepdim=True)
     tol += (n / 16 + n / 128 + 152) * 2.0 ** -23 * big + (32 + n / 128 + 152) * 2.0 ** -24 * o.abs()
     if v_scale is not None:
-        tol += n * 2.0 ** -29 * (p * (127.0 * v_scale.double().clamp(min=2.0 ** -32))).amax(-1, keepdim=True)
+        tol += n * 2.0 ** -29 * (p * (127.0 * v_scale.double().abs().clamp(min=2.0 ** -32))).amax(-1, keepdim=True)
     elif q.dtype == torch.float16:
         tol += n * 2.0 ** -32 * p.amax(-1, keepdim=True) * v.abs().max()
     return o, tol + (2.0 ** -25 if q.dtype == torch.float16 else 0.0)

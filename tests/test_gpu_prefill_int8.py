@@ -3,6 +3,7 @@ import pytest
 import torch
 
 import _bounds
+import _operators as op
 from test_gpu_prefill import Batch, dev  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -82,3 +83,19 @@ def test_scales_outside_the_codecs_range(dev, v_scale):  # noqa: F811
     assert ((g - want).abs() <= tol)[fits].all() and not torch.isnan(g).any()
     assert (g[want.abs() > 66000].abs() == float("inf")).all()
     assert torch.equal(g.sign()[~fits], want.sign()[~fits])
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_negative_scales(dev, D):  # noqa: F811
+    """V scales of either sign: right, and no slower for it (sums that leave fp16 would send every row through
+    the plain row pass, some 100 times as long)."""
+    from test_gpu_prefill_nonfinite import _time
+    b = Batch(dev, "int8", D, 8, 2, [600], [2600], q_gain=2.0)
+    plain = _time(b)
+    b.sc[:, :, 1, ::3] *= -300.0
+    b.sc[:, :, 1, 1::3] *= -1.0
+    t = _time(b)
+    print(f"{plain * 1e3:.0f} us, {t * 1e3:.0f} us with negative scales")
+    at, want, tol = _bounds.attention_rows(b, 0, [0, 1, 63, 64, 300, 598, 599])
+    op.assert_within(b.out[at], want, tol, "negative scales")
+    assert t < 4 * plain + 0.02
