@@ -33,18 +33,23 @@
 // score and its V scale's exponent, and l and O carry that factor. (Under the largest score alone, with
 // a shift for the largest scale an fp16 row gives, 516, values of at most 0.0025 left weights of 2^-12
 // of the largest no bits at all. The exponents cost an 8192-token prompt 1 %.) Their shift is 2^5: m has
-// no slack there, so products may come to 65504 before it moves. The weights' rounding to 16 bits is the products' operand type; scores,
-// sums and O stay fp32.
+// no slack there, so products may come to 65504 before it moves. The weights' rounding to 16 bits is the
+// products' operand type; scores, sums and O stay fp32.
 //
 // Measured (32 query heads on 8 KV heads of 128 dimensions; a large library product of bf16
 // reaches 1895 TFLOP/s). A KV tile against two row tiles is 2050 cycles of products; it takes
 // 2500 to 2600 where only the softmax's instructions compete.
-//   8192-token prompt    bf16 361 us, 1522 TFLOP/s: the products' operands and the softmax's
-//                        chain from scores to weights share the SM (tensor pipe busy 65 %), and
-//                        25 us are the ends of pieces; 16384 tokens 1320 us, 1666 TFLOP/s.
-//                        E5M2 422 us: widening, a second pass through shared memory (its stores
-//                        alone are 20 us). INT8 507 us: its row scales, two 16-byte reads a thread
-//                        for every four scores.
+//   8192-token prompt    bf16 358 us, 1537 TFLOP/s: the products' operands and the softmax's
+//                        chain from scores to weights share the SM (tensor pipe busy 66 %), and
+//                        25 us are the ends of pieces; 16384 tokens 1320 us, 1665 TFLOP/s.
+//                        E5M2 428 us: the stores of the widening pass are 20 us of the difference; the
+//                        rest has no cause found (a ring of four stages, as here, costs bf16 nothing).
+//                        INT8 513 us: its row scales, two 16-byte reads a thread for every four scores
+//                        (the LSU's data pipe is busy 54 %, so not at its limit).
+//   prompts of 512 / 1024 / 2048 tokens (bf16)   17 / 26 / 48 us: the start, some 8000 cycles from plan to
+//                        first weights, and the ends of pieces, of 4000 to 10000, over few tiles.
+//   head size 64         8192 tokens 312 us bf16, 327 E5M2, 406 INT8: half of the products, and the
+//                        same chain from scores to weights, which is what a tile takes there.
 //   100 tokens over a context of 130972 (bf16)   193 us, 537 MB read once: 80 us of memory time,
 //                        113 of products; rows fill 400 of 512.
 //   one token            10 us: five of launch and planning, five of one chain through the CTA.

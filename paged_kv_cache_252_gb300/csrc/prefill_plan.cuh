@@ -9,7 +9,9 @@
 // cut by a stretch's end becomes pieces that are merged by the last to finish. While stretches
 // are short (kPfWholeShare) a unit of at most kPfWhole positions is not cut: all of it belongs
 // to the CTA whose stretch holds its start, since writing and merging pieces takes as long as some
-// five tiles (eight prompts of 512 tokens: 43 us; 49 with kPfWholeShare 1600, where they are cut).
+// five tiles (eight prompts of 512 tokens: 43 us; 49 with kPfWholeShare 1600, where they are cut). One
+// bf16 prompt of 32 + 8 heads, whole / cut: 512 tokens 17.1 / 20.9 us, 1024 25.2 / 31.2, 1536 41.1 / 37.1, 2048
+// (a share of 2425, so cut) 49.0 / 47.2.
 #pragma once
 
 #include <cuda_runtime.h>
