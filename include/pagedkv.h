@@ -54,7 +54,8 @@ typedef enum {
   PKV_FP16 = 0,
   PKV_BF16 = 1,
   PKV_FP8_E5M2 = 2,
-  PKV_INT8 = 3      /* int8 codes with float32 row scales: see pkv_kv_cache_write_int8 */
+  PKV_INT8 = 3,     /* int8 codes with float32 row scales: see pkv_kv_cache_write_int8 */
+  PKV_INT4 = 4      /* 4-bit codes with fp16 scales: see pkv_kv_cache_write_int4 */
 } pkv_dtype;
 
 typedef enum {
@@ -310,6 +311,63 @@ int pkv_paged_attention_decode_int8_tree(void* out, const void* q, const int32_t
                                          const int32_t* context_lens, float scale, void* workspace,
                                          size_t workspace_bytes, int32_t* device_status, void* stream);
 
+/* ==== INT4 KV cache ===========================================================
+ *
+ * Four bits an element (the survey's LMDeploy section lists KV cache quantisation
+ * without a codec; this one is ours): a row (token, KV head) is head_size / 64 groups of
+ * 64 dimensions, each with two fp16 numbers
+ *   z = the largest fp16 number not above the group's least value,
+ *   s = the smallest fp16 number not below (its largest value - z) / 15,
+ * and codes c in 0..15: dimension d stands for z + s c_d, the nearest of the sixteen values
+ * (halfway between two: the even code). Values beyond +-65504 count as +-65504; a group that
+ * holds an infinity or NaN gets s = NaN and reads back as NaN.
+ *
+ * Caches: [num_blocks][num_kv_heads][16][head_size / 2] bytes. A row is head_size / 8 32-bit
+ * words (little endian); word i * (head_size / 64) + g holds the eight dimensions
+ * 64 g + 8 i + e: even e at bit 2 e, odd e at bit 16 + 2 (e - 1). scales: one array
+ * [num_blocks][num_kv_heads][2][16][head_size / 64] of fp16 pairs (s, z), K's then V's. All
+ * 16-byte aligned; an all-zero cache with all-zero scales holds zeros. The cache descriptor's
+ * head_size counts dimensions. kv_dtype PKV_INT4 is taken by pkv_kv_cache_read, pkv_copy_blocks
+ * and pkv_kv_cache_accept (whose `scales` then points at these words) and by the calls below;
+ * the other calls return PKV_ERR_UNSUPPORTED for it.
+ *
+ * key/value: fp16 or bf16 (src_dtype) [num_tokens][num_kv_heads][head_size]. Slots as in
+ * pkv_kv_cache_write (-1 skipped, other out-of-range slots skipped and flagged). A slot that
+ * occurs twice in one call holds afterwards a mixture of its tokens. */
+int pkv_kv_cache_write_int4(const void* key, const void* value, pkv_dtype src_dtype, int32_t num_tokens,
+                            const int32_t* slot_mapping, void* k_cache, void* v_cache, void* scales,
+                            const pkv_cache_desc* cache, int32_t* device_status, void* stream);
+
+/* Rows of a cache of any type read back by slot: key/value [num_tokens][num_kv_heads][head_size]
+ * fp16 or bf16 (dst_dtype) become the values that the cache stands for, rounded once to
+ * dst_dtype (beyond its range: an infinity). A slot of -1 leaves its rows as they are, as do other
+ * slots out of range (flagged); a slot may occur any number of times. scales: of an INT8 or INT4
+ * cache, else NULL. key and value must not overlap each other or an input. */
+int pkv_kv_cache_read(void* key, void* value, pkv_dtype dst_dtype, int32_t num_tokens, const int32_t* slot_mapping,
+                      const void* k_cache, const void* v_cache, const void* scales, pkv_dtype kv_dtype,
+                      const pkv_cache_desc* cache, int32_t* device_status, void* stream);
+
+/* Decode attention over an INT4 cache, for fp16 or bf16 queries and outputs (q_dtype): arguments as
+ * for pkv_paged_attention_decode (cu_q_lens and tree_masks NULL), _varlen (cu_q_lens) and _tree
+ * (tree_masks, with or without cu_q_lens; then max_q_per_seq <= 64). num_q_rows: rows of q / out (and tree_masks).
+ * Workspace as for pkv_paged_attention_decode (pkv_decode_workspace_bytes). Rows of a sequence
+ * beyond its context, and draft tokens that a row's mask hides, may hold anything. */
+int pkv_paged_attention_decode_int4(void* out, const void* q, pkv_dtype q_dtype, const int32_t* cu_q_lens,
+                                    const uint64_t* tree_masks, int32_t num_q_rows, int32_t num_seqs,
+                                    int32_t num_q_heads, int32_t max_q_per_seq, const void* k_cache,
+                                    const void* v_cache, const void* scales, const pkv_cache_desc* cache,
+                                    const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                    const int32_t* context_lens, float scale, void* workspace,
+                                    size_t workspace_bytes, int32_t* device_status, void* stream);
+
+/* pkv_paged_attention_decode_chunked (below) over an INT4 cache. */
+int pkv_paged_attention_decode_int4_chunked(void* out, const void* q, pkv_dtype q_dtype, const int32_t* host_q_lens,
+                                            const int32_t* host_context_lens, int32_t num_seqs, int32_t num_q_heads,
+                                            const void* k_cache, const void* v_cache, const void* scales,
+                                            const pkv_cache_desc* cache, const int32_t* block_tables,
+                                            int32_t max_blocks_per_seq, float scale, void* workspace,
+                                            size_t workspace_bytes, int32_t* device_status, void* stream);
+
 /*
  * pkv_paged_attention_decode_chunked — decode attention for a batch whose sequences
  * may carry ANY number of query tokens: prefill chunks beside decode and verify
@@ -441,7 +499,7 @@ int pkv_paged_attention_prefill(void* out, const void* q, const int32_t* cu_q_le
  * _varlen or _tree): sequence s's last n_s positions hold its drafts; the accepted ones, in
  * the order given, move together behind the context:
  *     row base + i  <-  row base + accepted[s][i],  i < num_accepted[s],  base = context_lens[s] - n_s
- * for every KV head of both caches (and an INT8 cache's row scales), all rows read before any
+ * for every KV head of both caches (and an INT8 or INT4 cache's scales), all rows read before any
  * is written, so any order and repeated indices are allowed; new_context_lens[s] = base +
  * num_accepted[s]. Rows behind the new length keep what they held.
  *
@@ -553,7 +611,7 @@ int pkv_seq_add_cached(pkv_allocator* a, int64_t seq, const int32_t* tokens, int
  * For i < n: physical block dst[i] of both caches becomes a copy of block
  * src[i] (every head's 16 rows), and for an INT8 cache (kv_dtype PKV_INT8) so do
  * the block's row scales in `scales` ([num_blocks][num_kv_heads][2][16] floats,
- * 16-byte aligned; NULL for every other cache). src and dst are DEVICE int32
+ * 16-byte aligned; an INT4 cache's words for PKV_INT4; NULL for every other cache). src and dst are DEVICE int32
  * arrays; ids out of range are skipped and set PKV_DEV_BAD_BLOCK. The pairs
  * must not overlap in a way that reads a block after it was written in the same
  * call. Asynchronous on stream. */

@@ -13,6 +13,9 @@ Around them, what a serving step runs:
 * :func:`rotary_write` (and :func:`rotary_embed`) turns q and k by their positions and
   writes the cache in the same pass; :func:`rotary_inv_freq` gives the frequencies.
 * :func:`paged_attention_prefill` is the attention of prompts and prompt chunks.
+* :func:`kv_cache_write_int4` quantises tokens to four bits as they are written,
+  :func:`paged_attention_decode_int4` (and the varlen, tree and chunked calls) attends over such a
+  cache, and :func:`kv_cache_read` reads rows of a cache of any type back.
 * :func:`kv_cache_accept` keeps the accepted drafts of a speculative verify, and
   :meth:`BlockAllocator.truncate` gives the dropped ones' blocks back.
 
@@ -25,7 +28,7 @@ not load the library; the first call does, and fails loudly if it is missing.
 """
 from . import workloads  # noqa: F401
 from .api import (  # noqa: F401
-    KV_FP16, KV_BF16, KV_E5M2, KV_INT8,
+    KV_FP16, KV_BF16, KV_E5M2, KV_INT8, KV_INT4,
     kv_cache_write, paged_attention_decode, paged_attention_decode_varlen,
     paged_attention_decode_tree, paged_attention_decode_chunked, selftest_bounded_wait,
     paged_attention_decode_noalloc, decode_workspace_bytes,
@@ -33,4 +36,5 @@ from .api import (  # noqa: F401
     BlockAllocator, copy_blocks,
     alloc_kv_scales, kv_cache_write_int8, paged_attention_decode_int8, int8_codes,
     rotary_inv_freq, rotary_embed, rotary_write, paged_attention_prefill, prefill_workspace_bytes, kv_cache_accept,
+    kv_cache_write_int4, kv_cache_read, paged_attention_decode_int4,
 )

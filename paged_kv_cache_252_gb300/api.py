@@ -16,8 +16,9 @@ import threading
 import numpy as np
 import torch
 
-KV_FP16, KV_BF16, KV_E5M2, KV_INT8 = 0, 1, 2, 3
-_NAMES = {"fp16": KV_FP16, "bf16": KV_BF16, "e5m2": KV_E5M2, "fp8_e5m2": KV_E5M2, "int8": KV_INT8}
+KV_FP16, KV_BF16, KV_E5M2, KV_INT8, KV_INT4 = 0, 1, 2, 3, 4
+_NAMES = {"fp16": KV_FP16, "bf16": KV_BF16, "e5m2": KV_E5M2, "fp8_e5m2": KV_E5M2, "int8": KV_INT8,
+          "int4": KV_INT4}
 _TORCH = {torch.float16: KV_FP16, torch.bfloat16: KV_BF16, torch.uint8: KV_E5M2,
           torch.float8_e5m2: KV_E5M2, torch.int8: KV_INT8}
 BLOCK_SIZE = 16
@@ -141,6 +142,17 @@ def load_library(path: str | None = None):
         lib.pkv_kv_cache_accept.argtypes = [vp, vp, vp, cint, P(_CacheDesc), vp, i32, vp, vp, i32, i32, vp, i32, vp,
                                             vp, vp, vp]
         lib.pkv_kv_cache_accept.restype = cint
+        lib.pkv_kv_cache_write_int4.argtypes = [vp, vp, cint, i32, vp, vp, vp, vp, P(_CacheDesc), vp, vp]
+        lib.pkv_kv_cache_write_int4.restype = cint
+        lib.pkv_kv_cache_read.argtypes = [vp, vp, cint, i32, vp, vp, vp, vp, cint, P(_CacheDesc), vp, vp]
+        lib.pkv_kv_cache_read.restype = cint
+        lib.pkv_paged_attention_decode_int4.argtypes = [vp, vp, cint, vp, vp, i32, i32, i32, i32, vp, vp, vp,
+                                                        P(_CacheDesc), vp, i32, vp, f32, vp, ctypes.c_size_t, vp, vp]
+        lib.pkv_paged_attention_decode_int4.restype = cint
+        lib.pkv_paged_attention_decode_int4_chunked.argtypes = [vp, vp, cint, vp, vp, i32, i32, vp, vp, vp,
+                                                                P(_CacheDesc), vp, i32, f32, vp, ctypes.c_size_t, vp,
+                                                                vp]
+        lib.pkv_paged_attention_decode_int4_chunked.restype = cint
         lib.pkv_selftest_bounded_wait.argtypes = [vp, ctypes.c_uint64, vp, vp]
         lib.pkv_selftest_bounded_wait.restype = ctypes.c_int
         lib.pkv_error_string.argtypes = [ctypes.c_int]
@@ -218,7 +230,13 @@ def _decode_shapes(out, q, k_cache, v_cache, block_tables, context_lens, rows=No
     return d, S
 
 
-def _scales_shape(k_cache, scales):
+def _scales_shape(k_cache, scales, code=KV_INT8):
+    if code == KV_INT4:
+        nb, hkv, _, half = k_cache.shape
+        want = (nb, hkv, 2, BLOCK_SIZE, half // 32, 2)
+        if tuple(scales.shape) != want or scales.dtype != torch.float16:
+            raise PagedKVError(f"scales must be float16 {want} (scale and least value of every 64 dimensions)")
+        return
     want = (int(k_cache.shape[0]), int(k_cache.shape[1]), 2, BLOCK_SIZE)
     if tuple(scales.shape) != want or scales.dtype != torch.float32:
         raise PagedKVError(f"scales must be float32 {want} (K then V row scales)")
@@ -246,20 +264,36 @@ def alloc_kv_cache(num_blocks: int, num_kv_heads: int, head_size: int, kv_dtype,
                    device="cuda", zero: bool = True):
     """Allocate a K/V cache pair [num_blocks, num_kv_heads, 16, head_size]. An INT8
     cache is a torch.int8 tensor whose bytes hold the codes in offset binary
-    (byte = code + 128; :func:`int8_codes` reads them back). ``zero`` fills the
-    caches with the value 0 (for INT8: code 0, byte 0x80)."""
+    (byte = code + 128; :func:`int8_codes` reads them back). An INT4 cache is a torch.uint8
+    tensor [num_blocks, num_kv_heads, 16, head_size / 2] of packed codes
+    (:func:`kv_cache_read` reads them back); calls on it name its type
+    (kv_dtype="int4"). ``zero`` fills the caches with the value 0 (for INT8: code 0, byte 0x80)."""
     code = _NAMES[kv_dtype] if isinstance(kv_dtype, str) else int(kv_dtype)
-    dt = {KV_FP16: torch.float16, KV_BF16: torch.bfloat16, KV_E5M2: torch.uint8, KV_INT8: torch.int8}[code]
-    shape = (num_blocks, num_kv_heads, BLOCK_SIZE, head_size)
+    dt = {KV_FP16: torch.float16, KV_BF16: torch.bfloat16, KV_E5M2: torch.uint8, KV_INT8: torch.int8,
+          KV_INT4: torch.uint8}[code]
+    if code == KV_INT4 and head_size not in (64, 128):
+        raise PagedKVError(f"an INT4 cache has head size 64 or 128, got {head_size}")
+    shape = (num_blocks, num_kv_heads, BLOCK_SIZE, head_size // 2 if code == KV_INT4 else head_size)
     if not zero:
         return torch.empty(shape, dtype=dt, device=device), torch.empty(shape, dtype=dt, device=device)
     fill = -128 if code == KV_INT8 else 0   # int8 -128 is the byte 0x80
     return (torch.full(shape, fill, dtype=dt, device=device), torch.full(shape, fill, dtype=dt, device=device))
 
 
-def alloc_kv_scales(num_blocks: int, num_kv_heads: int, device="cuda"):
+def alloc_kv_scales(num_blocks: int, num_kv_heads: int, device="cuda", *, kv_dtype="int8",
+                    head_size: int | None = None):
     """Row scales of an INT8 cache pair: one float32 tensor [num_blocks, num_kv_heads, 2, 16],
-    [..., 0, t] the K scale and [..., 1, t] the V scale of token t of a block."""
+    [..., 0, t] the K scale and [..., 1, t] the V scale of token t of a block. Of an INT4 cache pair
+    (kv_dtype="int4", head_size): float16 [num_blocks, num_kv_heads, 2, 16, head_size / 64, 2], the
+    scale and the least value of every 64 dimensions."""
+    code = _NAMES[kv_dtype] if isinstance(kv_dtype, str) else int(kv_dtype)
+    if code == KV_INT4:
+        if head_size not in (64, 128):
+            raise PagedKVError(f"an INT4 cache's scales need its head size, 64 or 128, got {head_size}")
+        return torch.zeros((num_blocks, num_kv_heads, 2, BLOCK_SIZE, head_size // 64, 2), dtype=torch.float16,
+                           device=device)
+    if code != KV_INT8:
+        raise PagedKVError("only INT8 and INT4 caches have scales")
     return torch.zeros((num_blocks, num_kv_heads, 2, BLOCK_SIZE), dtype=torch.float32, device=device)
 
 
@@ -430,12 +464,12 @@ def paged_attention_decode_noalloc(out, q, k_cache, v_cache, block_tables, conte
 
 
 def _int8_scales(code, k_cache, scales):
-    """An INT8 cache is read with its row scales; other caches take none."""
-    if (code == KV_INT8) != (scales is not None):
-        raise PagedKVError("an INT8 cache is read with its scales (alloc_kv_scales); other caches take none")
+    """An INT8 or INT4 cache is read with its scales; other caches take none."""
+    if (code in (KV_INT8, KV_INT4)) != (scales is not None):
+        raise PagedKVError("an INT8 or INT4 cache is read with its scales (alloc_kv_scales); other caches take none")
     if scales is not None:
         _need_cuda_contig("scales", scales)
-        _scales_shape(k_cache, scales)
+        _scales_shape(k_cache, scales, code)
 
 
 def paged_attention_decode_varlen(out, q, cu_q_lens, k_cache, v_cache, block_tables, context_lens,
@@ -444,7 +478,10 @@ def paged_attention_decode_varlen(out, q, cu_q_lens, k_cache, v_cache, block_tab
     """Decode attention for a batch whose sequences carry different numbers of query
     tokens, packed without padding: sequence s owns rows cu_q_lens[s]..cu_q_lens[s+1]-1
     of q/out ([total_rows, Hq, D]), 1 <= n_s <= max_q_per_seq, causal among its tokens.
-    An INT8 cache takes its row scales (``scales``)."""
+    An INT8 or INT4 cache takes its scales (``scales``)."""
+    if _is_int4(kv_dtype):
+        return _decode_int4("paged_attention_decode_varlen", out, q, cu_q_lens, None, k_cache, v_cache, scales,
+                            block_tables, context_lens, max_q_per_seq, scale, workspace, device_status, stream)
     for nm, t in (("out", out), ("q", q), ("cu_q_lens", cu_q_lens), ("k_cache", k_cache),
                   ("v_cache", v_cache), ("block_tables", block_tables), ("context_lens", context_lens)):
         _need_cuda_contig(nm, t)
@@ -515,14 +552,16 @@ def paged_attention_decode_chunked(out, q, q_lens, context_lens, k_cache, v_cach
     cl = _host_i32("context_lens", context_lens, S)
     if S and (ql.min() < 1 or np.any(cl < ql)):
         raise PagedKVError("every sequence needs 1 <= q_lens[s] <= context_lens[s]")
+    code = _kv_code(kv_dtype, k_cache)
     d = _pair(k_cache, v_cache)
+    if code == KV_INT4:
+        d.head_size *= 2
     if q.dim() != 3 or tuple(out.shape) != tuple(q.shape) or int(q.shape[0]) != int(ql.sum()):
         raise PagedKVError(f"q and out must both be [sum(q_lens) = {int(ql.sum())}, num_q_heads, head_size]")
-    if int(q.shape[2]) != int(k_cache.shape[3]):
-        raise PagedKVError(f"query head size {int(q.shape[2])} != cache head size {int(k_cache.shape[3])}")
+    if int(q.shape[2]) != d.head_size:
+        raise PagedKVError(f"query head size {int(q.shape[2])} != cache head size {d.head_size}")
     if block_tables.dim() != 2 or int(block_tables.shape[0]) < S:
         raise PagedKVError(f"block_tables must be [num_seqs, max_blocks_per_seq], got {tuple(block_tables.shape)}")
-    code = _kv_code(kv_dtype, k_cache)
     _int8_scales(code, k_cache, scales)
     Hq, mbs = int(q.shape[1]), int(block_tables.shape[1])
     lib = load_library()
@@ -533,11 +572,15 @@ def paged_attention_decode_chunked(out, q, q_lens, context_lens, k_cache, v_cach
             raise PagedKVError("paged_attention_decode_chunked: unsupported shape")
         if workspace is None:
             workspace = _workspace(need, q.device)
-        rc = lib.pkv_paged_attention_decode_chunked(
-            _ptr(out), _ptr(q), qp, cp, S, Hq, _ptr(k_cache), _ptr(v_cache), _ptr(scales), code,
-            ctypes.byref(d), _ptr(block_tables), mbs, float(scale), _ptr(workspace),
-            int(workspace.numel() * workspace.element_size()), _ptr(device_status),
-            _stream_handle(stream, q.device))
+        rest = (ctypes.byref(d), _ptr(block_tables), mbs, float(scale), _ptr(workspace),
+                int(workspace.numel() * workspace.element_size()), _ptr(device_status),
+                _stream_handle(stream, q.device))
+        if code == KV_INT4:
+            rc = lib.pkv_paged_attention_decode_int4_chunked(
+                _ptr(out), _ptr(q), _src_code(q), qp, cp, S, Hq, _ptr(k_cache), _ptr(v_cache), _ptr(scales), *rest)
+        else:
+            rc = lib.pkv_paged_attention_decode_chunked(
+                _ptr(out), _ptr(q), qp, cp, S, Hq, _ptr(k_cache), _ptr(v_cache), _ptr(scales), code, *rest)
     _check(rc, "paged_attention_decode_chunked")
     return out
 
@@ -565,7 +608,10 @@ def paged_attention_decode_tree(out, q, tree_masks, k_cache, v_cache, block_tabl
     """Speculative verify of a token tree: tree_masks (int64/uint64, one per query row)
     bit i lets a query token attend to its sequence's draft token i; the context before
     the drafts is always visible. cu_q_lens as for paged_attention_decode_varlen, or
-    None for max_q_per_seq tokens per sequence. An INT8 cache takes its row scales."""
+    None for max_q_per_seq tokens per sequence. An INT8 or INT4 cache takes its scales."""
+    if _is_int4(kv_dtype):
+        return _decode_int4("paged_attention_decode_tree", out, q, cu_q_lens, tree_masks, k_cache, v_cache, scales,
+                            block_tables, context_lens, max_q_per_seq, scale, workspace, device_status, stream)
     for nm, t in (("out", out), ("q", q), ("tree_masks", tree_masks), ("k_cache", k_cache),
                   ("v_cache", v_cache), ("block_tables", block_tables), ("context_lens", context_lens)):
         _need_cuda_contig(nm, t)
@@ -709,14 +755,19 @@ def _head_rows(name, t, dev, heads, head_size) -> int:
 _descs: dict = {}
 
 
-def _desc_of(k_cache, v_cache):
-    """A descriptor of the cache pair for the library (kept by its sizes), its KV heads and head size."""
+def _desc_of(k_cache, v_cache, packed=False):
+    """A descriptor of the cache pair for the library (kept by its sizes), its KV heads and head size
+    (packed: an INT4 cache, two dimensions a byte)."""
     shape = k_cache.shape
     if v_cache.shape != shape or v_cache.dtype != k_cache.dtype:
         raise PagedKVError("k_cache and v_cache must have the same shape and dtype")
     if len(shape) != 4 or shape[2] != BLOCK_SIZE:
         raise PagedKVError(f"cache must be [num_blocks, num_kv_heads, 16, head_size], got {tuple(shape)}")
     nb, hkv, _, d = shape
+    if packed:
+        d *= 2
+        if k_cache.dtype is not torch.uint8:
+            raise PagedKVError("an INT4 cache is a torch.uint8 tensor (alloc_kv_cache)")
     ref = _descs.get((nb, hkv, d))
     if ref is None:
         if len(_descs) > 256:
@@ -923,14 +974,15 @@ def kv_cache_accept(k_cache, v_cache, block_tables, context_lens, accepted, num_
     row base + i of sequence s becomes row base + accepted[s, i] for i < num_accepted[s] (all
     rows read before any is written) and new_context_lens[s] = base + num_accepted[s]. n_s is
     max_q_per_seq, or from cu_q_lens. accepted: int32 [num_seqs, max_accepted]; new_context_lens
-    may be None. An INT8 cache's row scales move along."""
+    may be None. An INT8 or INT4 cache's scales move along."""
     dev = _placed(_ACCEPT_NAMES, (k_cache, v_cache, block_tables, context_lens, accepted, num_accepted,
                                   new_context_lens, cu_q_lens, scales, device_status))
     for nm, t in (("block_tables", block_tables), ("context_lens", context_lens), ("accepted", accepted),
                   ("num_accepted", num_accepted), ("new_context_lens", new_context_lens), ("cu_q_lens", cu_q_lens)):
         if t is not None and t.dtype is not torch.int32:
             raise PagedKVError(f"{nm} must be int32")
-    desc, _, _ = _desc_of(k_cache, v_cache)
+    code = _kv_code(kv_dtype, k_cache)
+    desc, _, _ = _desc_of(k_cache, v_cache, code == KV_INT4)
     if context_lens.dim() != 1:
         raise PagedKVError("context_lens must be 1-D [num_seqs]")
     S = context_lens.shape[0]
@@ -943,7 +995,6 @@ def kv_cache_accept(k_cache, v_cache, block_tables, context_lens, accepted, num_
         raise PagedKVError("new_context_lens must be [num_seqs]")
     if cu_q_lens is not None and cu_q_lens.shape != (S + 1,):
         raise PagedKVError("cu_q_lens must have num_seqs + 1 entries")
-    code = _kv_code(kv_dtype, k_cache)
     _int8_scales(code, k_cache, scales)
     _status_word(device_status)
     lib = _lib or load_library()
@@ -955,6 +1006,154 @@ def kv_cache_accept(k_cache, v_cache, block_tables, context_lens, accepted, num_
     if rc:
         _check(rc, "kv_cache_accept")
     return new_context_lens
+
+
+# ------------------------------------------------------------------------------------
+# INT4 cache; reading any cache back
+# ------------------------------------------------------------------------------------
+
+def _is_int4(kv_dtype) -> bool:
+    return kv_dtype == "int4" or (type(kv_dtype) is int and kv_dtype == KV_INT4)
+
+
+_ROW_NAMES = ("key", "value", "slot_mapping", "k_cache", "v_cache", "scales", "device_status")
+
+
+def _row_shapes(key, value, slot_mapping, hkv, head) -> int:
+    """Tokens of key and value [T, Hkv, D] of one 16-bit type with one slot each."""
+    shape = key.shape
+    if len(shape) != 3 or shape[1] != hkv or shape[2] != head or value.shape != shape:
+        raise PagedKVError(f"key and value must both be [T, {hkv}, {head}], got {tuple(shape)} and "
+                           f"{tuple(value.shape)}")
+    if value.dtype is not key.dtype:
+        raise PagedKVError("key and value must share a dtype")
+    if slot_mapping.dtype is not torch.int32 or slot_mapping.shape != shape[:1]:
+        raise PagedKVError("slot_mapping must be int32 with one slot per token")
+    return shape[0]
+
+
+def kv_cache_write_int4(key, value, slot_mapping, k_cache, v_cache, scales, *, device_status=None, stream=None):
+    """Quantise fp16 or bf16 key/value [T, Hkv, D] into the slots of an INT4 cache (alloc_kv_cache(...,
+    "int4"), alloc_kv_scales(..., kv_dtype="int4")). Of every 64 dimensions of a row: z, the largest
+    fp16 number not above the least value; s, the smallest one not below (largest - z) / 15; and
+    the codes 0..15 whose values z + s c are nearest (halfway: the even one)."""
+    dev = _placed(_ROW_NAMES, (key, value, slot_mapping, k_cache, v_cache, scales, device_status))
+    desc, hkv, head = _desc_of(k_cache, v_cache, True)
+    T = _row_shapes(key, value, slot_mapping, hkv, head)
+    _scales_shape(k_cache, scales, KV_INT4)
+    _status_word(device_status)
+    lib = _lib or load_library()
+    with _at(dev):
+        rc = lib.pkv_kv_cache_write_int4(
+            key.data_ptr(), value.data_ptr(), _src_code(key), T, slot_mapping.data_ptr(), k_cache.data_ptr(),
+            v_cache.data_ptr(), scales.data_ptr(), desc, _addr(device_status), _stream_of(stream, dev))
+    if rc:
+        _check(rc, "kv_cache_write_int4")
+
+
+def kv_cache_read(key, value, slot_mapping, k_cache, v_cache, kv_dtype=None, *, scales=None, device_status=None,
+                  stream=None):
+    """key/value [T, Hkv, D] (fp16 or bf16, written) become the values that rows slot_mapping[t] of a
+    cache of any type stand for; the rows of a slot -1 stay as they are. An INT8 or INT4 cache
+    takes its scales."""
+    dev = _placed(_ROW_NAMES, (key, value, slot_mapping, k_cache, v_cache, scales, device_status))
+    code = _kv_code(kv_dtype, k_cache)
+    desc, hkv, head = _desc_of(k_cache, v_cache, code == KV_INT4)
+    T = _row_shapes(key, value, slot_mapping, hkv, head)
+    _int8_scales(code, k_cache, scales)
+    _status_word(device_status)
+    lib = _lib or load_library()
+    with _at(dev):
+        rc = lib.pkv_kv_cache_read(
+            key.data_ptr(), value.data_ptr(), _src_code(key), T, slot_mapping.data_ptr(), k_cache.data_ptr(),
+            v_cache.data_ptr(), _addr(scales), code, desc, _addr(device_status), _stream_of(stream, dev))
+    if rc:
+        _check(rc, "kv_cache_read")
+    return key, value
+
+
+_int4_workspaces: dict = {}
+_int4_ws_bytes: dict = {}
+
+
+def _int4_workspace(nbytes: int, dev: int, stream) -> torch.Tensor:
+    """Scratch of an INT4 decode: one buffer per (device, stream the call runs on), grown as
+    needed; a call that is being captured gets a buffer of its own from the graph's memory pool.
+    Its counters are tagged with the call's number, so what it holds does not matter."""
+    with _NOWHERE if stream is None else torch.cuda.stream(stream):
+        if torch.cuda.is_current_stream_capturing():
+            return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
+        key = (dev, _stream_of(stream, dev))
+        ws = _int4_workspaces.get(key)
+        if ws is None or ws.shape[0] < nbytes:
+            ws = _int4_workspaces[key] = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=dev)
+        return ws
+
+
+_DECODE4_NAMES = ("q", "out", "k_cache", "v_cache", "scales", "block_tables", "context_lens", "cu_q_lens", "tree_masks",
+                  "workspace", "device_status")
+
+
+def _decode_int4(what, out, q, cu_q_lens, tree_masks, k_cache, v_cache, scales, block_tables, context_lens,
+                 max_q_per_seq, scale, workspace, device_status, stream):
+    if scales is None:
+        raise PagedKVError("an INT4 cache is read with its scales (alloc_kv_scales)")
+    dev = _placed(_DECODE4_NAMES, (q, out, k_cache, v_cache, scales, block_tables, context_lens, cu_q_lens, tree_masks,
+                                   workspace, device_status))
+    i32 = torch.int32
+    if block_tables.dtype is not i32 or context_lens.dtype is not i32:
+        raise PagedKVError("block_tables and context_lens must be int32")
+    desc, _, D = _desc_of(k_cache, v_cache, True)
+    _scales_shape(k_cache, scales, KV_INT4)
+    shape = q.shape
+    if len(shape) != 3 or out.shape != shape or shape[2] != D:
+        raise PagedKVError(f"q and out must both be [rows, num_q_heads, {D}], got {tuple(shape)} and "
+                           f"{tuple(out.shape)}")
+    if out.dtype is not q.dtype:
+        raise PagedKVError("out and q must share a dtype")
+    R, Hq, _ = shape
+    if context_lens.dim() != 1:
+        raise PagedKVError("context_lens must be 1-D [num_seqs]")
+    S, n = context_lens.shape[0], int(max_q_per_seq)
+    tables = block_tables.shape
+    if len(tables) != 2 or tables[0] < S:
+        raise PagedKVError(f"block_tables must be [num_seqs, max_blocks_per_seq], got {tuple(tables)}")
+    if cu_q_lens is None:
+        if R != S * n:
+            raise PagedKVError(f"q must have num_seqs * q_per_seq = {S * n} rows, got {R}")
+    elif cu_q_lens.dtype is not i32 or cu_q_lens.shape != (S + 1,):
+        raise PagedKVError("cu_q_lens must be int32 with num_seqs + 1 entries")
+    elif not S <= R <= S * n:
+        raise PagedKVError(f"q must have between num_seqs and num_seqs * max_q_per_seq rows, got {R}")
+    if tree_masks is not None and (tree_masks.dtype not in (torch.int64, torch.uint64) or tree_masks.shape != (R,)):
+        raise PagedKVError("tree_masks must be 64-bit, one mask per query row")
+    _status_word(device_status)
+    lib = _lib or load_library()
+    with _at(dev):
+        if workspace is None:
+            key = (dev, S, Hq, n, k_cache.shape[1], D)
+            need = _int4_ws_bytes.get(key)
+            if need is None:
+                if len(_int4_ws_bytes) > 4096:
+                    _int4_ws_bytes.clear()
+                need = _int4_ws_bytes[key] = int(lib.pkv_decode_workspace_bytes(S, Hq, n, desc))
+            workspace = _int4_workspace(need, dev, stream)
+        rc = lib.pkv_paged_attention_decode_int4(
+            out.data_ptr(), q.data_ptr(), _src_code(q), _addr(cu_q_lens), _addr(tree_masks), R, S, Hq, n,
+            k_cache.data_ptr(), v_cache.data_ptr(), scales.data_ptr(), desc, block_tables.data_ptr(), tables[1],
+            context_lens.data_ptr(), scale, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+            _addr(device_status), _stream_of(stream, dev))
+    if rc:
+        _check(rc, what)
+    return out
+
+
+def paged_attention_decode_int4(out, q, k_cache, v_cache, scales, block_tables, context_lens, q_per_seq: int,
+                                scale: float, *, workspace=None, device_status=None, stream=None):
+    """paged_attention_decode over an INT4 cache with its scales (q/out fp16 or bf16).
+    paged_attention_decode_varlen, _tree and _chunked take one with kv_dtype="int4" and ``scales``."""
+    return _decode_int4("paged_attention_decode_int4", out, q, None, None, k_cache, v_cache, scales, block_tables,
+                        context_lens, q_per_seq, scale, workspace, device_status, stream)
 
 
 # ------------------------------------------------------------------------------------
@@ -1052,7 +1251,7 @@ class BlockAllocator:
 
 def copy_blocks(k_cache, v_cache, src, dst, kv_dtype=None, *, scales=None, device_status=None, stream=None):
     """Physical block dst[i] of both caches becomes a copy of block src[i]
-    (int32 device tensors of equal length); an INT8 cache's row scales
+    (int32 device tensors of equal length); an INT8 or INT4 cache's scales
     (``scales``, from alloc_kv_scales) are copied with its blocks."""
     for n_, t in (("k_cache", k_cache), ("v_cache", v_cache), ("src", src), ("dst", dst)):
         _need_cuda_contig(n_, t)
@@ -1060,11 +1259,13 @@ def copy_blocks(k_cache, v_cache, src, dst, kv_dtype=None, *, scales=None, devic
         raise PagedKVError("src and dst must be int32 tensors of equal length")
     d = _pair(k_cache, v_cache)
     code = _kv_code(kv_dtype, k_cache)
-    if (code == KV_INT8) != (scales is not None):
-        raise PagedKVError("an INT8 cache is copied with its scales; other caches take none")
+    if (code in (KV_INT8, KV_INT4)) != (scales is not None):
+        raise PagedKVError("an INT8 or INT4 cache is copied with its scales; other caches take none")
     if scales is not None:
         _need_cuda_contig("scales", scales)
-        _scales_shape(k_cache, scales)
+        _scales_shape(k_cache, scales, code)
+    if code == KV_INT4:
+        d.head_size *= 2
     rc = load_library().pkv_copy_blocks(_ptr(k_cache), _ptr(v_cache), _ptr(scales), code,
                                         ctypes.byref(d), _ptr(src), _ptr(dst), int(src.numel()),
                                         _ptr(device_status), _stream_handle(stream, k_cache.device))

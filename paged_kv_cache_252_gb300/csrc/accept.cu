@@ -26,7 +26,7 @@ constexpr int kMaxDrafts = 64;
 struct AcceptArgs {
   uint4* k_cache;
   uint4* v_cache;
-  float* scales;
+  uint32_t* scales;             // 32-bit words, scale_words a row, or null
   const int32_t* block_tables;
   const int32_t* context_lens;
   const int32_t* cu_q_lens;
@@ -35,7 +35,8 @@ struct AcceptArgs {
   int32_t* new_context_lens;    // may be null
   int32_t* status;
   int32_t num_blocks, num_kv_heads, max_blocks_per_seq, max_q_per_seq, max_accepted;
-  int32_t row_chunks;           // 16-byte chunks of one row (4, 8 or 16)
+  int32_t row_chunks;           // 16-byte chunks of one row (2, 4, 8 or 16)
+  int32_t scale_words;          // 0, 1 or 2
 };
 
 __global__ void __launch_bounds__(kAcceptThreads) accept_kernel(const AcceptArgs a) {
@@ -91,10 +92,18 @@ __global__ void __launch_bounds__(kAcceptThreads) accept_kernel(const AcceptArgs
       if (row >= 0) held[k] = (i < per_cache ? a.k_cache : a.v_cache)[row * a.row_chunks + r % a.row_chunks];
     }
   }
-  float scale = 0.f;   // an INT8 cache's row scales: K of row tid, then V of row tid - m
-  const bool has_scale = a.scales && tid < 2 * m;
-  const int sr = tid < m ? tid : tid - m, sv = tid < m ? 0 : 16;
-  if (has_scale && src_row[sr] >= 0) scale = a.scales[(src_row[sr] >> 4) * 32 + sv + (src_row[sr] & 15)];
+  // An INT8 or INT4 cache's scales: words of row 0's K, row 0's V, row 1's K, ...
+  constexpr int kHeldWords = 4 * kMaxDrafts / kAcceptThreads;
+  uint32_t words[kHeldWords];
+  const int sw = a.scale_words, per_row = 2 * sw, scale_total = m * per_row;
+  auto word_at = [&](long long row, int w) -> uint32_t& {   // [block][head][K, V][16][sw]
+    return a.scales[((row >> 4) * 32 + (w >= sw ? 16 : 0) + (row & 15)) * sw + (w >= sw ? w - sw : w)];
+  };
+#pragma unroll
+  for (int k = 0; k < kHeldWords; ++k) {
+    const int i = tid + k * kAcceptThreads;
+    if (i < scale_total && src_row[i / per_row] >= 0) words[k] = word_at(src_row[i / per_row], i % per_row);
+  }
   __syncthreads();   // every row is read before any is written
 #pragma unroll
   for (int k = 0; k < kHeld; ++k) {
@@ -105,7 +114,11 @@ __global__ void __launch_bounds__(kAcceptThreads) accept_kernel(const AcceptArgs
       if (src_row[d] >= 0) (i < per_cache ? a.k_cache : a.v_cache)[dst_row[d] * a.row_chunks + r % a.row_chunks] = held[k];
     }
   }
-  if (has_scale && src_row[sr] >= 0) a.scales[(dst_row[sr] >> 4) * 32 + sv + (dst_row[sr] & 15)] = scale;
+#pragma unroll
+  for (int k = 0; k < kHeldWords; ++k) {
+    const int i = tid + k * kAcceptThreads;
+    if (i < scale_total && src_row[i / per_row] >= 0) word_at(dst_row[i / per_row], i % per_row) = words[k];
+  }
 }
 
 }  // namespace pkv
@@ -119,11 +132,12 @@ extern "C" int pkv_kv_cache_accept(void* k_cache, void* v_cache, float* scales, 
   using namespace pkv;
   if (!cache_desc_ok(cache) || num_seqs < 0 || max_q_per_seq <= 0 || max_accepted <= 0 || max_blocks_per_seq <= 0)
     return PKV_ERR_INVALID_ARGUMENT;
-  if (kv_dtype != PKV_FP16 && kv_dtype != PKV_BF16 && kv_dtype != PKV_FP8_E5M2 && kv_dtype != PKV_INT8)
+  if (kv_dtype != PKV_FP16 && kv_dtype != PKV_BF16 && kv_dtype != PKV_FP8_E5M2 && kv_dtype != PKV_INT8 &&
+      kv_dtype != PKV_INT4)
     return PKV_ERR_UNSUPPORTED;
   if (max_q_per_seq > kMaxDrafts || max_blocks_per_seq > (1 << 26)) return PKV_ERR_UNSUPPORTED;
   if (static_cast<long long>(num_seqs) * cache->num_kv_heads >= (1ll << 31)) return PKV_ERR_UNSUPPORTED;
-  if ((kv_dtype == PKV_INT8) != (scales != nullptr)) return PKV_ERR_INVALID_ARGUMENT;
+  if ((kv_dtype == PKV_INT8 || kv_dtype == PKV_INT4) != (scales != nullptr)) return PKV_ERR_INVALID_ARGUMENT;
   if (num_seqs == 0) return PKV_OK;
   if (!k_cache || !v_cache || !block_tables || !context_lens || !accepted || !num_accepted)
     return PKV_ERR_INVALID_ARGUMENT;
@@ -142,7 +156,7 @@ extern "C" int pkv_kv_cache_accept(void* k_cache, void* v_cache, float* scales, 
   AcceptArgs a{};
   a.k_cache = static_cast<uint4*>(k_cache);
   a.v_cache = static_cast<uint4*>(v_cache);
-  a.scales = scales;
+  a.scales = reinterpret_cast<uint32_t*>(scales);
   a.block_tables = block_tables;
   a.context_lens = context_lens;
   a.cu_q_lens = cu_q_lens;
@@ -156,6 +170,7 @@ extern "C" int pkv_kv_cache_accept(void* k_cache, void* v_cache, float* scales, 
   a.max_q_per_seq = max_q_per_seq;
   a.max_accepted = max_accepted;
   a.row_chunks = tile_row_bytes(static_cast<int>(kv_dtype), cache->head_size) / 16;
+  a.scale_words = row_scale_words(static_cast<int>(kv_dtype), cache->head_size);
   void* args[1] = {&a};
   const long long grid = static_cast<long long>(num_seqs) * cache->num_kv_heads;
   return launch_overlapped(reinterpret_cast<const void*>(&accept_kernel), dim3(static_cast<unsigned>(grid)),

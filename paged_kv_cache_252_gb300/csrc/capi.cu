@@ -417,13 +417,14 @@ size_t pkv_decode_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t
   const int rows = (num_q_heads / cache->num_kv_heads) * q_per_seq;
   if (rows > kMaxRows) return 0;
   if (cache->head_size != 64 && cache->head_size != 128) return 0;
+  // The grid follows the kv dtype's occupancy; size for the largest over the
+  // supported dtypes so that one workspace serves any of them.
+  int ctas = 1;
+  if (decode_int4_ctas(cache->head_size, rows, &ctas)) return 0;
   std::lock_guard<std::mutex> lock(g_mu);
   DeviceState* st = nullptr;
   if (current_device_state(&st)) return 0;
   const long long units = static_cast<long long>(num_seqs) * cache->num_kv_heads;
-  // The grid follows the kv dtype's occupancy; size for the largest over the
-  // supported dtypes so that one workspace serves any of them.
-  int ctas = 1;
   for (int kv = kKvF16; kv <= kKvInt8; ++kv) {
     GeomEntry* ge = nullptr;
     if (get_geometry(st, kv, cache->head_size, rows, &ge)) return 0;

@@ -117,13 +117,12 @@ size_t pkv_decode_chunked_workspace_bytes(const int32_t* host_q_lens, int32_t nu
   return chunked_layout(tiles, max_blocks_per_seq, dec).total;
 }
 
-int pkv_paged_attention_decode_chunked(void* out, const void* q, const int32_t* host_q_lens,
-                                       const int32_t* host_context_lens, int32_t num_seqs, int32_t num_q_heads,
-                                       const void* k_cache, const void* v_cache, const float* scales,
-                                       pkv_dtype kv_dtype, const pkv_cache_desc* cache,
-                                       const int32_t* block_tables, int32_t max_blocks_per_seq, float scale,
-                                       void* workspace, size_t workspace_bytes, int32_t* device_status,
-                                       void* stream) {
+// q_dtype: of an INT4 cache's queries (the other caches' types name theirs).
+static int decode_chunked(void* out, const void* q, pkv_dtype q_dtype, const int32_t* host_q_lens,
+                          const int32_t* host_context_lens, int32_t num_seqs, int32_t num_q_heads,
+                          const void* k_cache, const void* v_cache, const void* scales, pkv_dtype kv_dtype,
+                          const pkv_cache_desc* cache, const int32_t* block_tables, int32_t max_blocks_per_seq,
+                          float scale, void* workspace, size_t workspace_bytes, int32_t* device_status, void* stream) {
   int q_tile = 0;
   long long tiles = 0, rows = 0;
   if (max_blocks_per_seq <= 0 || !count_tiles(host_q_lens, num_seqs, num_q_heads, cache, &q_tile, &tiles, &rows))
@@ -180,9 +179,16 @@ int pkv_paged_attention_decode_chunked(void* out, const void* q, const int32_t* 
     cudaGetLastError();
     return PKV_ERR_CUDA;
   }
+  if (kv_dtype == PKV_INT4) {
+    return pkv_paged_attention_decode_int4(out, q, q_dtype, d_cu, nullptr, static_cast<int32_t>(rows),
+                                           static_cast<int32_t>(T), num_q_heads, q_tile, k_cache, v_cache, scales,
+                                           cache, d_vbt, max_blocks_per_seq, d_ctx, scale, wdec, L.decode_bytes,
+                                           device_status, stream);
+  }
   if (kv_dtype == PKV_INT8) {
     return pkv_paged_attention_decode_int8_varlen(out, q, d_cu, static_cast<int32_t>(rows), static_cast<int32_t>(T),
-                                                  num_q_heads, q_tile, k_cache, v_cache, scales, cache, d_vbt,
+                                                  num_q_heads, q_tile, k_cache, v_cache,
+                                                  static_cast<const float*>(scales), cache, d_vbt,
                                                   max_blocks_per_seq, d_ctx, scale, wdec, L.decode_bytes,
                                                   device_status, stream);
   }
@@ -190,6 +196,30 @@ int pkv_paged_attention_decode_chunked(void* out, const void* q, const int32_t* 
                                            num_q_heads, q_tile, k_cache, v_cache, kv_dtype, cache, d_vbt,
                                            max_blocks_per_seq, d_ctx, scale, wdec, L.decode_bytes, device_status,
                                            stream);
+}
+
+int pkv_paged_attention_decode_chunked(void* out, const void* q, const int32_t* host_q_lens,
+                                       const int32_t* host_context_lens, int32_t num_seqs, int32_t num_q_heads,
+                                       const void* k_cache, const void* v_cache, const float* scales,
+                                       pkv_dtype kv_dtype, const pkv_cache_desc* cache,
+                                       const int32_t* block_tables, int32_t max_blocks_per_seq, float scale,
+                                       void* workspace, size_t workspace_bytes, int32_t* device_status,
+                                       void* stream) {
+  if (kv_dtype == PKV_INT4) return PKV_ERR_UNSUPPORTED;   // pkv_paged_attention_decode_int4_chunked
+  return decode_chunked(out, q, PKV_FP16, host_q_lens, host_context_lens, num_seqs, num_q_heads, k_cache, v_cache,
+                        scales, kv_dtype, cache, block_tables, max_blocks_per_seq, scale, workspace, workspace_bytes,
+                        device_status, stream);
+}
+
+int pkv_paged_attention_decode_int4_chunked(void* out, const void* q, pkv_dtype q_dtype, const int32_t* host_q_lens,
+                                            const int32_t* host_context_lens, int32_t num_seqs, int32_t num_q_heads,
+                                            const void* k_cache, const void* v_cache, const void* scales,
+                                            const pkv_cache_desc* cache, const int32_t* block_tables,
+                                            int32_t max_blocks_per_seq, float scale, void* workspace,
+                                            size_t workspace_bytes, int32_t* device_status, void* stream) {
+  return decode_chunked(out, q, q_dtype, host_q_lens, host_context_lens, num_seqs, num_q_heads, k_cache, v_cache,
+                        scales, PKV_INT4, cache, block_tables, max_blocks_per_seq, scale, workspace, workspace_bytes,
+                        device_status, stream);
 }
 
 }  // extern "C"

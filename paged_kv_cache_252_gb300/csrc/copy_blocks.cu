@@ -1,8 +1,8 @@
 // Block copy for copy-on-write (declared in include/pagedkv.h): physical block
-// dst[i] of the K and the V cache (and, for an INT8 cache, of its row scales)
+// dst[i] of the K and the V cache (and, for an INT8 or INT4 cache, of its scales)
 // becomes a copy of block src[i]. A block of one cache is contiguous
 // ([num_kv_heads][16][head_size] elements), and so are its scales
-// ([num_kv_heads][2][16] floats), so the copy is a grid-stride loop of 16-byte
+// ([num_kv_heads][2][16] rows of 32-bit words), so the copy is a grid-stride loop of 16-byte
 // loads and stores over (pair, array, chunk).
 #include <cuda_runtime.h>
 
@@ -16,7 +16,7 @@ namespace pkv {
 struct CopyBlocksArgs {
   uint4* k_cache;
   uint4* v_cache;
-  uint4* scales;                // INT8 row scales, or null
+  uint4* scales;                // INT8 or INT4 scales, or null
   const int32_t* src;
   const int32_t* dst;
   int32_t* status;
@@ -63,10 +63,11 @@ extern "C" int pkv_copy_blocks(void* k_cache, void* v_cache, float* scales, pkv_
                                int32_t* device_status, void* stream) {
   using namespace pkv;
   if (!cache || n < 0) return PKV_ERR_INVALID_ARGUMENT;
-  if (kv_dtype != PKV_FP16 && kv_dtype != PKV_BF16 && kv_dtype != PKV_FP8_E5M2 && kv_dtype != PKV_INT8)
+  if (kv_dtype != PKV_FP16 && kv_dtype != PKV_BF16 && kv_dtype != PKV_FP8_E5M2 && kv_dtype != PKV_INT8 &&
+      kv_dtype != PKV_INT4)
     return PKV_ERR_UNSUPPORTED;
-  // An INT8 cache's blocks are copied with their row scales; other caches have none.
-  if ((kv_dtype == PKV_INT8) != (scales != nullptr)) return PKV_ERR_INVALID_ARGUMENT;
+  // The blocks of an INT8 or INT4 cache are copied with their scales; other caches have none.
+  if ((kv_dtype == PKV_INT8 || kv_dtype == PKV_INT4) != (scales != nullptr)) return PKV_ERR_INVALID_ARGUMENT;
   if (scales && (reinterpret_cast<uintptr_t>(scales) & 15u)) return PKV_ERR_INVALID_ARGUMENT;
   if (cache->block_size != kBlockSize || cache->num_blocks <= 0 || cache->num_kv_heads <= 0 ||
       (cache->head_size != 64 && cache->head_size != 128))
@@ -84,9 +85,9 @@ extern "C" int pkv_copy_blocks(void* k_cache, void* v_cache, float* scales, pkv_
   a.src = src;
   a.dst = dst;
   a.status = device_status;
-  a.chunks_per_block = static_cast<long long>(cache->num_kv_heads) * kBlockSize * cache->head_size *
-                       kv_elem_bytes(static_cast<int>(kv_dtype)) / 16;
-  a.scale_chunks = scales ? static_cast<long long>(cache->num_kv_heads) * 2 * kBlockSize * 4 / 16 : 0;
+  const int kv = static_cast<int>(kv_dtype);
+  a.chunks_per_block = static_cast<long long>(cache->num_kv_heads) * tile_bytes(kv, cache->head_size) / 16;
+  a.scale_chunks = static_cast<long long>(cache->num_kv_heads) * 2 * kBlockSize * row_scale_words(kv, cache->head_size) / 4;
   a.num_blocks = cache->num_blocks;
   a.n = n;
   const long long total = static_cast<long long>(n) * (2 * a.chunks_per_block + a.scale_chunks);

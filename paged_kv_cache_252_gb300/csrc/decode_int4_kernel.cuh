@@ -1,0 +1,660 @@
+// Paged decode attention over an INT4 cache (layout and codec: pkv_int4.cuh). The work line, the
+// pieces and their combination are those of decode_common.cuh; this file is what a CTA does
+// with its share.
+//
+// Mathematics. With a group's codes c, scale s and least value z (K: per token and 64 dimensions):
+//   score(t, r) = sum over groups  s_tg (q_rg . c_tg) + z_tg sum(q_rg)
+//   out(r, d)   = sum over t  p_tr (z_tg + s_tg c_td) / sum over t p_tr
+//               = [ sum_t P_tr (c_td - 8)  +  sum_t p_tr (z_tg + 8 s_tg) ] / sum_t p_tr,   P = p s
+// so both products run on the codes themselves (mma.sync m16n8k16, fp16 operands, fp32
+// accumulators) and the scales touch only scores and weights. A code enters without any
+// conversion: four bits in the lowest bits of a 16-bit half are the fp16 number c 2^-24, four
+// bits above them c 2^-20, so one AND makes a pair of operands. The 2^-24 is exact and comes off in
+// fp32; where a pair is 16 times too large, q is stored 16 times smaller (K) or the output
+// row is scaled at the end (V). The 8 is taken off by a product with a constant operand, over the same
+// rounded P.
+//
+// Precision. q is scaled by a power of two per row so that its largest element lies in [2^11, 2^12):
+// fp16 then holds fp16 and bf16 queries (8 significant bits) exactly down to 2^-26 of the
+// largest. The running reference m of a row is of the score plus the exponent of the token's V scale, so
+// that P, rounded to fp16, is at most 2^15 and keeps all its bits down to 2^-25 of the largest contribution
+// whatever the scales' size. m starts from and moves on exact maxima, but only when a P (or a p beside a
+// zero scale) passes the limit: a rare, warp-wide event.
+//
+// Structure of a CTA: WR x WB warps. Row warp wr has 8 NT of the unit's rows; stream wb takes every
+// WB-th block of the share through a ring of its own of STAGES blocks, filled by cp.async of the stream's
+// own warps (no producer warp: at 2.3 KB a block one issuing thread would bound the CTA).
+// A lane's K words of a token (neighbouring 16 bytes) are the A operand of S^T = K Q^T as they
+// lie; V words of two tokens are paired by byte permutes for O^T = V^T P^T. The tokens of a
+// block take the 16 product slots in an order in which both reads hit all banks.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+
+#include "decode_common.cuh"
+#include "decode_int4.h"
+#include "pkv_int4.cuh"
+#include "pkv_internal.h"
+#include "pkv_ptx.cuh"
+
+namespace pkv {
+
+template <int D>
+struct Int4Tile {
+  static constexpr int G = D / kInt4Group;
+  static constexpr int RB = D / 2;               // bytes of a row
+  static constexpr int TILE = kBlockSize * RB;   // bytes of a block's K (or V)
+  static constexpr int META = 2 * kBlockSize * G * 4;
+  static constexpr int STAGE = 2 * TILE + META;
+};
+
+// Warps and ring of the kernel for a row count. Eight rows a CTA: twelve warps an SM in three
+// CTAs; wider units two CTAs.
+template <int NT_, int WR_, int WB_, int STAGES_, int CTAS_>
+struct Int4Shape {
+  static constexpr int NT = NT_, WR = WR_, WB = WB_, STAGES = STAGES_, CTAS = CTAS_;
+  static constexpr int ROWS = 8 * NT * WR, THREADS = 32 * WR * WB;
+};
+using Int4Rows8 = Int4Shape<1, 1, 4, 6, 3>;
+using Int4Rows16 = Int4Shape<2, 1, 4, 7, 2>;
+using Int4Rows32 = Int4Shape<2, 2, 2, 10, 2>;
+using Int4Rows64 = Int4Shape<2, 4, 1, 12, 2>;
+
+struct Int4Smem {
+  int qs, rf, qsum, mrg_o, mrg_ml, fin_ml, misc, total;
+};
+template <int D, class Sh>
+__host__ __device__ constexpr Int4Smem int4_smem(int rows) {
+  Int4Smem s{};
+  s.qs = Sh::WB * Sh::STAGES * Int4Tile<D>::STAGE;
+  s.rf = s.qs + Sh::ROWS * (D * 2 + 16);
+  s.qsum = s.rf + Sh::ROWS * 4;
+  s.mrg_o = s.qsum + Sh::ROWS * Int4Tile<D>::G * 4;
+  s.mrg_ml = s.mrg_o + Sh::WB * rows * (D + 4) * 4;
+  s.fin_ml = s.mrg_ml + (Sh::WB * rows * 8 + 15) / 16 * 16;
+  s.misc = s.fin_ml + (rows * 8 + 15) / 16 * 16;
+  s.total = s.misc + 256;
+  return s;
+}
+
+template <int N>
+__device__ __forceinline__ void cp_async_wait_groups() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+__device__ __forceinline__ uint4 lds_v4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+template <int N>
+__device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&w)[N]) {
+  if constexpr (N == 1) {
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(addr) : "memory");
+  } else if constexpr (N == 2) {
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr) : "memory");
+  } else {
+    const uint4 v = lds_v4(addr);
+    w[0] = v.x;
+    w[1] = v.y;
+    w[2] = v.z;
+    w[3] = v.w;
+  }
+}
+
+// The reference m of a row before any visible score: low enough to be left by any score.
+constexpr float kInt4Unset = -1e37f;
+constexpr float kInt4Shift = 11.f;     // P of the reference's own token: below 2^11
+constexpr float kInt4Limit = 32768.f;  // P that moves the reference
+constexpr float kInt4FarP = 1.0995116e12f;   // 2^40: a p that moves it (its scale may be 0)
+
+// e with |s| < 2^e, at least -25 (a scale of 0).
+__device__ __forceinline__ float int4_scale_exponent(float s) {
+  return fmaxf(static_cast<float>(static_cast<int>(__float_as_uint(fabsf(s)) >> 23) - 126), -25.f);
+}
+
+template <int D, class Sh, bool BF16>
+__global__ void __launch_bounds__(Sh::THREADS, Sh::CTAS) decode_int4_kernel(const __grid_constant__ DecodeInt4Args a) {
+  using T = Int4Tile<D>;
+  constexpr int G = T::G, NT = Sh::NT, WR = Sh::WR, WB = Sh::WB, STAGES = Sh::STAGES, NTHR = Sh::THREADS;
+  constexpr int QS = D * 2 + 16;
+  constexpr float kNegInf = -INFINITY;
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int R = a.rows;
+  const Int4Smem lay = int4_smem<D, Sh>(R);
+  uint8_t* qs = smem + lay.qs;
+  float* rf_s = reinterpret_cast<float*>(smem + lay.rf);
+  float* qsum_s = reinterpret_cast<float*>(smem + lay.qsum);
+  float* mrg_o = reinterpret_cast<float*>(smem + lay.mrg_o);
+  float* mrg_m = reinterpret_cast<float*>(smem + lay.mrg_ml);
+  float* mrg_l = mrg_m + WB * R;
+  float* fin_ml = reinterpret_cast<float*>(smem + lay.fin_ml);
+  long long* red = reinterpret_cast<long long*>(smem + lay.misc);
+  long long* plan = red + 10;
+  volatile int* fin = reinterpret_cast<volatile int*>(plan + 5);
+  volatile unsigned long long* fin_cur = reinterpret_cast<volatile unsigned long long*>(plan + 8);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int wr = warp % WR, wb = warp / WR;
+  const int i8 = lane >> 2, c4 = lane & 3;
+  const int row_base = wr * 8 * NT;
+
+  // Padding rows: zero queries and factors.
+  for (int idx = tid; idx < Sh::ROWS * (QS / 16); idx += NTHR) reinterpret_cast<uint4*>(qs)[idx] = make_uint4(0, 0, 0, 0);
+  for (int idx = tid; idx < Sh::ROWS * (1 + G); idx += NTHR) rf_s[idx] = 0.f;
+
+  prefetch_plan_inputs(a.context_lens, a.block_tables, a.num_seqs, a.max_blocks_per_seq);
+  // Everything below reads inputs a previous kernel in the stream may write.
+  pdl_wait_prior_grid();
+  const int Hkv = a.num_kv_heads, mbs = a.max_blocks_per_seq;
+  const int n = a.q_per_seq, Gq = a.group, Hq = a.num_q_heads;
+  const long long ncta = gridDim.x;
+  plan_cta_share(a, red, plan);
+  pdl_launch_dependents();
+  const long long total = plan[0], b0 = plan[1], b1 = plan[2];
+  if (b0 >= b1 || plan[3] < 0) return;
+
+  // Walk state: the unit (s, h), its first block's position ub on the work line, the first block
+  // lb this CTA takes of it.
+  const int pc0 = a.piece_cost;
+  int s = static_cast<int>(plan[3]);
+  int ctx = a.context_lens[s];
+  int nb = unit_blocks(ctx, mbs);
+  int h, lb;
+  long long ub;
+  {
+    const long long off = b0 - static_cast<long long>(Hkv) * plan[4];
+    h = static_cast<int>(off / (nb + pc0));
+    const int o = static_cast<int>(off % (nb + pc0));
+    lb = o > pc0 ? o - pc0 : 0;
+    ub = b0 - o + pc0;
+  }
+
+  // ---- the stream's fetching: the same walk, up to STAGES - 1 of its blocks ahead ----
+  const uint32_t ring = smem_addr(smem) + wb * (STAGES * T::STAGE);
+  int f_s = s, f_h = h, f_lb = lb, f_nb = nb;
+  long long f_ub = ub;
+  int f_take = static_cast<int>(min(static_cast<long long>(nb), b1 - ub)) - lb;
+  int f_k = wb;              // the stream's next block in the piece
+  int f_id = 0, f_pos = 32;  // 32 of the stream's block ids, one a lane; the next one's lane
+  bool f_more = true;
+  auto fetch = [&](int slot) {
+    if (f_more) {
+      while (f_k >= f_take) {
+        f_k -= f_take;
+        f_pos = 32;
+        if (f_lb + f_take < f_nb) {
+          f_more = false;
+          break;
+        }
+        f_ub += f_nb + pc0;
+        f_lb = 0;
+        if (f_ub >= b1) {
+          f_more = false;
+          break;
+        }
+        if (++f_h == Hkv) {
+          f_h = 0;
+          ++f_s;
+          f_nb = unit_blocks(a.context_lens[f_s], mbs);
+        }
+        f_take = static_cast<int>(min(static_cast<long long>(f_nb), b1 - f_ub));
+      }
+    }
+    if (f_more) {
+      if (f_pos == 32) {
+        const int k = f_k + lane * WB;
+        f_id = k < f_take ? a.block_tables[static_cast<size_t>(f_s) * mbs + f_lb + k] : 0;
+        f_pos = 0;
+      }
+      const int blk = __shfl_sync(0xffffffffu, f_id, f_pos);
+      ++f_pos;
+      f_k += WB;
+      const bool bad = static_cast<unsigned>(blk) >= static_cast<unsigned>(a.num_blocks);
+      if (bad && lane == 0 && wr == 0 && a.status) atomicOr(a.status, kDevBadBlock);
+      // A bad block id reads zeros.
+      const size_t tile = static_cast<size_t>(bad ? 0 : blk) * Hkv + f_h;
+      const uint32_t bytes = bad ? 0 : 16;
+      const uint8_t* k_src = a.k_cache + tile * T::TILE;
+      const uint8_t* v_src = a.v_cache + tile * T::TILE;
+      const uint8_t* m_src = a.meta + tile * T::META;
+      const uint32_t dst = ring + slot * T::STAGE;
+      constexpr int KC = T::TILE / 16, MC = T::META / 16, ALL = 2 * KC + MC;
+#pragma unroll
+      for (int x = 0; x < (ALL + 32 * WR - 1) / (32 * WR); ++x) {
+        const int base = 32 * (wr + WR * x);   // 32 chunks of 16 bytes of one part
+        if (base < 2 * KC) {
+          const int c = (base < KC ? base : base - KC) + lane;
+          // Head size 128: tokens 2 and 3 (mod 4) have their halves exchanged, so that V words of
+          // four tokens lie in different banks.
+          const int at = D == 128 ? c ^ ((c >> 2) & 2) : c;
+          cp_async_16(dst + (base < KC ? 0 : T::TILE) + 16 * at, (base < KC ? k_src : v_src) + 16 * c, bytes);
+        } else if (base + lane < ALL) {
+          cp_async_16(dst + 16 * (base + lane), m_src + 16 * (base + lane - 2 * KC), bytes);
+        }
+      }
+    }
+    cp_async_commit();
+  };
+  auto stream_sync = [&]() {
+    if constexpr (WR == 1) __syncwarp();
+    else named_bar_sync(4 + wb, 32 * WR);
+  };
+#pragma unroll 1
+  for (int x = 0; x < STAGES - 1; ++x) fetch(x);
+
+  // Token of product slot i8 (and of i8 + 8: 8 more): slots 2 j, 2 j + 1 hold tokens j, (j ^ 1) + 4.
+  const int tok = (i8 & 1) ? ((i8 >> 1) ^ 1) + 4 : i8 >> 1;
+  const int tv0 = c4, tv1 = (c4 ^ 1) + 4;
+  const uint32_t k_off = D == 128 ? tok * 64 + ((c4 ^ (tok & 2)) << 4) : tok * 32 + c4 * 8;
+  auto v_off = [&](int t) -> uint32_t {
+    return T::TILE + (D == 128 ? t * 64 + (((i8 >> 1) ^ (t & 2)) << 4) + 8 * (i8 & 1) : t * 32 + 4 * i8);
+  };
+  const uint32_t v_off0 = v_off(tv0), v_off1 = v_off(tv1);
+  const uint32_t m_off = 2 * T::TILE + tok * 4 * G;
+
+  int slot = 0, kk = wb;   // ring slot and piece-relative index of the stream's next block
+  while (ub < b1) {
+    const int take = static_cast<int>(min(static_cast<long long>(nb), b1 - ub)) - lb;
+    const bool first = (lb == 0), last = (lb + take == nb);
+    const bool split = !(first && last);
+    const int u = s * Hkv + h;
+    const int cap = mbs * kBlockSize;
+    const int ctx_eff = ctx < cap ? ctx : cap;
+    // Query rows as in the other decode kernels: a count outside [1, q_per_seq], or rows past the
+    // end of q, is flagged and the sequence gets no rows.
+    int n_s = n, qb = s * n;
+    if (a.cu_q_lens) {
+      qb = a.cu_q_lens[s];
+      n_s = a.cu_q_lens[s + 1] - qb;
+    }
+    const bool rows_ok = n_s >= 1 && n_s <= n && qb >= 0 && qb <= a.q_rows - n_s;
+    const int Rs = rows_ok ? Gq * n_s : 0;
+    if (!rows_ok) {
+      n_s = 1;
+      qb = 0;
+    }
+    if (first && tid == 0 && (!rows_ok || ctx < n_s || ctx > cap) && a.status) atomicOr(a.status, kDevBadCtx);
+
+    // Query rows, one a warp: scaled to a largest element in [2^11, 2^12), the odd pairs of every
+    // word by 2^-4 more; their sums by group; the factor that undoes it all.
+    for (int r = warp; r < Rs; r += WR * WB) {
+      const int j = r / Gq, gi = r - j * Gq;
+      constexpr int E = D / 32;   // elements of a lane
+      const uint16_t* src = static_cast<const uint16_t*>(a.q) + (static_cast<size_t>(qb + j) * Hq + h * Gq + gi) * D + E * lane;
+      float x[E];
+#pragma unroll
+      for (int e = 0; e < E; e += 2) {
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(src + e);
+        if constexpr (BF16) {
+          x[e] = __uint_as_float(w << 16);
+          x[e + 1] = __uint_as_float(w & 0xFFFF0000u);
+        } else {
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+          x[e] = f.x;
+          x[e + 1] = f.y;
+        }
+      }
+      float mx = 0.f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) mx = fmaxf(mx, fabsf(x[e]));
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      // 2^ex <= mx < 2^(ex + 1); rows beyond 2^+-100 keep a scale at which the factors are finite.
+      const int ex = max(-100, min(100, static_cast<int>(__float_as_uint(mx) >> 23) - 127));
+      const float up = __uint_as_float(static_cast<uint32_t>(127 + 11 - ex) << 23);
+      float sum = 0.f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        x[e] *= up;
+        sum += x[e];
+      }
+#pragma unroll
+      for (int o = 16 / G; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+#pragma unroll
+      for (int e = 0; e < E; e += 2) {
+        const float f = ((E * lane + e) >> 1) & 1 ? 0.0625f : 1.f;
+        *reinterpret_cast<uint32_t*>(qs + r * QS + (E * lane + e) * 2) = pack_f16x2(x[e] * f, x[e + 1] * f);
+      }
+      if (lane % (32 / G) == 0) qsum_s[r * G + lane / (32 / G)] = sum * 0x1p-24f;
+      if (lane == 0) rf_s[r] = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + 13 + ex) << 23);
+    }
+    __syncthreads();
+
+    uint32_t qf[NT][2 * G][4];   // word 2 c4 + x / G of group x % G
+    float rf[NT][2], qz[NT][G][2];
+    unsigned long long vis[NT][2];
+    float m_run[NT][2], l_run[NT][2];
+    float o_acc[NT][G][4][4], o_bias[NT][G][4], o_z[NT][G][2];
+    const int cb = ctx_eff - n_s;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int x = 0; x < 2 * G; ++x) {
+        const uint4 v = *reinterpret_cast<const uint4*>(qs + (row_base + nt * 8 + i8) * QS +
+                                                        (kInt4Group * (x % G) + 8 * (2 * c4 + x / G)) * 2);
+        qf[nt][x][0] = v.x;
+        qf[nt][x][1] = v.y;
+        qf[nt][x][2] = v.z;
+        qf[nt][x][3] = v.w;
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = row_base + nt * 8 + 2 * c4 + e;
+        rf[nt][e] = rf_s[r];
+        m_run[nt][e] = kInt4Unset;
+        l_run[nt][e] = 0.f;
+        const int j = r / Gq;
+        vis[nt][e] = (a.tree_masks && r < Rs) ? a.tree_masks[qb + j] : ((j >= 63) ? ~0ull : ((2ull << j) - 1ull));
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          qz[nt][g][e] = qsum_s[r * G + g];
+          o_z[nt][g][e] = 0.f;
+        }
+      }
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          o_bias[nt][g][x] = 0.f;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o_acc[nt][g][x][e] = 0.f;
+        }
+      }
+    }
+
+#pragma unroll 1
+    for (; kk < take; kk += WB) {
+      cp_async_wait_groups<STAGES - 2>();
+      stream_sync();   // the block is there for all of the stream's warps, and the last one is read
+      fetch(slot == 0 ? STAGES - 1 : slot - 1);
+      const uint32_t st = ring + slot * T::STAGE;
+      slot = slot + 1 == STAGES ? 0 : slot + 1;
+      if (row_base >= Rs) continue;
+      const int tok0 = (lb + kk) * kBlockSize;
+
+      // ---- S^T (16 tokens x 8 NT rows), one accumulator a group ----
+      float sa[NT][G][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int g = 0; g < G; ++g) sa[nt][g][0] = sa[nt][g][1] = sa[nt][g][2] = sa[nt][g][3] = 0.f;
+      uint32_t ka[2 * G], kb[2 * G], mk[2][G], mv[2][G];
+      lds_words<2 * G>(st + k_off, ka);
+      lds_words<2 * G>(st + k_off + 8 * T::RB, kb);
+      lds_words<G>(st + m_off, mk[0]);
+      lds_words<G>(st + m_off + 32 * G, mk[1]);
+      lds_words<G>(st + m_off + 64 * G, mv[0]);
+      lds_words<G>(st + m_off + 96 * G, mv[1]);
+#pragma unroll
+      for (int x = 0; x < 2 * G; ++x) {
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          const uint32_t wa = ka[x] >> (8 * hf), wb2 = kb[x] >> (8 * hf);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            mma_f16(sa[nt][x % G], wa & 0x000F000Fu, wb2 & 0x000F000Fu, wa & 0x00F000F0u, wb2 & 0x00F000F0u,
+                    qf[nt][x][2 * hf], qf[nt][x][2 * hf + 1]);
+        }
+      }
+
+      // ---- scales; scores in base 2 ----
+      float sk[2][G], zk[2][G], sv[2][G], zv[2][G];
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          const float2 fk = __half22float2(*reinterpret_cast<const __half2*>(&mk[x][g]));
+          const float2 fv = __half22float2(*reinterpret_cast<const __half2*>(&mv[x][g]));
+          sk[x][g] = fk.x;
+          zk[x][g] = fk.y;
+          sv[x][g] = fv.x;
+          zv[x][g] = fmaf(8.f, fv.x, fv.y);
+        }
+      float sc[NT][4];   // [2 x + e]: token tok + 8 x, row 2 c4 + e
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float v = 0.f;
+#pragma unroll
+            for (int g = 0; g < G; ++g) v = fmaf(sa[nt][g][2 * x + e], sk[x][g], fmaf(zk[x][g], qz[nt][g][e], v));
+            sc[nt][2 * x + e] = v * rf[nt][e];
+          }
+      const bool masked = tok0 + (kBlockSize - 1) >= cb;
+      if (masked) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int p = tok0 + tok + 8 * x;
+          const int d = p - cb;
+          if (p >= ctx_eff) {   // behind the context: whatever lies there
+#pragma unroll
+            for (int g = 0; g < G; ++g) sv[x][g] = zv[x][g] = 0.f;
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const bool seen = d < 0 || (p < ctx_eff && d < 64 && ((vis[nt][e] >> d) & 1ull));
+              if (!seen) sc[nt][2 * x + e] = kNegInf;
+            }
+        }
+      }
+
+      // ---- weights p = 2^(score - m) and P = p s; the reference moved where one is too large ----
+      float p[NT][4], P[NT][G][4];
+      auto weights = [&]() {
+        float far = 0.f, top = 0.f;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            p[nt][v] = fast_exp2(sc[nt][v] - m_run[nt][v & 1]);
+            far = fmaxf(far, p[nt][v]);
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+              P[nt][g][v] = p[nt][v] * sv[v >> 1][g];
+              top = fmaxf(top, fabsf(P[nt][g][v]));
+            }
+          }
+        return top > kInt4Limit || far > kInt4FarP;
+      };
+      if (__any_sync(0xffffffffu, weights())) {
+        float ve[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          ve[x] = int4_scale_exponent(sv[x][0]);
+          if constexpr (G == 2) ve[x] = fmaxf(ve[x], int4_scale_exponent(sv[x][1]));
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float mx = fmaxf(sc[nt][e] + ve[0], sc[nt][2 + e] + ve[1]);
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+            const float m_new = fmaxf(m_run[nt][e], mx - kInt4Shift);
+            const float alpha = fast_exp2(m_run[nt][e] - m_new);
+            m_run[nt][e] = m_new;
+            l_run[nt][e] *= alpha;
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+              o_z[nt][g][e] *= alpha;
+              o_bias[nt][g][e] *= alpha;
+              o_bias[nt][g][2 + e] *= alpha;
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                o_acc[nt][g][x][e] *= alpha;
+                o_acc[nt][g][x][2 + e] *= alpha;
+              }
+            }
+          }
+        weights();
+      }
+      if (masked) {   // a weight of 0 beside a NaN scale is 0
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+              if (sc[nt][v] == kNegInf) P[nt][g][v] = 0.f;
+      }
+      uint32_t pb[NT][G][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) l_run[nt][e] += p[nt][e] + p[nt][2 + e];
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            const float z = masked && sc[nt][v] == kNegInf ? 0.f : zv[v >> 1][g];
+            o_z[nt][g][v & 1] = fmaf(p[nt][v], z, o_z[nt][g][v & 1]);
+          }
+          // The S^T layout (token, rows 2 c4, 2 c4 + 1) transposed: (row i8, slots 2 c4, 2 c4 + 1).
+          pb[nt][g][0] = movmatrix_t(pack_f16x2(P[nt][g][0], P[nt][g][1]));
+          pb[nt][g][1] = movmatrix_t(pack_f16x2(P[nt][g][2], P[nt][g][3]));
+        }
+      }
+
+      // ---- O^T (dimensions x rows) += V^T P^T ----
+      uint32_t w0[G], w1[G], w2[G], w3[G];
+      lds_words<G>(st + v_off0, w0);
+      lds_words<G>(st + v_off1, w1);
+      lds_words<G>(st + v_off0 + 8 * T::RB, w2);
+      lds_words<G>(st + v_off1 + 8 * T::RB, w3);
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        // Even and odd dimensions of the two tokens of a slot pair.
+        const uint32_t x01 = __byte_perm(w0[g], w1[g], 0x5410), y01 = __byte_perm(w0[g], w1[g], 0x7632);
+        const uint32_t x23 = __byte_perm(w2[g], w3[g], 0x5410), y23 = __byte_perm(w2[g], w3[g], 0x7632);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const uint32_t keep = x & 1 ? 0x00F000F0u : 0x000F000Fu;
+          const int sh = 8 * (x >> 1);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            mma_f16(o_acc[nt][g][x], (x01 >> sh) & keep, (y01 >> sh) & keep, (x23 >> sh) & keep, (y23 >> sh) & keep,
+                    pb[nt][g][0], pb[nt][g][1]);
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)   // 8 in every element
+          mma_f16(o_bias[nt][g], 0x00080008u, 0x00080008u, 0x00080008u, 0x00080008u, pb[nt][g][0], pb[nt][g][1]);
+      }
+    }
+    kk -= take;
+
+    // ---- merge the streams of this piece ----
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = row_base + nt * 8 + 2 * c4 + e;
+        float lsum = l_run[nt][e];
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) lsum += __shfl_xor_sync(0xffffffffu, lsum, o);
+        if (i8 == 0 && r < R) {
+          mrg_m[wb * R + r] = m_run[nt][e];
+          mrg_l[wb * R + r] = lsum;
+        }
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          float z = o_z[nt][g][e];
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+          float y[8];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const float f = x & 1 ? 0.0625f : 1.f;
+            y[2 * x] = fmaf(fmaf(o_acc[nt][g][x][e], f, -o_bias[nt][g][e]), 0x1p24f, z);
+            y[2 * x + 1] = fmaf(fmaf(o_acc[nt][g][x][2 + e], f, -o_bias[nt][g][e]), 0x1p24f, z);
+          }
+          if (r < R) {
+            float4* mo = reinterpret_cast<float4*>(mrg_o + static_cast<size_t>(wb * R + r) * (D + 4) + kInt4Group * g + 8 * i8);
+            mo[0] = make_float4(y[0], y[1], y[2], y[3]);
+            mo[1] = make_float4(y[4], y[5], y[6], y[7]);
+          }
+        }
+      }
+    __syncthreads();
+    for (int idx = tid; idx < Rs * (D / 4); idx += NTHR) {
+      const int r = idx / (D / 4), d4 = idx % (D / 4);
+      float M = kNegInf;
+#pragma unroll
+      for (int w = 0; w < WB; ++w) M = fmaxf(M, mrg_m[w * R + r]);
+      float lsum = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < WB; ++w) {
+        const float f = fast_exp2(mrg_m[w * R + r] - M);
+        lsum += f * mrg_l[w * R + r];
+        const float4 v = *reinterpret_cast<const float4*>(mrg_o + static_cast<size_t>(w * R + r) * (D + 4) + d4 * 4);
+        acc.x += f * v.x;
+        acc.y += f * v.y;
+        acc.z += f * v.z;
+        acc.w += f * v.w;
+      }
+      if (!split) {
+        const float inv = lsum > 0.f ? 1.f / lsum : 0.f;
+        const int j = r / Gq, gi = r - j * Gq;
+        const size_t dst = (static_cast<size_t>(qb + j) * Hq + h * Gq + gi) * D + d4 * 4;
+        uint2 pk;
+        pk.x = pack_p<BF16 ? kKvBf16 : kKvF16>(acc.x * inv, acc.y * inv);
+        pk.y = pack_p<BF16 ? kKvBf16 : kKvF16>(acc.z * inv, acc.w * inv);
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + dst) = pk;
+      } else {
+        // (in place of stream 0's: only this thread reads or writes these four values)
+        *reinterpret_cast<float4*>(mrg_o + static_cast<size_t>(r) * (D + 4) + d4 * 4) = acc;
+        if (d4 == 0) {
+          fin_ml[r] = M;
+          fin_ml[R + r] = lsum;
+        }
+      }
+    }
+    if (split) {
+      finish_split_piece_smem<BF16 ? kKvBf16 : kKvF16, D>(a, u, ub, nb, total, ncta, Rs, qb, h, tid, NTHR, 3, fin,
+                                                          fin_cur, mrg_o, D + 4, fin_ml);
+    }
+
+    // ---- the next unit (a piece that stops before the unit's end ended the share) ----
+    if (lb + take < nb) break;
+    ub += nb + pc0;
+    lb = 0;
+    if (++h == Hkv) {
+      h = 0;
+      ++s;
+      if (ub < b1) {
+        ctx = a.context_lens[s];
+        nb = unit_blocks(ctx, mbs);
+      }
+    }
+  }
+  cp_async_wait_all();
+}
+
+template <int D, class Sh, bool BF16>
+DecodeInt4Kernel int4_kernel(int rows) {
+  return {reinterpret_cast<const void*>(&decode_int4_kernel<D, Sh, BF16>), Sh::THREADS,
+          static_cast<size_t>(int4_smem<D, Sh>(rows).total)};
+}
+template <bool BF16, class Sh>
+DecodeInt4Kernel int4_kernel(int d, int rows) {
+  return d == 128 ? int4_kernel<128, Sh, BF16>(rows) : int4_kernel<64, Sh, BF16>(rows);
+}
+template <bool BF16>
+DecodeInt4Kernel int4_kernel_for(int d, int rows) {
+  if (rows <= 8) return int4_kernel<BF16, Int4Rows8>(d, rows);
+  if (rows <= 16) return int4_kernel<BF16, Int4Rows16>(d, rows);
+  if (rows <= 32) return int4_kernel<BF16, Int4Rows32>(d, rows);
+  return int4_kernel<BF16, Int4Rows64>(d, rows);
+}
+
+}  // namespace pkv

@@ -14,7 +14,7 @@ namespace pkv {
 constexpr int kBlockSize = 16;       // tokens per KV block
 constexpr int kMaxRows = 64;         // GQA group size x query tokens handled per CTA
 constexpr int kMaxCtasPerSm = 8;     // upper bound on resident decode CTAs per SM
-constexpr int kKvF16 = 0, kKvBf16 = 1, kKvE5m2 = 2, kKvInt8 = 3;
+constexpr int kKvF16 = 0, kKvBf16 = 1, kKvE5m2 = 2, kKvInt8 = 3, kKvInt4 = 4;
 
 // Device-status bits (mirror the public PKV_DEV_* values).
 constexpr int32_t kDevBadSlot = 0x1;
@@ -71,7 +71,9 @@ struct DecodeGeometry {
 
 // Sizes derived from (kv dtype, head size).
 __host__ __device__ constexpr int kv_elem_bytes(int kv) { return (kv == kKvE5m2 || kv == kKvInt8) ? 1 : 2; }
-__host__ __device__ constexpr int tile_row_bytes(int kv, int d) { return d * kv_elem_bytes(kv); }
+__host__ __device__ constexpr int tile_row_bytes(int kv, int d) { return kv == kKvInt4 ? d / 2 : d * kv_elem_bytes(kv); }
+// 32-bit words of scales of one row (0: none): INT8 a float, INT4 an fp16 pair for every 64 dimensions.
+__host__ __device__ constexpr int row_scale_words(int kv, int d) { return kv == kKvInt8 ? 1 : (kv == kKvInt4 ? d / 64 : 0); }
 __host__ __device__ constexpr int tile_bytes(int kv, int d) { return kBlockSize * tile_row_bytes(kv, d); }
 
 // Floats in one split-KV partial slot: m[rows], l[rows] (padded to 4), o[rows][D].
@@ -148,6 +150,8 @@ const void* decode_kernel_ptr_e5m2(int d, int ntw);
 const void* decode_kernel_ptr_int8(int d, int ntw);
 // The 96-thread kernel for units of at most 8 rows over a bf16 cache (nullptr if none).
 const void* decode_kernel_narrow_ptr_bf16(int d);
+// CTAs of the INT4 decode kernel an SM holds, for units of `rows` rows; a pkv_status.
+int decode_int4_ctas(int d, int rows, int* ctas);
 const void* kv_cache_write_kernel_ptr();
 const void* kv_cache_write_int8_kernel_ptr();
 
