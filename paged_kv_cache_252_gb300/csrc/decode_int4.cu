@@ -25,7 +25,7 @@ int shape_index(int rows) { return rows <= 8 ? 0 : rows <= 16 ? 1 : rows <= 32 ?
 
 // Fixed cost of a unit's piece on the work line, in blocks.
 #ifndef PKV_PIECE_COST_INT4
-#define PKV_PIECE_COST_INT4 16
+#define PKV_PIECE_COST_INT4 24
 #endif
 
 // Once per device, head size and shape: shared-memory limits of both query types' kernels and the CTAs an

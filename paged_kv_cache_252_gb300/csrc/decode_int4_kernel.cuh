@@ -34,6 +34,8 @@
 #include <cuda_runtime.h>
 #include <math.h>
 
+#include <type_traits>
+
 #include "decode_common.cuh"
 #include "decode_int4.h"
 #include "pkv_int4.cuh"
@@ -51,28 +53,48 @@ struct Int4Tile {
   static constexpr int STAGE = 2 * TILE + META;
 };
 
-// Warps and ring of the kernel for a row count. Eight rows a CTA: twelve warps an SM in three
-// CTAs; wider units two CTAs.
-template <int NT_, int WR_, int WB_, int STAGES_, int CTAS_>
+// Warps, ring (in steps), CTAs an SM and blocks a step of the kernel for a row count.
+template <int NT_, int WR_, int WB_, int RING_, int CTAS_, int STEP_>
 struct Int4Shape {
-  static constexpr int NT = NT_, WR = WR_, WB = WB_, STAGES = STAGES_, CTAS = CTAS_;
+  static constexpr int NT = NT_, WR = WR_, WB = WB_, RING = RING_, CTAS = CTAS_, STEP = STEP_;
+  static_assert(RING >= 2 && (STEP == 1 || STEP == 2), "ring");
   static constexpr int ROWS = 8 * NT * WR, THREADS = 32 * WR * WB;
 };
-using Int4Rows8 = Int4Shape<1, 1, 4, 6, 3>;
-using Int4Rows16 = Int4Shape<2, 1, 4, 7, 2>;
-using Int4Rows32 = Int4Shape<2, 2, 2, 10, 2>;
-using Int4Rows64 = Int4Shape<2, 4, 1, 12, 2>;
+#ifndef PKV_I4_R8
+#define PKV_I4_R8 1, 1, 4, 3, 3, 2
+#endif
+#ifndef PKV_I4_R16
+#define PKV_I4_R16 2, 1, 4, 4, 2, 2
+#endif
+#ifndef PKV_I4_R32
+#define PKV_I4_R32 2, 2, 2, 5, 2, 2
+#endif
+#ifndef PKV_I4_R64
+#define PKV_I4_R64 2, 4, 1, 5, 2, 2
+#endif
+using Int4Rows8 = Int4Shape<PKV_I4_R8>;
+using Int4Rows16 = Int4Shape<PKV_I4_R16>;
+using Int4Rows32 = Int4Shape<PKV_I4_R32>;
+using Int4Rows64 = Int4Shape<PKV_I4_R64>;
+
+// The walk of a stream's fetching, kept in shared memory: read once for up to 32 blocks.
+struct Int4Walk {
+  long long ub;
+  int s, h, nb, lb, take, k;
+};
 
 struct Int4Smem {
-  int qs, rf, qsum, mrg_o, mrg_ml, fin_ml, misc, total;
+  int qs, rf, qsum, vis, walk, mrg_o, mrg_ml, fin_ml, misc, total;
 };
 template <int D, class Sh>
 __host__ __device__ constexpr Int4Smem int4_smem(int rows) {
   Int4Smem s{};
-  s.qs = Sh::WB * Sh::STAGES * Int4Tile<D>::STAGE;
+  s.qs = Sh::WB * Sh::RING * Sh::STEP * Int4Tile<D>::STAGE;
   s.rf = s.qs + Sh::ROWS * (D * 2 + 16);
   s.qsum = s.rf + Sh::ROWS * 4;
-  s.mrg_o = s.qsum + Sh::ROWS * Int4Tile<D>::G * 4;
+  s.vis = s.qsum + Sh::ROWS * Int4Tile<D>::G * 4;
+  s.walk = s.vis + Sh::ROWS * 8;
+  s.mrg_o = s.walk + Sh::WR * Sh::WB * static_cast<int>(sizeof(Int4Walk));
   s.mrg_ml = s.mrg_o + Sh::WB * rows * (D + 4) * 4;
   s.fin_ml = s.mrg_ml + (Sh::WB * rows * 8 + 15) / 16 * 16;
   s.misc = s.fin_ml + (rows * 8 + 15) / 16 * 16;
@@ -85,6 +107,13 @@ __device__ __forceinline__ void cp_async_wait_groups() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+__device__ __forceinline__ void cp_async_16_full(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)) : "memory");
+}
+__device__ __forceinline__ void sts_zero_16(uint32_t dst) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(dst), "r"(0) : "memory");
+}
 
 __device__ __forceinline__ uint4 lds_v4(uint32_t addr) {
   uint4 v;
@@ -110,17 +139,37 @@ __device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&w)[N]) {
 constexpr float kInt4Unset = -1e37f;
 constexpr float kInt4Shift = 11.f;     // P of the reference's own token: below 2^11
 constexpr float kInt4Limit = 32768.f;  // P that moves the reference
-constexpr float kInt4FarP = 1.0995116e12f;   // 2^40: a p that moves it (its scale may be 0)
+constexpr float kInt4FarP = 1.0995116e12f;   // 2^40: a sum of two p that moves it (their scales may be 0)
 
-// e with |s| < 2^e, at least -25 (a scale of 0).
+// e with |s| < 2^e, at least -25 (a scale of 0); a NaN scale counts as 0, or it would push the row's other group out of range.
 __device__ __forceinline__ float int4_scale_exponent(float s) {
-  return fmaxf(static_cast<float>(static_cast<int>(__float_as_uint(fabsf(s)) >> 23) - 126), -25.f);
+  return s == s ? fmaxf(static_cast<float>(static_cast<int>(__float_as_uint(fabsf(s)) >> 23) - 126), -25.f) : -25.f;
+}
+
+// As mma_f16 and movmatrix_t, for the compiler to move between others.
+__device__ __forceinline__ void mma_acc(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_new(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ uint32_t transposed(uint32_t a) {
+  uint32_t d;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
 }
 
 template <int D, class Sh, bool BF16>
 __global__ void __launch_bounds__(Sh::THREADS, Sh::CTAS) decode_int4_kernel(const __grid_constant__ DecodeInt4Args a) {
   using T = Int4Tile<D>;
-  constexpr int G = T::G, NT = Sh::NT, WR = Sh::WR, WB = Sh::WB, STAGES = Sh::STAGES, NTHR = Sh::THREADS;
+  constexpr int G = T::G, NT = Sh::NT, WR = Sh::WR, WB = Sh::WB, RING = Sh::RING, STEP = Sh::STEP, UNIT = STEP * T::STAGE,
+                NTHR = Sh::THREADS;
   constexpr int QS = D * 2 + 16;
   constexpr float kNegInf = -INFINITY;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -129,6 +178,7 @@ __global__ void __launch_bounds__(Sh::THREADS, Sh::CTAS) decode_int4_kernel(cons
   uint8_t* qs = smem + lay.qs;
   float* rf_s = reinterpret_cast<float*>(smem + lay.rf);
   float* qsum_s = reinterpret_cast<float*>(smem + lay.qsum);
+  unsigned long long* vis_s = reinterpret_cast<unsigned long long*>(smem + lay.vis);
   float* mrg_o = reinterpret_cast<float*>(smem + lay.mrg_o);
   float* mrg_m = reinterpret_cast<float*>(smem + lay.mrg_ml);
   float* mrg_l = mrg_m + WB * R;
@@ -174,70 +224,92 @@ __global__ void __launch_bounds__(Sh::THREADS, Sh::CTAS) decode_int4_kernel(cons
     ub = b0 - o + pc0;
   }
 
-  // ---- the stream's fetching: the same walk, up to STAGES - 1 of its blocks ahead ----
-  const uint32_t ring = smem_addr(smem) + wb * (STAGES * T::STAGE);
-  int f_s = s, f_h = h, f_lb = lb, f_nb = nb;
-  long long f_ub = ub;
-  int f_take = static_cast<int>(min(static_cast<long long>(nb), b1 - ub)) - lb;
-  int f_k = wb;              // the stream's next block in the piece
-  int f_id = 0, f_pos = 32;  // 32 of the stream's block ids, one a lane; the next one's lane
+  // ---- the stream's fetching: the same walk, up to RING - 1 of its steps ahead ----
+  const uint32_t ring = smem_addr(smem) + wb * (RING * UNIT), ring_end = ring + RING * UNIT;
+  Int4Walk* walk = reinterpret_cast<Int4Walk*>(smem + lay.walk) + warp;
+  if (lane == 0) *walk = {ub, s, h, nb, lb, static_cast<int>(min(static_cast<long long>(nb), b1 - ub)) - lb, wb};
+  __syncwarp();
+  int f_id = 0, f_pos = 0, f_left = 0, f_h = 0;   // the stream's next block ids, one a lane; the next one's lane; how many
   bool f_more = true;
-  auto fetch = [&](int slot) {
-    if (f_more) {
-      while (f_k >= f_take) {
-        f_k -= f_take;
-        f_pos = 32;
-        if (f_lb + f_take < f_nb) {
-          f_more = false;
-          break;
-        }
-        f_ub += f_nb + pc0;
-        f_lb = 0;
-        if (f_ub >= b1) {
-          f_more = false;
-          break;
-        }
-        if (++f_h == Hkv) {
-          f_h = 0;
-          ++f_s;
-          f_nb = unit_blocks(a.context_lens[f_s], mbs);
-        }
-        f_take = static_cast<int>(min(static_cast<long long>(f_nb), b1 - f_ub));
+  // The next up to 32 blocks of the stream in the piece at hand, or in the next one that has any.
+  auto next_ids = [&]() {
+    long long w_ub = walk->ub;
+    int w_s = walk->s, w_h = walk->h, w_nb = walk->nb, w_lb = walk->lb, w_take = walk->take, w_k = walk->k;
+    int steps = (w_take + STEP - 1) / STEP;
+    while (w_k >= steps) {
+      w_k -= steps;
+      if (w_lb + w_take < w_nb || w_ub + w_nb + pc0 >= b1) {   // the share ends in this piece
+        f_more = false;
+        return;
       }
+      w_ub += w_nb + pc0;
+      w_lb = 0;
+      if (++w_h == Hkv) {
+        w_h = 0;
+        ++w_s;
+        w_nb = unit_blocks(a.context_lens[w_s], mbs);
+      }
+      w_take = static_cast<int>(min(static_cast<long long>(w_nb), b1 - w_ub));
+      steps = (w_take + STEP - 1) / STEP;
     }
-    if (f_more) {
-      if (f_pos == 32) {
-        const int k = f_k + lane * WB;
-        f_id = k < f_take ? a.block_tables[static_cast<size_t>(f_s) * mbs + f_lb + k] : 0;
-        f_pos = 0;
-      }
-      const int blk = __shfl_sync(0xffffffffu, f_id, f_pos);
-      ++f_pos;
-      f_k += WB;
-      const bool bad = static_cast<unsigned>(blk) >= static_cast<unsigned>(a.num_blocks);
-      if (bad && lane == 0 && wr == 0 && a.status) atomicOr(a.status, kDevBadBlock);
-      // A bad block id reads zeros.
-      const size_t tile = static_cast<size_t>(bad ? 0 : blk) * Hkv + f_h;
-      const uint32_t bytes = bad ? 0 : 16;
-      const uint8_t* k_src = a.k_cache + tile * T::TILE;
-      const uint8_t* v_src = a.v_cache + tile * T::TILE;
-      const uint8_t* m_src = a.meta + tile * T::META;
-      const uint32_t dst = ring + slot * T::STAGE;
-      constexpr int KC = T::TILE / 16, MC = T::META / 16, ALL = 2 * KC + MC;
+    const int mine = min(32 / STEP, (steps - w_k + WB - 1) / WB);
+    const int at = (w_k + lane / STEP * WB) * STEP + lane % STEP;
+    const bool there = lane / STEP < mine && at < w_take;
+    f_left = __popc(__ballot_sync(0xffffffffu, there));
+    f_pos = 0;
+    f_h = w_h;
+    f_id = there ? a.block_tables[static_cast<size_t>(w_s) * mbs + w_lb + at] : 0;
+    __syncwarp();
+    if (lane == 0) *walk = {w_ub, w_s, w_h, w_nb, w_lb, w_take, w_k + mine * WB};
+    __syncwarp();
+  };
+  constexpr int KC = T::TILE / 16, MC = T::META / 16, ALL = 2 * KC + MC;
+  // This thread's 16-byte chunk of every 32 WR. Head size 128: tokens 2 and 3 (mod 4) have their halves
+  // exchanged, so that V words of four tokens lie in different banks.
+  const int chunk = 32 * wr + lane;
+  const uint32_t chunk_at = 16u * (D == 128 ? chunk ^ ((chunk >> 2) & 2) : chunk);
+  const uint8_t* const k_base = a.k_cache + 16 * chunk;
+  const uint8_t* const v_base = a.v_cache + 16 * chunk;
+  const uint8_t* const m_base = a.meta + 16 * chunk;
+  auto fetch_block = [&](uint32_t dst, int blk) {
+    const uint32_t tile = static_cast<uint32_t>(blk) * Hkv + f_h;   // (the host keeps rows below 2^31)
+    const uint8_t* k_src = k_base + static_cast<size_t>(tile) * T::TILE;
+    const uint8_t* v_src = v_base + static_cast<size_t>(tile) * T::TILE;
+    const uint8_t* m_src = m_base + static_cast<size_t>(tile) * T::META;
 #pragma unroll
-      for (int x = 0; x < (ALL + 32 * WR - 1) / (32 * WR); ++x) {
-        const int base = 32 * (wr + WR * x);   // 32 chunks of 16 bytes of one part
-        if (base < 2 * KC) {
-          const int c = (base < KC ? base : base - KC) + lane;
-          // Head size 128: tokens 2 and 3 (mod 4) have their halves exchanged, so that V words of
-          // four tokens lie in different banks.
-          const int at = D == 128 ? c ^ ((c >> 2) & 2) : c;
-          cp_async_16(dst + (base < KC ? 0 : T::TILE) + 16 * at, (base < KC ? k_src : v_src) + 16 * c, bytes);
-        } else if (base + lane < ALL) {
-          cp_async_16(dst + 16 * (base + lane), m_src + 16 * (base + lane - 2 * KC), bytes);
+    for (int x = 0; x < (ALL + 32 * WR - 1) / (32 * WR); ++x) {
+      const int base = 32 * WR * x;   // a part's chunks come in multiples of 32
+      if (base + (WR == 1 ? 0 : 32 * wr) < KC) {
+        cp_async_16_full(dst + 16 * base + chunk_at, k_src + 16 * base);
+      } else if (base + (WR == 1 ? 0 : 32 * wr) < 2 * KC) {
+        cp_async_16_full(dst + 16 * base + chunk_at, v_src + 16 * (base - KC));
+      } else if (base + chunk < ALL) {
+        cp_async_16_full(dst + 16 * (base + chunk), m_src + 16 * (base - 2 * KC));
+      }
+    }
+  };
+  auto block_ok = [&](int blk) { return static_cast<unsigned>(blk) < static_cast<unsigned>(a.num_blocks); };
+  // The next step's blocks (one, where no second is left in the piece) to dst; nothing behind the share's end.
+  auto fetch = [&](uint32_t dst) {
+    if (f_left == 0 && f_more) next_ids();
+    const int blk0 = __shfl_sync(0xffffffffu, f_id, f_pos), blk1 = STEP == 2 ? __shfl_sync(0xffffffffu, f_id, f_pos + 1) : blk0;
+    if (f_left >= STEP && block_ok(blk0) && block_ok(blk1)) {
+      fetch_block(dst, blk0);
+      if constexpr (STEP == 2) fetch_block(dst + T::STAGE, blk1);
+      f_left -= STEP;
+    } else if (f_left > 0) {
+#pragma unroll 1
+      for (int y = 0; y < STEP && f_left > 0; ++y, --f_left) {
+        const int blk = y ? blk1 : blk0;
+        if (block_ok(blk)) {
+          fetch_block(dst + y * T::STAGE, blk);
+        } else {   // a bad block id reads zeros
+          if (lane == 0 && wr == 0 && a.status) atomicOr(a.status, kDevBadBlock);
+          for (int x = chunk; x < ALL; x += 32 * WR) sts_zero_16(dst + y * T::STAGE + 16 * x);
         }
       }
     }
+    f_pos += STEP;
     cp_async_commit();
   };
   auto stream_sync = [&]() {
@@ -245,7 +317,7 @@ __global__ void __launch_bounds__(Sh::THREADS, Sh::CTAS) decode_int4_kernel(cons
     else named_bar_sync(4 + wb, 32 * WR);
   };
 #pragma unroll 1
-  for (int x = 0; x < STAGES - 1; ++x) fetch(x);
+  for (int x = 0; x < RING - 1; ++x) fetch(ring + x * UNIT);
 
   // Token of product slot i8 (and of i8 + 8: 8 more): slots 2 j, 2 j + 1 hold tokens j, (j ^ 1) + 4.
   const int tok = (i8 & 1) ? ((i8 >> 1) ^ 1) + 4 : i8 >> 1;
@@ -257,7 +329,9 @@ __global__ void __launch_bounds__(Sh::THREADS, Sh::CTAS) decode_int4_kernel(cons
   const uint32_t v_off0 = v_off(tv0), v_off1 = v_off(tv1);
   const uint32_t m_off = 2 * T::TILE + tok * 4 * G;
 
-  int slot = 0, kk = wb;   // ring slot and piece-relative index of the stream's next block
+  // The stream's next step: where its blocks lie and where the last one's lay; its index in the piece.
+  uint32_t st = ring, st_last = ring_end - UNIT;
+  int kk = wb;
   while (ub < b1) {
     const int take = static_cast<int>(min(static_cast<long long>(nb), b1 - ub)) - lb;
     const bool first = (lb == 0), last = (lb + take == nb);
@@ -323,11 +397,14 @@ __global__ void __launch_bounds__(Sh::THREADS, Sh::CTAS) decode_int4_kernel(cons
       if (lane % (32 / G) == 0) qsum_s[r * G + lane / (32 / G)] = sum * 0x1p-24f;
       if (lane == 0) rf_s[r] = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + 13 + ex) << 23);
     }
+    for (int r = tid; r < Sh::ROWS; r += NTHR) {   // the drafts that a row sees
+      const int j = r / Gq;
+      vis_s[r] = (a.tree_masks && r < Rs) ? a.tree_masks[qb + j] : ((j >= 63) ? ~0ull : ((2ull << j) - 1ull));
+    }
     __syncthreads();
 
     uint32_t qf[NT][2 * G][4];   // word 2 c4 + x / G of group x % G
     float rf[NT][2], qz[NT][G][2];
-    unsigned long long vis[NT][2];
     float m_run[NT][2], l_run[NT][2];
     float o_acc[NT][G][4][4], o_bias[NT][G][4], o_z[NT][G][2];
     const int cb = ctx_eff - n_s;
@@ -348,8 +425,6 @@ __global__ void __launch_bounds__(Sh::THREADS, Sh::CTAS) decode_int4_kernel(cons
         rf[nt][e] = rf_s[r];
         m_run[nt][e] = kInt4Unset;
         l_run[nt][e] = 0.f;
-        const int j = r / Gq;
-        vis[nt][e] = (a.tree_masks && r < Rs) ? a.tree_masks[qb + j] : ((j >= 63) ? ~0ull : ((2ull << j) - 1ull));
 #pragma unroll
         for (int g = 0; g < G; ++g) {
           qz[nt][g][e] = qsum_s[r * G + g];
@@ -367,116 +442,133 @@ __global__ void __launch_bounds__(Sh::THREADS, Sh::CTAS) decode_int4_kernel(cons
       }
     }
 
-#pragma unroll 1
-    for (; kk < take; kk += WB) {
-      cp_async_wait_groups<STAGES - 2>();
-      stream_sync();   // the block is there for all of the stream's warps, and the last one is read
-      fetch(slot == 0 ? STAGES - 1 : slot - 1);
-      const uint32_t st = ring + slot * T::STAGE;
-      slot = slot + 1 == STAGES ? 0 : slot + 1;
-      if (row_base >= Rs) continue;
-      const int tok0 = (lb + kk) * kBlockSize;
-
-      // ---- S^T (16 tokens x 8 NT rows), one accumulator a group ----
-      float sa[NT][G][4];
+    // STEP blocks, at st; the first one's first token's position is tok0. Masked: any of their
+    // tokens may be hidden, and the second block may be absent.
+    auto step = [&](auto masked, const int tok0, const bool absent) {
+      constexpr int NB = STEP;
+      constexpr bool kMasked = decltype(masked)::value;
+      const uint32_t at[2] = {st, st + T::STAGE};
+      // ---- S^T (16 tokens x 8 NT rows a block), one accumulator a group ----
+      float sa[NB][NT][G][4];
+      uint32_t mk[NB][2][G], mv[NB][2][G];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int b = 0; b < NB; ++b) {
+        uint32_t ka[2 * G], kb[2 * G];
+        lds_words<2 * G>(at[b] + k_off, ka);
+        lds_words<2 * G>(at[b] + k_off + 8 * T::RB, kb);
+        lds_words<G>(at[b] + m_off, mk[b][0]);
+        lds_words<G>(at[b] + m_off + 32 * G, mk[b][1]);
+        lds_words<G>(at[b] + m_off + 64 * G, mv[b][0]);
+        lds_words<G>(at[b] + m_off + 96 * G, mv[b][1]);
 #pragma unroll
-        for (int g = 0; g < G; ++g) sa[nt][g][0] = sa[nt][g][1] = sa[nt][g][2] = sa[nt][g][3] = 0.f;
-      uint32_t ka[2 * G], kb[2 * G], mk[2][G], mv[2][G];
-      lds_words<2 * G>(st + k_off, ka);
-      lds_words<2 * G>(st + k_off + 8 * T::RB, kb);
-      lds_words<G>(st + m_off, mk[0]);
-      lds_words<G>(st + m_off + 32 * G, mk[1]);
-      lds_words<G>(st + m_off + 64 * G, mv[0]);
-      lds_words<G>(st + m_off + 96 * G, mv[1]);
+        for (int x = 0; x < 2 * G; ++x) {
 #pragma unroll
-      for (int x = 0; x < 2 * G; ++x) {
+          for (int hf = 0; hf < 2; ++hf) {
+            const uint32_t wa = ka[x] >> (8 * hf), wb2 = kb[x] >> (8 * hf);
+            const uint32_t a0 = wa & 0x000F000Fu, a1 = wb2 & 0x000F000Fu, a2 = wa & 0x00F000F0u, a3 = wb2 & 0x00F000F0u;
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          const uint32_t wa = ka[x] >> (8 * hf), wb2 = kb[x] >> (8 * hf);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            mma_f16(sa[nt][x % G], wa & 0x000F000Fu, wb2 & 0x000F000Fu, wa & 0x00F000F0u, wb2 & 0x00F000F0u,
-                    qf[nt][x][2 * hf], qf[nt][x][2 * hf + 1]);
+            for (int nt = 0; nt < NT; ++nt) {
+              if (x < G && hf == 0) mma_new(sa[b][nt][x % G], a0, a1, a2, a3, qf[nt][x][2 * hf], qf[nt][x][2 * hf + 1]);
+              else mma_acc(sa[b][nt][x % G], a0, a1, a2, a3, qf[nt][x][2 * hf], qf[nt][x][2 * hf + 1]);
+            }
+          }
         }
       }
+      // (the V words, ahead of the scores' arithmetic)
+      uint32_t w[NB][4][G];
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        lds_words<G>(at[b] + v_off0, w[b][0]);
+        lds_words<G>(at[b] + v_off1, w[b][1]);
+        lds_words<G>(at[b] + v_off0 + 8 * T::RB, w[b][2]);
+        lds_words<G>(at[b] + v_off1 + 8 * T::RB, w[b][3]);
+      }
 
-      // ---- scales; scores in base 2 ----
-      float sk[2][G], zk[2][G], sv[2][G], zv[2][G];
+      // ---- scales; scores before the row's factor ----
+      float sv[NB][2][G], zv[NB][2][G];
+      float sc[NB][NT][4];   // [2 x + e]: token tok + 8 x, row 2 c4 + e
+      bool hid[NB][NT][4];   // (all false without a mask)
 #pragma unroll
-      for (int x = 0; x < 2; ++x)
-#pragma unroll
-        for (int g = 0; g < G; ++g) {
-          const float2 fk = __half22float2(*reinterpret_cast<const __half2*>(&mk[x][g]));
-          const float2 fv = __half22float2(*reinterpret_cast<const __half2*>(&mv[x][g]));
-          sk[x][g] = fk.x;
-          zk[x][g] = fk.y;
-          sv[x][g] = fv.x;
-          zv[x][g] = fmaf(8.f, fv.x, fv.y);
-        }
-      float sc[NT][4];   // [2 x + e]: token tok + 8 x, row 2 c4 + e
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float v = 0.f;
-#pragma unroll
-            for (int g = 0; g < G; ++g) v = fmaf(sa[nt][g][2 * x + e], sk[x][g], fmaf(zk[x][g], qz[nt][g][e], v));
-            sc[nt][2 * x + e] = v * rf[nt][e];
-          }
-      const bool masked = tok0 + (kBlockSize - 1) >= cb;
-      if (masked) {
+      for (int b = 0; b < NB; ++b)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          const int p = tok0 + tok + 8 * x;
-          const int d = p - cb;
-          if (p >= ctx_eff) {   // behind the context: whatever lies there
+          float sk[G], zk[G];
 #pragma unroll
-            for (int g = 0; g < G; ++g) sv[x][g] = zv[x][g] = 0.f;
+          for (int g = 0; g < G; ++g) {
+            const float2 fk = __half22float2(*reinterpret_cast<const __half2*>(&mk[b][x][g]));
+            const float2 fv = __half22float2(*reinterpret_cast<const __half2*>(&mv[b][x][g]));
+            sk[g] = fk.x;
+            zk[g] = fk.y;
+            sv[b][x][g] = fv.x;
+            zv[b][x][g] = fmaf(8.f, fv.x, fv.y);
+          }
+          const int d = tok0 + 16 * b + tok + 8 * x - cb;   // (ctx_eff is cb + n_s)
+          const bool there = !kMasked || (d < n_s && !(b == 1 && absent));
+          if (!there) {   // behind the context: whatever lies there
+#pragma unroll
+            for (int g = 0; g < G; ++g) sv[b][x][g] = zv[b][x][g] = 0.f;
           }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const bool seen = d < 0 || (p < ctx_eff && d < 64 && ((vis[nt][e] >> d) & 1ull));
-              if (!seen) sc[nt][2 * x + e] = kNegInf;
+              float v = zk[0] * qz[nt][0][e];
+              if constexpr (G == 2) v = fmaf(zk[1], qz[nt][1][e], v);
+#pragma unroll
+              for (int g = 0; g < G; ++g) v = fmaf(sa[b][nt][g][2 * x + e], sk[g], v);
+              sc[b][nt][2 * x + e] = v;
+              hid[b][nt][2 * x + e] = kMasked && !(there && (d < 0 || (d < 64 && ((vis_s[row_base + nt * 8 + 2 * c4 + e] >> d) & 1ull))));
             }
         }
-      }
 
       // ---- weights p = 2^(score - m) and P = p s; the reference moved where one is too large ----
-      float p[NT][4], P[NT][G][4];
+      float p[NB][NT][4];
+      uint32_t ph[NB][NT][G][2];   // P of a token's two rows
       auto weights = [&]() {
-        float far = 0.f, top = 0.f;
+        float far = 0.f;
+        __half2 top = __half2half2(__ushort_as_half(0));
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int b = 0; b < NB; ++b)
 #pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            p[nt][v] = fast_exp2(sc[nt][v] - m_run[nt][v & 1]);
-            far = fmaxf(far, p[nt][v]);
+          for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-            for (int g = 0; g < G; ++g) {
-              P[nt][g][v] = p[nt][v] * sv[v >> 1][g];
-              top = fmaxf(top, fabsf(P[nt][g][v]));
+            for (int v = 0; v < 4; ++v) {
+              p[b][nt][v] = fast_exp2(fmaf(sc[b][nt][v], rf[nt][v & 1], -m_run[nt][v & 1]));
+              if (kMasked && hid[b][nt][v]) p[b][nt][v] = 0.f;
             }
+            far = fmaxf(far, fmaxf(p[b][nt][0] + p[b][nt][2], p[b][nt][1] + p[b][nt][3]));
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                float P0 = p[b][nt][2 * x] * sv[b][x][g], P1 = p[b][nt][2 * x + 1] * sv[b][x][g];
+                if (kMasked && hid[b][nt][2 * x]) P0 = 0.f;   // (beside a NaN scale too)
+                if (kMasked && hid[b][nt][2 * x + 1]) P1 = 0.f;
+                ph[b][nt][g][x] = pack_f16x2(P0, P1);
+                top = __hmax2(top, __habs2(*reinterpret_cast<const __half2*>(&ph[b][nt][g][x])));
+              }
           }
-        return top > kInt4Limit || far > kInt4FarP;
+        return !__hble2(top, __half2half2(__float2half(kInt4Limit))) || far > kInt4FarP;
       };
       if (__any_sync(0xffffffffu, weights())) {
-        float ve[2];
+        float ve[NB][2];
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          ve[x] = int4_scale_exponent(sv[x][0]);
-          if constexpr (G == 2) ve[x] = fmaxf(ve[x], int4_scale_exponent(sv[x][1]));
-        }
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            ve[b][x] = int4_scale_exponent(sv[b][x][0]);
+            if constexpr (G == 2) ve[b][x] = fmaxf(ve[b][x], int4_scale_exponent(sv[b][x][1]));
+          }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float mx = fmaxf(sc[nt][e] + ve[0], sc[nt][2 + e] + ve[1]);
+            float mx = kNegInf;
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+              for (int x = 0; x < 2; ++x)
+                if (!hid[b][nt][2 * x + e]) mx = fmaxf(mx, fmaf(sc[b][nt][2 * x + e], rf[nt][e], ve[b][x]));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
@@ -498,59 +590,65 @@ __global__ void __launch_bounds__(Sh::THREADS, Sh::CTAS) decode_int4_kernel(cons
           }
         weights();
       }
-      if (masked) {   // a weight of 0 beside a NaN scale is 0
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int v = 0; v < 4; ++v)
-#pragma unroll
-            for (int g = 0; g < G; ++g)
-              if (sc[nt][v] == kNegInf) P[nt][g][v] = 0.f;
-      }
-      uint32_t pb[NT][G][2];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) l_run[nt][e] += p[nt][e] + p[nt][2 + e];
-#pragma unroll
-        for (int g = 0; g < G; ++g) {
-#pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            const float z = masked && sc[nt][v] == kNegInf ? 0.f : zv[v >> 1][g];
-            o_z[nt][g][v & 1] = fmaf(p[nt][v], z, o_z[nt][g][v & 1]);
-          }
-          // The S^T layout (token, rows 2 c4, 2 c4 + 1) transposed: (row i8, slots 2 c4, 2 c4 + 1).
-          pb[nt][g][0] = movmatrix_t(pack_f16x2(P[nt][g][0], P[nt][g][1]));
-          pb[nt][g][1] = movmatrix_t(pack_f16x2(P[nt][g][2], P[nt][g][3]));
-        }
-      }
 
       // ---- O^T (dimensions x rows) += V^T P^T ----
-      uint32_t w0[G], w1[G], w2[G], w3[G];
-      lds_words<G>(st + v_off0, w0);
-      lds_words<G>(st + v_off1, w1);
-      lds_words<G>(st + v_off0 + 8 * T::RB, w2);
-      lds_words<G>(st + v_off1 + 8 * T::RB, w3);
 #pragma unroll
-      for (int g = 0; g < G; ++g) {
-        // Even and odd dimensions of the two tokens of a slot pair.
-        const uint32_t x01 = __byte_perm(w0[g], w1[g], 0x5410), y01 = __byte_perm(w0[g], w1[g], 0x7632);
-        const uint32_t x23 = __byte_perm(w2[g], w3[g], 0x5410), y23 = __byte_perm(w2[g], w3[g], 0x7632);
+      for (int b = 0; b < NB; ++b) {
+        uint32_t pb[NT][G][2];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const uint32_t keep = x & 1 ? 0x00F000F0u : 0x000F000Fu;
-          const int sh = 8 * (x >> 1);
+        for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            mma_f16(o_acc[nt][g][x], (x01 >> sh) & keep, (y01 >> sh) & keep, (x23 >> sh) & keep, (y23 >> sh) & keep,
-                    pb[nt][g][0], pb[nt][g][1]);
+          for (int e = 0; e < 2; ++e) l_run[nt][e] += p[b][nt][e] + p[b][nt][2 + e];
+#pragma unroll
+          for (int g = 0; g < G; ++g) {
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+              if (kMasked && hid[b][nt][v]) continue;
+              o_z[nt][g][v & 1] = fmaf(p[b][nt][v], zv[b][v >> 1][g], o_z[nt][g][v & 1]);
+            }
+            // The S^T layout (token, rows 2 c4, 2 c4 + 1) transposed: (row i8, slots 2 c4, 2 c4 + 1).
+            pb[nt][g][0] = transposed(ph[b][nt][g][0]);
+            pb[nt][g][1] = transposed(ph[b][nt][g][1]);
+          }
         }
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)   // 8 in every element
-          mma_f16(o_bias[nt][g], 0x00080008u, 0x00080008u, 0x00080008u, 0x00080008u, pb[nt][g][0], pb[nt][g][1]);
+        for (int g = 0; g < G; ++g) {
+          // Even and odd dimensions of the two tokens of a slot pair.
+          const uint32_t x01 = __byte_perm(w[b][0][g], w[b][1][g], 0x5410), y01 = __byte_perm(w[b][0][g], w[b][1][g], 0x7632);
+          const uint32_t x23 = __byte_perm(w[b][2][g], w[b][3][g], 0x5410), y23 = __byte_perm(w[b][2][g], w[b][3][g], 0x7632);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const uint32_t keep = x & 1 ? 0x00F000F0u : 0x000F000Fu;
+            const int sh = 8 * (x >> 1);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma_acc(o_acc[nt][g][x], (x01 >> sh) & keep, (y01 >> sh) & keep, (x23 >> sh) & keep, (y23 >> sh) & keep,
+                      pb[nt][g][0], pb[nt][g][1]);
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)   // 8 in every element
+            mma_acc(o_bias[nt][g], 0x00080008u, 0x00080008u, 0x00080008u, 0x00080008u, pb[nt][g][0], pb[nt][g][1]);
+        }
       }
+    };
+
+    // The steps whose tokens every row sees come first.
+    const int steps = (take + STEP - 1) / STEP;
+    const int clear = min(take, max(cb, 0) / kBlockSize - lb) / STEP;
+#pragma unroll 1
+    for (; kk < steps; kk += WB) {
+      cp_async_wait_groups<RING - 2>();
+      stream_sync();   // the step's blocks are there for all of the stream's warps, and the last step's are read
+      fetch(st_last);
+      if (row_base < Rs) {
+        const int tok0 = (lb + kk * STEP) * kBlockSize;
+        if (kk < clear) step(std::false_type{}, tok0, false);
+        else step(std::true_type{}, tok0, kk * STEP + 1 == take);
+      }
+      st_last = st;
+      st = st + UNIT == ring_end ? ring : st + UNIT;
     }
-    kk -= take;
+    kk -= steps;
 
     // ---- merge the streams of this piece ----
 #pragma unroll
