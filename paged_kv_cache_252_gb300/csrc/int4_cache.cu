@@ -2,8 +2,8 @@
 // (declared in include/pagedkv.h; "KVCache Quant" of "AI大模型推理速度翻倍，Colossal-Inference开源发布"
 // casts on the way in and out; the 4-bit codec is described in pkv_int4.cuh).
 //
-// Write: eight threads a row, each with eight dimensions of every group (one 16-byte load a
-// group); the group's least and largest value by three shuffles of a packed (least, -largest) pair.
+// Write: four threads a group of 64 dimensions, sixteen each; the group's least and largest value by two
+// shuffles of a packed (least, -largest) pair, and both its numbers computed by each of the four.
 // Read: D / 16 threads a row, sixteen dimensions each.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -35,6 +35,11 @@ __device__ __forceinline__ uint32_t min2_nan(uint32_t a, uint32_t b, bool bf16) 
   return d;
 }
 
+// th / heads: a 64-bit division costs more than all the rest of a row, so it is left to rows past 2^32.
+__device__ __forceinline__ int token_of(long long th, int heads) {
+  return static_cast<int>((th >> 32) == 0 ? static_cast<uint32_t>(th) / static_cast<uint32_t>(heads) : th / heads);
+}
+
 template <bool BF16>
 __device__ __forceinline__ float2 floats_of(uint32_t w) {
   if constexpr (BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
@@ -44,63 +49,64 @@ __device__ __forceinline__ float2 floats_of(uint32_t w) {
 template <int G, bool BF16>
 __global__ void __launch_bounds__(256) int4_write_kernel(const Int4WriteArgs a) {
   pdl_wait_prior_grid();
+  constexpr int TPR = 4 * G;   // threads of a row: 16 dimensions each
   const long long rows = 2ll * a.num_tokens * a.num_kv_heads;
-  const long long n = (rows * 8 + 31) / 32 * 32;   // whole warps: every lane takes part in the shuffles
+  const long long n = (rows * TPR + 31) / 32 * 32;   // whole warps: every lane takes part in the shuffles
   for (long long idx = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; idx < n;
        idx += static_cast<long long>(gridDim.x) * blockDim.x) {
-    const bool real = idx < rows * 8;
-    const long long row = real ? idx / 8 : rows - 1;
-    const int i = static_cast<int>(idx & 7);
+    const bool real = idx < rows * TPR;
+    const long long row = real ? idx / TPR : rows - 1;
+    const int i = static_cast<int>(idx % TPR), g = i >> 2;
     const int which = row >= rows / 2;
     const long long th = which ? row - rows / 2 : row;
-    const int t = static_cast<int>(th / a.num_kv_heads), h = static_cast<int>(th - static_cast<long long>(t) * a.num_kv_heads);
-    const long long slot = a.slot_mapping[t];
-    const uint4* src = which ? a.src[1] : a.src[0];
-    uint4 v[G];
+    const int t = token_of(th, a.num_kv_heads), h = static_cast<int>(th - static_cast<long long>(t) * a.num_kv_heads);
+    const uint4* src = (which ? a.src[1] : a.src[0]) + th * (2 * TPR) + 2 * i;
+    const uint4 v0 = src[0], v1 = src[1];
+    const int slot = a.slot_mapping[t];
+    const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+    constexpr uint32_t kNeg = 0x80008000u;
+    uint32_t lo2 = w[0], hi2 = w[0] ^ kNeg;
 #pragma unroll
-    for (int g = 0; g < G; ++g) v[g] = src[th * (8 * G) + 8 * g + i];
-    uint32_t words[G], meta[G];
-#pragma unroll
-    for (int g = 0; g < G; ++g) {
-      const uint32_t w[4] = {v[g].x, v[g].y, v[g].z, v[g].w};
-      constexpr uint32_t kNeg = 0x80008000u;
-      uint32_t lo2 = min2_nan(min2_nan(w[0], w[1], BF16), min2_nan(w[2], w[3], BF16), BF16);
-      uint32_t hi2 = min2_nan(min2_nan(w[0] ^ kNeg, w[1] ^ kNeg, BF16), min2_nan(w[2] ^ kNeg, w[3] ^ kNeg, BF16), BF16);
-      // (least, -largest) of the eight, then of the group
-      uint32_t both = min2_nan(__byte_perm(lo2, hi2, 0x5410), __byte_perm(lo2, hi2, 0x7632), BF16);
-#pragma unroll
-      for (int o = 1; o < 8; o <<= 1) both = min2_nan(both, __shfl_xor_sync(0xffffffffu, both, o), BF16);
-      const float2 lh = floats_of<BF16>(both);
-      const bool finite = lh.x > -INFINITY && lh.y > -INFINITY && lh.x < INFINITY && lh.y < INFINITY;
-      const float lo = fminf(fmaxf(lh.x, -65504.f), 65504.f), hi = fminf(fmaxf(-lh.y, -65504.f), 65504.f);
-      const Int4Group q = int4_group(finite ? lo : 0.f, finite ? hi : 0.f);
-      words[g] = 0;
-#pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        const float2 x = floats_of<BF16>(w[m]);
-        if (finite) {
-          const float x0 = BF16 ? fminf(fmaxf(x.x, -65504.f), 65504.f) : x.x, x1 = BF16 ? fminf(fmaxf(x.y, -65504.f), 65504.f) : x.y;
-          words[g] |= int4_code(x0, q) << int4_bit(2 * m) | int4_code(x1, q) << int4_bit(2 * m + 1);
-        }
-      }
-      meta[g] = finite ? pack_f16x2(q.s, q.z) : 0x00007FFFu;
+    for (int m = 1; m < 8; ++m) {
+      lo2 = min2_nan(lo2, w[m], BF16);
+      hi2 = min2_nan(hi2, w[m] ^ kNeg, BF16);
     }
+    // (least, -largest) of the sixteen, then of the group
+    uint32_t both = min2_nan(__byte_perm(lo2, hi2, 0x5410), __byte_perm(lo2, hi2, 0x7632), BF16);
+    both = min2_nan(both, __shfl_xor_sync(0xffffffffu, both, 1), BF16);
+    both = min2_nan(both, __shfl_xor_sync(0xffffffffu, both, 2), BF16);
     if (!real || slot == -1) continue;
     if (slot < 0 || slot >= a.num_slots) {
       if (i == 0 && a.status) atomicOr(a.status, kDevBadSlot);
       continue;
     }
-    const long long blk = slot / kBlockSize, off = slot - blk * kBlockSize;
-    const long long tile = blk * a.num_kv_heads + h;
-    uint32_t* dst = (which ? a.codes[1] : a.codes[0]) + ((tile * kBlockSize + off) * 8 + i) * G;
-    uint32_t* sc = a.scales + (tile * 2 * kBlockSize + which * kBlockSize + off) * G;
-    if constexpr (G == 2) {
-      *reinterpret_cast<uint2*>(dst) = make_uint2(words[0], words[1]);
-      if (i == 0) *reinterpret_cast<uint2*>(sc) = make_uint2(meta[0], meta[1]);
-    } else {
-      *dst = words[0];
-      if (i == 0) *sc = meta[0];
+    const float2 lh = floats_of<BF16>(both);
+    uint32_t words[2] = {0, 0}, meta = 0x00007FFFu;
+    if (lh.x > -INFINITY && lh.y > -INFINITY && lh.x < INFINITY && lh.y < INFINITY) {
+      const bool beyond = BF16 && (lh.x < -65504.f || -lh.y > 65504.f || -lh.y < -65504.f || lh.x > 65504.f);
+      const Int4Group q = int4_group(fminf(fmaxf(lh.x, -65504.f), 65504.f), fminf(fmaxf(-lh.y, -65504.f), 65504.f));
+      meta = pack_f16x2(q.s, q.z);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        float2 x[4];
+#pragma unroll
+        for (int m = 0; m < 4; ++m) x[m] = floats_of<BF16>(w[4 * k + m]);
+        if (beyond) {
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            x[m].x = fminf(fmaxf(x[m].x, -65504.f), 65504.f);
+            x[m].y = fminf(fmaxf(x[m].y, -65504.f), 65504.f);
+          }
+        }
+        words[k] = int4_word(x, q);
+      }
     }
+    const int blk = slot / kBlockSize, off = slot - blk * kBlockSize;
+    const long long tile = static_cast<long long>(blk) * a.num_kv_heads + h;
+    uint32_t* dst = (which ? a.codes[1] : a.codes[0]) + ((tile * kBlockSize + off) * 8 + 2 * (i & 3)) * G + g;
+    dst[0] = words[0];
+    dst[G] = words[1];
+    if ((i & 3) == 0) a.scales[(tile * 2 * kBlockSize + which * kBlockSize + off) * G + g] = meta;
   }
   pdl_launch_dependents();
 }
@@ -133,15 +139,15 @@ __global__ void __launch_bounds__(256) cache_read_kernel(const ReadArgs a) {
     const int i = static_cast<int>(idx % TPR);
     const int which = row >= rows / 2;
     const long long th = which ? row - rows / 2 : row;
-    const int t = static_cast<int>(th / a.num_kv_heads), h = static_cast<int>(th - static_cast<long long>(t) * a.num_kv_heads);
-    const long long slot = a.slot_mapping[t];
+    const int t = token_of(th, a.num_kv_heads), h = static_cast<int>(th - static_cast<long long>(t) * a.num_kv_heads);
+    const int slot = a.slot_mapping[t];
     if (slot == -1) continue;
     if (slot < 0 || slot >= a.num_slots) {
       if (i == 0 && a.status) atomicOr(a.status, kDevBadSlot);
       continue;
     }
-    const long long blk = slot / kBlockSize, off = slot - blk * kBlockSize;
-    const long long tile = blk * a.num_kv_heads + h, at = tile * kBlockSize + off;
+    const int blk = slot / kBlockSize, off = slot - blk * kBlockSize;
+    const long long tile = static_cast<long long>(blk) * a.num_kv_heads + h, at = tile * kBlockSize + off;
     const void* cache = which ? a.cache[1] : a.cache[0];
     uint32_t out[8];
     if constexpr (KV == kKvInt4) {
@@ -263,7 +269,7 @@ int pkv_kv_cache_write_int4(const void* key, const void* value, pkv_dtype src_dt
                         : (bf16 ? reinterpret_cast<const void*>(&int4_write_kernel<1, true>)
                                 : reinterpret_cast<const void*>(&int4_write_kernel<1, false>));
   void* args[1] = {&a};
-  return launch_overlapped(fn, dim3(row_grid(16ll * num_tokens * cache->num_kv_heads, sms)), dim3(256), 0, stream, args);
+  return launch_overlapped(fn, dim3(row_grid(2ll * num_tokens * cache->num_kv_heads * (cache->head_size / 16), sms)), dim3(256), 0, stream, args);
 }
 
 int pkv_kv_cache_read(void* key, void* value, pkv_dtype dst_dtype, int32_t num_tokens, const int32_t* slot_mapping,

@@ -37,7 +37,7 @@ __device__ __forceinline__ float two_sum(float x, float y, float& err) {
 }
 
 struct Int4Group {
-  float z, s, inv;   // inv: 1 / s, 0 for s = 0
+  float z, s, inv;   // inv: 1 / s to a bit, 0 for s = 0
 };
 
 // z and s of a group from its least and largest value (within +-65504): exactly as defined, in fp32.
@@ -51,7 +51,8 @@ __device__ __forceinline__ Int4Group int4_group(float lo, float hi) {
   // the rounded difference and the exact one is larger.
   if (__fmul_rn(15.f, __half2float(s)) == d && err > 0.f) s = __ushort_as_half(__half_as_ushort(s) + 1);
   q.s = __half2float(s);
-  q.inv = q.s > 0.f ? __frcp_rn(q.s) : 0.f;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q.inv) : "f"(q.s));   // (s is 0 or normal in fp32)
+  if (q.s == 0.f) q.inv = 0.f;
   q.z += 0.f;        // (-0 is 0)
   return q;
 }
@@ -67,13 +68,63 @@ static __device__ __noinline__ float int4_code_exact(float x, float z, float s, 
   return below * 0.5f == floorf(below * 0.5f) ? below : below + 1.f;   // halfway: the even code
 }
 
-// A quotient in fp32 is off by less than 16 * 3 * 2^-24 < 3e-6: codes of quotients nearer than 1e-5 to
-// a border are settled exactly.
-__device__ __forceinline__ uint32_t int4_code(float x, const Int4Group& q) {
-  const float v = (x - q.z) * q.inv;
+// Two fp32 operations an instruction, each rounded by itself.
+__device__ __forceinline__ uint64_t f32x2(float lo, float hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ float2 halves_of(uint64_t v) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+  return f;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+
+// The code of x, its quotient v: settled exactly where v lies near a border.
+__device__ __forceinline__ uint32_t int4_code(float x, float v, const Int4Group& q) {
   float c = rintf(v);
   if (fabsf(v - c) > 0.5f - 1e-5f) c = int4_code_exact(x, q.z, q.s, floorf(v));
   return static_cast<uint32_t>(__float2int_rn(c));
+}
+
+// The codes of a word's dimensions, x[m] = dimensions 2 m and 2 m + 1. Adding 1.5 * 2^23 to a quotient rounds it
+// to the nearest code (halfway: the even one). A quotient in fp32 is off by less than 16 * 4 * 2^-24 < 4e-6: words with one
+// nearer than 1e-5 to a border are settled exactly (one word in 5 of a warp's on 8-bit mantissas).
+__device__ __forceinline__ uint32_t int4_word(const float2 (&x)[4], const Int4Group& q) {
+  const uint64_t minus_z = f32x2(-q.z, -q.z), inv = f32x2(q.inv, q.inv), minus_inv = f32x2(-q.inv, -q.inv);
+  const uint64_t magic = f32x2(12582912.f, 12582912.f), minus_magic = f32x2(-12582912.f, -12582912.f);
+  uint64_t c[4];
+  float off = 0.f;
+#pragma unroll
+  for (int m = 0; m < 4; ++m) {
+    const uint64_t d = add2(f32x2(x[m].x, x[m].y), minus_z);
+    c[m] = add2(fma2(d, inv, magic), minus_magic);
+    const float2 o = halves_of(fma2(d, minus_inv, c[m]));
+    off = fmaxf(off, fmaxf(fabsf(o.x), fabsf(o.y)));
+  }
+  if (off > 0.5f - 1e-5f) {
+    uint32_t w = 0;
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      w |= int4_code(x[m].x, (x[m].x - q.z) * q.inv, q) << int4_bit(2 * m);
+      w |= int4_code(x[m].y, (x[m].y - q.z) * q.inv, q) << int4_bit(2 * m + 1);
+    }
+    return w;
+  }
+  // Four codes of 4 bits in a float's integer: the even dimensions' and the odd ones'.
+  const uint64_t k16 = f32x2(16.f, 16.f);
+  const float2 h = halves_of(add2(fma2(fma2(fma2(c[3], k16, c[2]), k16, c[1]), k16, c[0]), f32x2(8388608.f, 8388608.f)));
+  return __byte_perm(__float_as_uint(h.x), __float_as_uint(h.y), 0x5410);
 }
 
 // Pair m (dimensions 2 m and 2 m + 1) of a word as fp16 numbers 0..15.
