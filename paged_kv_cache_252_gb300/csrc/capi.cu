@@ -419,18 +419,20 @@ size_t pkv_decode_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t
   if (cache->head_size != 64 && cache->head_size != 128) return 0;
   // The grid follows the kv dtype's occupancy; size for the largest over the
   // supported dtypes so that one workspace serves any of them.
-  int ctas = 1;
-  if (decode_int4_ctas(cache->head_size, rows, &ctas)) return 0;
+  const long long units = static_cast<long long>(num_seqs) * cache->num_kv_heads;
+  const size_t int4 = decode_int4_workspace_bytes(units, cache->head_size, rows);
+  if (int4 == 0) return 0;
   std::lock_guard<std::mutex> lock(g_mu);
   DeviceState* st = nullptr;
   if (current_device_state(&st)) return 0;
-  const long long units = static_cast<long long>(num_seqs) * cache->num_kv_heads;
+  int ctas = 1;
   for (int kv = kKvF16; kv <= kKvInt8; ++kv) {
     GeomEntry* ge = nullptr;
     if (get_geometry(st, kv, cache->head_size, rows, &ge)) return 0;
     if (ge->ctas_per_sm > ctas) ctas = ge->ctas_per_sm;
   }
-  return workspace_bytes_for(units, st->sm_count, ctas, rows, cache->head_size);
+  const size_t others = workspace_bytes_for(units, st->sm_count, ctas, rows, cache->head_size);
+  return int4 > others ? int4 : others;
 }
 
 }  // extern "C"

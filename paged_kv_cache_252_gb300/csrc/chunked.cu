@@ -175,7 +175,10 @@ static int decode_chunked(void* out, const void* q, pkv_dtype q_dtype, const int
 
   void* wdec = ws + L.decode;
   // The tiles' piece counters start clear (the region may hold another call's data).
-  if (cudaMemsetAsync(wdec, 0, pkv::decode_counter_bytes(T * cache->num_kv_heads), st) != cudaSuccess) {
+  const long long units = T * cache->num_kv_heads;
+  const size_t counters = kv_dtype == PKV_INT4 ? pkv::decode_int4_counter_bytes(units, cache->head_size, q_tile * (num_q_heads / cache->num_kv_heads))
+                                               : pkv::decode_counter_bytes(units);
+  if (cudaMemsetAsync(wdec, 0, counters, st) != cudaSuccess) {
     cudaGetLastError();
     return PKV_ERR_CUDA;
   }

@@ -25,7 +25,7 @@ int shape_index(int rows) { return rows <= 8 ? 0 : rows <= 16 ? 1 : rows <= 32 ?
 
 // Fixed cost of a unit's piece on the work line, in blocks.
 #ifndef PKV_PIECE_COST_INT4
-#define PKV_PIECE_COST_INT4 24
+#define PKV_PIECE_COST_INT4 32
 #endif
 
 // Once per device, head size and shape: shared-memory limits of both query types' kernels and the CTAs an
@@ -61,11 +61,35 @@ int resident_ctas(int d, int rows, int* ctas) {
   return PKV_OK;
 }
 
+// A call's workspace: units + CTAs slots, as a shared unit's pieces use slots unit + CTA, behind a counter for every slot.
+struct Space {
+  long long ctas;
+  size_t counters, bytes;
+};
+int space_of(long long units, int d, int rows, Space* sp) {
+  int sms = 0, per_sm = 0;
+  if (int rc = device_sm_count(&sms)) return rc;
+  if (int rc = resident_ctas(d, rows, &per_sm)) return rc;
+  sp->ctas = static_cast<long long>(sms) * per_sm;
+  if (sp->ctas > 4096) return PKV_ERR_UNSUPPORTED;   // four levels of eight
+  sp->counters = decode_counter_bytes(units + sp->ctas);
+  sp->bytes = sp->counters + static_cast<size_t>(units + sp->ctas) * partial_slot_floats(rows, d) * sizeof(float);
+  return PKV_OK;
+}
+
 }  // namespace
 
 namespace pkv {
 
-int decode_int4_ctas(int d, int rows, int* ctas) { return resident_ctas(d, rows, ctas); }
+size_t decode_int4_workspace_bytes(long long units, int d, int rows) {
+  Space sp{};
+  return space_of(units, d, rows, &sp) ? 0 : sp.bytes;
+}
+
+size_t decode_int4_counter_bytes(long long units, int d, int rows) {
+  Space sp{};
+  return space_of(units, d, rows, &sp) ? 0 : sp.counters;
+}
 
 }  // namespace pkv
 
@@ -99,17 +123,13 @@ extern "C" int pkv_paged_attention_decode_int4(void* out, const void* q, pkv_dty
     return PKV_ERR_INVALID_ARGUMENT;
 
   const int d = cache->head_size, rows = static_cast<int>(rows_ll);
-  int sms = 0, ctas = 0;
-  if (int rc = device_sm_count(&sms)) return rc;
-  if (int rc = resident_ctas(d, rows, &ctas)) return rc;
   const long long units = static_cast<long long>(num_seqs) * cache->num_kv_heads;
-  const long long wave = static_cast<long long>(sms) * ctas;
-  const int slot = partial_slot_floats(rows, d);
-  if (workspace_bytes < decode_counter_bytes(units) + static_cast<size_t>(units + wave) * slot * sizeof(float))
-    return PKV_ERR_WORKSPACE_TOO_SMALL;
+  Space sp{};
+  if (int rc = space_of(units, d, rows, &sp)) return rc;
+  if (workspace_bytes < sp.bytes) return PKV_ERR_WORKSPACE_TOO_SMALL;
   // One wave: every CTA resident at once; never more CTAs than blocks could exist.
   const long long most = units * max_blocks_per_seq;
-  const long long grid = wave < most ? wave : most;
+  const long long grid = sp.ctas < most ? sp.ctas : most;
 
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   DecodeInt4Args a{};
@@ -121,7 +141,7 @@ extern "C" int pkv_paged_attention_decode_int4(void* out, const void* q, pkv_dty
   a.q_rows = num_q_rows;
   a.tree_masks = reinterpret_cast<const unsigned long long*>(tree_masks);
   a.piece_counts = reinterpret_cast<unsigned long long*>(ws);
-  a.partials = reinterpret_cast<float*>(ws + decode_counter_bytes(units));
+  a.partials = reinterpret_cast<float*>(ws + sp.counters);
   a.status = device_status;
   a.num_seqs = num_seqs;
   a.num_q_heads = num_q_heads;
@@ -131,7 +151,7 @@ extern "C" int pkv_paged_attention_decode_int4(void* out, const void* q, pkv_dty
   a.rows = rows;
   a.max_blocks_per_seq = max_blocks_per_seq;
   a.num_blocks = cache->num_blocks;
-  a.slot_floats = slot;
+  a.slot_floats = partial_slot_floats(rows, d);
   a.scale_log2 = scale * 1.4426950408889634f;
   a.epoch = next_call_epoch();
   a.piece_cost = PKV_PIECE_COST_INT4;

@@ -84,8 +84,10 @@ struct Int4Walk {
 };
 
 struct Int4Smem {
-  int qs, rf, qsum, vis, walk, mrg_o, mrg_ml, fin_ml, misc, total;
+  int qs, rf, qsum, vis, walk, mrg_o, mrg_ml, fin_ml, fac, misc, total;
 };
+constexpr int kInt4FanLog = 3, kInt4Fan = 1 << kInt4FanLog;   // children of a node of the join
+
 template <int D, class Sh>
 __host__ __device__ constexpr Int4Smem int4_smem(int rows) {
   Int4Smem s{};
@@ -97,7 +99,8 @@ __host__ __device__ constexpr Int4Smem int4_smem(int rows) {
   s.mrg_o = s.walk + Sh::WR * Sh::WB * static_cast<int>(sizeof(Int4Walk));
   s.mrg_ml = s.mrg_o + Sh::WB * rows * (D + 4) * 4;
   s.fin_ml = s.mrg_ml + (Sh::WB * rows * 8 + 15) / 16 * 16;
-  s.misc = s.fin_ml + (rows * 8 + 15) / 16 * 16;
+  s.fac = s.fin_ml + (rows * 8 + 15) / 16 * 16;
+  s.misc = s.fac + (kInt4Fan * rows * 4 + 15) / 16 * 16;
   s.total = s.misc + 256;
   return s;
 }
@@ -165,6 +168,183 @@ __device__ __forceinline__ uint32_t transposed(uint32_t a) {
   return d;
 }
 
+// Joins the pieces of a unit that several CTAs share (the split-softmax rule of decode_common.cuh) in a tree: a
+// node is merged by the last of its kInt4Fan children to arrive, which goes on as that node. A child's (m, l, o) lie in slot (unit +
+// its first CTA); a node's arrivals are counted in a byte a level of that slot's counter, tagged with the call. The first
+// child, usually the last to arrive, first tries to count itself as the completing one, unpublished. One CTA that joins all pieces reads
+// 38 of 64 rows in some 80 us (1 sequence of 262144 tokens: 401 us instead of 320).
+// FEW (at most 8 rows, an item or two a thread): an item's weights and values in one round trip; else the rows' weights first.
+// The piece: o[r] at o + r * (D + 4), m and l at ml[r], ml[R + r], complete before the call. Returns true in the
+// CTA that holds the whole unit there. Every thread of the CTA calls it.
+template <int D, int NTHR, bool FEW>
+__device__ __forceinline__ bool int4_join(const DecodeArgs& a, int u, int c_first, int c_last, int Rs, float* o, float* ml, float* fac,
+                                          volatile int* fin) {
+  const int tid = threadIdx.x, R = a.rows, ooff = partial_o_offset(R);
+  const long long slot0 = static_cast<long long>(u) + c_first;
+  const int items = Rs * (D / 4);
+  int idx = static_cast<int>(blockIdx.x) - c_first, cnt = c_last - c_first + 1;
+#pragma unroll 1
+  for (int lv = 0; cnt > 1; ++lv, idx >>= kInt4FanLog, cnt = (cnt + kInt4Fan - 1) >> kInt4FanLog) {
+    const int kid0 = idx & ~(kInt4Fan - 1), kids = min(kInt4Fan, cnt - kid0), sh = kInt4FanLog * lv;
+    if (kids == 1) continue;
+    const unsigned long long one = 1ull << (8 * lv), tag = static_cast<unsigned long long>(a.epoch) << 32;
+    unsigned long long* ctr = a.piece_counts + slot0 + (static_cast<long long>(kid0) << sh);
+    unsigned long long cur = 0ull;   // (thread 0's guess of the counter)
+    __syncthreads();
+    if (tid == 0) {
+      bool done = false;
+      if (idx == kid0) {
+        const unsigned long long others = tag | one * (kids - 1);
+        cur = atomicCAS(ctr, others, others + one);
+        done = cur == others;
+        if (done) fence_acq_rel_gpu();   // acquire: the other children's slots are read next
+      }
+      fin[0] = done;
+    }
+    __syncthreads();
+    if (!fin[0]) {
+      float* P = a.partials + static_cast<size_t>(slot0 + (static_cast<long long>(idx) << sh)) * a.slot_floats;
+      for (int x = tid; x < items; x += NTHR) {
+        const int r = x / (D / 4), d4 = x % (D / 4);
+        *reinterpret_cast<float4*>(P + ooff + r * D + d4 * 4) = *reinterpret_cast<const float4*>(o + r * (D + 4) + d4 * 4);
+      }
+      for (int r = tid; r < Rs; r += NTHR) {
+        P[r] = ml[r];
+        P[R + r] = ml[R + r];
+      }
+      __syncthreads();   // every thread's stores before thread 0's release fence
+      if (tid == 0) {
+        fence_acq_rel_gpu();
+        unsigned long long want;
+        for (;;) {   // (a counter of another call reads as clear)
+          want = (cur >> 32) == a.epoch ? cur + one : tag | one;
+          const unsigned long long prev = atomicCAS(ctr, cur, want);
+          if (prev == cur) break;
+          cur = prev;
+        }
+        const bool done = static_cast<int>((want >> (8 * lv)) & 0xFFull) == kids;
+        if (done) fence_acq_rel_gpu();
+        fin[1] = done;
+      }
+      __syncthreads();
+      if (!fin[1]) return false;
+    }
+    // M = max m, L = sum l 2^(m - M), o = sum o 2^(m - M) over the children in order (the bits do not depend on who joins them).
+    const float* base = a.partials + static_cast<size_t>(slot0 + (static_cast<long long>(kid0) << sh)) * a.slot_floats;
+    const size_t step = static_cast<size_t>(a.slot_floats) << sh;
+    const int own = idx - kid0;
+    if constexpr (FEW) {
+      float M[8 * (D / 4) / NTHR + 1], L[8 * (D / 4) / NTHR + 1];
+#pragma unroll
+      for (int e = 0; e < 8 * (D / 4) / NTHR; ++e) {
+        const int x = tid + e * NTHR, r = x / (D / 4), d4 = x % (D / 4);
+        if (x >= items) break;
+        float mc[kInt4Fan], lc[kInt4Fan];
+        float4 v[kInt4Fan];
+        M[e] = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < kInt4Fan; ++k) {
+          const bool far = k < kids && k != own;
+          mc[k] = far ? __ldcg(base + k * step + r) : -INFINITY;
+          lc[k] = far ? __ldcg(base + k * step + R + r) : 0.f;
+          v[k] = far ? __ldcg(reinterpret_cast<const float4*>(base + k * step + ooff + r * D + d4 * 4)) : make_float4(0.f, 0.f, 0.f, 0.f);
+          if (k == own) {
+            mc[k] = ml[r];
+            lc[k] = ml[R + r];
+            v[k] = *reinterpret_cast<const float4*>(o + r * (D + 4) + d4 * 4);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < kInt4Fan; ++k) M[e] = fmaxf(M[e], mc[k]);
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        L[e] = 0.f;
+#pragma unroll
+        for (int k = 0; k < kInt4Fan; ++k) {
+          const float f = fast_exp2(mc[k] - M[e]);   // (M is finite)
+          L[e] += f * lc[k];
+          acc.x += f * v[k].x;
+          acc.y += f * v[k].y;
+          acc.z += f * v[k].z;
+          acc.w += f * v[k].w;
+        }
+        *reinterpret_cast<float4*>(o + r * (D + 4) + d4 * 4) = acc;
+      }
+      __syncthreads();   // ml is read
+#pragma unroll
+      for (int e = 0; e < 8 * (D / 4) / NTHR; ++e) {
+        const int x = tid + e * NTHR, r = x / (D / 4);
+        if (x < items && x % (D / 4) == 0) {
+          ml[r] = M[e];
+          ml[R + r] = L[e];
+        }
+      }
+      if (tid == 0) atomicAdd(ctr, 0ull - one * kids);   // clear for a replay
+      continue;
+    }
+    for (int r = tid; r < Rs; r += NTHR) {
+      float mc[kInt4Fan], lc[kInt4Fan], M = -INFINITY, L = 0.f;
+#pragma unroll
+      for (int k = 0; k < kInt4Fan; ++k) {
+        const bool far = k < kids && k != own;
+        mc[k] = far ? __ldcg(base + k * step + r) : (k == own ? ml[r] : -INFINITY);
+        lc[k] = far ? __ldcg(base + k * step + R + r) : (k == own ? ml[R + r] : 0.f);
+        M = fmaxf(M, mc[k]);
+      }
+#pragma unroll
+      for (int k = 0; k < kInt4Fan; ++k) {
+        const float f = fast_exp2(mc[k] - M);   // (M is finite)
+        L += f * lc[k];
+        fac[k * R + r] = f;
+      }
+      ml[r] = M;
+      ml[R + r] = L;
+    }
+    __syncthreads();
+    // Four items of a thread at a time, a child's four loads in flight with the next child's.
+#pragma unroll 1
+    for (int x0 = tid; x0 < items; x0 += 4 * NTHR) {
+      float4 acc[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+      for (int k = 0; k < kids; k += 2) {
+        float4 v[2][4];
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int x = x0 + e * NTHR, r = x / (D / 4), d4 = x % (D / 4);
+            v[j][e] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (x < items && k + j < kids)
+              v[j][e] = k + j == own ? *reinterpret_cast<const float4*>(o + r * (D + 4) + d4 * 4)
+                                     : __ldcg(reinterpret_cast<const float4*>(base + (k + j) * step + ooff + r * D + d4 * 4));
+          }
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int x = x0 + e * NTHR;
+            if (x < items && k + j < kids) {
+              const float f = fac[(k + j) * R + x / (D / 4)];
+              acc[e].x += f * v[j][e].x;
+              acc[e].y += f * v[j][e].y;
+              acc[e].z += f * v[j][e].z;
+              acc[e].w += f * v[j][e].w;
+            }
+          }
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int x = x0 + e * NTHR, r = x / (D / 4), d4 = x % (D / 4);
+        if (x < items) *reinterpret_cast<float4*>(o + r * (D + 4) + d4 * 4) = acc[e];
+      }
+    }
+    if (tid == 0) atomicAdd(ctr, 0ull - one * kids);   // clear for a replay
+  }
+  __syncthreads();
+  return true;
+}
+
 template <int D, class Sh, bool BF16>
 __global__ void __launch_bounds__(Sh::THREADS, Sh::CTAS) decode_int4_kernel(const __grid_constant__ DecodeInt4Args a) {
   using T = Int4Tile<D>;
@@ -186,7 +366,6 @@ __global__ void __launch_bounds__(Sh::THREADS, Sh::CTAS) decode_int4_kernel(cons
   long long* red = reinterpret_cast<long long*>(smem + lay.misc);
   long long* plan = red + 10;
   volatile int* fin = reinterpret_cast<volatile int*>(plan + 5);
-  volatile unsigned long long* fin_cur = reinterpret_cast<volatile unsigned long long*>(plan + 8);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int wr = warp % WR, wb = warp / WR;
@@ -683,6 +862,14 @@ __global__ void __launch_bounds__(Sh::THREADS, Sh::CTAS) decode_int4_kernel(cons
         }
       }
     __syncthreads();
+    auto store_row = [&](int r, int d4, const float4& v, float l) {
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const int j = r / Gq, gi = r - j * Gq;
+      uint2 pk;
+      pk.x = pack_p<BF16 ? kKvBf16 : kKvF16>(v.x * inv, v.y * inv);
+      pk.y = pack_p<BF16 ? kKvBf16 : kKvF16>(v.z * inv, v.w * inv);
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + (static_cast<size_t>(qb + j) * Hq + h * Gq + gi) * D + d4 * 4) = pk;
+    };
     for (int idx = tid; idx < Rs * (D / 4); idx += NTHR) {
       const int r = idx / (D / 4), d4 = idx % (D / 4);
       float M = kNegInf;
@@ -701,13 +888,7 @@ __global__ void __launch_bounds__(Sh::THREADS, Sh::CTAS) decode_int4_kernel(cons
         acc.w += f * v.w;
       }
       if (!split) {
-        const float inv = lsum > 0.f ? 1.f / lsum : 0.f;
-        const int j = r / Gq, gi = r - j * Gq;
-        const size_t dst = (static_cast<size_t>(qb + j) * Hq + h * Gq + gi) * D + d4 * 4;
-        uint2 pk;
-        pk.x = pack_p<BF16 ? kKvBf16 : kKvF16>(acc.x * inv, acc.y * inv);
-        pk.y = pack_p<BF16 ? kKvBf16 : kKvF16>(acc.z * inv, acc.w * inv);
-        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + dst) = pk;
+        store_row(r, d4, acc, lsum);
       } else {
         // (in place of stream 0's: only this thread reads or writes these four values)
         *reinterpret_cast<float4*>(mrg_o + static_cast<size_t>(r) * (D + 4) + d4 * 4) = acc;
@@ -718,8 +899,14 @@ __global__ void __launch_bounds__(Sh::THREADS, Sh::CTAS) decode_int4_kernel(cons
       }
     }
     if (split) {
-      finish_split_piece_smem<BF16 ? kKvBf16 : kKvF16, D>(a, u, ub, nb, total, ncta, Rs, qb, h, tid, NTHR, 3, fin,
-                                                          fin_cur, mrg_o, D + 4, fin_ml);
+      int c_first, c_last;
+      unit_owners(a, ub, nb, total, ncta, &c_first, &c_last);
+      if (int4_join<D, NTHR, (Sh::ROWS <= 8)>(a, u, c_first, c_last, Rs, mrg_o, fin_ml, reinterpret_cast<float*>(smem + lay.fac), fin)) {
+        for (int idx = tid; idx < Rs * (D / 4); idx += NTHR) {
+          const int r = idx / (D / 4), d4 = idx % (D / 4);
+          store_row(r, d4, *reinterpret_cast<const float4*>(mrg_o + r * (D + 4) + d4 * 4), fin_ml[R + r]);
+        }
+      }
     }
 
     // ---- the next unit (a piece that stops before the unit's end ended the share) ----

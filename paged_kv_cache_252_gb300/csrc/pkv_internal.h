@@ -150,8 +150,10 @@ const void* decode_kernel_ptr_e5m2(int d, int ntw);
 const void* decode_kernel_ptr_int8(int d, int ntw);
 // The 96-thread kernel for units of at most 8 rows over a bf16 cache (nullptr if none).
 const void* decode_kernel_narrow_ptr_bf16(int d);
-// CTAs of the INT4 decode kernel an SM holds, for units of `rows` rows; a pkv_status.
-int decode_int4_ctas(int d, int rows, int* ctas);
+// Workspace of a decode over an INT4 cache on the current device (0: no device) and of its counters, with which
+// it starts.
+size_t decode_int4_workspace_bytes(long long units, int d, int rows);
+size_t decode_int4_counter_bytes(long long units, int d, int rows);
 const void* kv_cache_write_kernel_ptr();
 const void* kv_cache_write_int8_kernel_ptr();
 
