@@ -59,6 +59,9 @@ struct Int4Shape {
   static constexpr int NT = NT_, WR = WR_, WB = WB_, RING = RING_, CTAS = CTAS_, STEP = STEP_;
   static_assert(RING >= 2 && (STEP == 1 || STEP == 2), "ring");
   static constexpr int ROWS = 8 * NT * WR, THREADS = 32 * WR * WB;
+  // A piece's queries: prepared once a row and shared by the streams, or by every warp for its own rows. Four streams save
+  // more by sharing than the barrier costs (64 sequences 30.5 us against 32.0), two do not (32 rows: 348 against 336).
+  static constexpr bool kShareQ = WB > 2;
 };
 #ifndef PKV_I4_R8
 #define PKV_I4_R8 1, 1, 4, 3, 3, 2
@@ -92,10 +95,10 @@ template <int D, class Sh>
 __host__ __device__ constexpr Int4Smem int4_smem(int rows) {
   Int4Smem s{};
   s.qs = Sh::WB * Sh::RING * Sh::STEP * Int4Tile<D>::STAGE;
-  s.rf = s.qs + Sh::ROWS * (D * 2 + 16);
-  s.qsum = s.rf + Sh::ROWS * 4;
-  s.vis = s.qsum + Sh::ROWS * Int4Tile<D>::G * 4;
-  s.walk = s.vis + Sh::ROWS * 8;
+  s.rf = s.qs + (Sh::kShareQ ? Sh::ROWS * (D * 2 + 16) : 0);
+  s.qsum = s.rf + (Sh::kShareQ ? Sh::ROWS * 4 : 0);
+  s.vis = s.qsum + (Sh::kShareQ ? Sh::ROWS * Int4Tile<D>::G * 4 : 0);
+  s.walk = s.vis + Sh::WB * Sh::ROWS * 8;
   s.mrg_o = s.walk + Sh::WR * Sh::WB * static_cast<int>(sizeof(Int4Walk));
   s.mrg_ml = s.mrg_o + Sh::WB * rows * (D + 4) * 4;
   s.fin_ml = s.mrg_ml + (Sh::WB * rows * 8 + 15) / 16 * 16;
@@ -350,15 +353,10 @@ __global__ void __launch_bounds__(Sh::THREADS, Sh::CTAS) decode_int4_kernel(cons
   using T = Int4Tile<D>;
   constexpr int G = T::G, NT = Sh::NT, WR = Sh::WR, WB = Sh::WB, RING = Sh::RING, STEP = Sh::STEP, UNIT = STEP * T::STAGE,
                 NTHR = Sh::THREADS;
-  constexpr int QS = D * 2 + 16;
   constexpr float kNegInf = -INFINITY;
   extern __shared__ __align__(128) uint8_t smem[];
   const int R = a.rows;
   const Int4Smem lay = int4_smem<D, Sh>(R);
-  uint8_t* qs = smem + lay.qs;
-  float* rf_s = reinterpret_cast<float*>(smem + lay.rf);
-  float* qsum_s = reinterpret_cast<float*>(smem + lay.qsum);
-  unsigned long long* vis_s = reinterpret_cast<unsigned long long*>(smem + lay.vis);
   float* mrg_o = reinterpret_cast<float*>(smem + lay.mrg_o);
   float* mrg_m = reinterpret_cast<float*>(smem + lay.mrg_ml);
   float* mrg_l = mrg_m + WB * R;
@@ -371,10 +369,16 @@ __global__ void __launch_bounds__(Sh::THREADS, Sh::CTAS) decode_int4_kernel(cons
   const int wr = warp % WR, wb = warp / WR;
   const int i8 = lane >> 2, c4 = lane & 3;
   const int row_base = wr * 8 * NT;
+  constexpr int QS = D * 2 + 16;
+  uint8_t* qs = smem + lay.qs;
+  float* rf_s = reinterpret_cast<float*>(smem + lay.rf);
+  float* qsum_s = reinterpret_cast<float*>(smem + lay.qsum);
+  unsigned long long* vis_s = reinterpret_cast<unsigned long long*>(smem + lay.vis) + warp * 8 * NT;
 
-  // Padding rows: zero queries and factors.
-  for (int idx = tid; idx < Sh::ROWS * (QS / 16); idx += NTHR) reinterpret_cast<uint4*>(qs)[idx] = make_uint4(0, 0, 0, 0);
-  for (int idx = tid; idx < Sh::ROWS * (1 + G); idx += NTHR) rf_s[idx] = 0.f;
+  if constexpr (Sh::kShareQ) {   // padding rows: zero queries and factors
+    for (int idx = tid; idx < Sh::ROWS * (QS / 16); idx += NTHR) reinterpret_cast<uint4*>(qs)[idx] = make_uint4(0, 0, 0, 0);
+    for (int idx = tid; idx < Sh::ROWS * (1 + G); idx += NTHR) rf_s[idx] = 0.f;
+  }
 
   prefetch_plan_inputs(a.context_lens, a.block_tables, a.num_seqs, a.max_blocks_per_seq);
   // Everything below reads inputs a previous kernel in the stream may write.
@@ -533,82 +537,154 @@ __global__ void __launch_bounds__(Sh::THREADS, Sh::CTAS) decode_int4_kernel(cons
     }
     if (first && tid == 0 && (!rows_ok || ctx < n_s || ctx > cap) && a.status) atomicOr(a.status, kDevBadCtx);
 
-    // Query rows, one a warp: scaled to a largest element in [2^11, 2^12), the odd pairs of every
-    // word by 2^-4 more; their sums by group; the factor that undoes it all.
-    for (int r = warp; r < Rs; r += WR * WB) {
-      const int j = r / Gq, gi = r - j * Gq;
-      constexpr int E = D / 32;   // elements of a lane
-      const uint16_t* src = static_cast<const uint16_t*>(a.q) + (static_cast<size_t>(qb + j) * Hq + h * Gq + gi) * D + E * lane;
-      float x[E];
+    const int cb = ctx_eff - n_s;
+    // Element offset of a row of q and out: row r is query token r / Gq, query head h Gq + r % Gq.
+    auto row_at = [&](int r) {
+      const int j = r / Gq;
+      return (static_cast<size_t>(qb + j) * Hq + h * Gq + (r - j * Gq)) * D;
+    };
+
+    // Queries: lane (i8, c4) holds row i8's words 2 c4 and 2 c4 + 1 of every group, the B operand of S^T as they
+    // lie, scaled to the row's largest element in [2^11, 2^12), the odd pairs of a word by 2^-4 more.
+    uint32_t qf[NT][2 * G][4];   // word 2 c4 + x / G of group x % G
+    float rf[NT][2], qz[NT][G][2];   // rows 2 c4, 2 c4 + 1: the factor that undoes all scaling; sums by group
+    if constexpr (Sh::kShareQ) {
+      // One row a warp; the last piece's were read before its streams merged.
+#pragma unroll 2
+      for (int r = warp; r < Rs; r += WR * WB) {
+        const int j = r / Gq, gi = r - j * Gq;
+        constexpr int E = D / 32;   // elements of a lane
+        const uint16_t* src = static_cast<const uint16_t*>(a.q) + (static_cast<size_t>(qb + j) * Hq + h * Gq + gi) * D + E * lane;
+        float x[E];
 #pragma unroll
-      for (int e = 0; e < E; e += 2) {
-        const uint32_t w = *reinterpret_cast<const uint32_t*>(src + e);
-        if constexpr (BF16) {
-          x[e] = __uint_as_float(w << 16);
-          x[e + 1] = __uint_as_float(w & 0xFFFF0000u);
-        } else {
-          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
-          x[e] = f.x;
-          x[e + 1] = f.y;
+        for (int e = 0; e < E; e += 2) {
+          const uint32_t w = *reinterpret_cast<const uint32_t*>(src + e);
+          if constexpr (BF16) {
+            x[e] = __uint_as_float(w << 16);
+            x[e + 1] = __uint_as_float(w & 0xFFFF0000u);
+          } else {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+            x[e] = f.x;
+            x[e + 1] = f.y;
+          }
+        }
+        float mx = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) mx = fmaxf(mx, fabsf(x[e]));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        // 2^ex <= mx < 2^(ex + 1); rows beyond 2^+-100 keep a scale at which the factors are finite.
+        const int ex = max(-100, min(100, static_cast<int>(__float_as_uint(mx) >> 23) - 127));
+        const float up = __uint_as_float(static_cast<uint32_t>(127 + 11 - ex) << 23);
+        float sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          x[e] *= up;
+          sum += x[e];
+        }
+#pragma unroll
+        for (int o = 16 / G; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {
+          const float f = ((E * lane + e) >> 1) & 1 ? 0.0625f : 1.f;
+          *reinterpret_cast<uint32_t*>(qs + r * QS + (E * lane + e) * 2) = pack_f16x2(x[e] * f, x[e + 1] * f);
+        }
+        if (lane % (32 / G) == 0) qsum_s[r * G + lane / (32 / G)] = sum * 0x1p-24f;
+        if (lane == 0) rf_s[r] = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + 13 + ex) << 23);
+      }
+      __syncthreads();
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int x = 0; x < 2 * G; ++x) {
+          const uint4 v = *reinterpret_cast<const uint4*>(qs + (row_base + nt * 8 + i8) * QS +
+                                                          (kInt4Group * (x % G) + 8 * (2 * c4 + x / G)) * 2);
+          qf[nt][x][0] = v.x;
+          qf[nt][x][1] = v.y;
+          qf[nt][x][2] = v.z;
+          qf[nt][x][3] = v.w;
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = row_base + nt * 8 + 2 * c4 + e;
+          rf[nt][e] = rf_s[r];
+#pragma unroll
+          for (int g = 0; g < G; ++g) qz[nt][g][e] = qsum_s[r * G + g];
         }
       }
-      float mx = 0.f;
+    } else {
 #pragma unroll
-      for (int e = 0; e < E; ++e) mx = fmaxf(mx, fabsf(x[e]));
+      for (int nt = 0; nt < NT; ++nt) {
+        const int r = row_base + nt * 8 + i8;
+        float x[2 * G][8];
+        float mx = 0.f;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      // 2^ex <= mx < 2^(ex + 1); rows beyond 2^+-100 keep a scale at which the factors are finite.
-      const int ex = max(-100, min(100, static_cast<int>(__float_as_uint(mx) >> 23) - 127));
-      const float up = __uint_as_float(static_cast<uint32_t>(127 + 11 - ex) << 23);
-      float sum = 0.f;
+        for (int k = 0; k < 2 * G; ++k) {
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (r < Rs)
+            v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + row_at(r) + kInt4Group * (k % G) + 8 * (2 * c4 + k / G));
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        x[e] *= up;
-        sum += x[e];
+          for (int m = 0; m < 4; ++m) {
+            if constexpr (BF16) {
+              x[k][2 * m] = __uint_as_float(w[m] << 16);
+              x[k][2 * m + 1] = __uint_as_float(w[m] & 0xFFFF0000u);
+            } else {
+              const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[m]));
+              x[k][2 * m] = f.x;
+              x[k][2 * m + 1] = f.y;
+            }
+            mx = fmaxf(mx, fmaxf(fabsf(x[k][2 * m]), fabsf(x[k][2 * m + 1])));
+          }
+        }
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        // 2^ex <= mx < 2^(ex + 1); rows beyond 2^+-100 keep a scale at which the factors are finite.
+        const int ex = max(-100, min(100, static_cast<int>(__float_as_uint(mx) >> 23) - 127));
+        const float up = __uint_as_float(static_cast<uint32_t>(127 + 11 - ex) << 23);
+        float sum[G];
+#pragma unroll
+        for (int g = 0; g < G; ++g) sum[g] = 0.f;
+#pragma unroll
+        for (int k = 0; k < 2 * G; ++k)
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            const float x0 = x[k][2 * m] * up, x1 = x[k][2 * m + 1] * up, f = m & 1 ? 0.0625f : 1.f;
+            sum[k % G] += x0 + x1;
+            qf[nt][k][m] = pack_f16x2(x0 * f, x1 * f);
+          }
+        const float back = r < Rs ? a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + 13 + ex) << 23) : 0.f;
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 1);
+          sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 2);
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int from = 4 * (2 * c4 + e);
+          rf[nt][e] = __shfl_sync(0xffffffffu, back, from);
+#pragma unroll
+          for (int g = 0; g < G; ++g) qz[nt][g][e] = __shfl_sync(0xffffffffu, sum[g], from) * 0x1p-24f;
+        }
       }
-#pragma unroll
-      for (int o = 16 / G; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-#pragma unroll
-      for (int e = 0; e < E; e += 2) {
-        const float f = ((E * lane + e) >> 1) & 1 ? 0.0625f : 1.f;
-        *reinterpret_cast<uint32_t*>(qs + r * QS + (E * lane + e) * 2) = pack_f16x2(x[e] * f, x[e + 1] * f);
-      }
-      if (lane % (32 / G) == 0) qsum_s[r * G + lane / (32 / G)] = sum * 0x1p-24f;
-      if (lane == 0) rf_s[r] = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + 13 + ex) << 23);
     }
-    for (int r = tid; r < Sh::ROWS; r += NTHR) {   // the drafts that a row sees
-      const int j = r / Gq;
-      vis_s[r] = (a.tree_masks && r < Rs) ? a.tree_masks[qb + j] : ((j >= 63) ? ~0ull : ((2ull << j) - 1ull));
+    __syncwarp();
+    if (lane < 8 * NT) {   // the drafts that a row sees
+      const int r = row_base + lane, j = r / Gq;
+      vis_s[lane] = (a.tree_masks && r < Rs) ? a.tree_masks[qb + j] : ((j >= 63) ? ~0ull : ((2ull << j) - 1ull));
     }
-    __syncthreads();
+    __syncwarp();
 
-    uint32_t qf[NT][2 * G][4];   // word 2 c4 + x / G of group x % G
-    float rf[NT][2], qz[NT][G][2];
     float m_run[NT][2], l_run[NT][2];
     float o_acc[NT][G][4][4], o_bias[NT][G][4], o_z[NT][G][2];
-    const int cb = ctx_eff - n_s;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-      for (int x = 0; x < 2 * G; ++x) {
-        const uint4 v = *reinterpret_cast<const uint4*>(qs + (row_base + nt * 8 + i8) * QS +
-                                                        (kInt4Group * (x % G) + 8 * (2 * c4 + x / G)) * 2);
-        qf[nt][x][0] = v.x;
-        qf[nt][x][1] = v.y;
-        qf[nt][x][2] = v.z;
-        qf[nt][x][3] = v.w;
-      }
-#pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int r = row_base + nt * 8 + 2 * c4 + e;
-        rf[nt][e] = rf_s[r];
         m_run[nt][e] = kInt4Unset;
         l_run[nt][e] = 0.f;
 #pragma unroll
-        for (int g = 0; g < G; ++g) {
-          qz[nt][g][e] = qsum_s[r * G + g];
-          o_z[nt][g][e] = 0.f;
-        }
+        for (int g = 0; g < G; ++g) o_z[nt][g][e] = 0.f;
       }
 #pragma unroll
       for (int g = 0; g < G; ++g) {
@@ -696,7 +772,7 @@ __global__ void __launch_bounds__(Sh::THREADS, Sh::CTAS) decode_int4_kernel(cons
 #pragma unroll
               for (int g = 0; g < G; ++g) v = fmaf(sa[b][nt][g][2 * x + e], sk[g], v);
               sc[b][nt][2 * x + e] = v;
-              hid[b][nt][2 * x + e] = kMasked && !(there && (d < 0 || (d < 64 && ((vis_s[row_base + nt * 8 + 2 * c4 + e] >> d) & 1ull))));
+              hid[b][nt][2 * x + e] = kMasked && !(there && (d < 0 || (d < 64 && ((vis_s[nt * 8 + 2 * c4 + e] >> d) & 1ull))));
             }
         }
 
@@ -830,6 +906,7 @@ __global__ void __launch_bounds__(Sh::THREADS, Sh::CTAS) decode_int4_kernel(cons
     kk -= steps;
 
     // ---- merge the streams of this piece ----
+    if constexpr (!Sh::kShareQ) __syncthreads();   // every warp has left the last merge
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
