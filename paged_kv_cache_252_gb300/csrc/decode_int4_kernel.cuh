@@ -141,6 +141,13 @@ __device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&w)[N]) {
   }
 }
 
+// Steps after which the 8s come off the accumulators. The tensor core's accumulation cuts off what lies below its sum's last
+// bit, half of it a product on average; a result of n similar weights is some sqrt(n) times smaller than the sums of 8 P and c P,
+// so that many steps lose its bits (4 sequences of 131072 tokens: 6e-4 of the result, with 8 steps of two blocks less than 1e-4).
+#ifndef PKV_INT4_FLUSH
+#define PKV_INT4_FLUSH 8
+#endif
+constexpr int kInt4Flush = PKV_INT4_FLUSH;
 // The reference m of a row before any visible score: low enough to be left by any score.
 constexpr float kInt4Unset = -1e37f;
 constexpr float kInt4Shift = 11.f;     // P of the reference's own token: below 2^11
@@ -890,6 +897,7 @@ __global__ void __launch_bounds__(Sh::THREADS, Sh::CTAS) decode_int4_kernel(cons
     // The steps whose tokens every row sees come first.
     const int steps = (take + STEP - 1) / STEP;
     const int clear = min(take, max(cb, 0) / kBlockSize - lb) / STEP;
+    int since = 0;
 #pragma unroll 1
     for (; kk < steps; kk += WB) {
       cp_async_wait_groups<RING - 2>();
@@ -899,6 +907,19 @@ __global__ void __launch_bounds__(Sh::THREADS, Sh::CTAS) decode_int4_kernel(cons
         const int tok0 = (lb + kk * STEP) * kBlockSize;
         if (kk < clear) step(std::false_type{}, tok0, false);
         else step(std::true_type{}, tok0, kk * STEP + 1 == take);
+        if (++since == kInt4Flush) {
+          since = 0;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+#pragma unroll
+                for (int x = 0; x < 4; ++x) o_acc[nt][g][x][e] = fmaf(o_bias[nt][g][e], x & 1 ? -16.f : -1.f, o_acc[nt][g][x][e]);
+                o_bias[nt][g][e] = 0.f;
+              }
+        }
       }
       st_last = st;
       st = st + UNIT == ring_end ? ring : st + UNIT;
