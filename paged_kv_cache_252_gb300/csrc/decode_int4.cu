@@ -19,9 +19,10 @@ struct Entry {
   size_t smem;   // largest dynamic shared memory asked for so far; 0: not set up
   int ctas;      // resident CTAs at that size
 };
-Entry g_i4[kMaxDevices][2][4];   // [head size][rows]
+Entry g_i4[kMaxDevices][2][5];   // [head size][rows]
 
-int shape_index(int rows) { return rows <= 8 ? 0 : rows <= 16 ? 1 : rows <= 32 ? 2 : 3; }
+// One a kernel: two entries that share one would set its shared-memory limit in turn.
+int shape_index(int d, int rows) { return rows <= 4 && d == 128 ? 0 : rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 32 ? 3 : 4; }
 
 // Fixed cost of a unit's piece on the work line, in blocks.
 #ifndef PKV_PIECE_COST_INT4
@@ -36,11 +37,11 @@ int resident_ctas(int d, int rows, int* ctas) {
     cudaGetLastError();
     return PKV_ERR_NO_DEVICE;
   }
-  const int x = shape_index(rows);
+  const int x = shape_index(d, rows);
   std::lock_guard<std::mutex> lock(g_i4_mu);
   Entry& e = g_i4[dev][d == 128][x];
   if (e.smem == 0) {
-    const int most = 8 << x;
+    const int most = 4 << x;
     int least = 0;
     for (int bf16 = 0; bf16 < 2; ++bf16) {
       const DecodeInt4Kernel k = decode_int4_kernel_of(d, most, bf16 != 0);

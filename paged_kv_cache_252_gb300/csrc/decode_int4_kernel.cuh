@@ -54,8 +54,13 @@ struct Int4Tile {
 };
 
 // Warps, ring (in steps), CTAs an SM and blocks a step of the kernel for a row count.
-template <int NT_, int WR_, int WB_, int RING_, int CTAS_, int STEP_>
+template <int NT_, int WR_, int WB_, int RING_, int CTAS_, int STEP_, bool PAIR_ = false>
 struct Int4Shape {
+  // PAIR: units of at most 4 rows of two groups. A row takes two of the products' eight columns, r for the first group and
+  // r + 4 for the second, so that a lane holds scores, scales and weights of one group where it would hold those of two, half of
+  // them of padding rows.
+  static constexpr bool PAIR = PAIR_;
+  static_assert(!PAIR_ || (NT_ == 1 && WR_ == 1 && WB_ > 2), "pair");
   static constexpr int NT = NT_, WR = WR_, WB = WB_, RING = RING_, CTAS = CTAS_, STEP = STEP_;
   static_assert(RING >= 2 && (STEP == 1 || STEP == 2), "ring");
   static constexpr int ROWS = 8 * NT * WR, THREADS = 32 * WR * WB;
@@ -66,6 +71,9 @@ struct Int4Shape {
 #ifndef PKV_I4_R8
 #define PKV_I4_R8 1, 1, 4, 3, 3, 2
 #endif
+#ifndef PKV_I4_R4
+#define PKV_I4_R4 1, 1, 4, 3, 3, 2, true
+#endif
 #ifndef PKV_I4_R16
 #define PKV_I4_R16 2, 1, 4, 4, 2, 2
 #endif
@@ -75,6 +83,7 @@ struct Int4Shape {
 #ifndef PKV_I4_R64
 #define PKV_I4_R64 2, 4, 1, 5, 2, 2
 #endif
+using Int4Rows4 = Int4Shape<PKV_I4_R4>;
 using Int4Rows8 = Int4Shape<PKV_I4_R8>;
 using Int4Rows16 = Int4Shape<PKV_I4_R16>;
 using Int4Rows32 = Int4Shape<PKV_I4_R32>;
@@ -288,65 +297,64 @@ __device__ __forceinline__ bool int4_join(const DecodeArgs& a, int u, int c_firs
           ml[R + r] = L[e];
         }
       }
-      if (tid == 0) atomicAdd(ctr, 0ull - one * kids);   // clear for a replay
-      continue;
-    }
-    for (int r = tid; r < Rs; r += NTHR) {
-      float mc[kInt4Fan], lc[kInt4Fan], M = -INFINITY, L = 0.f;
+    } else {
+      for (int r = tid; r < Rs; r += NTHR) {
+        float mc[kInt4Fan], lc[kInt4Fan], M = -INFINITY, L = 0.f;
 #pragma unroll
-      for (int k = 0; k < kInt4Fan; ++k) {
-        const bool far = k < kids && k != own;
-        mc[k] = far ? __ldcg(base + k * step + r) : (k == own ? ml[r] : -INFINITY);
-        lc[k] = far ? __ldcg(base + k * step + R + r) : (k == own ? ml[R + r] : 0.f);
-        M = fmaxf(M, mc[k]);
+        for (int k = 0; k < kInt4Fan; ++k) {
+          const bool far = k < kids && k != own;
+          mc[k] = far ? __ldcg(base + k * step + r) : (k == own ? ml[r] : -INFINITY);
+          lc[k] = far ? __ldcg(base + k * step + R + r) : (k == own ? ml[R + r] : 0.f);
+          M = fmaxf(M, mc[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < kInt4Fan; ++k) {
+          const float f = fast_exp2(mc[k] - M);   // (M is finite)
+          L += f * lc[k];
+          fac[k * R + r] = f;
+        }
+        ml[r] = M;
+        ml[R + r] = L;
       }
-#pragma unroll
-      for (int k = 0; k < kInt4Fan; ++k) {
-        const float f = fast_exp2(mc[k] - M);   // (M is finite)
-        L += f * lc[k];
-        fac[k * R + r] = f;
-      }
-      ml[r] = M;
-      ml[R + r] = L;
-    }
-    __syncthreads();
-    // Four items of a thread at a time, a child's four loads in flight with the next child's.
+      __syncthreads();
+      // Four items of a thread at a time, a child's four loads in flight with the next child's.
 #pragma unroll 1
-    for (int x0 = tid; x0 < items; x0 += 4 * NTHR) {
-      float4 acc[4];
+      for (int x0 = tid; x0 < items; x0 += 4 * NTHR) {
+        float4 acc[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int e = 0; e < 4; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-      for (int k = 0; k < kids; k += 2) {
-        float4 v[2][4];
+        for (int k = 0; k < kids; k += 2) {
+          float4 v[2][4];
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+          for (int j = 0; j < 2; ++j)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int x = x0 + e * NTHR, r = x / (D / 4), d4 = x % (D / 4);
-            v[j][e] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (x < items && k + j < kids)
-              v[j][e] = k + j == own ? *reinterpret_cast<const float4*>(o + r * (D + 4) + d4 * 4)
-                                     : __ldcg(reinterpret_cast<const float4*>(base + (k + j) * step + ooff + r * D + d4 * 4));
-          }
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int x = x0 + e * NTHR;
-            if (x < items && k + j < kids) {
-              const float f = fac[(k + j) * R + x / (D / 4)];
-              acc[e].x += f * v[j][e].x;
-              acc[e].y += f * v[j][e].y;
-              acc[e].z += f * v[j][e].z;
-              acc[e].w += f * v[j][e].w;
+            for (int e = 0; e < 4; ++e) {
+              const int x = x0 + e * NTHR, r = x / (D / 4), d4 = x % (D / 4);
+              v[j][e] = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (x < items && k + j < kids)
+                v[j][e] = k + j == own ? *reinterpret_cast<const float4*>(o + r * (D + 4) + d4 * 4)
+                                       : __ldcg(reinterpret_cast<const float4*>(base + (k + j) * step + ooff + r * D + d4 * 4));
             }
-          }
-      }
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int x = x0 + e * NTHR, r = x / (D / 4), d4 = x % (D / 4);
-        if (x < items) *reinterpret_cast<float4*>(o + r * (D + 4) + d4 * 4) = acc[e];
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int x = x0 + e * NTHR;
+              if (x < items && k + j < kids) {
+                const float f = fac[(k + j) * R + x / (D / 4)];
+                acc[e].x += f * v[j][e].x;
+                acc[e].y += f * v[j][e].y;
+                acc[e].z += f * v[j][e].z;
+                acc[e].w += f * v[j][e].w;
+              }
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int x = x0 + e * NTHR, r = x / (D / 4), d4 = x % (D / 4);
+          if (x < items) *reinterpret_cast<float4*>(o + r * (D + 4) + d4 * 4) = acc[e];
+        }
       }
     }
     if (tid == 0) atomicAdd(ctr, 0ull - one * kids);   // clear for a replay
@@ -360,6 +368,8 @@ __global__ void __launch_bounds__(Sh::THREADS, Sh::CTAS) decode_int4_kernel(cons
   using T = Int4Tile<D>;
   constexpr int G = T::G, NT = Sh::NT, WR = Sh::WR, WB = Sh::WB, RING = Sh::RING, STEP = Sh::STEP, UNIT = STEP * T::STAGE,
                 NTHR = Sh::THREADS;
+  constexpr bool PAIR = Sh::PAIR;
+  constexpr int GS = PAIR ? 1 : G;   // groups whose scales and weights a lane holds
   constexpr float kNegInf = -INFINITY;
   extern __shared__ __align__(128) uint8_t smem[];
   const int R = a.rows;
@@ -376,6 +386,8 @@ __global__ void __launch_bounds__(Sh::THREADS, Sh::CTAS) decode_int4_kernel(cons
   const int wr = warp % WR, wb = warp / WR;
   const int i8 = lane >> 2, c4 = lane & 3;
   const int row_base = wr * 8 * NT;
+  const int row2 = PAIR ? 2 * (c4 & 1) : 2 * c4;   // first of the two rows of a lane's columns of n-tile 0
+  const int own_g = PAIR ? c4 >> 1 : 0;            // PAIR: the columns' group
   constexpr int QS = D * 2 + 16;
   uint8_t* qs = smem + lay.qs;
   float* rf_s = reinterpret_cast<float*>(smem + lay.rf);
@@ -517,7 +529,7 @@ __global__ void __launch_bounds__(Sh::THREADS, Sh::CTAS) decode_int4_kernel(cons
     return T::TILE + (D == 128 ? t * 64 + (((i8 >> 1) ^ (t & 2)) << 4) + 8 * (i8 & 1) : t * 32 + 4 * i8);
   };
   const uint32_t v_off0 = v_off(tv0), v_off1 = v_off(tv1);
-  const uint32_t m_off = 2 * T::TILE + tok * 4 * G;
+  const uint32_t m_off = 2 * T::TILE + tok * 4 * G + 4 * own_g;
 
   // The stream's next step: where its blocks lie and where the last one's lay; its index in the piece.
   uint32_t st = ring, st_last = ring_end - UNIT;
@@ -554,7 +566,7 @@ __global__ void __launch_bounds__(Sh::THREADS, Sh::CTAS) decode_int4_kernel(cons
     // Queries: lane (i8, c4) holds row i8's words 2 c4 and 2 c4 + 1 of every group, the B operand of S^T as they
     // lie, scaled to the row's largest element in [2^11, 2^12), the odd pairs of a word by 2^-4 more.
     uint32_t qf[NT][2 * G][4];   // word 2 c4 + x / G of group x % G
-    float rf[NT][2], qz[NT][G][2];   // rows 2 c4, 2 c4 + 1: the factor that undoes all scaling; sums by group
+    float rf[NT][2], qz[NT][GS][2];   // rows row2, row2 + 1: the factor that undoes all scaling; sums by group
     if constexpr (Sh::kShareQ) {
       // One row a warp; the last piece's were read before its streams merged.
 #pragma unroll 2
@@ -604,8 +616,9 @@ __global__ void __launch_bounds__(Sh::THREADS, Sh::CTAS) decode_int4_kernel(cons
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
         for (int x = 0; x < 2 * G; ++x) {
-          const uint4 v = *reinterpret_cast<const uint4*>(qs + (row_base + nt * 8 + i8) * QS +
-                                                          (kInt4Group * (x % G) + 8 * (2 * c4 + x / G)) * 2);
+          const int r = PAIR ? i8 & 3 : row_base + nt * 8 + i8;
+          uint4 v = *reinterpret_cast<const uint4*>(qs + r * QS + (kInt4Group * (x % G) + 8 * (2 * c4 + x / G)) * 2);
+          if (PAIR && (i8 >> 2) != x % G) v = make_uint4(0, 0, 0, 0);
           qf[nt][x][0] = v.x;
           qf[nt][x][1] = v.y;
           qf[nt][x][2] = v.z;
@@ -613,10 +626,10 @@ __global__ void __launch_bounds__(Sh::THREADS, Sh::CTAS) decode_int4_kernel(cons
         }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int r = row_base + nt * 8 + 2 * c4 + e;
+          const int r = row_base + nt * 8 + row2 + e;
           rf[nt][e] = rf_s[r];
 #pragma unroll
-          for (int g = 0; g < G; ++g) qz[nt][g][e] = qsum_s[r * G + g];
+          for (int g = 0; g < GS; ++g) qz[nt][g][e] = qsum_s[r * G + (PAIR ? own_g : g)];
         }
       }
     } else {
@@ -683,7 +696,7 @@ __global__ void __launch_bounds__(Sh::THREADS, Sh::CTAS) decode_int4_kernel(cons
     __syncwarp();
 
     float m_run[NT][2], l_run[NT][2];
-    float o_acc[NT][G][4][4], o_bias[NT][G][4], o_z[NT][G][2];
+    float o_acc[NT][G][4][4], o_bias[NT][GS][4], o_z[NT][GS][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -691,13 +704,13 @@ __global__ void __launch_bounds__(Sh::THREADS, Sh::CTAS) decode_int4_kernel(cons
         m_run[nt][e] = kInt4Unset;
         l_run[nt][e] = 0.f;
 #pragma unroll
-        for (int g = 0; g < G; ++g) o_z[nt][g][e] = 0.f;
+        for (int g = 0; g < GS; ++g) o_z[nt][g][e] = 0.f;
       }
 #pragma unroll
       for (int g = 0; g < G; ++g) {
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          o_bias[nt][g][x] = 0.f;
+          if (g < GS) o_bias[nt][g][x] = 0.f;
 #pragma unroll
           for (int e = 0; e < 4; ++e) o_acc[nt][g][x][e] = 0.f;
         }
@@ -712,16 +725,16 @@ __global__ void __launch_bounds__(Sh::THREADS, Sh::CTAS) decode_int4_kernel(cons
       const uint32_t at[2] = {st, st + T::STAGE};
       // ---- S^T (16 tokens x 8 NT rows a block), one accumulator a group ----
       float sa[NB][NT][G][4];
-      uint32_t mk[NB][2][G], mv[NB][2][G];
+      uint32_t mk[NB][2][GS], mv[NB][2][GS];
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         uint32_t ka[2 * G], kb[2 * G];
         lds_words<2 * G>(at[b] + k_off, ka);
         lds_words<2 * G>(at[b] + k_off + 8 * T::RB, kb);
-        lds_words<G>(at[b] + m_off, mk[b][0]);
-        lds_words<G>(at[b] + m_off + 32 * G, mk[b][1]);
-        lds_words<G>(at[b] + m_off + 64 * G, mv[b][0]);
-        lds_words<G>(at[b] + m_off + 96 * G, mv[b][1]);
+        lds_words<GS>(at[b] + m_off, mk[b][0]);
+        lds_words<GS>(at[b] + m_off + 32 * G, mk[b][1]);
+        lds_words<GS>(at[b] + m_off + 64 * G, mv[b][0]);
+        lds_words<GS>(at[b] + m_off + 96 * G, mv[b][1]);
 #pragma unroll
         for (int x = 0; x < 2 * G; ++x) {
 #pragma unroll
@@ -730,11 +743,18 @@ __global__ void __launch_bounds__(Sh::THREADS, Sh::CTAS) decode_int4_kernel(cons
             const uint32_t a0 = wa & 0x000F000Fu, a1 = wb2 & 0x000F000Fu, a2 = wa & 0x00F000F0u, a3 = wb2 & 0x00F000F0u;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              if (x < G && hf == 0) mma_new(sa[b][nt][x % G], a0, a1, a2, a3, qf[nt][x][2 * hf], qf[nt][x][2 * hf + 1]);
-              else mma_acc(sa[b][nt][x % G], a0, a1, a2, a3, qf[nt][x][2 * hf], qf[nt][x][2 * hf + 1]);
+              float(&acc)[4] = sa[b][nt][PAIR ? hf : x % G];   // (PAIR: two chains, added below)
+              if (PAIR ? x == 0 : (x < G && hf == 0)) mma_new(acc, a0, a1, a2, a3, qf[nt][x][2 * hf], qf[nt][x][2 * hf + 1]);
+              else mma_acc(acc, a0, a1, a2, a3, qf[nt][x][2 * hf], qf[nt][x][2 * hf + 1]);
             }
           }
         }
+      }
+      if constexpr (PAIR) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int v = 0; v < 4; ++v) sa[b][0][0][v] += sa[b][0][G - 1][v];
       }
       // (the V words, ahead of the scores' arithmetic)
       uint32_t w[NB][4][G];
@@ -747,16 +767,16 @@ __global__ void __launch_bounds__(Sh::THREADS, Sh::CTAS) decode_int4_kernel(cons
       }
 
       // ---- scales; scores before the row's factor ----
-      float sv[NB][2][G], zv[NB][2][G];
+      float sv[NB][2][GS], zv[NB][2][GS];
       float sc[NB][NT][4];   // [2 x + e]: token tok + 8 x, row 2 c4 + e
       bool hid[NB][NT][4];   // (all false without a mask)
 #pragma unroll
       for (int b = 0; b < NB; ++b)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          float sk[G], zk[G];
+          float sk[GS], zk[GS];
 #pragma unroll
-          for (int g = 0; g < G; ++g) {
+          for (int g = 0; g < GS; ++g) {
             const float2 fk = __half22float2(*reinterpret_cast<const __half2*>(&mk[b][x][g]));
             const float2 fv = __half22float2(*reinterpret_cast<const __half2*>(&mv[b][x][g]));
             sk[g] = fk.x;
@@ -768,24 +788,25 @@ __global__ void __launch_bounds__(Sh::THREADS, Sh::CTAS) decode_int4_kernel(cons
           const bool there = !kMasked || (d < n_s && !(b == 1 && absent));
           if (!there) {   // behind the context: whatever lies there
 #pragma unroll
-            for (int g = 0; g < G; ++g) sv[b][x][g] = zv[b][x][g] = 0.f;
+            for (int g = 0; g < GS; ++g) sv[b][x][g] = zv[b][x][g] = 0.f;
           }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               float v = zk[0] * qz[nt][0][e];
-              if constexpr (G == 2) v = fmaf(zk[1], qz[nt][1][e], v);
+              if constexpr (GS == 2) v = fmaf(zk[1], qz[nt][1][e], v);
 #pragma unroll
-              for (int g = 0; g < G; ++g) v = fmaf(sa[b][nt][g][2 * x + e], sk[g], v);
+              for (int g = 0; g < GS; ++g) v = fmaf(sa[b][nt][g][2 * x + e], sk[g], v);
+              if constexpr (PAIR) v += __shfl_xor_sync(0xffffffffu, v, 2);   // the other group's part
               sc[b][nt][2 * x + e] = v;
-              hid[b][nt][2 * x + e] = kMasked && !(there && (d < 0 || (d < 64 && ((vis_s[nt * 8 + 2 * c4 + e] >> d) & 1ull))));
+              hid[b][nt][2 * x + e] = kMasked && !(there && (d < 0 || (d < 64 && ((vis_s[nt * 8 + row2 + e] >> d) & 1ull))));
             }
         }
 
       // ---- weights p = 2^(score - m) and P = p s; the reference moved where one is too large ----
       float p[NB][NT][4];
-      uint32_t ph[NB][NT][G][2];   // P of a token's two rows
+      uint32_t ph[NB][NT][GS][2];   // P of a token's two rows
       auto weights = [&]() {
         float far = 0.f;
         __half2 top = __half2half2(__ushort_as_half(0));
@@ -800,7 +821,7 @@ __global__ void __launch_bounds__(Sh::THREADS, Sh::CTAS) decode_int4_kernel(cons
             }
             far = fmaxf(far, fmaxf(p[b][nt][0] + p[b][nt][2], p[b][nt][1] + p[b][nt][3]));
 #pragma unroll
-            for (int g = 0; g < G; ++g)
+            for (int g = 0; g < GS; ++g)
 #pragma unroll
               for (int x = 0; x < 2; ++x) {
                 float P0 = p[b][nt][2 * x] * sv[b][x][g], P1 = p[b][nt][2 * x + 1] * sv[b][x][g];
@@ -819,7 +840,8 @@ __global__ void __launch_bounds__(Sh::THREADS, Sh::CTAS) decode_int4_kernel(cons
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             ve[b][x] = int4_scale_exponent(sv[b][x][0]);
-            if constexpr (G == 2) ve[b][x] = fmaxf(ve[b][x], int4_scale_exponent(sv[b][x][1]));
+            if constexpr (GS == 2) ve[b][x] = fmaxf(ve[b][x], int4_scale_exponent(sv[b][x][1]));
+            if constexpr (PAIR) ve[b][x] = fmaxf(ve[b][x], __shfl_xor_sync(0xffffffffu, ve[b][x], 2));
           }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -840,9 +862,11 @@ __global__ void __launch_bounds__(Sh::THREADS, Sh::CTAS) decode_int4_kernel(cons
             l_run[nt][e] *= alpha;
 #pragma unroll
             for (int g = 0; g < G; ++g) {
-              o_z[nt][g][e] *= alpha;
-              o_bias[nt][g][e] *= alpha;
-              o_bias[nt][g][2 + e] *= alpha;
+              if (g < GS) {
+                o_z[nt][g][e] *= alpha;
+                o_bias[nt][g][e] *= alpha;
+                o_bias[nt][g][2 + e] *= alpha;
+              }
 #pragma unroll
               for (int x = 0; x < 4; ++x) {
                 o_acc[nt][g][x][e] *= alpha;
@@ -856,13 +880,13 @@ __global__ void __launch_bounds__(Sh::THREADS, Sh::CTAS) decode_int4_kernel(cons
       // ---- O^T (dimensions x rows) += V^T P^T ----
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        uint32_t pb[NT][G][2];
+        uint32_t pb[NT][GS][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
           for (int e = 0; e < 2; ++e) l_run[nt][e] += p[b][nt][e] + p[b][nt][2 + e];
 #pragma unroll
-          for (int g = 0; g < G; ++g) {
+          for (int g = 0; g < GS; ++g) {
 #pragma unroll
             for (int v = 0; v < 4; ++v) {
               if (kMasked && hid[b][nt][v]) continue;
@@ -885,8 +909,9 @@ __global__ void __launch_bounds__(Sh::THREADS, Sh::CTAS) decode_int4_kernel(cons
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
               mma_acc(o_acc[nt][g][x], (x01 >> sh) & keep, (y01 >> sh) & keep, (x23 >> sh) & keep, (y23 >> sh) & keep,
-                      pb[nt][g][0], pb[nt][g][1]);
+                      pb[nt][PAIR ? 0 : g][0], pb[nt][PAIR ? 0 : g][1]);
           }
+          if (g >= GS) continue;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)   // 8 in every element
             mma_acc(o_bias[nt][g], 0x00080008u, 0x00080008u, 0x00080008u, 0x00080008u, pb[nt][g][0], pb[nt][g][1]);
@@ -912,13 +937,15 @@ __global__ void __launch_bounds__(Sh::THREADS, Sh::CTAS) decode_int4_kernel(cons
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int g = 0; g < G; ++g)
+            for (int e = 0; e < 4; ++e) {
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
+              for (int g = 0; g < G; ++g)
 #pragma unroll
-                for (int x = 0; x < 4; ++x) o_acc[nt][g][x][e] = fmaf(o_bias[nt][g][e], x & 1 ? -16.f : -1.f, o_acc[nt][g][x][e]);
-                o_bias[nt][g][e] = 0.f;
-              }
+                for (int x = 0; x < 4; ++x)
+                  o_acc[nt][g][x][e] = fmaf(o_bias[nt][PAIR ? 0 : g][e], x & 1 ? -16.f : -1.f, o_acc[nt][g][x][e]);
+#pragma unroll
+              for (int g = 0; g < GS; ++g) o_bias[nt][g][e] = 0.f;
+            }
         }
       }
       st_last = st;
@@ -932,27 +959,27 @@ __global__ void __launch_bounds__(Sh::THREADS, Sh::CTAS) decode_int4_kernel(cons
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int r = row_base + nt * 8 + 2 * c4 + e;
+        const int r = row_base + nt * 8 + row2 + e;
         float lsum = l_run[nt][e];
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) lsum += __shfl_xor_sync(0xffffffffu, lsum, o);
-        if (i8 == 0 && r < R) {
+        if (i8 == 0 && own_g == 0 && r < R) {
           mrg_m[wb * R + r] = m_run[nt][e];
           mrg_l[wb * R + r] = lsum;
         }
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-          float z = o_z[nt][g][e];
+          float z = o_z[nt][PAIR ? 0 : g][e];
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
           float y[8];
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
             const float f = x & 1 ? 0.0625f : 1.f;
-            y[2 * x] = fmaf(fmaf(o_acc[nt][g][x][e], f, -o_bias[nt][g][e]), 0x1p24f, z);
-            y[2 * x + 1] = fmaf(fmaf(o_acc[nt][g][x][2 + e], f, -o_bias[nt][g][e]), 0x1p24f, z);
+            y[2 * x] = fmaf(fmaf(o_acc[nt][g][x][e], f, -o_bias[nt][PAIR ? 0 : g][e]), 0x1p24f, z);
+            y[2 * x + 1] = fmaf(fmaf(o_acc[nt][g][x][2 + e], f, -o_bias[nt][PAIR ? 0 : g][e]), 0x1p24f, z);
           }
-          if (r < R) {
+          if (r < R && (!PAIR || g == own_g)) {
             float4* mo = reinterpret_cast<float4*>(mrg_o + static_cast<size_t>(wb * R + r) * (D + 4) + kInt4Group * g + 8 * i8);
             mo[0] = make_float4(y[0], y[1], y[2], y[3]);
             mo[1] = make_float4(y[4], y[5], y[6], y[7]);
@@ -1034,6 +1061,7 @@ DecodeInt4Kernel int4_kernel(int d, int rows) {
 }
 template <bool BF16>
 DecodeInt4Kernel int4_kernel_for(int d, int rows) {
+  if (rows <= 4 && d == 128) return int4_kernel<128, Int4Rows4, BF16>(rows);
   if (rows <= 8) return int4_kernel<BF16, Int4Rows8>(d, rows);
   if (rows <= 16) return int4_kernel<BF16, Int4Rows16>(d, rows);
   if (rows <= 32) return int4_kernel<BF16, Int4Rows32>(d, rows);

@@ -257,3 +257,44 @@ def test_a_workspace_full_of_small_numbers():
     for fill in (0, 1, 7, -1):
         ws = torch.full((need // 4 + 64,), fill, dtype=torch.int32, device=DEV)
         assert torch.equal(c.fixed(workspace=ws), want)
+
+
+@pytest.mark.parametrize("hq", [2, 8, 16, 32, 64])
+def test_one_unit_over_the_whole_device(hq):
+    """Every CTA has a piece of one unit: a join of several levels, and again from a replayed graph."""
+    c = Case([262144 - 5], hq, 1, 128, torch.bfloat16, seed=hq)
+    i4.assert_within(c.fixed(), *c.want())
+    want = c.fixed()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = c.fixed()
+    for _ in range(5):
+        out.zero_()
+        g.replay()
+        assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("hq", [4, 32])
+def test_long_contexts_keep_the_results_bits(hq):
+    """Over n similar weights the result is some sqrt(n) times smaller than the sums of codes times weights. A rounding to fp16 of
+    a number with mantissa m in [1, 2) has the relative variance (2^-20 / 12) / m^2. The outputs' mantissas take all values (evenly
+    in log m: the mean of 1 / m^2 is 3 / (8 ln 2) = 0.541); the weights P may all lie near m = 1. Both roundings together have at most
+    1 + 1 / 0.541 = 2.85 times the variance of the output's alone, 3.1 = 1.76^2 times with all else half an output's rounding."""
+    c = Case([131072], hq, 1, 128, torch.float16, seed=hq)
+    c.q *= 0.25
+    want, _ = c.want()
+    alone = (want.half().double() - want).norm()
+    assert (c.fixed().double() - want).norm() <= 1.76 * alone
+
+
+@pytest.mark.parametrize("g,n", [(2, 1), (4, 1), (8, 1), (4, 4), (8, 4), (8, 8)])
+def test_a_spoilt_group_spoils_its_own_dimensions(g, n):
+    """A value group that read back as NaN makes NaN of its 64 dimensions in the rows that see it; the other 64 stay within the bound."""
+    c = Case([40, 700], 2 * g, 2, 128, torch.float16, n=n, seed=g)
+    for s, at in ((0, 3), (1, 500)):
+        c.sc[int(c.tables[s, at // 16]), :, 1, at % 16, s, 0] = math.nan
+    out, (want, tol) = c.fixed(), c.want()
+    rows = c.cu[1]
+    for part, bad, good in ((slice(0, rows), slice(0, 64), slice(64, 128)), (slice(rows, None), slice(64, 128), slice(0, 64))):
+        assert out[part, :, bad].isnan().all()
+        i4.assert_within(out[part, :, good], want[part, :, good], tol[part, :, good])
