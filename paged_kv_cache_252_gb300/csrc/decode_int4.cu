@@ -24,10 +24,9 @@ Entry g_i4[kMaxDevices][2][5];   // [head size][rows]
 // One a kernel: two entries that share one would set its shared-memory limit in turn.
 int shape_index(int d, int rows) { return rows <= 4 && d == 128 ? 0 : rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 32 ? 3 : 4; }
 
-// Fixed cost of a unit's piece on the work line, in blocks.
-#ifndef PKV_PIECE_COST_INT4
-#define PKV_PIECE_COST_INT4 32
-#endif
+// Fixed cost of a unit's piece on the work line, in blocks: 12 leaves 64 sequences at 35 us and 32 rows at 405, 20 at 31 and
+// 351, 32 at 30 and 336, 56 at 31 and 350.
+constexpr int kPieceCostInt4 = 32;
 
 // Once per device, head size and shape: shared-memory limits of both query types' kernels and the CTAs an
 // SM holds (of the shape's largest row count, so that one workspace size serves the shape).
@@ -155,7 +154,7 @@ extern "C" int pkv_paged_attention_decode_int4(void* out, const void* q, pkv_dty
   a.slot_floats = partial_slot_floats(rows, d);
   a.scale_log2 = scale * 1.4426950408889634f;
   a.epoch = next_call_epoch();
-  a.piece_cost = PKV_PIECE_COST_INT4;
+  a.piece_cost = kPieceCostInt4;
   a.k_cache = static_cast<const uint8_t*>(k_cache);
   a.v_cache = static_cast<const uint8_t*>(v_cache);
   a.meta = static_cast<const uint8_t*>(scales);

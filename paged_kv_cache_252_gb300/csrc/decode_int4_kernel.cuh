@@ -12,7 +12,7 @@
 // bits above them c 2^-20, so one AND makes a pair of operands. The 2^-24 is exact and comes off in
 // fp32; where a pair is 16 times too large, q is stored 16 times smaller (K) or the output
 // row is scaled at the end (V). The 8 is taken off by a product with a constant operand, over the same
-// rounded P.
+// rounded P, every few steps.
 //
 // Precision. q is scaled by a power of two per row so that its largest element lies in [2^11, 2^12):
 // fp16 then holds fp16 and bf16 queries (8 significant bits) exactly down to 2^-26 of the
@@ -22,11 +22,18 @@
 // zero scale) passes the limit: a rare, warp-wide event.
 //
 // Structure of a CTA: WR x WB warps. Row warp wr has 8 NT of the unit's rows; stream wb takes every
-// WB-th block of the share through a ring of its own of STAGES blocks, filled by cp.async of the stream's
-// own warps (no producer warp: at 2.3 KB a block one issuing thread would bound the CTA).
+// WB-th step of STEP blocks of the share through a ring of its own of RING steps, filled by cp.async of the
+// stream's own warps (no producer warp: at 2.3 KB a block one issuing thread would bound the CTA).
 // A lane's K words of a token (neighbouring 16 bytes) are the A operand of S^T = K Q^T as they
 // lie; V words of two tokens are paired by byte permutes for O^T = V^T P^T. The tokens of a
 // block take the 16 product slots in an order in which both reads hit all banks.
+//
+// What bounds it. One query token of 4 heads a KV head: instructions, 253 a warp and block (64 of them the ANDs that
+// unpack), issued on 52 % of the cycles with three warps a scheduler, most stalls on fixed latencies: 4 sequences of 131072
+// tokens take 98 us, 5.25 TB/s, 78 % of the copy rate, where the bytes alone take 77. 32 rows: 732 instructions a
+// block over its two row warps and two warps a scheduler: 343 us where the bytes take 95 and the products 37. A tcgen05 form for more
+// than 16 rows (a token a thread, codes unpacked to tensor memory, a product a group and exact scales on the scores) took as
+// many instructions, 777, and 408 us; so did sixteen warps in place of eight.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -58,7 +65,7 @@ template <int NT_, int WR_, int WB_, int RING_, int CTAS_, int STEP_, bool PAIR_
 struct Int4Shape {
   // PAIR: units of at most 4 rows of two groups. A row takes two of the products' eight columns, r for the first group and
   // r + 4 for the second, so that a lane holds scores, scales and weights of one group where it would hold those of two, half of
-  // them of padding rows.
+  // them of padding rows: 253 instructions a block in place of 272, 4 x 131072 tokens 98 us in place of 101.
   static constexpr bool PAIR = PAIR_;
   static_assert(!PAIR_ || (NT_ == 1 && WR_ == 1 && WB_ > 2), "pair");
   static constexpr int NT = NT_, WR = WR_, WB = WB_, RING = RING_, CTAS = CTAS_, STEP = STEP_;
@@ -68,26 +75,14 @@ struct Int4Shape {
   // more by sharing than the barrier costs (64 sequences 30.5 us against 32.0), two do not (32 rows: 348 against 336).
   static constexpr bool kShareQ = WB > 2;
 };
-#ifndef PKV_I4_R8
-#define PKV_I4_R8 1, 1, 4, 3, 3, 2
-#endif
-#ifndef PKV_I4_R4
-#define PKV_I4_R4 1, 1, 4, 3, 3, 2, true
-#endif
-#ifndef PKV_I4_R16
-#define PKV_I4_R16 2, 1, 4, 4, 2, 2
-#endif
-#ifndef PKV_I4_R32
-#define PKV_I4_R32 2, 2, 2, 5, 2, 2
-#endif
-#ifndef PKV_I4_R64
-#define PKV_I4_R64 2, 4, 1, 5, 2, 2
-#endif
-using Int4Rows4 = Int4Shape<PKV_I4_R4>;
-using Int4Rows8 = Int4Shape<PKV_I4_R8>;
-using Int4Rows16 = Int4Shape<PKV_I4_R16>;
-using Int4Rows32 = Int4Shape<PKV_I4_R32>;
-using Int4Rows64 = Int4Shape<PKV_I4_R64>;
+// Two blocks a step against one: 4 rows 30.0 against 31.3 us (64 sequences), 8 rows 76 against 85, 16 rows 116 against 122, 32
+// rows 343 against 409. A row count takes the smallest shape that holds it (on the next one: 8 rows 107 us, 16 rows 145,
+// 32 rows 648). Rings and CTAs an SM: as many CTAs as the registers allow, and the deepest ring beside them.
+using Int4Rows4 = Int4Shape<1, 1, 4, 3, 3, 2, true>;
+using Int4Rows8 = Int4Shape<1, 1, 4, 3, 3, 2>;
+using Int4Rows16 = Int4Shape<2, 1, 4, 4, 2, 2>;
+using Int4Rows32 = Int4Shape<2, 2, 2, 5, 2, 2>;
+using Int4Rows64 = Int4Shape<2, 4, 1, 5, 2, 2>;
 
 // The walk of a stream's fetching, kept in shared memory: read once for up to 32 blocks.
 struct Int4Walk {
@@ -153,10 +148,8 @@ __device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&w)[N]) {
 // Steps after which the 8s come off the accumulators. The tensor core's accumulation cuts off what lies below its sum's last
 // bit, half of it a product on average; a result of n similar weights is some sqrt(n) times smaller than the sums of 8 P and c P,
 // so that many steps lose its bits (4 sequences of 131072 tokens: 6e-4 of the result, with 8 steps of two blocks less than 1e-4).
-#ifndef PKV_INT4_FLUSH
-#define PKV_INT4_FLUSH 8
-#endif
-constexpr int kInt4Flush = PKV_INT4_FLUSH;
+// Costs 2 % (99 -> 101 us).
+constexpr int kInt4Flush = 8;
 // The reference m of a row before any visible score: low enough to be left by any score.
 constexpr float kInt4Unset = -1e37f;
 constexpr float kInt4Shift = 11.f;     // P of the reference's own token: below 2^11
