@@ -234,7 +234,7 @@ def _scales_shape(k_cache, scales, code=KV_INT8):
     if code == KV_INT4:
         nb, hkv, _, half = k_cache.shape
         want = (nb, hkv, 2, BLOCK_SIZE, half // 32, 2)
-        if tuple(scales.shape) != want or scales.dtype != torch.float16:
+        if scales.shape != want or scales.dtype is not torch.float16:
             raise PagedKVError(f"scales must be float16 {want} (scale and least value of every 64 dimensions)")
         return
     want = (int(k_cache.shape[0]), int(k_cache.shape[1]), 2, BLOCK_SIZE)
@@ -719,8 +719,9 @@ def _placed(names, tensors) -> int:
     that serve single steps check placement, types and shapes in few attribute reads each: on
     the host they cost as much as the kernels."""
     dev = tensors[0].get_device()
-    for n, t in zip(names, tensors):
+    for t in tensors:
         if t is not None and (t.get_device() != dev or dev < 0 or not t.is_contiguous()):
+            n = next(n for n, x in zip(names, tensors) if x is t)
             _need_cuda_contig(n, t)
             raise PagedKVError(f"{n} is on {t.device}, not on {tensors[0].device}")
     return dev
@@ -787,9 +788,21 @@ def _stream_of(stream, dev: int) -> int:
     return torch.cuda.current_stream(dev).cuda_stream
 
 
+# (With a CUDA tensor at hand the device runtime is up: torch.cuda.current_device without its checks.)
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _at(dev: int):
     """The device context of a call: entered only when dev is not the current device."""
-    return _NOWHERE if torch.cuda.current_device() == dev else torch.cuda.device(dev)
+    return _NOWHERE if _device() == dev else torch.cuda.device(dev)
+
+
+def _call(dev: int, fn, *args) -> int:
+    """fn(*args) on device dev."""
+    if _device() == dev:
+        return fn(*args)
+    with torch.cuda.device(dev):
+        return fn(*args)
 
 
 _NOWHERE = contextlib.nullcontext()
@@ -1042,11 +1055,9 @@ def kv_cache_write_int4(key, value, slot_mapping, k_cache, v_cache, scales, *, d
     T = _row_shapes(key, value, slot_mapping, hkv, head)
     _scales_shape(k_cache, scales, KV_INT4)
     _status_word(device_status)
-    lib = _lib or load_library()
-    with _at(dev):
-        rc = lib.pkv_kv_cache_write_int4(
-            key.data_ptr(), value.data_ptr(), _src_code(key), T, slot_mapping.data_ptr(), k_cache.data_ptr(),
-            v_cache.data_ptr(), scales.data_ptr(), desc, _addr(device_status), _stream_of(stream, dev))
+    rc = _call(dev, (_lib or load_library()).pkv_kv_cache_write_int4, key.data_ptr(), value.data_ptr(), _src_code(key), T,
+               slot_mapping.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), scales.data_ptr(), desc, _addr(device_status),
+               _stream_of(stream, dev))
     if rc:
         _check(rc, "kv_cache_write_int4")
 
@@ -1062,11 +1073,9 @@ def kv_cache_read(key, value, slot_mapping, k_cache, v_cache, kv_dtype=None, *, 
     T = _row_shapes(key, value, slot_mapping, hkv, head)
     _int8_scales(code, k_cache, scales)
     _status_word(device_status)
-    lib = _lib or load_library()
-    with _at(dev):
-        rc = lib.pkv_kv_cache_read(
-            key.data_ptr(), value.data_ptr(), _src_code(key), T, slot_mapping.data_ptr(), k_cache.data_ptr(),
-            v_cache.data_ptr(), _addr(scales), code, desc, _addr(device_status), _stream_of(stream, dev))
+    rc = _call(dev, (_lib or load_library()).pkv_kv_cache_read, key.data_ptr(), value.data_ptr(), _src_code(key), T,
+               slot_mapping.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _addr(scales), code, desc,
+               _addr(device_status), _stream_of(stream, dev))
     if rc:
         _check(rc, "kv_cache_read")
     return key, value
