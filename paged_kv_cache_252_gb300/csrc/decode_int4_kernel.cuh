@@ -28,9 +28,9 @@
 // lie; V words of two tokens are paired by byte permutes for O^T = V^T P^T. The tokens of a
 // block take the 16 product slots in an order in which both reads hit all banks.
 //
-// What bounds it. One query token of 4 heads a KV head: instructions, 253 a warp and block (64 of them the ANDs that
+// What bounds it. One query token of 4 heads a KV head: instructions, 247 a warp and block (64 of them the ANDs that
 // unpack), issued on 52 % of the cycles with three warps a scheduler, most stalls on fixed latencies: 4 sequences of 131072
-// tokens take 98 us, 5.25 TB/s, 78 % of the copy rate, where the bytes alone take 77. 32 rows: 732 instructions a
+// tokens take 96 us, 5.3 TB/s, 79 % of the copy rate, where the bytes alone take 77 and fetching them without computing 86. 32 rows: 732 instructions a
 // block over its two row warps and two warps a scheduler: 343 us where the bytes take 95 and the products 37. A tcgen05 form for more
 // than 16 rows (a token a thread, codes unpacked to tensor memory, a product a group and exact scales on the scores) took as
 // many instructions, 777, and 408 us; so did sixteen warps in place of eight.
@@ -65,7 +65,7 @@ template <int NT_, int WR_, int WB_, int RING_, int CTAS_, int STEP_, bool PAIR_
 struct Int4Shape {
   // PAIR: units of at most 4 rows of two groups. A row takes two of the products' eight columns, r for the first group and
   // r + 4 for the second, so that a lane holds scores, scales and weights of one group where it would hold those of two, half of
-  // them of padding rows: 253 instructions a block in place of 272, 4 x 131072 tokens 98 us in place of 101.
+  // them of padding rows: 247 instructions a block in place of 272, 4 x 131072 tokens 96 us in place of 101.
   static constexpr bool PAIR = PAIR_;
   static_assert(!PAIR_ || (NT_ == 1 && WR_ == 1 && WB_ > 2), "pair");
   static constexpr int NT = NT_, WR = WR_, WB = WB_, RING = RING_, CTAS = CTAS_, STEP = STEP_;
@@ -717,7 +717,7 @@ __global__ void __launch_bounds__(Sh::THREADS, Sh::CTAS) decode_int4_kernel(cons
       constexpr bool kMasked = decltype(masked)::value;
       const uint32_t at[2] = {st, st + T::STAGE};
       // ---- S^T (16 tokens x 8 NT rows a block), one accumulator a group ----
-      float sa[NB][NT][G][4];
+      float sa[NB][NT][GS][4];
       uint32_t mk[NB][2][GS], mv[NB][2][GS];
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
@@ -736,18 +736,12 @@ __global__ void __launch_bounds__(Sh::THREADS, Sh::CTAS) decode_int4_kernel(cons
             const uint32_t a0 = wa & 0x000F000Fu, a1 = wb2 & 0x000F000Fu, a2 = wa & 0x00F000F0u, a3 = wb2 & 0x00F000F0u;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              float(&acc)[4] = sa[b][nt][PAIR ? hf : x % G];   // (PAIR: two chains, added below)
-              if (PAIR ? x == 0 : (x < G && hf == 0)) mma_new(acc, a0, a1, a2, a3, qf[nt][x][2 * hf], qf[nt][x][2 * hf + 1]);
+              float(&acc)[4] = sa[b][nt][PAIR ? 0 : x % G];
+              if (x < (PAIR ? 1 : G) && hf == 0) mma_new(acc, a0, a1, a2, a3, qf[nt][x][2 * hf], qf[nt][x][2 * hf + 1]);
               else mma_acc(acc, a0, a1, a2, a3, qf[nt][x][2 * hf], qf[nt][x][2 * hf + 1]);
             }
           }
         }
-      }
-      if constexpr (PAIR) {
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-#pragma unroll
-          for (int v = 0; v < 4; ++v) sa[b][0][0][v] += sa[b][0][G - 1][v];
       }
       // (the V words, ahead of the scores' arithmetic)
       uint32_t w[NB][4][G];
@@ -798,7 +792,7 @@ __global__ void __launch_bounds__(Sh::THREADS, Sh::CTAS) decode_int4_kernel(cons
         }
 
       // ---- weights p = 2^(score - m) and P = p s; the reference moved where one is too large ----
-      float p[NB][NT][4];
+      float p[NB][NT][4], p2[NB][NT][2];   // and p of a row's two tokens together
       uint32_t ph[NB][NT][GS][2];   // P of a token's two rows
       auto weights = [&]() {
         float far = 0.f;
@@ -812,7 +806,9 @@ __global__ void __launch_bounds__(Sh::THREADS, Sh::CTAS) decode_int4_kernel(cons
               p[b][nt][v] = fast_exp2(fmaf(sc[b][nt][v], rf[nt][v & 1], -m_run[nt][v & 1]));
               if (kMasked && hid[b][nt][v]) p[b][nt][v] = 0.f;
             }
-            far = fmaxf(far, fmaxf(p[b][nt][0] + p[b][nt][2], p[b][nt][1] + p[b][nt][3]));
+#pragma unroll
+            for (int e = 0; e < 2; ++e) p2[b][nt][e] = p[b][nt][e] + p[b][nt][2 + e];
+            far = fmaxf(far, fmaxf(p2[b][nt][0], p2[b][nt][1]));
 #pragma unroll
             for (int g = 0; g < GS; ++g)
 #pragma unroll
@@ -877,7 +873,7 @@ __global__ void __launch_bounds__(Sh::THREADS, Sh::CTAS) decode_int4_kernel(cons
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-          for (int e = 0; e < 2; ++e) l_run[nt][e] += p[b][nt][e] + p[b][nt][2 + e];
+          for (int e = 0; e < 2; ++e) l_run[nt][e] += p2[b][nt][e];
 #pragma unroll
           for (int g = 0; g < GS; ++g) {
 #pragma unroll
