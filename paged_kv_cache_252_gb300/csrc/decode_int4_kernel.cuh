@@ -77,12 +77,16 @@ struct Int4Shape {
 };
 // Two blocks a step against one: 4 rows 30.0 against 31.3 us (64 sequences), 8 rows 76 against 85, 16 rows 116 against 122, 32
 // rows 343 against 409. A row count takes the smallest shape that holds it (on the next one: 8 rows 107 us, 16 rows 145,
-// 32 rows 648). Rings and CTAs an SM: as many CTAs as the registers allow, and the deepest ring beside them.
+// 32 rows 648). Rings and CTAs an SM: as many CTAs as the registers allow, and the deepest ring beside them. 16 rows: two
+// streams a CTA and four CTAs 113 us, four and two 115, one and eight 147. 64 rows of 64 dimensions leave registers for
+// four n-tiles a warp, so that half as many warps unpack the same words: 126 us against 135 (64 sequences to 8192 tokens); for 32 such
+// rows it is the other way round (73 against 68).
 using Int4Rows4 = Int4Shape<1, 1, 4, 3, 3, 2, true>;
 using Int4Rows8 = Int4Shape<1, 1, 4, 3, 3, 2>;
-using Int4Rows16 = Int4Shape<2, 1, 4, 4, 2, 2>;
+using Int4Rows16 = Int4Shape<2, 1, 2, 4, 4, 2>;
 using Int4Rows32 = Int4Shape<2, 2, 2, 5, 2, 2>;
 using Int4Rows64 = Int4Shape<2, 4, 1, 5, 2, 2>;
+using Int4Rows64Narrow = Int4Shape<4, 2, 2, 5, 2, 1>;   // head size 64
 
 // The walk of a stream's fetching, kept in shared memory: read once for up to 32 blocks.
 struct Int4Walk {
@@ -1044,9 +1048,9 @@ DecodeInt4Kernel int4_kernel(int rows) {
   return {reinterpret_cast<const void*>(&decode_int4_kernel<D, Sh, BF16>), Sh::THREADS,
           static_cast<size_t>(int4_smem<D, Sh>(rows).total)};
 }
-template <bool BF16, class Sh>
+template <bool BF16, class Sh, class Sh64 = Sh>
 DecodeInt4Kernel int4_kernel(int d, int rows) {
-  return d == 128 ? int4_kernel<128, Sh, BF16>(rows) : int4_kernel<64, Sh, BF16>(rows);
+  return d == 128 ? int4_kernel<128, Sh, BF16>(rows) : int4_kernel<64, Sh64, BF16>(rows);
 }
 template <bool BF16>
 DecodeInt4Kernel int4_kernel_for(int d, int rows) {
@@ -1054,7 +1058,7 @@ DecodeInt4Kernel int4_kernel_for(int d, int rows) {
   if (rows <= 8) return int4_kernel<BF16, Int4Rows8>(d, rows);
   if (rows <= 16) return int4_kernel<BF16, Int4Rows16>(d, rows);
   if (rows <= 32) return int4_kernel<BF16, Int4Rows32>(d, rows);
-  return int4_kernel<BF16, Int4Rows64>(d, rows);
+  return int4_kernel<BF16, Int4Rows64, Int4Rows64Narrow>(d, rows);
 }
 
 }  // namespace pkv
