@@ -237,8 +237,8 @@ def _scales_shape(k_cache, scales, code=KV_INT8):
         if scales.shape != want or scales.dtype is not torch.float16:
             raise PagedKVError(f"scales must be float16 {want} (scale and least value of every 64 dimensions)")
         return
-    want = (int(k_cache.shape[0]), int(k_cache.shape[1]), 2, BLOCK_SIZE)
-    if tuple(scales.shape) != want or scales.dtype != torch.float32:
+    want = (*k_cache.shape[:2], 2, BLOCK_SIZE)
+    if scales.shape != want or scales.dtype != torch.float32:
         raise PagedKVError(f"scales must be float32 {want} (K then V row scales)")
 
 
@@ -1071,7 +1071,10 @@ def kv_cache_read(key, value, slot_mapping, k_cache, v_cache, kv_dtype=None, *, 
     code = _kv_code(kv_dtype, k_cache)
     desc, hkv, head = _desc_of(k_cache, v_cache, code == KV_INT4)
     T = _row_shapes(key, value, slot_mapping, hkv, head)
-    _int8_scales(code, k_cache, scales)
+    if scales is None or code not in (KV_INT8, KV_INT4):
+        _int8_scales(code, k_cache, scales)
+    else:
+        _scales_shape(k_cache, scales, code)
     _status_word(device_status)
     rc = _call(dev, (_lib or load_library()).pkv_kv_cache_read, key.data_ptr(), value.data_ptr(), _src_code(key), T,
                slot_mapping.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _addr(scales), code, desc,
