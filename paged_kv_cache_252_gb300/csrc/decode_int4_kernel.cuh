@@ -30,8 +30,9 @@
 //
 // What bounds it. One query token of 4 heads a KV head: instructions, 247 a warp and block (64 of them the ANDs that
 // unpack), issued on 52 % of the cycles with three warps a scheduler, most stalls on fixed latencies: 4 sequences of 131072
-// tokens take 96 us, 5.3 TB/s, 79 % of the copy rate, where the bytes alone take 77 and fetching them without computing 86. 32 rows: 732 instructions a
-// block over its two row warps and two warps a scheduler: 343 us where the bytes take 95 and the products 37. A tcgen05 form for more
+// tokens take 96 us, 5.3 TB/s, 79 % of the copy rate, where the bytes alone take 77 and fetching them without computing 86.
+// 32 rows: 743 instructions a block over its two row warps, two warps a scheduler: 343 us (128 sequences to 8192 tokens)
+// where the bytes take 95, the products 37 and fetching with the pieces' ends 156. A tcgen05 form for more
 // than 16 rows (a token a thread, codes unpacked to tensor memory, a product a group and exact scales on the scores) took as
 // many instructions, 777, and 408 us; so did sixteen warps in place of eight.
 #pragma once

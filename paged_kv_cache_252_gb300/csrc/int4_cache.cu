@@ -4,7 +4,9 @@
 //
 // Write: four threads a group of 64 dimensions, sixteen each; the group's least and largest value by two
 // shuffles of a packed (least, -largest) pair, and both its numbers computed by each of the four.
-// Read: D / 16 threads a row, sixteen dimensions each.
+// Bound by instructions: 365 a warp, issued on 65 % of the cycles (16.7 us for 8192 tokens of 8 heads of 128, where the bytes
+// take 6.4); with eight dimensions of each group a thread and every code settled by itself it was 517 and 20.8 us.
+// Read: D / 16 threads a row, sixteen dimensions each. Bound by memory: 65536 tokens in 60 us, 5.7 TB/s (85 % of a copy).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
