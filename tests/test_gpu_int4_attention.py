@@ -298,3 +298,27 @@ def test_a_spoilt_group_spoils_its_own_dimensions(g, n):
     for part, bad, good in ((slice(0, rows), slice(0, 64), slice(64, 128)), (slice(rows, None), slice(64, 128), slice(0, 64))):
         assert out[part, :, bad].isnan().all()
         i4.assert_within(out[part, :, good], want[part, :, good], tol[part, :, good])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("g,n", [(1, 3), (1, 4), (2, 2), (3, 1), (2, 4), (5, 3), (7, 4), (9, 7)])
+def test_ragged_counts_of_every_shape(g, n, d):
+    """Sequences of fewer rows than the shape holds, behind sequences of more, one of them with queries that are not finite: what
+    earlier rows leave behind does not show."""
+    r = random.Random(g * 10 + n)
+    counts = [n, 1, max(1, n - 1), 1] * 6
+    lens = [max(c, r.randint(1, 600)) for c in counts]
+    c = Case(lens, 2 * g, 2, d, torch.float16, n=n, counts=counts, seed=g)
+    want = c.want()
+    i4.assert_within(c.varlen(), *want)
+    clean = c.varlen()
+    bad = [s for s in range(len(counts)) if s % 4 == 0]
+    for k, s in enumerate(bad):
+        c.q[c.cu[s]:c.cu[s + 1]] = (math.nan, math.inf, -math.inf)[k % 3]
+    out = c.varlen()
+    for s in range(len(counts)):
+        rows = slice(c.cu[s], c.cu[s + 1])
+        if s in bad:
+            assert not out[rows].isfinite().all()
+        else:
+            assert torch.equal(out[rows], clean[rows])
