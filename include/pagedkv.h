@@ -227,9 +227,9 @@ int pkv_paged_attention_decode_tree(void* out, const void* q, const int32_t* cu_
  *   without the workspace: the split-KV scratch comes from a buffer of
  *   PKV_NOALLOC_SCRATCH_BYTES built into the library. Inputs and outputs are
  *   still the caller's. The call itself allocates nothing.
- *   - Limit: a problem whose pkv_decode_workspace_bytes(...) exceeds
- *     PKV_NOALLOC_SCRATCH_BYTES is rejected with PKV_ERR_WORKSPACE_TOO_SMALL
- *     before anything is launched (use pkv_paged_attention_decode with your own
+ *   - Limit: a problem whose pkv_decode_workspace_bytes(...), less what only an
+ *     INT4 cache would need of it, exceeds PKV_NOALLOC_SCRATCH_BYTES is rejected
+ *     with PKV_ERR_WORKSPACE_TOO_SMALL before anything is launched (use pkv_paged_attention_decode with your own
  *     workspace for it). Arguments the regular entry point refuses get the
  *     status it returns for them.
  *   - The buffer occupies PKV_NOALLOC_SCRATCH_BYTES of device memory on every

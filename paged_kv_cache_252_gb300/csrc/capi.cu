@@ -412,6 +412,18 @@ int pkv_kv_cache_write(const void* key, const void* value, pkv_dtype src_dtype, 
 
 size_t pkv_decode_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t q_per_seq,
                                   const pkv_cache_desc* cache) {
+  const size_t others = pkv::decode_workspace_bytes_but_int4(num_seqs, num_q_heads, q_per_seq, cache);
+  if (others == 0) return 0;
+  const size_t int4 = pkv::decode_int4_workspace_bytes(static_cast<long long>(num_seqs) * cache->num_kv_heads, cache->head_size,
+                                                       (num_q_heads / cache->num_kv_heads) * q_per_seq);
+  if (int4 == 0) return 0;
+  return int4 > others ? int4 : others;
+}
+
+}  // extern "C"
+
+size_t pkv::decode_workspace_bytes_but_int4(int32_t num_seqs, int32_t num_q_heads, int32_t q_per_seq,
+                                            const pkv_cache_desc* cache) {
   if (num_seqs < 0 || num_q_heads <= 0 || q_per_seq <= 0 || !valid_cache(cache)) return 0;
   if (num_q_heads % cache->num_kv_heads != 0) return 0;
   const int rows = (num_q_heads / cache->num_kv_heads) * q_per_seq;
@@ -420,8 +432,6 @@ size_t pkv_decode_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t
   // The grid follows the kv dtype's occupancy; size for the largest over the
   // supported dtypes so that one workspace serves any of them.
   const long long units = static_cast<long long>(num_seqs) * cache->num_kv_heads;
-  const size_t int4 = decode_int4_workspace_bytes(units, cache->head_size, rows);
-  if (int4 == 0) return 0;
   std::lock_guard<std::mutex> lock(g_mu);
   DeviceState* st = nullptr;
   if (current_device_state(&st)) return 0;
@@ -431,11 +441,8 @@ size_t pkv_decode_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t
     if (get_geometry(st, kv, cache->head_size, rows, &ge)) return 0;
     if (ge->ctas_per_sm > ctas) ctas = ge->ctas_per_sm;
   }
-  const size_t others = workspace_bytes_for(units, st->sm_count, ctas, rows, cache->head_size);
-  return int4 > others ? int4 : others;
+  return workspace_bytes_for(units, st->sm_count, ctas, rows, cache->head_size);
 }
-
-}  // extern "C"
 
 namespace {
 

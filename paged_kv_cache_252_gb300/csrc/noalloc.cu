@@ -69,7 +69,7 @@ extern "C" int pkv_paged_attention_decode_noalloc(void* out, const void* q, int3
                                       kv_dtype, cache, block_tables, max_blocks_per_seq,
                                       context_lens, scale, nullptr, 0, device_status, stream);
   }
-  const size_t need = pkv_decode_workspace_bytes(num_seqs, num_q_heads, q_per_seq, cache);
+  const size_t need = pkv::decode_workspace_bytes_but_int4(num_seqs, num_q_heads, q_per_seq, cache);
   if (need == 0) {
     // The shape was refused (invalid, unsupported, or no device). Let the regular
     // entry point's host checks pick the status it would return: it is given a

@@ -153,6 +153,8 @@ const void* decode_kernel_narrow_ptr_bf16(int d);
 // Workspace of a decode over an INT4 cache on the current device (0: no device) and of its counters, with which
 // it starts.
 size_t decode_int4_workspace_bytes(long long units, int d, int rows);
+// pkv_decode_workspace_bytes for the caches of 8 bits and more.
+size_t decode_workspace_bytes_but_int4(int32_t num_seqs, int32_t num_q_heads, int32_t q_per_seq, const pkv_cache_desc* cache);
 size_t decode_int4_counter_bytes(long long units, int d, int rows);
 const void* kv_cache_write_kernel_ptr();
 const void* kv_cache_write_int8_kernel_ptr();

@@ -98,3 +98,18 @@ def test_steps(dtype, d):
     pkv.paged_attention_decode_varlen(out, q, cu, kc, vc, tables((0, 1, 2)), ctx, 4, scale, "int4", scales=sc, device_status=st)
     check(out, q, (0, 1, 2), [0, 1, 5, 7])
     assert int(st) == 0
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_the_call_with_a_buffer_of_its_own_takes_what_it_took(d):
+    """pkv_decode_workspace_bytes covers an INT4 cache, whose units of 16 rows need more than the others'; the call that takes no
+    workspace keeps its limit. (Misaligned pointers: no call gets as far as a launch.)"""
+    import ctypes
+    from paged_kv_cache_252_gb300.api import _CacheDesc, load_library
+    lib, desc, fake = load_library(), _CacheDesc(1024, 16, 8, d), ctypes.c_void_p(257)
+
+    def status(S):
+        return lib.pkv_paged_attention_decode_noalloc(fake, fake, S, 64, 2, fake, fake, 0, ctypes.byref(desc), fake, 4, fake,
+                                                      ctypes.c_float(0.1), None, None)
+    S = next(S for S in range(1, 5000) if lib.pkv_decode_workspace_bytes(S, 64, 2, ctypes.byref(desc)) > 32 << 20)
+    assert status(S) == -1 and status(2 * S) == -3
