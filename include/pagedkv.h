@@ -115,6 +115,14 @@ size_t pkv_decode_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t
                                   const pkv_cache_desc* cache);
 
 /*
+ * pkv_decode_counter_bytes — the bytes at the start of that buffer that hold the counters of a
+ * call over a cache of type kv_dtype: what to zero in a buffer that held other data. Every launch
+ * leaves them clear. Returns 0 on invalid arguments.
+ */
+size_t pkv_decode_counter_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t q_per_seq,
+                                const pkv_cache_desc* cache, pkv_dtype kv_dtype);
+
+/*
  * pkv_paged_attention_decode — decode attention over the blocked cache
  * ("kernel2" of the KVCache Quant section, the PagedAttention section's decode
  * kernel, with the GQA grouping of 2.2.2 and the multi-token verify of the
@@ -618,6 +626,18 @@ int pkv_seq_add_cached(pkv_allocator* a, int64_t seq, const int32_t* tokens, int
 int pkv_copy_blocks(void* k_cache, void* v_cache, float* scales, pkv_dtype kv_dtype,
                     const pkv_cache_desc* cache, const int32_t* src, const int32_t* dst, int32_t n,
                     int32_t* device_status, void* stream);
+
+/* ==== Captured calls =========================================================
+ * For a binding that keeps a buffer for the calls captured into a CUDA graph: such a buffer must
+ * live, and hold nothing else, as long as the graph can be replayed.
+ *
+ * pkv_capture_watch: *id becomes the capture that `stream` takes part in (unique in the process),
+ * 0 if it is not being captured. If it is and watch is not NULL, *watch becomes a handle that
+ * watches the graph being captured. pkv_capture_gone: 1 once that graph and every executable
+ * graph made from it are destroyed; the handle is then released and must not be used again.
+ * Else 0. The driver reports the end some time after the last of them was destroyed. */
+int pkv_capture_watch(void* stream, uint64_t* id, void** watch);
+int pkv_capture_gone(void* watch);
 
 /* Static description of a status code. Never NULL. */
 const char* pkv_error_string(int code);

@@ -26,8 +26,6 @@ BLOCK_SIZE = 16
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _lock = threading.Lock()
 _lib = None
-_workspaces: dict = {}
-_ws_bytes_cache: dict = {}
 
 
 class PagedKVError(RuntimeError):
@@ -153,6 +151,12 @@ def load_library(path: str | None = None):
                                                                 P(_CacheDesc), vp, i32, f32, vp, ctypes.c_size_t, vp,
                                                                 vp]
         lib.pkv_paged_attention_decode_int4_chunked.restype = cint
+        lib.pkv_decode_counter_bytes.argtypes = [i32, i32, i32, P(_CacheDesc), cint]
+        lib.pkv_decode_counter_bytes.restype = ctypes.c_size_t
+        lib.pkv_capture_watch.argtypes = [vp, P(ctypes.c_uint64), P(vp)]
+        lib.pkv_capture_watch.restype = cint
+        lib.pkv_capture_gone.argtypes = [vp]
+        lib.pkv_capture_gone.restype = cint
         lib.pkv_selftest_bounded_wait.argtypes = [vp, ctypes.c_uint64, vp, vp]
         lib.pkv_selftest_bounded_wait.restype = ctypes.c_int
         lib.pkv_error_string.argtypes = [ctypes.c_int]
@@ -339,9 +343,9 @@ def paged_attention_decode_int8(out, q, k_cache, v_cache, scales, block_tables, 
     Hq = int(q.shape[1])
     lib = load_library()
     with _on_device(q.device):
-        need = _ws_bytes(lib, q.device, S, Hq, int(q_per_seq), d)
         if workspace is None:
-            workspace = _workspace(need, q.device)
+            workspace = _decode_workspace(lib, q.get_device(), stream, S, Hq, int(q_per_seq), ctypes.byref(d), d.num_kv_heads,
+                                          d.head_size, KV_INT8)
         rc = lib.pkv_paged_attention_decode_int8(
             _ptr(out), _ptr(q), S, Hq, int(q_per_seq), _ptr(k_cache), _ptr(v_cache), _ptr(scales),
             ctypes.byref(d), _ptr(block_tables), int(block_tables.shape[1]), _ptr(context_lens),
@@ -385,25 +389,89 @@ def _on_device(device):
     return torch.cuda.device(device)
 
 
-def _ws_bytes(lib, device, S, Hq, n, d) -> int:
-    """pkv_decode_workspace_bytes, remembered per device and problem shape."""
-    key = (device.index, S, Hq, n, d.num_blocks, d.block_size, d.num_kv_heads, d.head_size)
-    v = _ws_bytes_cache.get(key)
-    if v is None:
-        v = int(lib.pkv_decode_workspace_bytes(S, Hq, n, ctypes.byref(d)))
-        _ws_bytes_cache[key] = v
-    return v
+class _Scratch:
+    """A buffer of calls that follow one another on a stream. Its first ``clean`` bytes hold nothing
+    but piece counters, which every launch leaves clear; a call that has more of them clears the
+    rest first."""
+    __slots__ = ("ws", "clean")
+
+    def __init__(self):
+        self.ws, self.clean = None, 0
+
+    def take(self, nbytes: int, counters: int, dev: int) -> torch.Tensor:
+        ws = self.ws
+        if ws is None or ws.shape[0] < nbytes:
+            ws = self.ws = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
+            self.clean = 0
+        if self.clean < counters:
+            ws[self.clean:counters].zero_()
+        self.clean = counters
+        return ws
 
 
-def _workspace(nbytes: int, device) -> torch.Tensor:
-    key = (str(device), torch.cuda.current_stream(device).cuda_stream)
-    ws = _workspaces.get(key)
-    if ws is None or ws.numel() < nbytes:
-        # Zeroed once: the piece counters then start clear whatever the allocator
-        # held there before (later calls leave them clear).
-        ws = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
-        _workspaces[key] = ws
-    return ws
+class _Capture:
+    """Scratch of the calls captured into one graph, from its memory pool and held until the graph
+    and its executables are gone: what a replay writes to is nobody else's, and nothing else
+    leaves its numbers where a replay expects clear counters."""
+    __slots__ = ("watch", "scratch", "outgrown")
+
+    def __init__(self, watch):
+        self.watch, self.scratch, self.outgrown = watch, {}, []
+
+
+_scratches: dict = {}   # (kind, device, stream): _Scratch
+_captures: dict = {}    # capture: _Capture
+
+
+def _scratch(kind: str, nbytes: int, counters: int, dev: int, stream) -> torch.Tensor:
+    """Scratch of a call whose first ``counters`` bytes are its piece counters: one buffer per kind,
+    device and stream that calls run on, grown as needed; a graph's own for captured calls."""
+    with _NOWHERE if stream is None else torch.cuda.stream(stream):
+        handle = _stream_of(stream, dev)
+        if torch.cuda.is_current_stream_capturing():
+            return _captured_scratch((kind, dev, handle), nbytes, counters)
+        s = _scratches.get((kind, dev, handle))
+        if s is None:
+            s = _scratches[kind, dev, handle] = _Scratch()
+        return s.take(nbytes, counters, dev)
+
+
+def _captured_scratch(key, nbytes: int, counters: int) -> torch.Tensor:
+    lib, capture, watch = load_library(), ctypes.c_uint64(), ctypes.c_void_p()
+    with _lock_captures:
+        _check(lib.pkv_capture_watch(key[2], ctypes.byref(capture), None), "capture")
+        held = _captures.get(capture.value)
+        if held is None:
+            for gone in [c for c, h in _captures.items() if lib.pkv_capture_gone(h.watch)]:
+                del _captures[gone]
+            _check(lib.pkv_capture_watch(key[2], ctypes.byref(capture), ctypes.byref(watch)), "capture")
+            held = _captures[capture.value] = _Capture(watch.value)
+        s = held.scratch.get(key)
+        if s is None:
+            s = held.scratch[key] = _Scratch()
+        old = s.ws
+        ws = s.take(nbytes, counters, key[1])
+        if old is not None and old is not ws:
+            held.outgrown.append(old)
+        return ws
+
+
+_lock_captures = threading.Lock()
+_decode_sizes: dict = {}
+
+
+def _decode_workspace(lib, dev: int, stream, S, Hq, n, desc, hkv, head, code) -> torch.Tensor:
+    """Scratch of a decode call (sizes kept per device and problem shape)."""
+    key = (dev, S, Hq, n, hkv, head, code)
+    sizes = _decode_sizes.get(key)
+    if sizes is None:
+        sizes = (int(lib.pkv_decode_workspace_bytes(S, Hq, n, desc)),
+                 int(lib.pkv_decode_counter_bytes(S, Hq, n, desc, code)))
+        if sizes[0]:   # (else refused: the call says why)
+            if len(_decode_sizes) > 4096:
+                _decode_sizes.clear()
+            _decode_sizes[key] = sizes
+    return _scratch("decode", *sizes, dev, stream)
 
 
 def paged_attention_decode(out, q, k_cache, v_cache, block_tables, context_lens, q_per_seq: int,
@@ -424,9 +492,9 @@ def paged_attention_decode(out, q, k_cache, v_cache, block_tables, context_lens,
     code = _kv_code(kv_dtype, k_cache)
     lib = load_library()
     with _on_device(q.device):
-        need = _ws_bytes(lib, q.device, S, Hq, int(q_per_seq), d)
         if workspace is None:
-            workspace = _workspace(need, q.device)
+            workspace = _decode_workspace(lib, q.get_device(), stream, S, Hq, int(q_per_seq), ctypes.byref(d), d.num_kv_heads,
+                                          d.head_size, code)
         rc = lib.pkv_paged_attention_decode(
             _ptr(out), _ptr(q), S, Hq, int(q_per_seq), _ptr(k_cache), _ptr(v_cache), code,
             ctypes.byref(d), _ptr(block_tables), int(block_tables.shape[1]), _ptr(context_lens),
@@ -499,9 +567,9 @@ def paged_attention_decode_varlen(out, q, cu_q_lens, k_cache, v_cache, block_tab
     Hq = int(q.shape[1])
     lib = load_library()
     with _on_device(q.device):
-        need = _ws_bytes(lib, q.device, S, Hq, int(max_q_per_seq), d)
         if workspace is None:
-            workspace = _workspace(need, q.device)
+            workspace = _decode_workspace(lib, q.get_device(), stream, S, Hq, int(max_q_per_seq), ctypes.byref(d), d.num_kv_heads,
+                                          d.head_size, code)
         ws = (_ptr(workspace), int(workspace.numel() * workspace.element_size()))
         if code == KV_INT8:
             rc = lib.pkv_paged_attention_decode_int8_varlen(
@@ -571,7 +639,7 @@ def paged_attention_decode_chunked(out, q, q_lens, context_lens, k_cache, v_cach
         if S and need == 0:
             raise PagedKVError("paged_attention_decode_chunked: unsupported shape")
         if workspace is None:
-            workspace = _workspace(need, q.device)
+            workspace = _scratch("decode", need, 0, q.get_device(), stream)   # (the call clears its counters itself)
         rest = (ctypes.byref(d), _ptr(block_tables), mbs, float(scale), _ptr(workspace),
                 int(workspace.numel() * workspace.element_size()), _ptr(device_status),
                 _stream_handle(stream, q.device))
@@ -635,9 +703,9 @@ def paged_attention_decode_tree(out, q, tree_masks, k_cache, v_cache, block_tabl
     Hq = int(q.shape[1])
     lib = load_library()
     with _on_device(q.device):
-        need = _ws_bytes(lib, q.device, S, Hq, int(max_q_per_seq), d)
         if workspace is None:
-            workspace = _workspace(need, q.device)
+            workspace = _decode_workspace(lib, q.get_device(), stream, S, Hq, int(max_q_per_seq), ctypes.byref(d), d.num_kv_heads,
+                                          d.head_size, code)
         ws = (_ptr(workspace), int(workspace.numel() * workspace.element_size()))
         if code == KV_INT8:
             rc = lib.pkv_paged_attention_decode_int8_tree(

@@ -38,7 +38,7 @@ VARIANTS = {  # name -> (object dir, library, extra nvcc flags)
 SOURCES = ["capi.cu", "kv_cache_write.cu", "decode_f16.cu", "decode_bf16.cu", "decode_e5m2.cu",
            "decode_tc.cu", "decode_int8.cu", "noalloc.cu", "copy_blocks.cu", "chunked.cu", "selftest.cu",
            "rotary.cu", "accept.cu", "prefill.cu", "int4_cache.cu", "decode_int4.cu", "decode_int4_f16.cu",
-           "decode_int4_bf16.cu", "block_allocator.cpp"]
+           "decode_int4_bf16.cu", "block_allocator.cpp", "capture.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -420,6 +420,20 @@ size_t pkv_decode_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t
   return int4 > others ? int4 : others;
 }
 
+size_t pkv_decode_counter_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t q_per_seq,
+                                const pkv_cache_desc* cache, pkv_dtype kv_dtype) {
+  if (num_seqs < 0 || num_q_heads <= 0 || q_per_seq <= 0 || !valid_cache(cache) || num_q_heads % cache->num_kv_heads != 0)
+    return 0;
+  const long long units = static_cast<long long>(num_seqs) * cache->num_kv_heads;
+  const long long rows = static_cast<long long>(num_q_heads / cache->num_kv_heads) * q_per_seq;
+  if (rows > kMaxRows) return 0;
+  switch (static_cast<int>(kv_dtype)) {
+    case kKvF16: case kKvBf16: case kKvE5m2: case kKvInt8: return desc_bytes(units);
+    case kKvInt4: return pkv::decode_int4_counter_bytes(units, cache->head_size, static_cast<int>(rows));
+    default: return 0;
+  }
+}
+
 }  // extern "C"
 
 size_t pkv::decode_workspace_bytes_but_int4(int32_t num_seqs, int32_t num_q_heads, int32_t q_per_seq,
