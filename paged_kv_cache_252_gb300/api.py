@@ -1152,24 +1152,6 @@ def kv_cache_read(key, value, slot_mapping, k_cache, v_cache, kv_dtype=None, *, 
     return key, value
 
 
-_int4_workspaces: dict = {}
-_int4_ws_bytes: dict = {}
-
-
-def _int4_workspace(nbytes: int, dev: int, stream) -> torch.Tensor:
-    """Scratch of an INT4 decode: one buffer per (device, stream the call runs on), grown as
-    needed; a call that is being captured gets a buffer of its own from the graph's memory pool.
-    Its counters are tagged with the call's number, so what it holds does not matter."""
-    with _NOWHERE if stream is None else torch.cuda.stream(stream):
-        if torch.cuda.is_current_stream_capturing():
-            return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
-        key = (dev, _stream_of(stream, dev))
-        ws = _int4_workspaces.get(key)
-        if ws is None or ws.shape[0] < nbytes:
-            ws = _int4_workspaces[key] = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=dev)
-        return ws
-
-
 _DECODE4_NAMES = ("q", "out", "k_cache", "v_cache", "scales", "block_tables", "context_lens", "cu_q_lens", "tree_masks",
                   "workspace", "device_status")
 
@@ -1183,7 +1165,7 @@ def _decode_int4(what, out, q, cu_q_lens, tree_masks, k_cache, v_cache, scales, 
     i32 = torch.int32
     if block_tables.dtype is not i32 or context_lens.dtype is not i32:
         raise PagedKVError("block_tables and context_lens must be int32")
-    desc, _, D = _desc_of(k_cache, v_cache, True)
+    desc, hkv, D = _desc_of(k_cache, v_cache, True)
     _scales_shape(k_cache, scales, KV_INT4)
     shape = q.shape
     if len(shape) != 3 or out.shape != shape or shape[2] != D:
@@ -1211,13 +1193,7 @@ def _decode_int4(what, out, q, cu_q_lens, tree_masks, k_cache, v_cache, scales, 
     lib = _lib or load_library()
     with _at(dev):
         if workspace is None:
-            key = (dev, S, Hq, n, k_cache.shape[1], D)
-            need = _int4_ws_bytes.get(key)
-            if need is None:
-                if len(_int4_ws_bytes) > 4096:
-                    _int4_ws_bytes.clear()
-                need = _int4_ws_bytes[key] = int(lib.pkv_decode_workspace_bytes(S, Hq, n, desc))
-            workspace = _int4_workspace(need, dev, stream)
+            workspace = _decode_workspace(lib, dev, stream, S, Hq, n, desc, hkv, D, KV_INT4)
         rc = lib.pkv_paged_attention_decode_int4(
             out.data_ptr(), q.data_ptr(), _src_code(q), _addr(cu_q_lens), _addr(tree_masks), R, S, Hq, n,
             k_cache.data_ptr(), v_cache.data_ptr(), scales.data_ptr(), desc, block_tables.data_ptr(), tables[1],

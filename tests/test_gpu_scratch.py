@@ -172,3 +172,38 @@ def test_a_graph_that_is_gone_gives_its_scratch_back():
             break
         torch.cuda._sleep(10_000_000)
     assert not held & set(api._captures)
+
+
+def _epoch(n):
+    """The tag of the process's n-th call with piece counters."""
+    m = 0xFFFFFFFF
+    n ^= n >> 16
+    n = n * 0x7FEB352D & m
+    n ^= n >> 15
+    n = n * 0x846CA68B & m
+    return n ^ n >> 16
+
+
+def test_nodes_behind_a_captured_call_do_not_reach_its_counters():
+    """The graph's own later tensors take the memory that the captured call gave back, if any, and fill it with words that
+    are that call's counters to the letter, half counted."""
+    c = Call("decode", "int4", [9000, 40, 700, 3], seed=6)
+    want = c()
+    need = pkv.api.load_library().pkv_decode_workspace_bytes(4, 8, 3, pkv.api._desc_of(c.k, c.v, True)[0])
+    ws = torch.zeros(need, dtype=torch.uint8, device=DEV)
+    c(workspace=ws)
+    tag = {w >> 32 & 0xFFFFFFFF for w in ws[:256].view(torch.int64).tolist()} - {0}   # (a counter keeps its call's tag)
+    n = next(n for n in range(1, 1 << 20) if {_epoch(n)} == tag)
+    g, out = torch.cuda.CUDAGraph(), c.out()
+    s = torch.cuda.Stream()
+    with torch.cuda.graph(g, stream=s):
+        c(out)
+        later = [torch.empty(need // 8, dtype=torch.int64, device=DEV) for _ in range(4)]
+        word = _epoch(n + 1) << 32 | 1
+        for x in later:
+            x.fill_(word - (1 << 64) if word >> 63 else word)
+    for _ in range(4):
+        out.fill_(math.nan)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)

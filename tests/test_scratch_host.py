@@ -141,7 +141,7 @@ def test_scratch_goes_by_the_stream_the_call_runs_on(world, form, kv):
     assert [c[1].cuda_stream for c in world.calls] == [1, 11, 12, 11, 1, 12]   # made on that stream
 
 
-@pytest.mark.parametrize("form,kv", [x for x in ALL if x[0] == "chunked" or x[1] != "int4"])
+@pytest.mark.parametrize("form,kv", ALL)
 def test_a_captured_call_shares_its_scratch_with_its_graph_alone(world, form, kv):
     live = lambda p: next(t for q, (t, _) in reversed(world.made) if q == p)()
     eager = Stream(21)
@@ -165,7 +165,7 @@ def test_a_captured_call_shares_its_scratch_with_its_graph_alone(world, form, kv
 
 
 @pytest.mark.parametrize("captured", [False, True])
-@pytest.mark.parametrize("form,kv", [x for x in ALL if x[0] != "chunked" and x[1] != "int4"])   # (which clears its counters itself)
+@pytest.mark.parametrize("form,kv", [x for x in ALL if x[0] != "chunked"])   # (which clears its counters itself)
 def test_counters_are_clear_before_every_call(world, form, kv, captured):
     """The sums of a call with fewer counters, and of a chunked one, lie where a later call's counters are."""
     with world.on(Stream(31, 5 if captured else 0)):
