@@ -467,7 +467,7 @@ def _decode_workspace(lib, dev: int, stream, S, Hq, n, desc, hkv, head, code) ->
     if sizes is None:
         sizes = (int(lib.pkv_decode_workspace_bytes(S, Hq, n, desc)),
                  int(lib.pkv_decode_counter_bytes(S, Hq, n, desc, code)))
-        if sizes[0]:   # (else refused: the call says why)
+        if sizes[0] and sizes[1]:   # (else refused: the call says why)
             if len(_decode_sizes) > 4096:
                 _decode_sizes.clear()
             _decode_sizes[key] = sizes

@@ -175,3 +175,13 @@ def test_counters_are_clear_before_every_call(world, form, kv, captured):
         _call(world, form, kv, S=4)
         calls = [c for i, c in enumerate(world.calls) if i != 6]
         assert len({c[0] for c in calls}) == 1 and all(c[2] for c in calls)
+
+
+@pytest.mark.parametrize("form,kv", [x for x in ALL if x[0] != "chunked"])
+def test_a_size_that_could_not_be_told_is_asked_for_again(world, form, kv, monkeypatch):
+    with monkeypatch.context() as m:
+        m.setattr(Library, "pkv_decode_workspace_bytes", lambda self, S, Hq, n, desc: 0)   # (a device error, say)
+        _call(world, form, kv)
+    _call(world, form, kv)
+    ws = next(t for p, (t, _) in reversed(world.made) if p == world.calls[-1][0])()
+    assert ws.shape[0] >= 2 * 4096
