@@ -16,8 +16,7 @@ constexpr int kMaxDevices = 64;
 
 std::mutex g_i4_mu;
 struct Entry {
-  size_t smem;   // largest dynamic shared memory asked for so far; 0: not set up
-  int ctas;      // resident CTAs at that size
+  int ctas;      // resident CTAs of the shape's largest row count; 0: not set up
 };
 Entry g_i4[kMaxDevices][2][5];   // [head size][rows]
 
@@ -39,7 +38,7 @@ int resident_ctas(int d, int rows, int* ctas) {
   const int x = shape_index(d, rows);
   std::lock_guard<std::mutex> lock(g_i4_mu);
   Entry& e = g_i4[dev][d == 128][x];
-  if (e.smem == 0) {
+  if (e.ctas == 0) {
     const int most = 4 << x;
     int least = 0;
     for (int bf16 = 0; bf16 < 2; ++bf16) {
@@ -53,9 +52,8 @@ int resident_ctas(int d, int rows, int* ctas) {
         return PKV_ERR_CUDA;
       }
       least = bf16 == 0 || blocks < least ? blocks : least;
-      e.smem = k.smem;
     }
-    e.ctas = least;
+    e.ctas = least;   // (both kernels are set up)
   }
   *ctas = e.ctas;
   return PKV_OK;
