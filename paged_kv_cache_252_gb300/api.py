@@ -174,6 +174,8 @@ def _check(rc: int, what: str):
 
 def _kv_code(kv_dtype, cache: torch.Tensor) -> int:
     if kv_dtype is None:
+        if cache.dtype is torch.uint8 and getattr(cache, "_pkv_int4", False):
+            raise PagedKVError('calls on an INT4 cache name its type (kv_dtype="int4")')
         return _TORCH[cache.dtype]
     if isinstance(kv_dtype, str):
         return _NAMES[kv_dtype]
@@ -270,18 +272,25 @@ def alloc_kv_cache(num_blocks: int, num_kv_heads: int, head_size: int, kv_dtype,
     cache is a torch.int8 tensor whose bytes hold the codes in offset binary
     (byte = code + 128; :func:`int8_codes` reads them back). An INT4 cache is a torch.uint8
     tensor [num_blocks, num_kv_heads, 16, head_size / 2] of packed codes
-    (:func:`kv_cache_read` reads them back); calls on it name its type
-    (kv_dtype="int4"). ``zero`` fills the caches with the value 0 (for INT8: code 0, byte 0x80)."""
+    (:func:`kv_cache_read` reads them back); calls on it name its type (kv_dtype="int4") and are
+    refused if they do not. (The tensors of this call are marked; a view or a copy of one is not,
+    and counts as an E5M2 cache in a call that names no type.) ``zero`` fills the caches with the
+    value 0 (for INT8: code 0, byte 0x80)."""
     code = _NAMES[kv_dtype] if isinstance(kv_dtype, str) else int(kv_dtype)
     dt = {KV_FP16: torch.float16, KV_BF16: torch.bfloat16, KV_E5M2: torch.uint8, KV_INT8: torch.int8,
           KV_INT4: torch.uint8}[code]
     if code == KV_INT4 and head_size not in (64, 128):
         raise PagedKVError(f"an INT4 cache has head size 64 or 128, got {head_size}")
     shape = (num_blocks, num_kv_heads, BLOCK_SIZE, head_size // 2 if code == KV_INT4 else head_size)
-    if not zero:
-        return torch.empty(shape, dtype=dt, device=device), torch.empty(shape, dtype=dt, device=device)
-    fill = -128 if code == KV_INT8 else 0   # int8 -128 is the byte 0x80
-    return (torch.full(shape, fill, dtype=dt, device=device), torch.full(shape, fill, dtype=dt, device=device))
+    if zero:
+        fill = -128 if code == KV_INT8 else 0   # int8 -128 is the byte 0x80
+        pair = torch.full(shape, fill, dtype=dt, device=device), torch.full(shape, fill, dtype=dt, device=device)
+    else:
+        pair = torch.empty(shape, dtype=dt, device=device), torch.empty(shape, dtype=dt, device=device)
+    if code == KV_INT4:
+        for t in pair:
+            t._pkv_int4 = True   # bytes like an E5M2 cache's
+    return pair
 
 
 def alloc_kv_scales(num_blocks: int, num_kv_heads: int, device="cuda", *, kv_dtype="int8",

@@ -1,0 +1,53 @@
+"""An INT4 cache is bytes, as an E5M2 cache is: what calls do that say which it is, say nothing, or say it of another cache."""
+import pytest
+import torch
+
+import paged_kv_cache_252_gb300 as pkv
+from paged_kv_cache_252_gb300 import api
+
+
+@pytest.fixture
+def no_gpu(monkeypatch):
+    """Argument checks on host tensors; a call that passes them must not get to the library."""
+    class Library:
+        def __getattr__(self, name):
+            def call(*args):
+                if name.endswith("_bytes"):
+                    return 4096
+                raise AssertionError(f"{name} was called")
+            return call
+    monkeypatch.setattr(api, "_lib", Library())
+    monkeypatch.setattr(api, "_placed", lambda names, tensors: 0)
+    monkeypatch.setattr(api, "_need_cuda_contig", lambda name, t: None)
+    monkeypatch.setattr(api, "_head_rows", lambda name, t, dev, heads, head: heads)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("zero", [True, False])
+def test_calls_that_do_not_name_the_type_are_refused(no_gpu, d, zero):
+    k, v = pkv.alloc_kv_cache(3, 2, d, "int4", "cpu", zero)
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32)
+    x, slots = torch.zeros((4, 2, d // 2), dtype=torch.float16), i32(0, 1, 2, 3)
+    q, tables, lens, cu = torch.zeros((4, 8, d // 2), dtype=torch.float16), i32(0, 1, 2, 0).view(4, 1), i32(1, 1, 1, 1), i32(0, 1, 2, 3, 4)
+    masks = torch.ones(4, dtype=torch.int64)
+    for call in (lambda: pkv.copy_blocks(k, v, i32(0), i32(1)),
+                 lambda: pkv.kv_cache_accept(k, v, tables, lens, i32(0, 0, 0, 0).view(4, 1), lens, None, 1),
+                 lambda: pkv.kv_cache_write(x, x, slots, k, v),
+                 lambda: pkv.kv_cache_read(x, x, slots, k, v),
+                 lambda: pkv.paged_attention_decode(q, q, k, v, tables, lens, 1, 0.1),
+                 lambda: pkv.paged_attention_decode_noalloc(q, q, k, v, tables, lens, 1, 0.1),
+                 lambda: pkv.paged_attention_decode_varlen(q, q, cu, k, v, tables, lens, 1, 0.1),
+                 lambda: pkv.paged_attention_decode_tree(q, q, masks, k, v, tables, lens, 1, 0.1),
+                 lambda: pkv.paged_attention_decode_chunked(q, q, [1] * 4, [1] * 4, k, v, tables, 0.1),
+                 lambda: pkv.paged_attention_prefill(q, q, cu, k, v, tables, lens, 0.1),
+                 lambda: pkv.rotary_write(q, q, x, x, slots, slots, k, v, torch.ones(8, dtype=torch.float64))):
+        with pytest.raises(pkv.PagedKVError):
+            call()
+
+
+def test_other_caches_need_no_name():
+    for kv, code in (("fp16", 0), ("bf16", 1), ("e5m2", 2), ("int8", 3)):
+        k, _ = pkv.alloc_kv_cache(2, 1, 64, kv, "cpu")
+        assert api._kv_code(None, k) == code
+    k, _ = pkv.alloc_kv_cache(2, 1, 64, "int4", "cpu")
+    assert api._kv_code("int4", k) == api._kv_code(pkv.KV_INT4, k) == 4
