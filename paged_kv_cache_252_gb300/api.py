@@ -384,8 +384,11 @@ def kv_cache_write(key, value, slot_mapping, k_cache, v_cache, kv_dtype=None, *,
     _check(rc, "kv_cache_write")
 
 
-def decode_workspace_bytes(num_seqs: int, num_q_heads: int, q_per_seq: int, k_cache) -> int:
+def decode_workspace_bytes(num_seqs: int, num_q_heads: int, q_per_seq: int, k_cache, kv_dtype=None) -> int:
+    """Bytes of workspace a decode call needs for this problem on the cache's device."""
     d = _desc(k_cache)
+    if _kv_code(kv_dtype, k_cache) == KV_INT4:   # (two dimensions a byte)
+        d.head_size *= 2
     with torch.cuda.device(k_cache.device):
         return int(load_library().pkv_decode_workspace_bytes(num_seqs, num_q_heads, q_per_seq,
                                                              ctypes.byref(d)))

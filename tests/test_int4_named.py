@@ -51,3 +51,36 @@ def test_other_caches_need_no_name():
         assert api._kv_code(None, k) == code
     k, _ = pkv.alloc_kv_cache(2, 1, 64, "int4", "cpu")
     assert api._kv_code("int4", k) == api._kv_code(pkv.KV_INT4, k) == 4
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_workspace_of_an_int4_cache_is_of_its_head_size(monkeypatch, d):
+    import contextlib
+    asked = []
+
+    class Library:
+        def pkv_decode_workspace_bytes(self, S, Hq, n, desc):
+            asked.append(desc._obj.head_size)
+            return 1000 * desc._obj.head_size
+    monkeypatch.setattr(api, "_lib", Library())
+    monkeypatch.setattr(torch.cuda, "device", lambda dev: contextlib.nullcontext())
+    k, _ = pkv.alloc_kv_cache(2, 1, d, "int4", "cpu")
+    for name in ("int4", pkv.KV_INT4):
+        assert pkv.decode_workspace_bytes(8, 4, 1, k, name) == 1000 * d
+    with pytest.raises(pkv.PagedKVError):
+        pkv.decode_workspace_bytes(8, 4, 1, k)
+    e, _ = pkv.alloc_kv_cache(2, 1, d, "e5m2", "cpu")
+    assert pkv.decode_workspace_bytes(8, 4, 1, e) == pkv.decode_workspace_bytes(8, 4, 1, e, "e5m2") == 1000 * d
+    assert asked == [d] * 4
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_workspace_of_the_told_size_serves_the_call(d):
+    import _int4 as i4
+    from test_gpu_scratch import Call
+    c = Call("decode", "int4", [700, 3, 2000], d=d)
+    want = c()
+    ws = torch.zeros(pkv.decode_workspace_bytes(3, 8, 3, c.k, "int4"), dtype=torch.uint8, device="cuda")
+    assert torch.equal(c(workspace=ws), want)
+    i4.assert_within(want, *i4.attention(c.q, c.k, c.v, c.sc, c.tables, c.lens, c.cu, c.scale))
