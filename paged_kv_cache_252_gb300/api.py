@@ -208,10 +208,14 @@ def _desc(cache: torch.Tensor) -> _CacheDesc:
     return _CacheDesc(cache.shape[0], cache.shape[2], cache.shape[1], cache.shape[3])
 
 
-def _pair(k_cache, v_cache) -> _CacheDesc:
+def _pair(k_cache, v_cache, packed=False) -> _CacheDesc:
     d = _desc(k_cache)
     if tuple(v_cache.shape) != tuple(k_cache.shape) or v_cache.dtype != k_cache.dtype:
         raise PagedKVError("k_cache and v_cache must have the same shape and dtype")
+    if packed:   # an INT4 cache, two dimensions a byte
+        if k_cache.dtype is not torch.uint8:
+            raise PagedKVError("an INT4 cache is a torch.uint8 tensor (alloc_kv_cache)")
+        d.head_size *= 2
     return d
 
 
@@ -633,9 +637,7 @@ def paged_attention_decode_chunked(out, q, q_lens, context_lens, k_cache, v_cach
     if S and (ql.min() < 1 or np.any(cl < ql)):
         raise PagedKVError("every sequence needs 1 <= q_lens[s] <= context_lens[s]")
     code = _kv_code(kv_dtype, k_cache)
-    d = _pair(k_cache, v_cache)
-    if code == KV_INT4:
-        d.head_size *= 2
+    d = _pair(k_cache, v_cache, code == KV_INT4)
     if q.dim() != 3 or tuple(out.shape) != tuple(q.shape) or int(q.shape[0]) != int(ql.sum()):
         raise PagedKVError(f"q and out must both be [sum(q_lens) = {int(ql.sum())}, num_q_heads, head_size]")
     if int(q.shape[2]) != d.head_size:
@@ -1325,15 +1327,13 @@ def copy_blocks(k_cache, v_cache, src, dst, kv_dtype=None, *, scales=None, devic
         _need_cuda_contig(n_, t)
     if src.dtype != torch.int32 or dst.dtype != torch.int32 or src.numel() != dst.numel():
         raise PagedKVError("src and dst must be int32 tensors of equal length")
-    d = _pair(k_cache, v_cache)
     code = _kv_code(kv_dtype, k_cache)
+    d = _pair(k_cache, v_cache, code == KV_INT4)
     if (code in (KV_INT8, KV_INT4)) != (scales is not None):
         raise PagedKVError("an INT8 or INT4 cache is copied with its scales; other caches take none")
     if scales is not None:
         _need_cuda_contig("scales", scales)
         _scales_shape(k_cache, scales, code)
-    if code == KV_INT4:
-        d.head_size *= 2
     rc = load_library().pkv_copy_blocks(_ptr(k_cache), _ptr(v_cache), _ptr(scales), code,
                                         ctypes.byref(d), _ptr(src), _ptr(dst), int(src.numel()),
                                         _ptr(device_status), _stream_handle(stream, k_cache.device))

@@ -74,6 +74,24 @@ def test_workspace_of_an_int4_cache_is_of_its_head_size(monkeypatch, d):
     assert asked == [d] * 4
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", [torch.int8, torch.float8_e5m2, torch.float16])
+def test_other_tensors_named_an_int4_cache_are_refused(no_gpu, d, dtype):
+    k = torch.zeros((3, 2, 16, d // 2), dtype=torch.uint8).to(dtype)
+    v, sc = k.clone(), pkv.alloc_kv_scales(3, 2, "cpu", kv_dtype="int4", head_size=d)
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32)
+    x, slots = torch.zeros((4, 2, d), dtype=torch.float16), i32(0, 1, 2, 3)
+    q, tables, lens = torch.zeros((4, 8, d), dtype=torch.float16), i32(0, 1, 2, 0).view(4, 1), i32(1, 1, 1, 1)
+    for call in (lambda: pkv.copy_blocks(k, v, i32(0), i32(1), "int4", scales=sc),
+                 lambda: pkv.kv_cache_accept(k, v, tables, lens, i32(0, 0, 0, 0).view(4, 1), lens, None, 1, "int4", scales=sc),
+                 lambda: pkv.kv_cache_write_int4(x, x, slots, k, v, sc),
+                 lambda: pkv.kv_cache_read(x, x, slots, k, v, "int4", scales=sc),
+                 lambda: pkv.paged_attention_decode_int4(q, q, k, v, sc, tables, lens, 1, 0.1),
+                 lambda: pkv.paged_attention_decode_chunked(q, q, [1] * 4, [1] * 4, k, v, tables, 0.1, "int4", scales=sc)):
+        with pytest.raises(pkv.PagedKVError, match="uint8"):
+            call()
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("d", [64, 128])
 def test_a_workspace_of_the_told_size_serves_the_call(d):
