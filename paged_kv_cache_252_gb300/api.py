@@ -173,15 +173,22 @@ def _check(rc: int, what: str):
 
 
 def _kv_code(kv_dtype, cache: torch.Tensor) -> int:
+    """The cache's type: as named, which must have elements of the tensor's size (a wider one would lie
+    beyond the tensor), or by the tensor's dtype."""
     if kv_dtype is None:
         if cache.dtype is torch.uint8 and getattr(cache, "_pkv_int4", False):
             raise PagedKVError('calls on an INT4 cache name its type (kv_dtype="int4")')
         return _TORCH[cache.dtype]
     if isinstance(kv_dtype, str):
-        return _NAMES[kv_dtype]
-    if isinstance(kv_dtype, torch.dtype):
-        return _TORCH[kv_dtype]
-    return int(kv_dtype)
+        code = _NAMES[kv_dtype]
+    elif isinstance(kv_dtype, torch.dtype):
+        code = _TORCH[kv_dtype]
+    else:
+        code = int(kv_dtype)
+    if 0 <= code <= KV_INT4 and cache.element_size() != (2 if code <= KV_BF16 else 1):
+        raise PagedKVError(f"a {cache.dtype} tensor is no cache of type {kv_dtype}" +
+                           (" (torch.uint8)" if code == KV_INT4 else ""))
+    return code
 
 
 def _src_code(t: torch.Tensor) -> int:

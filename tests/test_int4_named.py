@@ -92,6 +92,33 @@ def test_other_tensors_named_an_int4_cache_are_refused(no_gpu, d, dtype):
             call()
 
 
+@pytest.mark.parametrize("held,named", [(a, b) for a in ("fp16", "bf16", "e5m2", "int8") for b in ("fp16", "bf16", "e5m2", "int8", "int4")
+                                        if (a in ("fp16", "bf16")) != (b in ("fp16", "bf16"))])
+def test_a_cache_named_wider_or_narrower_than_it_is_is_refused(no_gpu, held, named):
+    """Elements twice as large as the tensor's would lie beyond it."""
+    d = 64
+    k, v = pkv.alloc_kv_cache(3, 2, d, held, "cpu")
+    sc = pkv.alloc_kv_scales(3, 2, "cpu") if named == "int8" else (
+        torch.zeros((3, 2, 2, 16, 2, 2), dtype=torch.float16) if named == "int4" else None)
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32)
+    head = 2 * d if named == "int4" else d
+    x, slots = torch.zeros((4, 2, head), dtype=torch.float16), i32(0, 1, 2, 3)
+    q, tables, lens, cu = torch.zeros((4, 8, head), dtype=torch.float16), i32(0, 1, 2, 0).view(4, 1), i32(1, 1, 1, 1), i32(0, 1, 2, 3, 4)
+    for call in (lambda: pkv.copy_blocks(k, v, i32(0), i32(1), named, scales=sc),
+                 lambda: pkv.kv_cache_accept(k, v, tables, lens, i32(0, 0, 0, 0).view(4, 1), lens, None, 1, named, scales=sc),
+                 lambda: pkv.kv_cache_write(x, x, slots, k, v, named),
+                 lambda: pkv.kv_cache_read(x, x, slots, k, v, named, scales=sc),
+                 lambda: pkv.paged_attention_decode(q, q, k, v, tables, lens, 1, 0.1, named),
+                 lambda: pkv.paged_attention_decode_noalloc(q, q, k, v, tables, lens, 1, 0.1, named),
+                 lambda: pkv.paged_attention_decode_varlen(q, q, cu, k, v, tables, lens, 1, 0.1, named, scales=sc),
+                 lambda: pkv.paged_attention_decode_tree(q, q, slots.long(), k, v, tables, lens, 1, 0.1, named, scales=sc),
+                 lambda: pkv.paged_attention_decode_chunked(q, q, [1] * 4, [1] * 4, k, v, tables, 0.1, named, scales=sc),
+                 lambda: pkv.paged_attention_prefill(q, q, cu, k, v, tables, lens, 0.1, named, scales=sc),
+                 lambda: pkv.rotary_write(q, q, x, x, slots, slots, k, v, torch.ones(8, dtype=torch.float64), named, scales=sc)):
+        with pytest.raises(pkv.PagedKVError):
+            call()
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("d", [64, 128])
 def test_a_workspace_of_the_told_size_serves_the_call(d):
