@@ -347,8 +347,10 @@ int pkv_kv_cache_write_int4(const void* key, const void* value, pkv_dtype src_dt
                             const pkv_cache_desc* cache, int32_t* device_status, void* stream);
 
 /* Rows of a cache of any type read back by slot: key/value [num_tokens][num_kv_heads][head_size]
- * fp16 or bf16 (dst_dtype) become the values that the cache stands for, rounded once to
- * dst_dtype (beyond its range: an infinity). A slot of -1 leaves its rows as they are, as do other
+ * fp16 or bf16 (dst_dtype) become the values that the cache stands for, rounded to dst_dtype
+ * (beyond its range: an infinity). INT8 values (code times scale), and INT4 values read as bf16,
+ * are rounded to fp32 first: beside a border of dst_dtype they may be off by 2^-24 more than half a
+ * step. A slot of -1 leaves its rows as they are, as do other
  * slots out of range (flagged); a slot may occur any number of times. scales: of an INT8 or INT4
  * cache, else NULL. key and value must not overlap each other or an input. */
 int pkv_kv_cache_read(void* key, void* value, pkv_dtype dst_dtype, int32_t num_tokens, const int32_t* slot_mapping,
