@@ -758,9 +758,11 @@ __global__ void __launch_bounds__(Sh::THREADS, Sh::CTAS) decode_int4_kernel(cons
         lds_words<G>(at[b] + v_off1 + 8 * T::RB, w[b][3]);
       }
 
-      // ---- scales; scores before the row's factor ----
+      // ---- scales; scores ----
       float sv[NB][2][GS], zv[NB][2][GS];
-      float sc[NB][NT][4];   // [2 x + e]: token tok + 8 x, row 2 c4 + e
+      // [2 x + e]: token tok + 8 x, row 2 c4 + e. Rounded: a product that m were taken off unrounded would differ from the rounded one
+      // in m by half its last place, which for scores beyond 2^26 passes the range of p.
+      float sc[NB][NT][4];
       bool hid[NB][NT][4];   // (all false without a mask)
 #pragma unroll
       for (int b = 0; b < NB; ++b)
@@ -783,7 +785,7 @@ __global__ void __launch_bounds__(Sh::THREADS, Sh::CTAS) decode_int4_kernel(cons
             for (int g = 0; g < GS; ++g) sv[b][x][g] = zv[b][x][g] = 0.f;
           }
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+          for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               float v = zk[0] * qz[nt][0][e];
@@ -794,6 +796,10 @@ __global__ void __launch_bounds__(Sh::THREADS, Sh::CTAS) decode_int4_kernel(cons
               sc[b][nt][2 * x + e] = v;
               hid[b][nt][2 * x + e] = kMasked && !(there && (d < 0 || (d < 64 && ((vis_s[nt * 8 + row2 + e] >> d) & 1ull))));
             }
+            const float2 f = halves_of(mul2(f32x2(sc[b][nt][2 * x], sc[b][nt][2 * x + 1]), f32x2(rf[nt][0], rf[nt][1])));
+            sc[b][nt][2 * x] = f.x;
+            sc[b][nt][2 * x + 1] = f.y;
+          }
         }
 
       // ---- weights p = 2^(score - m) and P = p s; the reference moved where one is too large ----
@@ -807,9 +813,12 @@ __global__ void __launch_bounds__(Sh::THREADS, Sh::CTAS) decode_int4_kernel(cons
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-            for (int v = 0; v < 4; ++v) {
-              p[b][nt][v] = fast_exp2(fmaf(sc[b][nt][v], rf[nt][v & 1], -m_run[nt][v & 1]));
-              if (kMasked && hid[b][nt][v]) p[b][nt][v] = 0.f;
+            for (int x = 0; x < 2; ++x) {
+              const float2 d = halves_of(add2(f32x2(sc[b][nt][2 * x], sc[b][nt][2 * x + 1]), f32x2(-m_run[nt][0], -m_run[nt][1])));
+              p[b][nt][2 * x] = fast_exp2(d.x);
+              p[b][nt][2 * x + 1] = fast_exp2(d.y);
+              if (kMasked && hid[b][nt][2 * x]) p[b][nt][2 * x] = 0.f;
+              if (kMasked && hid[b][nt][2 * x + 1]) p[b][nt][2 * x + 1] = 0.f;
             }
 #pragma unroll
             for (int e = 0; e < 2; ++e) p2[b][nt][e] = p[b][nt][e] + p[b][nt][2 + e];
@@ -846,11 +855,11 @@ __global__ void __launch_bounds__(Sh::THREADS, Sh::CTAS) decode_int4_kernel(cons
             for (int b = 0; b < NB; ++b)
 #pragma unroll
               for (int x = 0; x < 2; ++x)
-                if (!hid[b][nt][2 * x + e]) mx = fmaxf(mx, fmaf(sc[b][nt][2 * x + e], rf[nt][e], ve[b][x]));
+                if (!hid[b][nt][2 * x + e]) mx = fmaxf(mx, __fadd_ru(sc[b][nt][2 * x + e], ve[b][x] - kInt4Shift));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-            const float m_new = fmaxf(m_run[nt][e], mx - kInt4Shift);
+            const float m_new = fmaxf(m_run[nt][e], mx);   // (rounded up: no P above 2^11)
             const float alpha = fast_exp2(m_run[nt][e] - m_new);
             m_run[nt][e] = m_new;
             l_run[nt][e] *= alpha;
