@@ -14,9 +14,9 @@
 // row is scaled at the end (V). The 8 is taken off by a product with a constant operand, over the same
 // rounded P, every few steps.
 //
-// Precision. q is scaled by a power of two per row so that its largest element lies in [2^11, 2^12):
-// fp16 then holds fp16 and bf16 queries (8 significant bits) exactly down to 2^-26 of the
-// largest. The running reference m of a row is of the score plus the exponent of the token's V scale, so
+// Precision. q is scaled by a power of two per row so that its largest element lies in [2^11, 2^12) (every other pair of
+// dimensions 16 times lower): fp16 then holds the 11 bits of an fp16 query exactly down to 2^-21 of the largest, a bf16
+// query's 8 down to 2^-24. The running reference m of a row is of the score plus the exponent of the token's V scale, so
 // that P, rounded to fp16, is at most 2^15 and keeps all its bits down to 2^-25 of the largest contribution
 // whatever the scales' size. m starts from and moves on exact maxima, but only when a P (or a p beside a
 // zero scale) passes the limit: a rare, warp-wide event.
@@ -164,6 +164,17 @@ constexpr float kInt4FarP = 1.0995116e12f;   // 2^40: a sum of two p that moves 
 // e with |s| < 2^e, at least -25 (a scale of 0); a NaN scale counts as 0, or it would push the row's other group out of range.
 __device__ __forceinline__ float int4_scale_exponent(float s) {
   return s == s ? fmaxf(static_cast<float>(static_cast<int>(__float_as_uint(fabsf(s)) >> 23) - 126), -25.f) : -25.f;
+}
+
+// ex of a row of queries, 2^ex <= its largest element < 2^(ex + 1), from -116 (rows below are scaled by 2^127, the most
+// there is) to 127 (an infinity or NaN counts as that and stays what it is); and the factor that undoes the row's scaling by
+// 2^(11 - ex) and the codes' by 2^-24.
+__device__ __forceinline__ int int4_q_exponent(float mx) {
+  return max(-116, min(127, static_cast<int>(__float_as_uint(mx) >> 23) - 127));
+}
+__device__ __forceinline__ float int4_q_factor(float scale_log2, int ex) {
+  const int e = min(13 + ex, 127);   // (2^(13 + ex) may pass fp32's range)
+  return scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * static_cast<float>(1 << (13 + ex - e));
 }
 
 // As mma_f16 and movmatrix_t, for the compiler to move between others.
@@ -590,8 +601,7 @@ __global__ void __launch_bounds__(Sh::THREADS, Sh::CTAS) decode_int4_kernel(cons
         for (int e = 0; e < E; ++e) mx = fmaxf(mx, fabsf(x[e]));
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        // 2^ex <= mx < 2^(ex + 1); rows beyond 2^+-100 keep a scale at which the factors are finite.
-        const int ex = max(-100, min(100, static_cast<int>(__float_as_uint(mx) >> 23) - 127));
+        const int ex = int4_q_exponent(mx);
         const float up = __uint_as_float(static_cast<uint32_t>(127 + 11 - ex) << 23);
         float sum = 0.f;
 #pragma unroll
@@ -607,7 +617,7 @@ __global__ void __launch_bounds__(Sh::THREADS, Sh::CTAS) decode_int4_kernel(cons
           *reinterpret_cast<uint32_t*>(qs + r * QS + (E * lane + e) * 2) = pack_f16x2(x[e] * f, x[e + 1] * f);
         }
         if (lane % (32 / G) == 0) qsum_s[r * G + lane / (32 / G)] = sum * 0x1p-24f;
-        if (lane == 0) rf_s[r] = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + 13 + ex) << 23);
+        if (lane == 0) rf_s[r] = int4_q_factor(a.scale_log2, ex);
       }
       __syncthreads();
 #pragma unroll
@@ -657,8 +667,7 @@ __global__ void __launch_bounds__(Sh::THREADS, Sh::CTAS) decode_int4_kernel(cons
         }
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        // 2^ex <= mx < 2^(ex + 1); rows beyond 2^+-100 keep a scale at which the factors are finite.
-        const int ex = max(-100, min(100, static_cast<int>(__float_as_uint(mx) >> 23) - 127));
+        const int ex = int4_q_exponent(mx);
         const float up = __uint_as_float(static_cast<uint32_t>(127 + 11 - ex) << 23);
         float sum[G];
 #pragma unroll
@@ -671,7 +680,7 @@ __global__ void __launch_bounds__(Sh::THREADS, Sh::CTAS) decode_int4_kernel(cons
             sum[k % G] += x0 + x1;
             qf[nt][k][m] = pack_f16x2(x0 * f, x1 * f);
           }
-        const float back = r < Rs ? a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + 13 + ex) << 23) : 0.f;
+        const float back = r < Rs ? int4_q_factor(a.scale_log2, ex) : 0.f;
 #pragma unroll
         for (int g = 0; g < G; ++g) {
           sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 1);
