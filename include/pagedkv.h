@@ -361,7 +361,9 @@ int pkv_kv_cache_read(void* key, void* value, pkv_dtype dst_dtype, int32_t num_t
  * for pkv_paged_attention_decode (cu_q_lens and tree_masks NULL), _varlen (cu_q_lens) and _tree
  * (tree_masks, with or without cu_q_lens; then max_q_per_seq <= 64). num_q_rows: rows of q / out (and tree_masks).
  * Workspace as for pkv_paged_attention_decode (pkv_decode_workspace_bytes). Rows of a sequence
- * beyond its context, and draft tokens that a row's mask hides, may hold anything. */
+ * beyond its context, and draft tokens that a row's mask hides, may hold anything. Weights times
+ * value scales are rounded to fp16, at one size for a row's groups and tokens: where a contribution
+ * p s is less than 2^-24 of the row's largest, it loses bits. */
 int pkv_paged_attention_decode_int4(void* out, const void* q, pkv_dtype q_dtype, const int32_t* cu_q_lens,
                                     const uint64_t* tree_masks, int32_t num_q_rows, int32_t num_seqs,
                                     int32_t num_q_heads, int32_t max_q_per_seq, const void* k_cache,
