@@ -21,6 +21,11 @@ _NAMES = {"fp16": KV_FP16, "bf16": KV_BF16, "e5m2": KV_E5M2, "fp8_e5m2": KV_E5M2
           "int4": KV_INT4}
 _TORCH = {torch.float16: KV_FP16, torch.bfloat16: KV_BF16, torch.uint8: KV_E5M2,
           torch.float8_e5m2: KV_E5M2, torch.int8: KV_INT8}
+# Types as calls name them, with the tensors' dtypes that hold them (a uint8 tensor without a name is looked at).
+_KNOWN = {(name, dt): code for named in (_NAMES.items(), _TORCH.items(), zip(range(5), range(5)))
+          for name, code in named
+          for dt in ((torch.float16, torch.bfloat16) if code <= KV_BF16 else (torch.uint8, torch.int8, torch.float8_e5m2))}
+_KNOWN.update({(None, dt): code for dt, code in _TORCH.items() if dt is not torch.uint8})
 BLOCK_SIZE = 16
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -175,6 +180,9 @@ def _check(rc: int, what: str):
 def _kv_code(kv_dtype, cache: torch.Tensor) -> int:
     """The cache's type: as named, which must have elements of the tensor's size (a wider one would lie
     beyond the tensor), or by the tensor's dtype."""
+    code = _KNOWN.get((kv_dtype, cache.dtype))
+    if code is not None:
+        return code
     if kv_dtype is None:
         if cache.dtype is torch.uint8 and getattr(cache, "_pkv_int4", False):
             raise PagedKVError('calls on an INT4 cache name its type (kv_dtype="int4")')
@@ -416,20 +424,20 @@ class _Scratch:
     """A buffer of calls that follow one another on a stream. Its first ``clean`` bytes hold nothing
     but piece counters, which every launch leaves clear; a call that has more of them clears the
     rest first."""
-    __slots__ = ("ws", "clean")
+    __slots__ = ("ws", "size", "clean")
 
     def __init__(self):
-        self.ws, self.clean = None, 0
+        self.ws, self.size, self.clean = None, 0, -1
 
     def take(self, nbytes: int, counters: int, dev: int) -> torch.Tensor:
-        ws = self.ws
-        if ws is None or ws.shape[0] < nbytes:
-            ws = self.ws = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
-            self.clean = 0
-        if self.clean < counters:
-            ws[self.clean:counters].zero_()
-        self.clean = counters
-        return ws
+        if self.clean != counters or self.size < nbytes:
+            if self.ws is None or self.size < nbytes:
+                self.size, self.clean = max(nbytes, 256), 0
+                self.ws = torch.empty(self.size, dtype=torch.uint8, device=dev)
+            if self.clean < counters:
+                self.ws[self.clean:counters].zero_()
+            self.clean = counters
+        return self.ws
 
 
 class _Capture:
@@ -449,14 +457,19 @@ _captures: dict = {}    # capture: _Capture
 def _scratch(kind: str, nbytes: int, counters: int, dev: int, stream) -> torch.Tensor:
     """Scratch of a call whose first ``counters`` bytes are its piece counters: one buffer per kind,
     device and stream that calls run on, grown as needed; a graph's own for captured calls."""
-    with _NOWHERE if stream is None else torch.cuda.stream(stream):
-        handle = _stream_of(stream, dev)
-        if torch.cuda.is_current_stream_capturing():
-            return _captured_scratch((kind, dev, handle), nbytes, counters)
-        s = _scratches.get((kind, dev, handle))
-        if s is None:
-            s = _scratches[kind, dev, handle] = _Scratch()
-        return s.take(nbytes, counters, dev)
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return _scratch_here((kind, dev, stream.cuda_stream), nbytes, counters)
+    return _scratch_here((kind, dev, _stream_of(None, dev)), nbytes, counters)
+
+
+def _scratch_here(key, nbytes: int, counters: int) -> torch.Tensor:
+    if torch.cuda.is_current_stream_capturing():
+        return _captured_scratch(key, nbytes, counters)
+    s = _scratches.get(key)
+    if s is None:
+        s = _scratches[key] = _Scratch()
+    return s.take(nbytes, counters, key[1])
 
 
 def _captured_scratch(key, nbytes: int, counters: int) -> torch.Tensor:

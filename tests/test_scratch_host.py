@@ -185,3 +185,12 @@ def test_a_size_that_could_not_be_told_is_asked_for_again(world, form, kv, monke
     _call(world, form, kv)
     ws = next(t for p, (t, _) in reversed(world.made) if p == world.calls[-1][0])()
     assert ws.shape[0] >= 2 * 4096
+
+
+@pytest.mark.parametrize("form,kv", [x for x in ALL if x[0] != "chunked"])
+def test_a_shape_that_the_library_refuses_gets_as_far_as_its_refusal(world, form, kv, monkeypatch):
+    for name in ("pkv_decode_workspace_bytes", "pkv_decode_counter_bytes"):
+        monkeypatch.setattr(Library, name, lambda self, *a: 0)
+    world.S = 0
+    _call(world, form, kv)
+    assert len(world.calls) == 1
