@@ -673,7 +673,7 @@ def paged_attention_decode_chunked(out, q, q_lens, context_lens, k_cache, v_cach
         if S and need == 0:
             raise PagedKVError("paged_attention_decode_chunked: unsupported shape")
         if workspace is None:
-            workspace = _scratch("decode", need, 0, q.get_device(), stream)   # (the call clears its counters itself)
+            workspace = _scratch("chunked", need, 0, q.get_device(), stream)   # (it clears its counters itself)
         rest = (ctypes.byref(d), _ptr(block_tables), mbs, float(scale), _ptr(workspace),
                 int(workspace.numel() * workspace.element_size()), _ptr(device_status),
                 _stream_handle(stream, q.device))
