@@ -23,8 +23,8 @@ Entry g_i4[kMaxDevices][2][5];   // [head size][rows]
 // One a kernel: two entries that share one would set its shared-memory limit in turn.
 int shape_index(int d, int rows) { return rows <= 4 && d == 128 ? 0 : rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 32 ? 3 : 4; }
 
-// Fixed cost of a unit's piece on the work line, in blocks: 12 leaves 64 sequences at 35 us and 32 rows at 405, 20 at 31 and
-// 351, 32 at 30 and 336, 56 at 31 and 350.
+// Fixed cost of a unit's piece on the work line, in blocks: 12 leaves 64 sequences at 34 us, 256 at 139 and 32 rows at 385, 20 at
+// 30.6, 130 and 359, 32 at 30, 127 and 347, 56 at 30.6, 131 and 357.
 constexpr int kPieceCostInt4 = 32;
 
 // Once per device, head size and shape: shared-memory limits of both query types' kernels and the CTAs an

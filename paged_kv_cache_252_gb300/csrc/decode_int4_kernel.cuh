@@ -28,13 +28,17 @@
 // lie; V words of two tokens are paired by byte permutes for O^T = V^T P^T. The tokens of a
 // block take the 16 product slots in an order in which both reads hit all banks.
 //
-// What bounds it. One query token of 4 heads a KV head: instructions, 247 a warp and block (64 of them the ANDs that
+// What bounds it. One query token of 4 heads a KV head: instructions, 248 a warp and block (64 of them the ANDs that
 // unpack), issued on 52 % of the cycles with three warps a scheduler, most stalls on fixed latencies: 4 sequences of 131072
-// tokens take 96 us, 5.3 TB/s, 79 % of the copy rate, where the bytes alone take 77 and fetching them without computing 86.
-// 32 rows: 743 instructions a block over its two row warps, two warps a scheduler: 343 us (128 sequences to 8192 tokens)
+// tokens take 95 us, 5.4 TB/s, 80 % of the copy rate, where the bytes alone take 77 and fetching them without computing 86.
+// 32 rows: 727 instructions a block over its two row warps, each of which unpacks every word for itself (128 ANDs where 64 would
+// do), two warps a scheduler, issued on 49 % of the cycles: 347 us (128 sequences to 8192 tokens)
 // where the bytes take 95, the products 37 and fetching with the pieces' ends 156. A tcgen05 form for more
 // than 16 rows (a token a thread, codes unpacked to tensor memory, a product a group and exact scales on the scores) took as
 // many instructions, 777, and 408 us; so did sixteen warps in place of eight.
+//
+// (Figures of forms that were not taken, here and below, stand beside what this one measured at the time: scores are rounded since,
+// two an instruction, at 247 -> 248 and 743 -> 727 instructions, 96 -> 95 and 343 -> 347 us.)
 #pragma once
 
 #include <cuda_bf16.h>
