@@ -337,8 +337,8 @@ class Prepared:
 
     def graph_of(self, n: int, body):
         """A CUDA graph of body(0), ..., body(n-1) (library calls only), captured on
-        a side stream. One call runs on that stream before the capture, so the
-        binding's workspace for it exists outside the capture."""
+        a side stream. One call runs on that stream before the capture, so that
+        its kernels are loaded and set up outside it."""
         cur = torch.cuda.current_stream(self.dev)
         s = torch.cuda.Stream(self.dev)
         s.wait_stream(cur)
@@ -547,7 +547,7 @@ def run_ours(args, rank, world, local):
             # into the capture, replayed once untimed and once timed.
             cap = torch.cuda.Stream(dev)
             cap.wait_stream(comp)
-            with torch.cuda.stream(cap):          # the binding's workspace for this stream, outside the capture
+            with torch.cuda.stream(cap):          # kernels loaded and set up outside the capture
                 P.decode(outs[0], qs[0], caches[0], P.bt, P.cl, P.cu)
             comp.wait_stream(cap)
             torch.cuda.synchronize(dev)

@@ -467,9 +467,18 @@ def _scratch_here(key, nbytes: int, counters: int) -> torch.Tensor:
     if torch.cuda.is_current_stream_capturing():
         return _captured_scratch(key, nbytes, counters)
     s = _scratches.get(key)
-    if s is None:
-        s = _scratches[key] = _Scratch()
+    if s is None or s.size < nbytes:
+        with _lock_captures:
+            _let_go(load_library())
+        if s is None:
+            s = _scratches[key] = _Scratch()
     return s.take(nbytes, counters, key[1])
+
+
+def _let_go(lib):
+    """Gives back the scratch of graphs that are gone (looked at whenever a buffer is about to be made)."""
+    for gone in [c for c, h in _captures.items() if lib.pkv_capture_gone(h.watch)]:
+        del _captures[gone]
 
 
 def _captured_scratch(key, nbytes: int, counters: int) -> torch.Tensor:
@@ -478,8 +487,7 @@ def _captured_scratch(key, nbytes: int, counters: int) -> torch.Tensor:
         _check(lib.pkv_capture_watch(key[2], ctypes.byref(capture), None), "capture")
         held = _captures.get(capture.value)
         if held is None:
-            for gone in [c for c, h in _captures.items() if lib.pkv_capture_gone(h.watch)]:
-                del _captures[gone]
+            _let_go(lib)
             _check(lib.pkv_capture_watch(key[2], ctypes.byref(capture), ctypes.byref(watch)), "capture")
             held = _captures[capture.value] = _Capture(watch.value)
         s = held.scratch.get(key)

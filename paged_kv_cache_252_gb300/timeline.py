@@ -89,7 +89,7 @@ def run(config: str, num_seqs: int = 0, iters: int = 5):
     side = torch.cuda.Stream()
     side.wait_stream(cur)
     with torch.cuda.stream(side):
-        decode()                 # the binding's workspace for this stream, outside the capture
+        decode()                 # kernels loaded and set up outside the capture
     cur.wait_stream(side)
     torch.cuda.synchronize()
     g = torch.cuda.CUDAGraph()

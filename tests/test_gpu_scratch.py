@@ -159,10 +159,14 @@ def test_a_graph_that_is_gone_gives_its_scratch_back():
         with torch.cuda.graph(g, stream=s):
             c()
         return g
-    g = capture()
-    g.replay()
-    torch.cuda.synchronize()
-    held = set(api._captures)
+    def captured():
+        before = set(api._captures)
+        g = capture()
+        g.replay()
+        torch.cuda.synchronize()
+        return g, set(api._captures) - before
+    (g, held), (kept, live) = captured(), captured()
+    assert len(held) == len(live) == 1 and held <= set(api._captures)
     del g
     gc.collect()
     for _ in range(50):      # (the driver reports it some time later)
@@ -171,7 +175,8 @@ def test_a_graph_that_is_gone_gives_its_scratch_back():
         if not held & set(api._captures):
             break
         torch.cuda._sleep(10_000_000)
-    assert not held & set(api._captures)
+    assert not held & set(api._captures) and live <= set(api._captures)
+    kept.replay()
 
 
 def _epoch(n):

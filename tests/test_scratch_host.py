@@ -162,6 +162,12 @@ def test_a_captured_call_shares_its_scratch_with_its_graph_alone(world, form, kv
     with world.on(Stream(21, 9)):
         _call(world, form, kv)
     assert all(t() is None for t in held) and live(p[4]) is not None
+    held = [weakref.ref(live(x)) for x in (p[4], p[6])]
+    world.gone.add(8)
+    _call(world, form, kv, S=3, stream=eager)                           # (nothing to make: not looked at)
+    assert all(t() is not None for t in held)
+    _call(world, form, kv, S=30, stream=eager)
+    assert all(t() is None for t in held)
 
 
 @pytest.mark.parametrize("captured", [False, True])
@@ -194,3 +200,18 @@ def test_a_shape_that_the_library_refuses_gets_as_far_as_its_refusal(world, form
     world.S = 0
     _call(world, form, kv)
     assert len(world.calls) == 1
+
+
+def test_counter_bytes_and_captures_on_the_host():
+    from paged_kv_cache_252_gb300 import build
+    lib = ctypes.CDLL(build.build())
+    lib.pkv_decode_counter_bytes.restype = ctypes.c_size_t
+    desc = lambda nb=8, bs=16, h=2, d=64: ctypes.byref(api._CacheDesc(nb, bs, h, d))
+    for kv in range(4):
+        assert lib.pkv_decode_counter_bytes(5, 8, 1, desc(), kv) == 256 and lib.pkv_decode_counter_bytes(33, 8, 4, desc(), kv) == 768
+        assert lib.pkv_decode_counter_bytes(0, 8, 1, desc(), kv) == 0
+    for bad in ((-1, 8, 1, desc(), 0), (5, 0, 1, desc(), 0), (5, 7, 1, desc(), 0), (5, 8, 0, desc(), 0), (5, 8, 17, desc(), 0),
+                (5, 8, 1, None, 0), (5, 8, 1, desc(d=96), 0), (5, 8, 1, desc(bs=8), 0), (5, 8, 1, desc(nb=0), 0), (5, 8, 1, desc(), 5)):
+        assert lib.pkv_decode_counter_bytes(*bad) == 0
+    assert lib.pkv_capture_watch(None, None, None) == -1
+    assert lib.pkv_capture_gone(None) == 0
