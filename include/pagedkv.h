@@ -117,7 +117,7 @@ size_t pkv_decode_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t
 /*
  * pkv_decode_counter_bytes — the bytes at the start of that buffer that hold the counters of a
  * call over a cache of type kv_dtype: what to zero in a buffer that held other data. Every launch
- * leaves them clear. Returns 0 on invalid arguments.
+ * that completes leaves them clear. Returns 0 on invalid arguments.
  */
 size_t pkv_decode_counter_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t q_per_seq,
                                 const pkv_cache_desc* cache, pkv_dtype kv_dtype);
@@ -639,7 +639,7 @@ int pkv_copy_blocks(void* k_cache, void* v_cache, float* scales, pkv_dtype kv_dt
  * 0 if it is not being captured. If it is and watch is not NULL, *watch becomes a handle that
  * watches the graph being captured. pkv_capture_gone: 1 once that graph and every executable
  * graph made from it are destroyed; the handle is then released and must not be used again.
- * Else 0. The driver reports the end some time after the last of them was destroyed. */
+ * Else 0. CUDA reports the end some time after the last of them was destroyed. */
 int pkv_capture_watch(void* stream, uint64_t* id, void** watch);
 int pkv_capture_gone(void* watch);
 

@@ -1,5 +1,5 @@
 // Graphs under capture and their end (declared in include/pagedkv.h). The watch is a user object
-// of the captured graph: the driver holds it for the graph and for its executables and calls
+// of the captured graph: CUDA holds it for the graph and for its executables and calls
 // ended() from a thread of its own when the last of them goes.
 #include <cuda_runtime.h>
 

@@ -169,7 +169,7 @@ def test_a_graph_that_is_gone_gives_its_scratch_back():
     assert len(held) == len(live) == 1 and held <= set(api._captures)
     del g
     gc.collect()
-    for _ in range(50):      # (the driver reports it some time later)
+    for _ in range(50):      # (CUDA reports it some time later)
         torch.cuda.synchronize()
         g = capture()
         if not held & set(api._captures):
